@@ -14,6 +14,7 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+CSRC_TRAIN = os.path.join(CSRC, "train")  # operators beside the layer: gated scan, AdamW, gradient norm
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libwtconv.so")
@@ -30,7 +31,7 @@ def nvcc() -> str:
 
 
 def sources() -> list[str]:
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    return sorted(glob.glob(os.path.join(CSRC, "*.cu"))) + sorted(glob.glob(os.path.join(CSRC_TRAIN, "*.cu")))
 
 
 def _stale(target: str, deps: list[str]) -> bool:
@@ -42,8 +43,8 @@ def _stale(target: str, deps: list[str]) -> bool:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     srcs = sources()
-    headers = glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h"))
+    headers = [h for d in (CSRC, CSRC_TRAIN, INCLUDE) for pat in ("*.h", "*.cuh")
+               for h in glob.glob(os.path.join(d, pat))]
     if not force and not _stale(LIB, srcs + headers + [__file__]):
         return LIB
     os.makedirs(BUILD, exist_ok=True)

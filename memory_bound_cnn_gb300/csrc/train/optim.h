@@ -1,0 +1,44 @@
+// Tensor tables and launch functions of the AdamW step and the gradient norm.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "train_common.h"
+#include "wtconv_optim.h"
+
+namespace wtconv {
+
+constexpr int kChunk = 2048;  // elements of one work item: eight warps, one 8-bit block each
+
+// The tensors of one launch, passed as a kernel parameter (constant memory: no upload, and a
+// captured graph keeps its own copy).  first[i] is tensor i's first chunk; first[count] the total.
+template <int CAP> struct TensorTable {
+    wtconv_optim_tensor t[CAP];
+    int first[CAP + 1];
+    int count;
+};
+// Two capacities: a table of 24 keeps the parameter block of a small model small (a launch copies
+// all of it), one of 448 is the most that fits the 32,764 bytes of a kernel's parameters.
+constexpr int kSmallTable = 24, kLargeTable = 448;
+
+struct StepScalars {
+    float beta1, one_minus_beta1, beta2, one_minus_beta2;
+    float keep;       // 1 - lr weight_decay
+    float rate;       // lr / (1 - beta1^t)
+    float root_scale; // 1 / sqrt(1 - beta2^t)
+    float eps;
+    uint32_t threshold0;  // t K2, the step's part of the rounding threshold
+    int state_bits, grad_dtype, copy_dtype;
+};
+
+// Part of the norm: chunks of one table summed into `blocks` doubles at part.
+int norm_blocks(long long chunks);
+
+template <int CAP> cudaError_t launch_adamw(const TensorTable<CAP> &table, const StepScalars &s, const float *clip, cudaStream_t st);
+template <int CAP>
+cudaError_t launch_norm_part(const TensorTable<CAP> &table, int grad_dtype, double *part, int blocks, cudaStream_t st);
+cudaError_t launch_norm_final(const double *part, int count, double max_norm, float *out, cudaStream_t st);
+// param / copy of each descriptor stand for m_out / v_out
+template <int CAP> cudaError_t launch_state_values(const TensorTable<CAP> &table, cudaStream_t st);
+
+}  // namespace wtconv

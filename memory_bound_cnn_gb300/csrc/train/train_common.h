@@ -1,0 +1,32 @@
+// Host-side helpers shared by the operators beside the WTConv layer (gated scan, AdamW, norm).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <stdlib.h>
+
+#include "wtconv.h"
+
+namespace wtconv {
+
+inline int elem_bytes_of(int dtype) { return dtype == WTCONV_F32 ? 4 : 2; }
+inline bool dtype_ok(int dtype) { return dtype == WTCONV_F32 || dtype == WTCONV_BF16 || dtype == WTCONV_F16; }
+inline bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline bool fault_injected() {
+    const char *e = getenv("WTCONV_INJECT_FAULT");
+    return e != nullptr && e[0] == '1';
+}
+inline int status_of(cudaError_t e) { return e == cudaSuccess ? WTCONV_OK : WTCONV_ERR_CUDA; }
+
+// SMs of the current device (148 if it cannot be asked: a plan is then only less balanced)
+inline int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
+        cudaGetLastError();
+        return 148;
+    }
+    return sms;
+}
+
+}  // namespace wtconv

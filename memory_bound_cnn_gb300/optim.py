@@ -1,0 +1,188 @@
+"""Python binding of the AdamW step and the gradient norm (include/wtconv_optim.h).
+
+``AdamW`` is the object a training program builds once over its parameters and their gradient
+buffers: it checks them, keeps their states and the descriptors that the library reads, and every
+step is one call.  It marshals arguments only; the update runs in the library's CUDA kernels.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from .wtconv import DTYPE_CODE, _on, _raise, _stream, load
+
+ADAMW_BLOCK = 256  # WTCONV_ADAMW_BLOCK
+
+EXPORTED = ("wtconv_adamw_step", "wtconv_adamw_state_values", "wtconv_grad_norm", "wtconv_grad_norm_workspace_size")
+
+
+class OptimTensor(ctypes.Structure):
+    """wtconv_optim_tensor."""
+
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "m", "v", "m_max", "v_max", "copy")] + \
+        [("n", ctypes.c_longlong)]
+
+
+class AdamWConfig(ctypes.Structure):
+    """wtconv_adamw_config."""
+
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + \
+        [("step", ctypes.c_longlong)] + [(n, ctypes.c_int) for n in ("state_bits", "grad_dtype", "copy_dtype")]
+
+
+_lib = None
+
+
+def _load() -> ctypes.CDLL:
+    global _lib
+    if _lib is None:
+        lib = load()
+        i, vp, sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+        tensors = ctypes.POINTER(OptimTensor)
+        lib.wtconv_adamw_step.restype = i
+        lib.wtconv_adamw_step.argtypes = [i, tensors, ctypes.POINTER(AdamWConfig), vp, vp]
+        lib.wtconv_adamw_state_values.restype = i
+        lib.wtconv_adamw_state_values.argtypes = [i, tensors, ctypes.POINTER(vp), ctypes.POINTER(vp), vp]
+        lib.wtconv_grad_norm_workspace_size.restype = sz
+        lib.wtconv_grad_norm_workspace_size.argtypes = [i, tensors]
+        lib.wtconv_grad_norm.restype = i
+        lib.wtconv_grad_norm.argtypes = [i, tensors, i, ctypes.c_double, vp, vp, sz, vp]
+        _lib = lib
+    return _lib
+
+
+class AdamW:
+    """AdamW over many tensors in one call per step.
+
+    params: contiguous fp32 CUDA tensors, updated in place.  grads: one contiguous tensor per
+    parameter, of its size and one dtype (fp32, bf16 or fp16); the buffers that the backward
+    writes each step (``set_grads`` if they move).  copies: optional 16-bit working copies of the
+    parameters, rewritten by each step (None entries: no copy).  state_bits: 32 or 8.
+    states: adopt existing ones, as ``state_dict`` gives them (they are used in place), ``count``
+    steps having been taken.
+    """
+
+    def __init__(self, params, grads, state_bits=32, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+                 copies=None, states=None, count=0):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("no parameters")
+        if state_bits not in (32, 8):
+            raise ValueError(f"state_bits must be 32 or 8, not {state_bits}")
+        self.state_bits, self.count = state_bits, int(count)
+        self.device = self.params[0].device
+        n = len(self.params)
+        self._tensors = (OptimTensor * n)()
+        for k, p in enumerate(self.params):
+            self._check(p, f"params[{k}]", torch.float32, p.numel())
+            self._tensors[k].param, self._tensors[k].n = p.data_ptr(), p.numel()
+        self.copies = [None] * n if copies is None else list(copies)
+        if len(self.copies) != n:
+            raise ValueError(f"{len(self.copies)} copies for {n} parameters")
+        kinds = {c.dtype for c in self.copies if c is not None}
+        if len(kinds) > 1 or kinds - {torch.bfloat16, torch.float16}:
+            raise ValueError(f"copies must all be bf16 or all fp16, not {kinds}")
+        for k, c in enumerate(self.copies):
+            if c is not None:
+                self._check(c, f"copies[{k}]", c.dtype, self.params[k].numel())
+                self._tensors[k].copy = c.data_ptr()
+        if states is None:
+            states = self._new_states()
+        self.states = {name: list(ts) for name, ts in states.items()}
+        want = self._state_layout()
+        if set(self.states) != set(want):
+            raise ValueError(f"states hold {sorted(self.states)}, expected {sorted(want)}")
+        for name, (dtype, per) in want.items():
+            if len(self.states[name]) != n:
+                raise ValueError(f"{len(self.states[name])} states {name} for {n} parameters")
+            for k, t in enumerate(self.states[name]):
+                self._check(t, f"states[{name!r}][{k}]", dtype, -(-self.params[k].numel() // per))
+                setattr(self._tensors[k], name, t.data_ptr())
+        copy_dtype = DTYPE_CODE[kinds.pop()] if kinds else 0
+        self._config = AdamWConfig(lr, betas[0], betas[1], eps, weight_decay, 0, state_bits, 0, copy_dtype)
+        self.set_grads(grads)
+
+    def _check(self, t, name, dtype, numel):
+        if not t.is_cuda or t.device != self.device or t.dtype != dtype or t.numel() != numel or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements on {self.device}")
+
+    def _state_layout(self):
+        if self.state_bits == 32:
+            return {"m": (torch.float32, 1), "v": (torch.float32, 1)}
+        return {"m": (torch.int8, 1), "v": (torch.uint8, 1), "m_max": (torch.float32, ADAMW_BLOCK),
+                "v_max": (torch.float32, ADAMW_BLOCK)}
+
+    def _new_states(self):
+        return {name: [torch.zeros(-(-p.numel() // per), dtype=dtype, device=self.device) for p in self.params]
+                for name, (dtype, per) in self._state_layout().items()}
+
+    def set_grads(self, grads):
+        """Take the gradients from these buffers from now on."""
+        grads = list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
+        dtype = grads[0].dtype
+        if dtype not in DTYPE_CODE:
+            raise ValueError(f"gradients have unsupported dtype {dtype}")
+        for k, g in enumerate(grads):
+            self._check(g, f"grads[{k}]", dtype, self.params[k].numel())
+        for k, g in enumerate(grads):
+            self._tensors[k].grad = g.data_ptr()
+        self.grads = grads
+        self._config.grad_dtype = DTYPE_CODE[dtype]
+        self._norm_bytes = _load().wtconv_grad_norm_workspace_size(len(self.params), self._tensors)
+
+    def state_dict(self):
+        return {"states": self.states, "count": self.count}
+
+    def grad_norm(self, max_norm=float("inf"), out=None, workspace=None, stream=None) -> torch.Tensor:
+        """Device tensor (norm, factor): the norm over every gradient and the factor that limits it
+        to max_norm (NaN where the norm is not finite), for ``step(clip=...)``."""
+        if out is None:
+            out = torch.empty(2, dtype=torch.float32, device=self.device)
+        self._check(out, "out", torch.float32, 2)
+        with _on(self.device, stream, workspace):
+            if workspace is None:
+                workspace = torch.empty(self._norm_bytes, dtype=torch.uint8, device=self.device)
+            rc = _load().wtconv_grad_norm(len(self.params), self._tensors, self._config.grad_dtype, max_norm,
+                                          out.data_ptr(), workspace.data_ptr(),
+                                          workspace.numel() * workspace.element_size(), _stream(stream))
+        _raise(rc, "wtconv_grad_norm")
+        return out
+
+    def step(self, clip=None, lr=None, count=None, stream=None) -> None:
+        """One update of every parameter.  clip: what ``grad_norm`` returned (a factor that is not
+        finite leaves everything as it is).  count: the step's number, from 1 (default: the next)."""
+        config = self._config
+        if lr is not None:
+            config.lr = lr
+        config.step = self.count + 1 if count is None else count
+        clip_p = None
+        if clip is not None:
+            self._check(clip, "clip", torch.float32, 2)
+            clip_p = clip.data_ptr() + 4
+        with _on(self.device, stream, None):
+            rc = _load().wtconv_adamw_step(len(self.params), self._tensors, config, clip_p, _stream(stream))
+        _raise(rc, "wtconv_adamw_step")
+        self.count = config.step
+
+    def state_values(self, m_out=None, v_out=None, stream=None):
+        """The averages (m, v) as lists of fp32 tensors: the states themselves in 32 bits, else what
+        the 8-bit codes stand for, written to m_out and v_out (lists of fp32 tensors; new ones if
+        not given)."""
+        if self.state_bits == 32:
+            return self.states["m"], self.states["v"]
+        outs = []
+        for given, name in ((m_out, "m_out"), (v_out, "v_out")):
+            outs.append([torch.empty(p.numel(), dtype=torch.float32, device=self.device) for p in self.params]
+                        if given is None else list(given))
+            if len(outs[-1]) != len(self.params):
+                raise ValueError(f"{len(outs[-1])} tensors in {name} for {len(self.params)} parameters")
+            for k, t in enumerate(outs[-1]):
+                self._check(t, f"{name}[{k}]", torch.float32, self.params[k].numel())
+        pointers = [(ctypes.c_void_p * len(self.params))(*[t.data_ptr() for t in ts]) for ts in outs]
+        with _on(self.device, stream, None):
+            rc = _load().wtconv_adamw_state_values(len(self.params), self._tensors, *pointers, _stream(stream))
+        _raise(rc, "wtconv_adamw_state_values")
+        return outs[0], outs[1]
