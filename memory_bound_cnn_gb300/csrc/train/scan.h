@@ -26,9 +26,13 @@ struct ScanArgs {
     void *workspace;
 };
 
-size_t scan_workspace(int op, const ScanArgs &a);
-cudaError_t launch_scan_forward(const ScanArgs &a, cudaStream_t st);
-cudaError_t launch_scan_backward(const ScanArgs &a, cudaStream_t st);
+// planes (scan_planes.cu) and tokens (scan_tokens.cu)
+size_t scan_planes_workspace(int op, const ScanArgs &a);
+cudaError_t launch_scan_planes_forward(const ScanArgs &a, cudaStream_t st);
+cudaError_t launch_scan_planes_backward(const ScanArgs &a, cudaStream_t st);
+size_t scan_tokens_workspace(int op, const ScanArgs &a);
+cudaError_t launch_scan_tokens_forward(const ScanArgs &a, cudaStream_t st);
+cudaError_t launch_scan_tokens_backward(const ScanArgs &a, cudaStream_t st);
 cudaError_t launch_scan_step(int B, int C, int dtype, const ScanTensor &x, const ScanTensor &gate, const float *gate_bias,
                              float *pool, int n_states, const int *slots, const ScanTensor &y, cudaStream_t st);
 

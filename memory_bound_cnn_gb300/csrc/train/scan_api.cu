@@ -40,6 +40,10 @@ ScanArgs shape_args(int B, int T, int C, int layout, int dtype) {
     return a;
 }
 
+size_t scan_workspace(int op, const ScanArgs &a) {
+    return a.layout == WTCONV_SCAN_PLANES ? scan_planes_workspace(op, a) : scan_tokens_workspace(op, a);
+}
+
 int check_workspace(int op, const ScanArgs &a, const void *workspace, size_t bytes) {
     const size_t need = scan_workspace(op, a);
     if (need == 0) return WTCONV_OK;
@@ -73,7 +77,8 @@ int wtconv_scan_forward(int B, int T, int C, int layout, int dtype, const void *
     a.workspace = workspace;
     if ((rc = check_workspace(WTCONV_SCAN_OP_FORWARD, a, workspace, workspace_bytes)) != WTCONV_OK) return rc;
     if (fault_injected()) return WTCONV_ERR_INJECTED;
-    return status_of(launch_scan_forward(a, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return status_of(layout == WTCONV_SCAN_PLANES ? launch_scan_planes_forward(a, st) : launch_scan_tokens_forward(a, st));
 }
 
 int wtconv_scan_backward(int B, int T, int C, int layout, int dtype, const void *x, long long x_batch, long long x_row,
@@ -96,7 +101,8 @@ int wtconv_scan_backward(int B, int T, int C, int layout, int dtype, const void 
     a.d_gate_bias = d_gate_bias, a.d_h0 = d_h0, a.workspace = workspace;
     if ((rc = check_workspace(WTCONV_SCAN_OP_BACKWARD, a, workspace, workspace_bytes)) != WTCONV_OK) return rc;
     if (fault_injected()) return WTCONV_ERR_INJECTED;
-    return status_of(launch_scan_backward(a, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return status_of(layout == WTCONV_SCAN_PLANES ? launch_scan_planes_backward(a, st) : launch_scan_tokens_backward(a, st));
 }
 
 int wtconv_scan_step(int B, int C, int dtype, const void *x, long long x_row, const void *gate, long long gate_row,

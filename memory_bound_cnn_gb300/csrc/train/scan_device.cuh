@@ -1,4 +1,4 @@
-// Arithmetic of the gated scan (wtconv_scan.h).
+// Arithmetic of the gated scan (wtconv_scan.h) and its loads and stores.
 #pragma once
 
 #include "scan.h"
@@ -12,10 +12,15 @@ namespace wtconv {
 struct Gate {
     float a, b;
 };
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
 __device__ __forceinline__ Gate gate_of(float z) {
     const float e = __expf(-z);
     Gate g;
-    g.a = __frcp_rn(1.f + e);
+    g.a = reciprocal(1.f + e);
     g.b = e > 1.f ? 1.f - g.a : e * g.a;
     return g;
 }
@@ -26,5 +31,91 @@ __device__ __forceinline__ int scan_length(const int *lengths, int b, int T) {
     const int n = lengths[b];
     return n < 0 ? 0 : (n < T ? n : T);
 }
+
+// A stretch of the recurrence as the map h -> a h + u of the state before it; `then` appends the
+// stretch that follows.
+struct Span {
+    float a, u;
+    __device__ __forceinline__ Span then(Span next) const { return {a * next.a, fmaf(next.a, u, next.u)}; }
+    __device__ __forceinline__ float of(float h) const { return fmaf(a, h, u); }
+};
+
+// Inclusive scan of spans over groups of WIDTH lanes: forward (lane l ends with lanes 0..l), or
+// backward (lanes WIDTH-1 down to l).
+template <int WIDTH, bool BACKWARD> __device__ __forceinline__ Span warp_scan(Span s, int lane) {
+#pragma unroll
+    for (int d = 1; d < WIDTH; d <<= 1) {
+        Span o;
+        o.a = BACKWARD ? __shfl_down_sync(0xffffffffu, s.a, d, WIDTH) : __shfl_up_sync(0xffffffffu, s.a, d, WIDTH);
+        o.u = BACKWARD ? __shfl_down_sync(0xffffffffu, s.u, d, WIDTH) : __shfl_up_sync(0xffffffffu, s.u, d, WIDTH);
+        const int l = lane & (WIDTH - 1);
+        if (BACKWARD ? l + d < WIDTH : l >= d) s = o.then(s);
+    }
+    return s;
+}
+// The scan's result of the lane before (after, if BACKWARD): the identity for the first.
+template <int WIDTH, bool BACKWARD> __device__ __forceinline__ Span lane_before(Span s, int lane) {
+    Span o;
+    o.a = BACKWARD ? __shfl_down_sync(0xffffffffu, s.a, 1, WIDTH) : __shfl_up_sync(0xffffffffu, s.a, 1, WIDTH);
+    o.u = BACKWARD ? __shfl_down_sync(0xffffffffu, s.u, 1, WIDTH) : __shfl_up_sync(0xffffffffu, s.u, 1, WIDTH);
+    const int l = lane & (WIDTH - 1);
+    if (BACKWARD ? l == WIDTH - 1 : l == 0) o = {1.f, 0.f};
+    return o;
+}
+
+// Eight consecutive elements as raw words, and as fp32.
+template <typename T> struct Eight {
+    uint32_t w[2 * sizeof(T)];
+    __device__ __forceinline__ float get(int j) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+        else {
+            const uint16_t h = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+            return to_f32(*reinterpret_cast<const T *>(&h));
+        }
+    }
+    __device__ __forceinline__ void set(int j, float a, float b) {  // elements j (even) and j + 1
+        if constexpr (sizeof(T) == 4) {
+            w[j] = __float_as_uint(a), w[j + 1] = __float_as_uint(b);
+        } else {
+            const T lo = from_f32<T>(a), hi = from_f32<T>(b);
+            w[j >> 1] = (uint32_t)*reinterpret_cast<const uint16_t *>(&lo) |
+                        (uint32_t)*reinterpret_cast<const uint16_t *>(&hi) << 16;
+        }
+    }
+    // elements 0 .. valid-1 from p (all of them: vectors if VEC); the rest zeros
+    template <bool VEC> __device__ __forceinline__ void load(const T *p, int valid) {
+        if (VEC && valid >= 8) {
+#pragma unroll
+            for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
+                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p) + k);
+                w[4 * k] = q.x, w[4 * k + 1] = q.y, w[4 * k + 2] = q.z, w[4 * k + 3] = q.w;
+            }
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < 2 * (int)sizeof(T); ++k) w[k] = 0;
+        if (valid <= 0) return;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j >= valid) continue;
+            if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(p[j]);
+            else w[j >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t *>(p + j) << (16 * (j & 1));
+        }
+    }
+    template <bool VEC> __device__ __forceinline__ void store(T *p, int valid) const {
+        if (VEC && valid >= 8) {
+#pragma unroll
+            for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+                reinterpret_cast<uint4 *>(p)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j >= valid) continue;
+            if constexpr (sizeof(T) == 4) p[j] = __uint_as_float(w[j]);
+            else *reinterpret_cast<uint16_t *>(p + j) = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+        }
+    }
+};
 
 }  // namespace wtconv

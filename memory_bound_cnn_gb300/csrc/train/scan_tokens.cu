@@ -107,11 +107,11 @@ __global__ void __launch_bounds__(256) scan_step_kernel(int C, int parts, ScanTe
 
 }  // namespace
 
-size_t scan_workspace(int op, const ScanArgs &a) {
+size_t scan_tokens_workspace(int op, const ScanArgs &a) {
     return op == WTCONV_SCAN_OP_BACKWARD ? ((size_t)a.B * a.C * sizeof(float) + 255) / 256 * 256 : 0;
 }
 
-cudaError_t launch_scan_forward(const ScanArgs &a, cudaStream_t st) {
+cudaError_t launch_scan_tokens_forward(const ScanArgs &a, cudaStream_t st) {
     const unsigned grid = (unsigned)(((long long)a.B * a.C + kRowThreads - 1) / kRowThreads);
     if (a.dtype == WTCONV_F32) scan_rows_forward_kernel<float><<<grid, kRowThreads, 0, st>>>(a);
     else if (a.dtype == WTCONV_BF16) scan_rows_forward_kernel<__nv_bfloat16><<<grid, kRowThreads, 0, st>>>(a);
@@ -119,7 +119,7 @@ cudaError_t launch_scan_forward(const ScanArgs &a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_scan_backward(const ScanArgs &a, cudaStream_t st) {
+cudaError_t launch_scan_tokens_backward(const ScanArgs &a, cudaStream_t st) {
     const unsigned grid = (unsigned)(((long long)a.B * a.C + kRowThreads - 1) / kRowThreads);
     if (a.dtype == WTCONV_F32) scan_rows_backward_kernel<float><<<grid, kRowThreads, 0, st>>>(a);
     else if (a.dtype == WTCONV_BF16) scan_rows_backward_kernel<__nv_bfloat16><<<grid, kRowThreads, 0, st>>>(a);
