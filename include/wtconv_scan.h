@@ -46,9 +46,9 @@ enum wtconv_scan_layout { WTCONV_SCAN_PLANES = 0, WTCONV_SCAN_TOKENS = 1 };
 /* Operation selector for wtconv_scan_workspace_size. */
 enum wtconv_scan_op { WTCONV_SCAN_OP_FORWARD = 0, WTCONV_SCAN_OP_BACKWARD = 1 };
 
-/* Positions between two kept states: states holds the state before positions 0, 128, 256, ...,
- * ceil(T / 128) of them per sequence and channel, [B][C][n] for planes and [B][n][C] for tokens. */
-#define WTCONV_SCAN_KEEP 128
+/* Positions between two kept states: states holds the state before positions 0, 64, 128, ...
+ * ceil(T / 64) of them per sequence and channel, [B][C][n] for planes and [B][n][C] for tokens. */
+#define WTCONV_SCAN_KEEP 64
 
 /* Bytes of device workspace `op` needs on the current device (16-byte aligned; 0 if none, and 0
  * for an invalid shape). */

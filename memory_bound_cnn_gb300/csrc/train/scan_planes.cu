@@ -19,6 +19,7 @@ namespace {
 
 constexpr int kWarpSpan = 256;  // positions of a warp's round
 constexpr int kMaxWarps = 8;
+constexpr int kKeepLanes = WTCONV_SCAN_KEEP / 8;  // lanes between two kept states
 
 enum Mode { kReduce, kApply };
 
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) scan_planes_forward_kernel(con
             continue;
         }
         float h = before.of(exchange(span, 31, slots[round & 1], warp, warps, lane, false, carry));
-        if (a.states_out != nullptr && (lane & 15) == 0 && t < a.T) a.states_out[s.row * a.keep + t / WTCONV_SCAN_KEEP] = h;
+        if (a.states_out != nullptr && (lane & (kKeepLanes - 1)) == 0 && t < a.T) a.states_out[s.row * a.keep + t / WTCONV_SCAN_KEEP] = h;
         Eight<T> out;
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
@@ -202,11 +203,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32) scan_planes_backward_kernel(co
         if (round > s.round0) fetch(t - round_span);
         float diff[8];  // h_{t-1} - x_t
         if (MODE == kApply) {
-            // h again, by half warps: a kept state stands before every sixteen lanes
+            // h again, by groups of lanes: a kept state stands before each
             Span fwd = {1.f, 0.f};
 #pragma unroll
             for (int j = 0; j < 8; ++j) fwd = fwd.then({av[j], bv[j] * ex.get(j)});
-            float h = lane_before<16, false>(warp_scan<16, false>(fwd, lane), lane).of(kept);
+            float h = lane_before<kKeepLanes, false>(warp_scan<kKeepLanes, false>(fwd, lane), lane).of(kept);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float xv = ex.get(j);

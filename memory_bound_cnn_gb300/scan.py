@@ -15,7 +15,7 @@ import torch
 from .wtconv import DTYPE_CODE, _on, _ptr, _raise, _stream, load
 
 LAYOUTS = {"planes": 0, "tokens": 1}
-SCAN_KEEP = 128  # WTCONV_SCAN_KEEP
+SCAN_KEEP = 64  # WTCONV_SCAN_KEEP
 OP_SCAN_FORWARD, OP_SCAN_BACKWARD = 0, 1
 
 EXPORTED = ("wtconv_scan_workspace_size", "wtconv_scan_forward", "wtconv_scan_backward", "wtconv_scan_step")
