@@ -1,7 +1,8 @@
-"""Build libwtconv.so (the C-ABI WTConv library) in-tree with nvcc for sm_103a.
+"""Build libwtconv.so (the C-ABI WTConv library) in-tree with nvcc for sm_103a, and _binding.so, the
+compiled Python binding of the operators beside the layer, with g++ against the installed PyTorch.
 
 Each translation unit is compiled in parallel; the library is relinked only when a source or
-header is newer than it.  The result lands next to this file, so it is found without any
+header is newer than it.  The results land next to this file, so they are found without any
 installation step.
 """
 from __future__ import annotations
@@ -10,6 +11,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,8 @@ CSRC_TRAIN = os.path.join(CSRC, "train")  # operators beside the layer: gated sc
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libwtconv.so")
+BINDING_SRC = os.path.join(CSRC, "binding", "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
@@ -41,18 +45,55 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _compile_binding() -> tuple[list[str], str]:
+    """Command that compiles the binding's object, and the object."""
+    import torch
+
+    torch_dir = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD, "binding.o")
+    includes = [INCLUDE, os.path.join(torch_dir, "include"),
+                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", *["-I" + d for d in includes],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-c", BINDING_SRC, "-o", obj]
+    return cmd, obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+
+    lib_dir = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".{os.getpid()}.tmp"
+    subprocess.run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libwtconv.so",
+                    "-Wl,-rpath,$ORIGIN", "-L" + lib_dir, "-Wl,-rpath," + lib_dir, "-ltorch_python", "-ltorch", "-ltorch_cpu",
+                    "-ltorch_cuda", "-lc10", "-lc10_cuda"], check=True)
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Build what is missing or stale; returns the library's path."""
     srcs = sources()
     headers = [h for d in (CSRC, CSRC_TRAIN, INCLUDE) for pat in ("*.h", "*.cuh")
                for h in glob.glob(os.path.join(d, pat))]
-    if not force and not _stale(LIB, srcs + headers + [__file__]):
+    lib_stale = force or _stale(LIB, srcs + headers + [__file__])
+    binding_stale = force or _stale(BINDING, [BINDING_SRC, *glob.glob(os.path.join(INCLUDE, "*.h")), __file__])
+    if not lib_stale and not binding_stale:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     procs = []
     objs = []
-    for src in srcs:
+    if binding_stale:
+        cmd, binding_obj = _compile_binding()
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    for src in srcs if lib_stale else ():
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
+        # a layer kernel uses the layer's headers, an operator of csrc/train that folder's own
+        used = [h for h in headers if os.path.dirname(h) in (INCLUDE, os.path.dirname(src))]
+        if not force and not _stale(obj, [src, *used, __file__]):
+            continue
         cmd = [nvcc(), *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
@@ -64,13 +105,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
             failed.append((cmd, out.decode(errors="replace")))
     if failed:
         msg = "\n".join(" ".join(c) + "\n" + o for c, o in failed)
-        raise RuntimeError("nvcc failed:\n" + msg)
-    tmp = LIB + f".{os.getpid()}.tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+        raise RuntimeError("compilation failed:\n" + msg)
+    if lib_stale:
+        tmp = LIB + f".{os.getpid()}.tmp"
+        cmd = [nvcc(), *ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-soname=libwtconv.so", "-o", tmp, *objs]
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, LIB)
+    if binding_stale:
+        _link_binding(binding_obj)
     return LIB
 
 

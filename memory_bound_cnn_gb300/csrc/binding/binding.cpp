@@ -1,0 +1,258 @@
+// Python binding of the operators beside the WTConv layer (include/wtconv_scan.h, wtconv_optim.h):
+// checks tensors, allocates outputs and scratch from PyTorch's caching allocator, and calls the C ABI
+// on the current stream.  Compiled, because these calls are short: a decoding step takes 4.5 us of
+// host time here and took 23 us through ctypes.
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/extension.h>
+
+#include <climits>
+#include <string>
+#include <vector>
+
+#include "wtconv.h"
+#include "wtconv_optim.h"
+#include "wtconv_scan.h"
+
+namespace py = pybind11;
+using at::Tensor;
+using c10::optional;
+
+namespace {
+
+[[noreturn]] void refuse(const std::string &why) { throw py::value_error(why); }
+
+void check_status(int status, const char *where) {
+    if (status == WTCONV_OK) return;
+    const py::object type = py::module_::import("memory_bound_cnn_gb300.wtconv").attr("WTConvError");
+    const py::object error = type(status, where);
+    PyErr_SetObject(type.ptr(), error.ptr());
+    throw py::error_already_set();
+}
+
+int dtype_code(at::ScalarType t) {
+    return t == at::kFloat ? WTCONV_F32 : t == at::kBFloat16 ? WTCONV_BF16 : t == at::kHalf ? WTCONV_F16 : -1;
+}
+
+std::string text(c10::IntArrayRef shape) {
+    std::string s = "(";
+    for (size_t i = 0; i < shape.size(); ++i) s += (i ? ", " : "") + std::to_string(shape[i]);
+    return s + ")";
+}
+
+// The caller's stream, or the tensors' device's current one.
+wtconv_stream_t stream_on(const py::object &stream, c10::Device device) {
+    if (stream.is_none()) return reinterpret_cast<wtconv_stream_t>(c10::cuda::getCurrentCUDAStream(device.index()).stream());
+    const py::object where = py::getattr(stream, "device", py::none());
+    if (!where.is_none() && py::cast<c10::Device>(where) != device) refuse("stream is on another device than the tensors");
+    return reinterpret_cast<wtconv_stream_t>(py::cast<uintptr_t>(stream.attr("cuda_stream")));
+}
+
+// One activation of the scan as strides of its batch and row axes.
+struct Act {
+    void *p;
+    int64_t batch, row;
+};
+Act activation(const Tensor &t, const char *name, bool planes, const Tensor *like = nullptr) {
+    if (!t.is_cuda() || dtype_code(t.scalar_type()) < 0)
+        refuse(std::string(name) + " must be a CUDA tensor of fp32, bf16 or fp16");
+    if (like != nullptr && (t.sizes() != like->sizes() || t.scalar_type() != like->scalar_type() || t.device() != like->device()))
+        refuse(std::string(name) + " must match x's shape, dtype and device");
+    if (t.dim() != 3 && !(t.dim() == 4 && planes))
+        refuse(std::string(name) + " must be (B, C, T) or (B, C, H, W) planes, or (B, T, C) tokens");
+    if (t.numel() == 0) refuse(std::string(name) + " is empty");
+    if (t.dim() == 4 && ((t.stride(3) != 1 && t.size(3) > 1) || (t.stride(2) != t.size(3) && t.size(2) > 1)))
+        refuse(std::string(name) + ": the pixels of a plane must be contiguous");
+    if (t.dim() == 3 && t.stride(2) != 1 && t.size(2) > 1) refuse(std::string(name) + ": the innermost axis must be contiguous");
+    return {t.data_ptr(), t.stride(0), t.stride(1)};
+}
+
+struct Dims {
+    int B, T, C, layout, dtype;
+};
+bool is_planes(const std::string &layout) {
+    if (layout != "planes" && layout != "tokens") refuse("layout must be 'planes' or 'tokens', not '" + layout + "'");
+    return layout == "planes";
+}
+Dims dims_of(const Tensor &x, bool planes) {
+    const int64_t last = x.dim() == 4 ? x.size(2) * x.size(3) : x.size(2);
+    const int64_t T = planes ? last : x.size(1), C = planes ? x.size(1) : last;
+    if (x.size(0) > INT_MAX || T > INT_MAX || C > INT_MAX) refuse("x is too large");
+    return {(int)x.size(0), (int)T, (int)C, planes ? WTCONV_SCAN_PLANES : WTCONV_SCAN_TOKENS, dtype_code(x.scalar_type())};
+}
+
+template <typename V>
+V *array(const optional<Tensor> &t, const char *name, c10::IntArrayRef shape, c10::Device device) {
+    if (!t.has_value()) return nullptr;
+    const at::ScalarType want = std::is_same<V, int>::value ? at::kInt : at::kFloat;
+    if (t->device() != device || t->scalar_type() != want || t->sizes() != shape || !t->is_contiguous())
+        refuse(std::string(name) + " must be a contiguous " + (want == at::kInt ? "int32" : "fp32") + " tensor of shape " +
+               text(shape) + " on " + device.str());
+    return static_cast<V *>(t->data_ptr());
+}
+
+Tensor empty(c10::IntArrayRef shape, at::ScalarType dtype, c10::Device device) {
+    return at::empty(shape, at::TensorOptions().dtype(dtype).device(device));
+}
+
+// The caller's scratch or a new one of `need` bytes.
+struct Scratch {
+    Tensor t;
+    void *p = nullptr;
+    size_t bytes = 0;
+};
+Scratch scratch(const optional<Tensor> &given, size_t need, c10::Device device) {
+    Scratch s;
+    if (given.has_value()) {
+        if (given->device() != device) refuse("workspace is on " + given->device().str() + ", the tensors on " + device.str());
+        if (!given->is_contiguous()) refuse("workspace must be contiguous");
+        s.t = *given;
+    } else if (need > 0) {
+        s.t = empty({(int64_t)need}, at::kByte, device);
+    }
+    if (s.t.defined()) s.p = s.t.data_ptr(), s.bytes = s.t.nbytes();
+    return s;
+}
+
+// ------------------------------------------------------------------------------------------- scan
+
+std::vector<int64_t> states_shape(const Dims &d) {
+    const int64_t n = (d.T + WTCONV_SCAN_KEEP - 1) / WTCONV_SCAN_KEEP;
+    if (d.layout == WTCONV_SCAN_PLANES) return {d.B, d.C, n};
+    return {d.B, n, d.C};
+}
+
+py::tuple scan_forward(const Tensor &x, const Tensor &gate, const Tensor &gate_bias, const optional<Tensor> &h0,
+                       const optional<Tensor> &lengths, const std::string &layout, bool keep_states,
+                       const optional<Tensor> &y_given, const optional<Tensor> &workspace, const py::object &stream) {
+    const bool planes = is_planes(layout);
+    const Act ax = activation(x, "x", planes), ag = activation(gate, "gate", planes, &x);
+    const Dims d = dims_of(x, planes);
+    const c10::Device dev = x.device();
+    const float *bias_p = array<float>(gate_bias, "gate_bias", {d.C}, dev);
+    const float *h0_p = array<float>(h0, "h0", {d.B, d.C}, dev);
+    const int *len_p = array<int>(lengths, "lengths", {d.B}, dev);
+    const Tensor y = y_given.has_value() ? *y_given : empty(x.sizes(), x.scalar_type(), dev);
+    const Act ay = activation(y, "y", planes, &x);
+    const Tensor h_last = empty({d.B, d.C}, at::kFloat, dev);
+    Tensor states;
+    if (keep_states) states = empty(states_shape(d), at::kFloat, dev);
+    const c10::cuda::CUDAGuard guard(dev);
+    const Scratch ws = scratch(workspace, wtconv_scan_workspace_size(WTCONV_SCAN_OP_FORWARD, d.B, d.T, d.C, d.layout, d.dtype), dev);
+    check_status(wtconv_scan_forward(d.B, d.T, d.C, d.layout, d.dtype, ax.p, ax.batch, ax.row, ag.p, ag.batch, ag.row, bias_p,
+                                     h0_p, len_p, ay.p, ay.batch, ay.row, h_last.data_ptr<float>(),
+                                     keep_states ? states.data_ptr<float>() : nullptr, ws.p, ws.bytes, stream_on(stream, dev)),
+                 "wtconv_scan_forward");
+    return py::make_tuple(y, h_last, keep_states ? py::cast(states) : py::none());
+}
+
+py::tuple scan_backward(const Tensor &x, const Tensor &gate, const Tensor &gate_bias, const optional<Tensor> &states,
+                        const Tensor &dy, const optional<Tensor> &dh_last, const optional<Tensor> &lengths,
+                        const std::string &layout, const optional<Tensor> &dx_given, const optional<Tensor> &d_gate_given,
+                        const optional<Tensor> &workspace, const py::object &stream) {
+    const bool planes = is_planes(layout);
+    const Act ax = activation(x, "x", planes), ag = activation(gate, "gate", planes, &x), ady = activation(dy, "dy", planes, &x);
+    const Dims d = dims_of(x, planes);
+    const c10::Device dev = x.device();
+    if (!states.has_value()) refuse("the backward needs the states of a forward with keep_states=True");
+    const float *bias_p = array<float>(gate_bias, "gate_bias", {d.C}, dev);
+    const float *states_p = array<float>(states, "states", states_shape(d), dev);
+    const float *dh_p = array<float>(dh_last, "dh_last", {d.B, d.C}, dev);
+    const int *len_p = array<int>(lengths, "lengths", {d.B}, dev);
+    const Tensor dx = dx_given.has_value() ? *dx_given : empty(x.sizes(), x.scalar_type(), dev);
+    const Tensor d_gate = d_gate_given.has_value() ? *d_gate_given : empty(x.sizes(), x.scalar_type(), dev);
+    const Act adx = activation(dx, "dx", planes, &x), adg = activation(d_gate, "d_gate", planes, &x);
+    const Tensor d_bias = empty({d.C}, at::kFloat, dev), d_h0 = empty({d.B, d.C}, at::kFloat, dev);
+    const c10::cuda::CUDAGuard guard(dev);
+    const Scratch ws = scratch(workspace, wtconv_scan_workspace_size(WTCONV_SCAN_OP_BACKWARD, d.B, d.T, d.C, d.layout, d.dtype), dev);
+    check_status(wtconv_scan_backward(d.B, d.T, d.C, d.layout, d.dtype, ax.p, ax.batch, ax.row, ag.p, ag.batch, ag.row, bias_p,
+                                      states_p, len_p, ady.p, ady.batch, ady.row, dh_p, adx.p, adx.batch, adx.row, adg.p,
+                                      adg.batch, adg.row, d_bias.data_ptr<float>(), d_h0.data_ptr<float>(), ws.p, ws.bytes,
+                                      stream_on(stream, dev)),
+                 "wtconv_scan_backward");
+    return py::make_tuple(dx, d_gate, d_bias, d_h0);
+}
+
+Tensor scan_step(const Tensor &x, const Tensor &gate, const Tensor &gate_bias, const Tensor &pool,
+                 const optional<Tensor> &slots, const optional<Tensor> &y_given, const py::object &stream) {
+    if (x.dim() != 2 || x.numel() == 0 || !x.is_cuda() || dtype_code(x.scalar_type()) < 0 || x.size(0) > INT_MAX ||
+        x.size(1) > INT_MAX)
+        refuse("x must be a non-empty (B, C) CUDA tensor of fp32, bf16 or fp16");
+    const int64_t B = x.size(0), C = x.size(1);
+    const c10::Device dev = x.device();
+    const Tensor y = y_given.has_value() ? *y_given : empty({B, C}, x.scalar_type(), dev);
+    const auto check = [&](const Tensor &t, const char *name) {
+        if (t.sizes() != x.sizes() || t.scalar_type() != x.scalar_type() || t.device() != dev || (t.stride(1) != 1 && C > 1))
+            refuse(std::string(name) + " must match x's shape, dtype and device and be contiguous along C");
+    };
+    check(x, "x"), check(gate, "gate"), check(y, "y");
+    if (pool.dim() != 2 || pool.size(1) != C || pool.size(0) < 1 || pool.size(0) > INT_MAX)
+        refuse("pool must be (n_states, " + std::to_string(C) + ")");
+    const float *bias_p = array<float>(gate_bias, "gate_bias", {C}, dev);
+    float *pool_p = array<float>(pool, "pool", pool.sizes(), dev);
+    const int *slots_p = array<int>(slots, "slots", {B}, dev);
+    const c10::cuda::CUDAGuard guard(dev);
+    check_status(wtconv_scan_step((int)B, (int)C, dtype_code(x.scalar_type()), x.data_ptr(), x.stride(0), gate.data_ptr(),
+                                  gate.stride(0), bias_p, pool_p, (int)pool.size(0), slots_p, y.data_ptr(), y.stride(0),
+                                  stream_on(stream, dev)),
+                 "wtconv_scan_step");
+    return y;
+}
+
+// ------------------------------------------------------------------------------------------ AdamW
+// `tensors` and `config` are addresses of the optimiser's wtconv_optim_tensor and
+// wtconv_adamw_config, checked when it was built.
+
+const wtconv_optim_tensor *table(uintptr_t address) { return reinterpret_cast<const wtconv_optim_tensor *>(address); }
+
+Tensor grad_norm(int n, uintptr_t tensors, int grad_dtype, const c10::Device &dev, double max_norm, const optional<Tensor> &out_given,
+                 const optional<Tensor> &workspace, size_t workspace_bytes, const py::object &stream) {
+    const Tensor out = out_given.has_value() ? *out_given : empty({2}, at::kFloat, dev);
+    float *out_p = array<float>(out, "out", {2}, dev);
+    const c10::cuda::CUDAGuard guard(dev);
+    const Scratch ws = scratch(workspace, workspace_bytes, dev);
+    check_status(wtconv_grad_norm(n, table(tensors), grad_dtype, max_norm, out_p, ws.p, ws.bytes, stream_on(stream, dev)),
+                 "wtconv_grad_norm");
+    return out;
+}
+
+void adamw_step(int n, uintptr_t tensors, uintptr_t config, const c10::Device &dev, const optional<Tensor> &clip,
+                const py::object &stream) {
+    const float *clip_p = array<float>(clip, "clip", {2}, dev);
+    const c10::cuda::CUDAGuard guard(dev);
+    check_status(wtconv_adamw_step(n, table(tensors), reinterpret_cast<const wtconv_adamw_config *>(config),
+                                   clip_p != nullptr ? clip_p + 1 : nullptr, stream_on(stream, dev)),
+                 "wtconv_adamw_step");
+}
+
+void state_values(int n, uintptr_t tensors, const c10::Device &dev, const std::vector<Tensor> &m_out,
+                  const std::vector<Tensor> &v_out, const py::object &stream) {
+    const auto pointers = [&](const std::vector<Tensor> &ts, const char *name) {
+        if ((int)ts.size() != n)
+            refuse(std::to_string(ts.size()) + " tensors in " + name + " for " + std::to_string(n) + " parameters");
+        std::vector<float *> p(n);
+        for (int i = 0; i < n; ++i) {
+            const Tensor &t = ts[i];
+            if (t.device() != dev || t.scalar_type() != at::kFloat || t.numel() != table(tensors)[i].n || !t.is_contiguous())
+                refuse(std::string(name) + "[" + std::to_string(i) + "] must be a contiguous fp32 tensor of " +
+                       std::to_string(table(tensors)[i].n) + " elements on " + dev.str());
+            p[i] = static_cast<float *>(t.data_ptr());
+        }
+        return p;
+    };
+    const std::vector<float *> m = pointers(m_out, "m_out"), v = pointers(v_out, "v_out");
+    const c10::cuda::CUDAGuard guard(dev);
+    check_status(wtconv_adamw_state_values(n, table(tensors), m.data(), v.data(), stream_on(stream, dev)),
+                 "wtconv_adamw_state_values");
+}
+
+}  // namespace
+
+PYBIND11_MODULE(_binding, m) {
+    m.def("scan_forward", &scan_forward);
+    m.def("scan_backward", &scan_backward);
+    m.def("scan_step", &scan_step);
+    m.def("grad_norm", &grad_norm);
+    m.def("adamw_step", &adamw_step);
+    m.def("state_values", &state_values);
+}

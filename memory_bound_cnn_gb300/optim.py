@@ -1,8 +1,8 @@
-"""Python binding of the AdamW step and the gradient norm (include/wtconv_optim.h).
+"""The AdamW step and the gradient norm (include/wtconv_optim.h) on PyTorch tensors.
 
 ``AdamW`` is the object a training program builds once over its parameters and their gradient
 buffers: it checks them, keeps their states and the descriptors that the library reads, and every
-step is one call.  It marshals arguments only; the update runs in the library's CUDA kernels.
+step is one call of the compiled binding.  The update runs in the library's CUDA kernels.
 """
 from __future__ import annotations
 
@@ -10,7 +10,7 @@ import ctypes
 
 import torch
 
-from .wtconv import DTYPE_CODE, _on, _raise, _stream, load
+from .wtconv import DTYPE_CODE, load, load_binding
 
 ADAMW_BLOCK = 256  # WTCONV_ADAMW_BLOCK
 
@@ -35,6 +35,7 @@ _lib = None
 
 
 def _load() -> ctypes.CDLL:
+    """The library with this header's signatures."""
     global _lib
     if _lib is None:
         lib = load()
@@ -101,6 +102,8 @@ class AdamW:
                 setattr(self._tensors[k], name, t.data_ptr())
         copy_dtype = DTYPE_CODE[kinds.pop()] if kinds else 0
         self._config = AdamWConfig(lr, betas[0], betas[1], eps, weight_decay, 0, state_bits, 0, copy_dtype)
+        self._ext = load_binding()
+        self._table, self._scalars = ctypes.addressof(self._tensors), ctypes.addressof(self._config)
         self.set_grads(grads)
 
     def _check(self, t, name, dtype, numel):
@@ -139,17 +142,8 @@ class AdamW:
     def grad_norm(self, max_norm=float("inf"), out=None, workspace=None, stream=None) -> torch.Tensor:
         """Device tensor (norm, factor): the norm over every gradient and the factor that limits it
         to max_norm (NaN where the norm is not finite), for ``step(clip=...)``."""
-        if out is None:
-            out = torch.empty(2, dtype=torch.float32, device=self.device)
-        self._check(out, "out", torch.float32, 2)
-        with _on(self.device, stream, workspace):
-            if workspace is None:
-                workspace = torch.empty(self._norm_bytes, dtype=torch.uint8, device=self.device)
-            rc = _load().wtconv_grad_norm(len(self.params), self._tensors, self._config.grad_dtype, max_norm,
-                                          out.data_ptr(), workspace.data_ptr(),
-                                          workspace.numel() * workspace.element_size(), _stream(stream))
-        _raise(rc, "wtconv_grad_norm")
-        return out
+        return self._ext.grad_norm(len(self.params), self._table, self._config.grad_dtype, self.device, max_norm, out,
+                                   workspace, self._norm_bytes, stream)
 
     def step(self, clip=None, lr=None, count=None, stream=None) -> None:
         """One update of every parameter.  clip: what ``grad_norm`` returned (a factor that is not
@@ -158,13 +152,7 @@ class AdamW:
         if lr is not None:
             config.lr = lr
         config.step = self.count + 1 if count is None else count
-        clip_p = None
-        if clip is not None:
-            self._check(clip, "clip", torch.float32, 2)
-            clip_p = clip.data_ptr() + 4
-        with _on(self.device, stream, None):
-            rc = _load().wtconv_adamw_step(len(self.params), self._tensors, config, clip_p, _stream(stream))
-        _raise(rc, "wtconv_adamw_step")
+        self._ext.adamw_step(len(self.params), self._table, self._scalars, self.device, clip, stream)
         self.count = config.step
 
     def state_values(self, m_out=None, v_out=None, stream=None):
@@ -173,16 +161,7 @@ class AdamW:
         not given)."""
         if self.state_bits == 32:
             return self.states["m"], self.states["v"]
-        outs = []
-        for given, name in ((m_out, "m_out"), (v_out, "v_out")):
-            outs.append([torch.empty(p.numel(), dtype=torch.float32, device=self.device) for p in self.params]
-                        if given is None else list(given))
-            if len(outs[-1]) != len(self.params):
-                raise ValueError(f"{len(outs[-1])} tensors in {name} for {len(self.params)} parameters")
-            for k, t in enumerate(outs[-1]):
-                self._check(t, f"{name}[{k}]", torch.float32, self.params[k].numel())
-        pointers = [(ctypes.c_void_p * len(self.params))(*[t.data_ptr() for t in ts]) for ts in outs]
-        with _on(self.device, stream, None):
-            rc = _load().wtconv_adamw_state_values(len(self.params), self._tensors, *pointers, _stream(stream))
-        _raise(rc, "wtconv_adamw_state_values")
+        outs = [[torch.empty(p.numel(), dtype=torch.float32, device=self.device) for p in self.params]
+                if given is None else given for given in (m_out, v_out)]
+        self._ext.state_values(len(self.params), self._table, self.device, *outs, stream)
         return outs[0], outs[1]

@@ -97,6 +97,20 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     return lib
 
 
+_binding = None
+
+
+def load_binding():
+    """The compiled binding of the operators beside the layer (built with the library)."""
+    global _binding
+    if _binding is None:
+        load()
+        from . import _binding as module  # the extension module _binding.so
+
+        _binding = module
+    return _binding
+
+
 def wtconv_version() -> int:
     return load().wtconv_version()
 
