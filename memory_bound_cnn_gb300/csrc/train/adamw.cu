@@ -88,11 +88,17 @@ template <bool VEC> __device__ __forceinline__ void store_codes(uint8_t *p, long
 
 // ------------------------------------------------------------------------- 8-bit states
 // Products and sums that decide a code are rounded one by one (no fused multiply-add), so that a
-// code is a function of its inputs that any fp32 program can follow.
+// code is a function of its inputs that any fp32 program can follow.  Conversions between bytes and
+// fp32 go through 2^23 + n, whose last bits are n: the conversion instructions run at an eighth of
+// the rate of an add, and with them and exact roots the step took 787 us for 130 M elements.
 
-__device__ __forceinline__ float m_value(int c, float unit) {  // unit = M / 127^2
-    return __fmul_rn((float)(c * abs(c)), unit);
+constexpr float kTwo23 = 8388608.f;
+
+// byte j of a word as fp32
+__device__ __forceinline__ float byte_of(uint32_t q, int j) {
+    return __uint_as_float(__byte_perm(q, 0x4b000000u, 0x7540 | j)) - kTwo23;
 }
+__device__ __forceinline__ float m_value(float c, float unit) { return __fmul_rn(__fmul_rn(c, fabsf(c)), unit); }  // unit = M / 127^2
 __device__ __forceinline__ float v_level(float c) {  // c^4
     const float q = __fmul_rn(c, c);
     return __fmul_rn(q, q);
@@ -114,22 +120,32 @@ __device__ __forceinline__ float inverse_unit(float most, float top_power) {
 __device__ __forceinline__ float threshold(uint32_t index, uint32_t threshold0) {
     return __fmul_rn((float)((index * kIndexStride + threshold0) >> 8), 5.9604644775390625e-8f);
 }
-// The code below y (in levels) or the one above, by the share of the way against u.  The square
-// roots only find the neighbour: where an inexact one lands on the wrong side of a level, y lies at
-// that level and the comparison picks the same code from the other side.
-__device__ __forceinline__ float pick(float y, float below, float above, float low, float u) {
-    return __fsub_rn(y, below) > __fmul_rn(u, __fsub_rn(above, below)) ? low + 1.f : low;
+__device__ __forceinline__ float root_of(float v) {
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
 }
-__device__ __forceinline__ float m_code(float size, float inverse, float u) {
-    const float y = __fmul_rn(size, inverse);
-    const float low = fminf(floorf(__fsqrt_rn(y)), 126.f);
-    return pick(y, low * low, (low + 1.f) * (low + 1.f), low, u);
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
 }
-__device__ __forceinline__ float v_code(float v, float inverse, float u) {
-    const float y = __fmul_rn(v, inverse);
-    const float low = fminf(floorf(__fsqrt_rn(__fsqrt_rn(y))), 254.f);
-    const float code = pick(y, v_level(low), v_level(low + 1.f), low, u);
-    return y > 0.f ? fmaxf(code, 1.f) : code;
+// The code of a magnitude at y levels: the one below it (the floor of `root`, the value's place on
+// the scale of codes) or the one above, by the share of the way against u.  far: the root was not
+// exact enough and y does not lie between the two.
+template <bool FOURTH> __device__ __forceinline__ uint32_t code_of(float y, float root, float u, bool &far) {
+    constexpr float top = FOURTH ? 255.f : 127.f;
+    const float r = __fadd_rd(fminf(root, top - 0.5f), kTwo23);  // last bits: floor(root)
+    const float low = r - kTwo23, next = low + 1.f;
+    const float below = FOURTH ? v_level(low) : low * low, above = FOURTH ? v_level(next) : next * next;
+    far |= y < below || (y > above && next < top);
+    const bool up = __fsub_rn(y, below) > __fmul_rn(u, __fsub_rn(above, below));
+    return (__float_as_uint(r) & 255u) + up;
+}
+template <bool FOURTH> __device__ __noinline__ uint32_t exact_code(float y, float u) {
+    bool far = false;
+    const float root = __fsqrt_rn(y);
+    return code_of<FOURTH>(y, FOURTH ? __fsqrt_rn(root) : root, u, far);
 }
 
 // ------------------------------------------------------------------------------- the step
@@ -140,47 +156,50 @@ __device__ __forceinline__ void update(const wtconv_optim_tensor &t, const StepS
     const long long n = t.n;
     const long long first = start + (threadIdx.x >> 5) * 256;
     if (first >= n) return;
-    float m[2][4], v[2][4];
+    float m[2][4], v[2][4], p[2][4], g[2][4];
     const long long blk = first / WTCONV_ADAMW_BLOCK;
-    if (BITS == 8) {
-        const float mu = m_unit(t.m_max[blk]), vu = v_unit(t.v_max[blk]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const long long i = first + h * 128 + lane * 4;
-            const uint32_t mc = load_codes<VEC>(static_cast<const uint8_t *>(t.m), i, n);
-            const uint32_t vc = load_codes<VEC>(static_cast<const uint8_t *>(t.v), i, n);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                m[h][j] = m_value((int)(int8_t)(mc >> (8 * j)), mu);
-                v[h][j] = __fmul_rn(v_level((float)((vc >> (8 * j)) & 255)), vu);
-            }
-        }
-    }
-    float m_most = 0.f, v_most = 0.f;
+    uint32_t mq[2], vq[2];
+    float mu = 0.f, vu = 0.f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const long long i = first + h * 128 + lane * 4;
-        float p[4], g[4];
-        load4<VEC>(t.param, i, n, p);
-        load4<VEC>(static_cast<const G *>(t.grad), i, n, g);
-        if (BITS == 32) {
+        if (BITS == 8) {
+            mq[h] = load_codes<VEC>(static_cast<const uint8_t *>(t.m), i, n);
+            vq[h] = load_codes<VEC>(static_cast<const uint8_t *>(t.v), i, n);
+        } else {
             load4<VEC>(static_cast<const float *>(t.m), i, n, m[h]);
             load4<VEC>(static_cast<const float *>(t.v), i, n, v[h]);
         }
+        load4<VEC>(t.param, i, n, p[h]);
+        load4<VEC>(static_cast<const G *>(t.grad), i, n, g[h]);
+    }
+    if (BITS == 8) mu = m_unit(t.m_max[blk]), vu = v_unit(t.v_max[blk]);
+    if (!(fabsf(clip) <= FLT_MAX)) return;  // a step over gradients without a norm is not taken
+    float m_most = 0.f, v_most = 0.f, root[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const long long i = first + h * 128 + lane * 4;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float gs = __fmul_rn(g[j], clip);
+            if (BITS == 8) {
+                m[h][j] = m_value(byte_of(mq[h] ^ 0x80808080u, j) - 128.f, mu);
+                v[h][j] = __fmul_rn(v_level(byte_of(vq[h], j)), vu);
+            }
+            const float gs = __fmul_rn(g[h][j], clip);
             m[h][j] = __fadd_rn(__fmul_rn(s.beta1, m[h][j]), __fmul_rn(s.one_minus_beta1, gs));
             v[h][j] = __fadd_rn(__fmul_rn(s.beta2, v[h][j]), __fmul_rn(s.one_minus_beta2, __fmul_rn(gs, gs)));
-            m_most = nan_max(m_most, fabsf(m[h][j]));
-            v_most = nan_max(v_most, v[h][j]);
-            const float root = fmaf(__fsqrt_rn(v[h][j]), s.root_scale, s.eps);
-            p[j] = __fsub_rn(__fmul_rn(p[j], s.keep), __fmul_rn(s.rate, __fdiv_rn(m[h][j], root)));
+            if (BITS == 8) {
+                m_most = nan_max(m_most, fabsf(m[h][j]));
+                v_most = nan_max(v_most, v[h][j]);
+            }
+            root[h][j] = root_of(v[h][j]);
+            const float step = m[h][j] * reciprocal(fmaf(root[h][j], s.root_scale, s.eps));
+            p[h][j] = fmaf(-s.rate, step, p[h][j] * s.keep);
         }
-        store4<VEC>(t.param, i, n, p);
+        store4<VEC>(t.param, i, n, p[h]);
         if (t.copy != nullptr) {
-            if (s.copy_dtype == WTCONV_BF16) store4<VEC>(static_cast<__nv_bfloat16 *>(t.copy), i, n, p);
-            else store4<VEC>(static_cast<__half *>(t.copy), i, n, p);
+            if (s.copy_dtype == WTCONV_BF16) store4<VEC>(static_cast<__nv_bfloat16 *>(t.copy), i, n, p[h]);
+            else store4<VEC>(static_cast<__half *>(t.copy), i, n, p[h]);
         }
         if (BITS == 32) {
             store4<VEC>(static_cast<float *>(t.m), i, n, m[h]);
@@ -193,19 +212,42 @@ __device__ __forceinline__ void update(const wtconv_optim_tensor &t, const StepS
         if (m_most < kLeastMax) m_most = 0.f;
         if (v_most < kLeastMax) v_most = 0.f;
         const float mi = inverse_unit(m_most, 127.f * 127.f), vi = inverse_unit(v_most, 4228250625.f);
+        const float v_scale = root_of(vi);  // sqrt(y) = sqrt(v) sqrt(vi)
+        bool far = false;
+        uint32_t mc[2] = {0, 0}, vc[2] = {0, 0};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float u = threshold((uint32_t)(first + h * 128 + lane * 4 + j), s.threshold0);
+                const float my = __fmul_rn(fabsf(m[h][j]), mi), vy = __fmul_rn(v[h][j], vi);
+                const uint32_t cm = code_of<false>(my, root_of(my), u, far);
+                const uint32_t cv = code_of<true>(vy, root_of(root[h][j] * v_scale), u, far);
+                mc[h] |= (m[h][j] < 0.f ? 0u - cm : cm) % 256u << (8 * j);
+                vc[h] |= max(cv, vy > 0.f ? 1u : 0u) << (8 * j);
+            }
+        if (far) {  // about one warp in a hundred
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+                const int h = k >> 2, j = k & 3;
+                float mv = 0.f, vv = 0.f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (q == k) mv = m[q >> 2][q & 3], vv = v[q >> 2][q & 3];
+                const float u = threshold((uint32_t)(first + h * 128 + lane * 4 + j), s.threshold0);
+                const float my = __fmul_rn(fabsf(mv), mi), vy = __fmul_rn(vv, vi);
+                const uint32_t cm = exact_code<false>(my, u), cv = max(exact_code<true>(vy, u), vy > 0.f ? 1u : 0u);
+                const uint32_t mask = 255u << (8 * j);
+                const uint32_t mw = (mv < 0.f ? 0u - cm : cm) % 256u << (8 * j), vw = cv << (8 * j);
+                if (h == 0) mc[0] = (mc[0] & ~mask) | mw, vc[0] = (vc[0] & ~mask) | vw;
+                else mc[1] = (mc[1] & ~mask) | mw, vc[1] = (vc[1] & ~mask) | vw;
+            }
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const long long i = first + h * 128 + lane * 4;
-            uint32_t mc = 0, vc = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float u = threshold((uint32_t)(i + j), s.threshold0);
-                const int mq = (int)m_code(fabsf(m[h][j]), mi, u);
-                mc |= (uint32_t)(uint8_t)(m[h][j] < 0.f ? -mq : mq) << (8 * j);
-                vc |= (uint32_t)(uint8_t)(int)v_code(v[h][j], vi, u) << (8 * j);
-            }
-            store_codes<VEC>(static_cast<uint8_t *>(t.m), i, n, mc);
-            store_codes<VEC>(static_cast<uint8_t *>(t.v), i, n, vc);
+            store_codes<VEC>(static_cast<uint8_t *>(t.m), i, n, mc[h]);
+            store_codes<VEC>(static_cast<uint8_t *>(t.v), i, n, vc[h]);
         }
         if (lane == 0) {
             t.m_max[blk] = m_most;
@@ -225,7 +267,6 @@ template <typename G, int BITS, int CAP>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ TensorTable<CAP> table, StepScalars s,
                                                          const float *clip) {
     const float scale = clip != nullptr ? *clip : 1.f;
-    if (!(fabsf(scale) <= FLT_MAX)) return;  // a step over gradients without a norm is not taken
     const int which = find_tensor(table, blockIdx.x);
     const wtconv_optim_tensor &t = table.t[which];
     const long long start = (long long)(blockIdx.x - table.first[which]) * kChunk;
@@ -233,23 +274,40 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     else update<G, BITS, false>(t, s, scale, start);
 }
 
+template <bool VEC> __device__ __forceinline__ void write_values(const wtconv_optim_tensor &t, long long start) {
+    const int lane = threadIdx.x & 31;
+    const long long n = t.n, first = start + (threadIdx.x >> 5) * 256;
+    if (first >= n) return;
+    float *const m_out = t.param, *const v_out = static_cast<float *>(t.copy);
+    const long long blk = first / WTCONV_ADAMW_BLOCK;
+    uint32_t mq[2], vq[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const long long i = first + h * 128 + lane * 4;
+        mq[h] = load_codes<VEC>(static_cast<const uint8_t *>(t.m), i, n);
+        vq[h] = load_codes<VEC>(static_cast<const uint8_t *>(t.v), i, n);
+    }
+    const float mu = m_unit(t.m_max[blk]), vu = v_unit(t.v_max[blk]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const long long i = first + h * 128 + lane * 4;
+        float m[4], v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            m[j] = m_value(byte_of(mq[h] ^ 0x80808080u, j) - 128.f, mu);
+            v[j] = __fmul_rn(v_level(byte_of(vq[h], j)), vu);
+        }
+        if (m_out != nullptr) store4<VEC>(m_out, i, n, m);
+        if (v_out != nullptr) store4<VEC>(v_out, i, n, v);
+    }
+}
+
 template <int CAP> __global__ void __launch_bounds__(kThreads) state_values_kernel(const __grid_constant__ TensorTable<CAP> table) {
     const int which = find_tensor(table, blockIdx.x);
     const wtconv_optim_tensor &t = table.t[which];
-    const long long n = t.n;
-    const long long first = (long long)(blockIdx.x - table.first[which]) * kChunk + (threadIdx.x >> 5) * 256;
-    if (first >= n) return;
-    const int lane = threadIdx.x & 31;
-    const long long blk = first / WTCONV_ADAMW_BLOCK;
-    float *const m_out = t.param, *const v_out = static_cast<float *>(t.copy);
-    const float mu = m_unit(t.m_max[blk]), vu = v_unit(t.v_max[blk]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const long long i = first + j * 32 + lane;
-        if (i >= n) break;
-        if (m_out != nullptr) m_out[i] = m_value(static_cast<const int8_t *>(t.m)[i], mu);
-        if (v_out != nullptr) v_out[i] = __fmul_rn(v_level((float)static_cast<const uint8_t *>(t.v)[i]), vu);
-    }
+    const long long start = (long long)(blockIdx.x - table.first[which]) * kChunk;
+    if (vector_ok(t)) write_values<true>(t, start);
+    else write_values<false>(t, start);
 }
 
 // ------------------------------------------------------------------------------- the norm
@@ -263,28 +321,60 @@ template <typename V> __device__ __forceinline__ V block_sum(V v, V *scratch) { 
     return v;
 }
 
+// Sum of squares of g[first..last), by the CTA: sixteen bytes a load, four loads in flight.
+template <typename G> __device__ __forceinline__ float squares(const G *g, long long first, long long last) {
+    constexpr int per = 16 / sizeof(G);
+    float mine[4] = {0.f, 0.f, 0.f, 0.f};
+    if ((reinterpret_cast<uintptr_t>(g) & 15) == 0) {  // first is a multiple of kChunk
+        long long i = first + threadIdx.x * per;
+        for (; i + 3 * kThreads * per + per <= last; i += 4 * kThreads * per) {
+            uint4 q[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) q[k] = __ldcs(reinterpret_cast<const uint4 *>(g + i + k * kThreads * per));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < per; ++j) {
+                    const float v = to_f32(reinterpret_cast<const G *>(&q[k])[j]);
+                    mine[k] = fmaf(v, v, mine[k]);
+                }
+        }
+        for (; i < last; i += kThreads * per)
+#pragma unroll
+            for (int j = 0; j < per; ++j) {
+                const float v = i + j < last ? to_f32(g[i + j]) : 0.f;
+                mine[j & 3] = fmaf(v, v, mine[j & 3]);
+            }
+    } else {
+        for (long long i = first + threadIdx.x; i < last; i += 4 * kThreads)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float v = i + k * kThreads < last ? to_f32(g[i + k * kThreads]) : 0.f;
+                mine[k] = fmaf(v, v, mine[k]);
+            }
+    }
+    return (mine[0] + mine[1]) + (mine[2] + mine[3]);
+}
+
+// A CTA takes a run of chunks, through one tensor after the other.  A thread's fp32 sum covers at
+// most kRun elements' share before it moves to fp64.
 template <typename G, int CAP>
 __global__ void __launch_bounds__(kThreads) norm_part_kernel(const __grid_constant__ TensorTable<CAP> table, double *part) {
     __shared__ double scratch[kThreads / 32];
+    constexpr int kRun = 64 * kChunk;
     double sum = 0.0;
     const int chunks = table.first[table.count];
-    for (int chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
-        const int which = find_tensor(table, chunk);
+    int chunk = (int)((long long)chunks * blockIdx.x / gridDim.x);
+    const int end = (int)((long long)chunks * (blockIdx.x + 1) / gridDim.x);
+    int which = find_tensor(table, chunk);
+    while (chunk < end) {
         const wtconv_optim_tensor &t = table.t[which];
-        const G *g = static_cast<const G *>(t.grad);
-        const long long n = t.n, start = (long long)(chunk - table.first[which]) * kChunk;
-        const bool vec = (reinterpret_cast<uintptr_t>(g) & 15) == 0;
-        float mine = 0.f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const long long i = start + h * 1024 + threadIdx.x * 4;
-            float v[4];
-            if (vec) load4<true>(g, i, n, v);
-            else load4<false>(g, i, n, v);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mine = fmaf(v[j], v[j], mine);
-        }
-        sum += mine;
+        const int upto = min(end, table.first[which + 1]);
+        const long long first = (long long)(chunk - table.first[which]) * kChunk;
+        const long long last = min((long long)(upto - table.first[which]) * kChunk, t.n);
+        for (long long i = first; i < last; i += kRun) sum += squares(static_cast<const G *>(t.grad), i, min(i + kRun, last));
+        chunk = upto;
+        ++which;
     }
     sum = block_sum(sum, scratch);
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
