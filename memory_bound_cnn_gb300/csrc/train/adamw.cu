@@ -87,65 +87,107 @@ template <bool VEC> __device__ __forceinline__ void store_codes(uint8_t *p, long
 }
 
 // ------------------------------------------------------------------------- 8-bit states
-// Products and sums that decide a code are rounded one by one (no fused multiply-add), so that a
-// code is a function of its inputs that any fp32 program can follow.  Conversions between bytes and
-// fp32 go through 2^23 + n, whose last bits are n: the conversion instructions run at an eighth of
-// the rate of an add, and with them and exact roots the step took 787 us for 130 M elements.
+// Products and sums that decide a code are rounded one by one (no fused multiply-add: `product`), so
+// that a code is a function of its inputs that any fp32 program can follow.  The step is bound by the issue
+// of instructions, so elements are worked on in pairs (Pair: one instruction for two), and bytes
+// become fp32 and back through 2^23 + n, whose last bits are n: conversion instructions run at an
+// eighth of the rate of an add.  130 M elements took 787 us one by one with conversions and exact
+// square roots, 551 us without those.
 
 constexpr float kTwo23 = 8388608.f;
 
-// byte j of a word as fp32
-__device__ __forceinline__ float byte_of(uint32_t q, int j) {
-    return __uint_as_float(__byte_perm(q, 0x4b000000u, 0x7540 | j)) - kTwo23;
+// bytes j and j + 1 of a word, plus 2^23, as fp32
+__device__ __forceinline__ Pair bytes_of(uint32_t q, int j) {
+    return {__uint_as_float(__byte_perm(q, 0x4b000000u, 0x7540 | j)), __uint_as_float(__byte_perm(q, 0x4b000000u, 0x7541 + j))};
 }
-__device__ __forceinline__ float m_value(float c, float unit) { return __fmul_rn(__fmul_rn(c, fabsf(c)), unit); }  // unit = M / 127^2
-__device__ __forceinline__ float v_level(float c) {  // c^4
-    const float q = __fmul_rn(c, c);
-    return __fmul_rn(q, q);
+// values of codes j, j + 1: m from bytes plus 128; the unit is M / 127^2 or M / 255^4
+__device__ __forceinline__ Pair m_values(uint32_t q, int j, Pair unit) {
+    const Pair c = add(bytes_of(q, j), Pair(-(kTwo23 + 128.f)));
+    return mul(mul(c, abs(c)), unit);
+}
+__device__ __forceinline__ Pair fourth(Pair c, Pair zero) {
+    const Pair q = mul(c, c);
+    return product(q, q, zero);
+}
+__device__ __forceinline__ Pair v_values(uint32_t q, int j, Pair unit) {
+    const Pair c = add(bytes_of(q, j), Pair(-kTwo23)), c2 = mul(c, c);
+    return mul(mul(c2, c2), unit);
 }
 __device__ __forceinline__ float m_unit(float most) { return __fmul_rn(most, (float)(1.0 / (127.0 * 127.0))); }
 __device__ __forceinline__ float v_unit(float most) { return __fmul_rn(most, (float)(1.0 / (255.0 * 255.0 * 255.0 * 255.0))); }
 
 // Largest magnitude of a warp's block; magnitudes compare as their bit patterns, NaN above all.
-__device__ __forceinline__ float block_max(float mine) {
-    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mine)));
-}
-__device__ __forceinline__ float nan_max(float a, float b) {  // of magnitudes: a NaN stays
-    return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+__device__ __forceinline__ float block_max(uint32_t mine) { return __uint_as_float(__reduce_max_sync(0xffffffffu, mine)); }
+__device__ __forceinline__ uint32_t larger(uint32_t most, Pair size) {
+    return max(most, max(__float_as_uint(size.lo()), __float_as_uint(size.hi())));
 }
 // levels per unit of magnitude: top^power / max (0 where the block is held as zeros)
 __device__ __forceinline__ float inverse_unit(float most, float top_power) {
     return most > 0.f ? __fmul_rn(__fdiv_rn(1.f, most), top_power) : most;
 }
-__device__ __forceinline__ float threshold(uint32_t index, uint32_t threshold0) {
-    return __fmul_rn((float)((index * kIndexStride + threshold0) >> 8), 5.9604644775390625e-8f);
+// thresholds of two elements from their Weyl integers
+__device__ __forceinline__ Pair thresholds(uint32_t w) {
+    return mul(Pair((float)(w >> 8), (float)((w + kIndexStride) >> 8)), Pair(5.9604644775390625e-8f));
 }
-__device__ __forceinline__ float root_of(float v) {
-    float r;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-__device__ __forceinline__ float reciprocal(float v) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-// The code of a magnitude at y levels: the one below it (the floor of `root`, the value's place on
-// the scale of codes) or the one above, by the share of the way against u.  far: the root was not
-// exact enough and y does not lie between the two.
-template <bool FOURTH> __device__ __forceinline__ uint32_t code_of(float y, float root, float u, bool &far) {
+// Codes of two magnitudes at y levels: the one below (the floor of `root`, the value's place on the
+// scale of codes) or the one above, by the share of the way against u.  far: a root was not exact
+// enough and its y does not lie between the two codes.
+struct Codes {
+    uint32_t lo, hi;
+};
+template <bool FOURTH> __device__ __forceinline__ Codes codes_of(Pair y, float root_lo, float root_hi, Pair u, Pair zero, bool &far) {
     constexpr float top = FOURTH ? 255.f : 127.f;
-    const float r = __fadd_rd(fminf(root, top - 0.5f), kTwo23);  // last bits: floor(root)
-    const float low = r - kTwo23, next = low + 1.f;
-    const float below = FOURTH ? v_level(low) : low * low, above = FOURTH ? v_level(next) : next * next;
-    far |= y < below || (y > above && next < top);
-    const bool up = __fsub_rn(y, below) > __fmul_rn(u, __fsub_rn(above, below));
-    return (__float_as_uint(r) & 255u) + up;
+    const Pair r = add_down(Pair(fminf(root_lo, top - 0.5f), fminf(root_hi, top - 0.5f)), Pair(kTwo23));  // last bits: the floor
+    const Pair low = add(r, Pair(-kTwo23)), next = add(low, Pair(1.f));
+    const Pair below = FOURTH ? fourth(low, zero) : product(low, low, zero), above = FOURTH ? fourth(next, zero) : product(next, next, zero);
+    const Pair past = sub(y, below), limit = mul(u, sub(above, below));
+    far |= past.lo() < 0.f || (y.lo() > above.lo() && next.lo() < top);
+    far |= past.hi() < 0.f || (y.hi() > above.hi() && next.hi() < top);
+    // r's bits are 0x4b000000 + the floor; the caller takes the last byte
+    return {__float_as_uint(r.lo()) + (past.lo() > limit.lo()), __float_as_uint(r.hi()) + (past.hi() > limit.hi())};
 }
-template <bool FOURTH> __device__ __noinline__ uint32_t exact_code(float y, float u) {
+// -c where the value is negative (in the last byte)
+__device__ __forceinline__ uint32_t with_sign(uint32_t c, float value) { return value < 0.f ? 0u - c : c; }
+// a positive v does not take code 0
+__device__ __forceinline__ uint32_t not_zero(uint32_t c, float y) { return y > 0.f ? max(c, 0x4b000001u) : c; }
+__device__ __forceinline__ uint32_t last_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// Codes of four consecutive elements (the first with Weyl integer w) as words.  ROOTS: how exact the
+// square roots are; `roots` holds approximate ones of v.
+template <bool EXACT>
+__device__ __forceinline__ bool four_codes(const Pair (&m)[2], const Pair (&v)[2], const Pair (&roots)[2], float mi, float vi,
+                                           float v_scale, uint32_t w, Pair zero, uint32_t &m_word, uint32_t &v_word) {
     bool far = false;
-    const float root = __fsqrt_rn(y);
-    return code_of<FOURTH>(y, FOURTH ? __fsqrt_rn(root) : root, u, far);
+    Codes mc[2], vc[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const Pair u = thresholds(w + 2 * k * kIndexStride);
+        const Pair my = product(abs(m[k]), Pair(mi), zero), vy = product(v[k], Pair(vi), zero);
+        if (EXACT) {
+            mc[k] = codes_of<false>(my, __fsqrt_rn(my.lo()), __fsqrt_rn(my.hi()), u, zero, far);
+            vc[k] = codes_of<true>(vy, __fsqrt_rn(__fsqrt_rn(vy.lo())), __fsqrt_rn(__fsqrt_rn(vy.hi())), u, zero, far);
+        } else {
+            const Pair root = mul(roots[k], Pair(v_scale));  // sqrt(vy) = sqrt(v) sqrt(vi)
+            mc[k] = codes_of<false>(my, root_of(my.lo()), root_of(my.hi()), u, zero, far);
+            vc[k] = codes_of<true>(vy, root_of(root.lo()), root_of(root.hi()), u, zero, far);
+        }
+        mc[k].lo = with_sign(mc[k].lo, m[k].lo()), mc[k].hi = with_sign(mc[k].hi, m[k].hi());
+        vc[k].lo = not_zero(vc[k].lo, vy.lo()), vc[k].hi = not_zero(vc[k].hi, vy.hi());
+    }
+    m_word = last_bytes(mc[0].lo, mc[0].hi, mc[1].lo, mc[1].hi);
+    v_word = last_bytes(vc[0].lo, vc[0].hi, vc[1].lo, vc[1].hi);
+    return far;
+}
+struct FourCodes {
+    uint32_t m, v;
+};
+__device__ __noinline__ FourCodes exact_codes(Pair m0, Pair m1, Pair v0, Pair v1, float mi, float vi, uint32_t w, Pair zero) {
+    const Pair m[2] = {m0, m1}, v[2] = {v0, v1};
+    FourCodes c;
+    four_codes<true>(m, v, v, mi, vi, 0.f, w, zero, c.m, c.v);
+    return c;
 }
 
 // ------------------------------------------------------------------------------- the step
@@ -156,7 +198,8 @@ __device__ __forceinline__ void update(const wtconv_optim_tensor &t, const StepS
     const long long n = t.n;
     const long long first = start + (threadIdx.x >> 5) * 256;
     if (first >= n) return;
-    float m[2][4], v[2][4], p[2][4], g[2][4];
+    Pair m[2][2], v[2][2], roots[2][2];  // [half of the block][pair]
+    float p[2][4], g[2][4], mf[2][4], vf[2][4];
     const long long blk = first / WTCONV_ADAMW_BLOCK;
     uint32_t mq[2], vq[2];
     float mu = 0.f, vu = 0.f;
@@ -164,37 +207,48 @@ __device__ __forceinline__ void update(const wtconv_optim_tensor &t, const StepS
     for (int h = 0; h < 2; ++h) {
         const long long i = first + h * 128 + lane * 4;
         if (BITS == 8) {
-            mq[h] = load_codes<VEC>(static_cast<const uint8_t *>(t.m), i, n);
+            mq[h] = load_codes<VEC>(static_cast<const uint8_t *>(t.m), i, n) ^ 0x80808080u;
             vq[h] = load_codes<VEC>(static_cast<const uint8_t *>(t.v), i, n);
         } else {
-            load4<VEC>(static_cast<const float *>(t.m), i, n, m[h]);
-            load4<VEC>(static_cast<const float *>(t.v), i, n, v[h]);
+            load4<VEC>(static_cast<const float *>(t.m), i, n, mf[h]);
+            load4<VEC>(static_cast<const float *>(t.v), i, n, vf[h]);
         }
         load4<VEC>(t.param, i, n, p[h]);
         load4<VEC>(static_cast<const G *>(t.grad), i, n, g[h]);
     }
     if (BITS == 8) mu = m_unit(t.m_max[blk]), vu = v_unit(t.v_max[blk]);
     if (!(fabsf(clip) <= FLT_MAX)) return;  // a step over gradients without a norm is not taken
-    float m_most = 0.f, v_most = 0.f, root[2][4];
+    const Pair zero(s.negative_zero);
+    uint32_t m_most = 0, v_most = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const long long i = first + h * 128 + lane * 4;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int k = 0; k < 2; ++k) {
             if (BITS == 8) {
-                m[h][j] = m_value(byte_of(mq[h] ^ 0x80808080u, j) - 128.f, mu);
-                v[h][j] = __fmul_rn(v_level(byte_of(vq[h], j)), vu);
+                m[h][k] = m_values(mq[h], 2 * k, Pair(mu));
+                v[h][k] = v_values(vq[h], 2 * k, Pair(vu));
+            } else {
+                m[h][k] = Pair(mf[h][2 * k], mf[h][2 * k + 1]);
+                v[h][k] = Pair(vf[h][2 * k], vf[h][2 * k + 1]);
             }
-            const float gs = __fmul_rn(g[h][j], clip);
-            m[h][j] = __fadd_rn(__fmul_rn(s.beta1, m[h][j]), __fmul_rn(s.one_minus_beta1, gs));
-            v[h][j] = __fadd_rn(__fmul_rn(s.beta2, v[h][j]), __fmul_rn(s.one_minus_beta2, __fmul_rn(gs, gs)));
+            const Pair gs = mul(Pair(g[h][2 * k], g[h][2 * k + 1]), Pair(clip));
+            m[h][k] = add(product(Pair(s.beta1), m[h][k], zero), product(Pair(s.one_minus_beta1), gs, zero));
+            v[h][k] = add(product(Pair(s.beta2), v[h][k], zero), product(Pair(s.one_minus_beta2), mul(gs, gs), zero));
             if (BITS == 8) {
-                m_most = nan_max(m_most, fabsf(m[h][j]));
-                v_most = nan_max(v_most, v[h][j]);
+                m_most = larger(m_most, abs(m[h][k]));
+                v_most = larger(v_most, v[h][k]);
             }
-            root[h][j] = root_of(v[h][j]);
-            const float step = m[h][j] * reciprocal(fmaf(root[h][j], s.root_scale, s.eps));
-            p[h][j] = fmaf(-s.rate, step, p[h][j] * s.keep);
+            // (at least the least normal number: its root is far below any useful eps)
+            roots[h][k] = Pair(root_of(fmaxf(v[h][k].lo(), FLT_MIN)), root_of(fmaxf(v[h][k].hi(), FLT_MIN)));
+            const Pair d = fma(roots[h][k], Pair(s.root_scale), Pair(s.eps));
+            const Pair step = mul(m[h][k], Pair(reciprocal(d.lo()), reciprocal(d.hi())));
+            const Pair q = fma(Pair(-s.rate), step, mul(Pair(p[h][2 * k], p[h][2 * k + 1]), Pair(s.keep)));
+            p[h][2 * k] = q.lo(), p[h][2 * k + 1] = q.hi();
+            if (BITS == 32) {
+                mf[h][2 * k] = m[h][k].lo(), mf[h][2 * k + 1] = m[h][k].hi();
+                vf[h][2 * k] = v[h][k].lo(), vf[h][2 * k + 1] = v[h][k].hi();
+            }
         }
         store4<VEC>(t.param, i, n, p[h]);
         if (t.copy != nullptr) {
@@ -202,56 +256,29 @@ __device__ __forceinline__ void update(const wtconv_optim_tensor &t, const StepS
             else store4<VEC>(static_cast<__half *>(t.copy), i, n, p[h]);
         }
         if (BITS == 32) {
-            store4<VEC>(static_cast<float *>(t.m), i, n, m[h]);
-            store4<VEC>(static_cast<float *>(t.v), i, n, v[h]);
+            store4<VEC>(static_cast<float *>(t.m), i, n, mf[h]);
+            store4<VEC>(static_cast<float *>(t.v), i, n, vf[h]);
         }
     }
     if (BITS == 8) {
-        m_most = block_max(m_most);
-        v_most = block_max(v_most);
-        if (m_most < kLeastMax) m_most = 0.f;
-        if (v_most < kLeastMax) v_most = 0.f;
-        const float mi = inverse_unit(m_most, 127.f * 127.f), vi = inverse_unit(v_most, 4228250625.f);
-        const float v_scale = root_of(vi);  // sqrt(y) = sqrt(v) sqrt(vi)
-        bool far = false;
-        uint32_t mc[2] = {0, 0}, vc[2] = {0, 0};
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float u = threshold((uint32_t)(first + h * 128 + lane * 4 + j), s.threshold0);
-                const float my = __fmul_rn(fabsf(m[h][j]), mi), vy = __fmul_rn(v[h][j], vi);
-                const uint32_t cm = code_of<false>(my, root_of(my), u, far);
-                const uint32_t cv = code_of<true>(vy, root_of(root[h][j] * v_scale), u, far);
-                mc[h] |= (m[h][j] < 0.f ? 0u - cm : cm) % 256u << (8 * j);
-                vc[h] |= max(cv, vy > 0.f ? 1u : 0u) << (8 * j);
-            }
-        if (far) {  // about one warp in a hundred
-#pragma unroll 1
-            for (int k = 0; k < 8; ++k) {
-                const int h = k >> 2, j = k & 3;
-                float mv = 0.f, vv = 0.f;
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (q == k) mv = m[q >> 2][q & 3], vv = v[q >> 2][q & 3];
-                const float u = threshold((uint32_t)(first + h * 128 + lane * 4 + j), s.threshold0);
-                const float my = __fmul_rn(fabsf(mv), mi), vy = __fmul_rn(vv, vi);
-                const uint32_t cm = exact_code<false>(my, u), cv = max(exact_code<true>(vy, u), vy > 0.f ? 1u : 0u);
-                const uint32_t mask = 255u << (8 * j);
-                const uint32_t mw = (mv < 0.f ? 0u - cm : cm) % 256u << (8 * j), vw = cv << (8 * j);
-                if (h == 0) mc[0] = (mc[0] & ~mask) | mw, vc[0] = (vc[0] & ~mask) | vw;
-                else mc[1] = (mc[1] & ~mask) | mw, vc[1] = (vc[1] & ~mask) | vw;
-            }
-        }
+        float m_max = block_max(m_most), v_max = block_max(v_most);
+        if (m_max < kLeastMax) m_max = 0.f;
+        if (v_max < kLeastMax) v_max = 0.f;
+        const float mi = inverse_unit(m_max, 127.f * 127.f), vi = inverse_unit(v_max, 4228250625.f);
+        const float v_scale = root_of(vi);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const long long i = first + h * 128 + lane * 4;
-            store_codes<VEC>(static_cast<uint8_t *>(t.m), i, n, mc[h]);
-            store_codes<VEC>(static_cast<uint8_t *>(t.v), i, n, vc[h]);
+            const uint32_t w = (uint32_t)i * kIndexStride + s.threshold0;
+            FourCodes c;
+            if (four_codes<false>(m[h], v[h], roots[h], mi, vi, v_scale, w, zero, c.m, c.v))  // one warp in some hundred
+                c = exact_codes(m[h][0], m[h][1], v[h][0], v[h][1], mi, vi, w, zero);
+            store_codes<VEC>(static_cast<uint8_t *>(t.m), i, n, c.m);
+            store_codes<VEC>(static_cast<uint8_t *>(t.v), i, n, c.v);
         }
         if (lane == 0) {
-            t.m_max[blk] = m_most;
-            t.v_max[blk] = v_most;
+            t.m_max[blk] = m_max;
+            t.v_max[blk] = v_max;
         }
     }
 }
@@ -293,9 +320,10 @@ template <bool VEC> __device__ __forceinline__ void write_values(const wtconv_op
         const long long i = first + h * 128 + lane * 4;
         float m[4], v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            m[j] = m_value(byte_of(mq[h] ^ 0x80808080u, j) - 128.f, mu);
-            v[j] = __fmul_rn(v_level(byte_of(vq[h], j)), vu);
+        for (int k = 0; k < 2; ++k) {
+            const Pair mk = m_values(mq[h] ^ 0x80808080u, 2 * k, Pair(mu)), vk = v_values(vq[h], 2 * k, Pair(vu));
+            m[2 * k] = mk.lo(), m[2 * k + 1] = mk.hi();
+            v[2 * k] = vk.lo(), v[2 * k + 1] = vk.hi();
         }
         if (m_out != nullptr) store4<VEC>(m_out, i, n, m);
         if (v_out != nullptr) store4<VEC>(v_out, i, n, v);

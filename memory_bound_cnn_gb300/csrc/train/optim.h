@@ -27,6 +27,7 @@ struct StepScalars {
     float rate;       // lr / (1 - beta1^t)
     float root_scale; // 1 / sqrt(1 - beta2^t)
     float eps;
+    float negative_zero;  // for `product` (train_device.cuh)
     uint32_t threshold0;  // t K2, the step's part of the rounding threshold
     int state_bits, grad_dtype, copy_dtype;
 };

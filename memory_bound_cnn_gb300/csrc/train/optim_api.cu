@@ -104,6 +104,7 @@ int wtconv_adamw_step(int n_tensors, const wtconv_optim_tensor *tensors, const w
     s.rate = (float)(c.lr / (1.0 - pow(c.beta1, (double)c.step)));
     s.root_scale = (float)(1.0 / sqrt(1.0 - pow(c.beta2, (double)c.step)));
     s.eps = (float)c.eps;
+    s.negative_zero = -0.f;
     s.threshold0 = (uint32_t)c.step * kStepStride;
     s.state_bits = c.state_bits, s.grad_dtype = c.grad_dtype, s.copy_dtype = c.copy_dtype;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -6,23 +6,53 @@
 
 namespace wtconv {
 
-// a = sigmoid(z) and b = 1 - a, both to a few units of their own last place: with e = exp(-z),
-// a = 1 / (1 + e) and b = e a, or 1 - a where e > 1 (a < 1/2 there, so nothing cancels, and an e
-// that overflowed gives a = 0, b = 1).  A NaN comes through.
-struct Gate {
-    float a, b;
+// Gates of two elements: a = sigmoid(z) and b = 1 - a, both to a few units of their own last place.
+// With e = exp(-z), a = 1 / (1 + e) and b = e a: nothing cancels.  e is held below 2^100, where a has
+// long been 0 to fp32's eyes beside any h that matters (2^-100) and b is 1.  A NaN comes through.
+struct Gates {
+    Pair a, b;
 };
-__device__ __forceinline__ float reciprocal(float v) {
+constexpr float kLog2E = 1.4426950408889634f;
+__device__ __forceinline__ float exp2_of(float v) {
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
-__device__ __forceinline__ Gate gate_of(float z) {
-    const float e = __expf(-z);
-    Gate g;
-    g.a = reciprocal(1.f + e);
-    g.b = e > 1.f ? 1.f - g.a : e * g.a;
+__device__ __forceinline__ float capped(float e) {  // min(e, 2^100), or NaN
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(e), "f"(1.2676506002282294e30f));
+    return r;
+}
+__device__ __forceinline__ Gates gates_of_exp(Pair e) {
+    const Pair d = add(e, Pair(1.f));
+    Gates g;
+    g.a = Pair(reciprocal(d.lo()), reciprocal(d.hi()));
+    g.b = mul(e, g.a);
     return g;
+}
+// bias: minus the channels' gate_bias, times log2 e
+__device__ __forceinline__ Gates gates_of(Pair gate, Pair bias) {
+    const Pair w = fma(gate, Pair(-kLog2E), bias);
+    return gates_of_exp(Pair(capped(exp2_of(w.lo())), capped(exp2_of(w.hi()))));
+}
+
+// Two 16-bit elements of a word as fp32, and back (rounded to nearest).
+template <typename T> __device__ __forceinline__ Pair widen(uint32_t w);
+template <> __device__ __forceinline__ Pair widen<__nv_bfloat16>(uint32_t w) {
+    return {__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)};
+}
+template <> __device__ __forceinline__ Pair widen<__half>(uint32_t w) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return {f.x, f.y};
+}
+template <typename T> __device__ __forceinline__ uint32_t narrow(Pair v);
+template <> __device__ __forceinline__ uint32_t narrow<__nv_bfloat16>(Pair v) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.lo(), v.hi());
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <> __device__ __forceinline__ uint32_t narrow<__half>(Pair v) {
+    const __half2 h = __floats2half2_rn(v.lo(), v.hi());
+    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // length of sequence b, clipped to [0, T]

@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) scan_planes_forward_kernel(con
     const T *x = static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c * a.x.row;
     const T *g = static_cast<const T *>(a.gate.p) + s.b * a.gate.batch + s.c * a.gate.row;
     T *y = static_cast<T *>(a.y.p) + s.b * a.y.batch + s.c * a.y.row;
-    const float bias = a.gate_bias[s.c];
+    const Pair bias(-kLog2E * a.gate_bias[s.c]);
 
     float carry = 0.f;
     Span whole = {1.f, 0.f};  // kReduce: the segment so far
@@ -109,13 +109,19 @@ __global__ void __launch_bounds__(kMaxWarps * 32) scan_planes_forward_kernel(con
         float av[8], uv[8];
         Span span = {1.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const Gate q = gate_of(eg.get(j) + bias);
-            const bool live = t + j < s.n;
-            av[j] = live ? q.a : 1.f;
-            uv[j] = live ? q.b * ex.get(j) : 0.f;
-            span = span.then({av[j], uv[j]});
+        for (int j = 0; j < 8; j += 2) {
+            const Gates q = gates_of(Pair(eg.get(j), eg.get(j + 1)), bias);
+            const Pair u = mul(q.b, Pair(ex.get(j), ex.get(j + 1)));
+            av[j] = q.a.lo(), av[j + 1] = q.a.hi();
+            uv[j] = u.lo(), uv[j + 1] = u.hi();
         }
+        if (t + 8 > s.n) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (t + j >= s.n) av[j] = 1.f, uv[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) span = span.then({av[j], uv[j]});
         if (round + 1 < s.round1) {
             nx.template load<VEC>(x + t + round_span, s.n - t - round_span);
             ng.template load<VEC>(g + t + round_span, s.n - t - round_span);
@@ -137,7 +143,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32) scan_planes_forward_kernel(con
         for (int j = 0; j < 8; j += 2) {
             const float h0 = fmaf(av[j], h, uv[j]);
             h = fmaf(av[j + 1], h0, uv[j + 1]);
-            out.set(j, t + j < s.n ? h0 : 0.f, t + j + 1 < s.n ? h : 0.f);
+            out.set(j, h0, h);
+        }
+        if (t + 8 > s.n) {  // past the length the state stands still, and y is 0
+#pragma unroll
+            for (int j = 0; j < 8; j += 2)
+                out.set(j, t + j < s.n ? out.get(j) : 0.f, t + j + 1 < s.n ? out.get(j + 1) : 0.f);
         }
         out.template store<VEC>(y + t, a.T - t);
     }
@@ -163,7 +174,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) scan_planes_backward_kernel(co
     const T *dy = static_cast<const T *>(a.dy.p) + s.b * a.dy.batch + s.c * a.dy.row;
     T *dx = static_cast<T *>(a.dx.p) + s.b * a.dx.batch + s.c * a.dx.row;
     T *dg = static_cast<T *>(a.d_gate.p) + s.b * a.d_gate.batch + s.c * a.d_gate.row;
-    const float bias = a.gate_bias[s.c];
+    const Pair bias(-kLog2E * a.gate_bias[s.c]);
 
     float carry = 0.f, sum = 0.f;  // carry: a_{t+1} dh_{t+1} of the position after this round
     Span whole = {1.f, 0.f};
@@ -191,11 +202,18 @@ __global__ void __launch_bounds__(kMaxWarps * 32) scan_planes_backward_kernel(co
         Span span = {1.f, 0.f};
         float flow = 0.f;
 #pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const Gates q = gates_of(Pair(eg.get(j), eg.get(j + 1)), bias);
+            av[j] = q.a.lo(), av[j + 1] = q.a.hi();
+            bv[j] = q.b.lo(), bv[j + 1] = q.b.hi();
+        }
+        if (t + 8 > s.n) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (t + j >= s.n) av[j] = 1.f, bv[j] = 0.f;
+        }
+#pragma unroll
         for (int j = 7; j >= 0; --j) {
-            const Gate q = gate_of(eg.get(j) + bias);
-            const bool live = t + j < s.n;
-            av[j] = live ? q.a : 1.f;
-            bv[j] = live ? q.b : 0.f;
             flow = av[j] * (edy.get(j) + flow);
             span.a *= av[j];
         }
@@ -204,9 +222,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32) scan_planes_backward_kernel(co
         float diff[8];  // h_{t-1} - x_t
         if (MODE == kApply) {
             // h again, by groups of lanes: a kept state stands before each
-            Span fwd = {1.f, 0.f};
+            Span fwd = {span.a, 0.f};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) fwd = fwd.then({av[j], bv[j] * ex.get(j)});
+            for (int j = 0; j < 8; ++j) fwd.u = fmaf(av[j], fwd.u, bv[j] * ex.get(j));
             float h = lane_before<kKeepLanes, false>(warp_scan<kKeepLanes, false>(fwd, lane), lane).of(kept);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
