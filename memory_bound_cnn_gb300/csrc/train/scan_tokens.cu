@@ -63,22 +63,31 @@ __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_
 template <int PENDING> __device__ __forceinline__ void wait_copies() {
     asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
-// rows: valid positions from `from` on; width: valid channels of the strip
-template <typename T, int CP>
-__device__ __forceinline__ void fetch_tile(Tile<T> &tile, const T *from, long long row, int rows, int width) {
-    constexpr int per_row = kRowBytes / CP, elems = CP / (int)sizeof(T), rows_at_once = kThreads<T> / per_row;
+// A thread's share of the copies of one tensor's tiles: column `c` of every `rows_at_once`-th row.
+template <typename T, int CP> struct Loader {
+    static constexpr int per_row = kRowBytes / CP, elems = CP / (int)sizeof(T), rows_at_once = kThreads<T> / per_row;
     static_assert(kThreads<T> % per_row == 0 && kSpan % rows_at_once == 0, "");
-    const int r0 = threadIdx.x / per_row, c = (threadIdx.x % per_row) * elems, left = width - c;
-    const int bytes = left <= 0 ? 0 : left >= elems ? CP : left * (int)sizeof(T);
-    from += r0 * row + (left > 0 ? c : 0);
+    const T *p;           // the thread's element of the next tile
+    long long round, stride;
+    // from: the strip's first channel at the CTA's first position; round: elements between its tiles
+    __device__ __forceinline__ Loader(const T *from, long long row, long long round_)
+        : p(from + (threadIdx.x / per_row) * row + (threadIdx.x % per_row) * elems), round(round_), stride(rows_at_once * row) {}
+    // rows: valid positions of the tile; width: valid channels of the strip
+    __device__ __forceinline__ void next(Tile<T> &tile, int rows, int width) {
+        const int r0 = threadIdx.x / per_row, c = (threadIdx.x % per_row) * elems, left = width - c;
+        const int bytes = left <= 0 ? 0 : left >= elems ? CP : left * (int)sizeof(T);
+        T *to = &tile.v[r0][c];
+        const T *from = p;
 #pragma unroll
-    for (int k = 0; k < kSpan; k += rows_at_once) {
-        T *to = &tile.v[r0 + k][c];
-        const bool valid = r0 + k < rows;
-        if constexpr (CP == 2) *to = valid && left > 0 ? from[k * row] : from_f32<T>(0.f);
-        else copy_async<CP>(to, valid ? from + k * row : from - r0 * row, valid ? bytes : 0);
+        for (int k = 0; k < kSpan; k += rows_at_once, from += stride) {
+            const bool valid = r0 + k < rows && bytes > 0;
+            if constexpr (CP == 2) to[k * kWidth<T>] = valid ? *from : from_f32<T>(0.f);
+            else copy_async<CP>(to + k * kWidth<T>, from, valid ? bytes : 0);  // of 0 bytes: the address is not read
+        }
+        p += round;
     }
-}
+    __device__ __forceinline__ void skip() { p += round; }
+};
 
 // Two channels of one row.  PAIRED: the address allows one store of both.
 template <typename T, bool PAIRED> __device__ __forceinline__ void store_two(T *p, Pair v, int width) {
@@ -96,6 +105,10 @@ template <typename T, bool PAIRED> __device__ __forceinline__ void store_two(T *
             if (width > 1) *reinterpret_cast<uint16_t *>(p + 1) = (uint16_t)(w >> 16);
         }
     }
+}
+template <typename T> __device__ __forceinline__ void store_pair(T *p, Pair v) {
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<float2 *>(p) = make_float2(v.lo(), v.hi());
+    else *reinterpret_cast<uint32_t *>(p) = narrow<T>(v);
 }
 __device__ __forceinline__ Pair load_two(const float *p, int width) {
     return {width > 0 ? p[0] : 0.f, width > 1 ? p[1] : 0.f};
@@ -150,13 +163,17 @@ __device__ __forceinline__ Pair exchange(const Map &mine, Maps<T> &sh, int parit
     }
     Map pre = identity();
     for (int i = 0; i < place; ++i) pre = pre.then(slot_map(i));
-    cg::cluster_group group = cg::this_cluster();
+    // Only the pushing warp orders its stores before the barrier: a release by every thread would wait
+    // for the outputs of the round before, too.
     if (place == kSlots - 1) {  // the last slot knows the CTA's map
         const Map all = pre.then(mine);
-        for (int r = 0; r < cluster; ++r) store_map(&group.map_shared_rank(&sh, r)->cta[parity][rank][lane], all);
+        for (int r = 0; r < cluster; ++r)
+            store_map(&cg::this_cluster().map_shared_rank(&sh, r)->cta[parity][rank][lane], all);
     }
     __syncwarp();
-    group.sync();
+    if (__any_sync(0xffffffffu, place == kSlots - 1)) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    else asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     Pair start = carry;
     for (int i = 0; i < cluster; ++i) {
         const int r = BACKWARD ? cluster - 1 - i : i;
@@ -243,20 +260,24 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
     const int round_span = p.cluster * kSpan, rounds = (a.T + round_span - 1) / round_span;
     const int round0 = s.seg * p.rounds_per, round1 = min(round0 + p.rounds_per, rounds);
     int t0 = round0 * round_span + s.rank * kSpan;  // the CTA's first position of the round
-    const T *x = static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c0 + t0 * a.x.row;
-    const T *g = static_cast<const T *>(a.gate.p) + s.b * a.gate.batch + s.c0 + t0 * a.gate.row;
+    Loader<T, CP> x(static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c0 + t0 * a.x.row, a.x.row, round_span * a.x.row);
+    Loader<T, CP> g(static_cast<const T *>(a.gate.p) + s.b * a.gate.batch + s.c0 + t0 * a.gate.row, a.gate.row,
+                    round_span * a.gate.row);
     T *y = static_cast<T *>(a.y.p) + s.b * a.y.batch + s.c + (t0 + slot * kSteps) * a.y.row;
-    const long long x_round = round_span * a.x.row, g_round = round_span * a.gate.row, y_round = round_span * a.y.row;
-    const auto fetch = [&](int k, int buf) {  // the round k rounds ahead
-        const int rows = s.n - t0 - k * round_span;
+    const long long y_round = round_span * a.y.row;
+    const bool whole_strip = PAIRED && s.c0 + kWidth<T> <= a.C;
+    int ahead = t0;  // first position of the next tiles to fetch
+    const auto fetch = [&](int buf) {
+        const int rows = s.n - ahead;
         if (rows > 0) {
-            fetch_tile<T, CP>(sh.x[buf], x + k * x_round, a.x.row, rows, a.C - s.c0);
-            fetch_tile<T, CP>(sh.g[buf], g + k * g_round, a.gate.row, rows, a.C - s.c0);
+            x.next(sh.x[buf], rows, a.C - s.c0);
+            g.next(sh.g[buf], rows, a.C - s.c0);
         }
         commit_copies();
+        ahead += round_span;
     };
-    fetch(0, round0 & 1);
-    if (round0 + 1 < round1) fetch(1, (round0 + 1) & 1);
+    fetch(round0 & 1);
+    if (round0 + 1 < round1) fetch((round0 + 1) & 1);
     else commit_copies();
 
     const Pair bias = mul(load_two(a.gate_bias + s.c, s.width), Pair(-kLog2E));
@@ -269,7 +290,9 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
     wait_copies<1>();
     if (p.cluster > 1) cg::this_cluster().sync();  // the others' shared memory is there
     else __syncthreads();
-    for (int round = round0; round < round1; ++round) {
+    // rounds of the whole cluster up to the length; what is left after it is filled below
+    const int live1 = min(round1, (s.n + round_span - 1) / round_span);
+    for (int round = round0; round < live1; ++round) {
         const int t = t0 + slot * kSteps;
         Pair av[kSteps], uv[kSteps];
         Map mine = identity();
@@ -289,18 +312,18 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
         wait_copies<0>();
         if constexpr (MODE == kReduce) {
             reduce_round<T, false>(mine, sh.maps, round & 1, slot, lane, whole);
-            if (round + 2 < round1) fetch(2, round & 1);
+            if (round + 2 < live1) fetch(round & 1);
         } else {
             Pair h = exchange<T, false>(mine, sh.maps, round & 1, slot, lane, p.cluster, s.rank, carry);
-            if (round + 2 < round1) fetch(2, round & 1);
+            if (round + 2 < live1) fetch(round & 1);
             if (a.states_out != nullptr && slot == 0 && t0 < a.T)
                 store_state(a.states_out + ((long long)s.b * a.keep + t0 / WTCONV_SCAN_KEEP) * a.C + s.c, h, s.width);
             T *to = y;
-            if (t + kSteps <= s.n) {
+            if (whole_strip && t + kSteps <= s.n) {
 #pragma unroll
                 for (int j = 0; j < kSteps; ++j, to += a.y.row) {
                     h = fma(av[j], h, uv[j]);
-                    store_two<T, PAIRED>(to, h, s.width);
+                    store_pair(to, h);
                 }
             } else {
 #pragma unroll
@@ -311,7 +334,16 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
             }
             y += y_round;
         }
-        t0 += round_span, x += x_round, g += g_round;
+        t0 += round_span;
+    }
+    if constexpr (MODE == kApply) {  // past the length the state stands still, and y is 0
+        for (int round = max(live1, round0); round < round1; ++round, t0 += round_span, y += y_round) {
+            if (a.states_out != nullptr && slot == 0 && t0 < a.T)
+                store_state(a.states_out + ((long long)s.b * a.keep + t0 / WTCONV_SCAN_KEEP) * a.C + s.c, carry, s.width);
+            T *to = y;
+            for (int j = 0; j < kSteps; ++j, to += a.y.row)
+                if (t0 + slot * kSteps + j < a.T) store_two<T, PAIRED>(to, Pair(0.f), s.width);
+        }
     }
     if constexpr (MODE == kReduce) {
         if (slot == 0) store_map(maps + (s.unit + s.seg) * kLanes<T> + lane, whole);
@@ -338,25 +370,42 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
     const Place s = place_of<T>(a, p, lane);
     const int round_span = p.cluster * kSpan, rounds = (a.T + round_span - 1) / round_span;
     const int round0 = s.seg * p.rounds_per, round1 = min(round0 + p.rounds_per, rounds);
-    int t0 = (round1 - 1) * round_span + s.rank * kSpan;
-    const T *x = static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c0 + t0 * a.x.row;
-    const T *g = static_cast<const T *>(a.gate.p) + s.b * a.gate.batch + s.c0 + t0 * a.gate.row;
-    const T *dy = static_cast<const T *>(a.dy.p) + s.b * a.dy.batch + s.c0 + t0 * a.dy.row;
+    // the rounds past the length come first: no gradient passes them, dx and d_gate are 0
+    const int live1 = max(round0, min(round1, (s.n + round_span - 1) / round_span));
+    int t0 = (live1 - 1) * round_span + s.rank * kSpan;
+    Loader<T, CP> x(static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c0 + t0 * a.x.row, a.x.row, -round_span * a.x.row);
+    Loader<T, CP> g(static_cast<const T *>(a.gate.p) + s.b * a.gate.batch + s.c0 + t0 * a.gate.row, a.gate.row,
+                    -round_span * a.gate.row);
+    Loader<T, CP> dy(static_cast<const T *>(a.dy.p) + s.b * a.dy.batch + s.c0 + t0 * a.dy.row, a.dy.row, -round_span * a.dy.row);
     T *dx = static_cast<T *>(a.dx.p) + s.b * a.dx.batch + s.c + (t0 + slot * kSteps + kSteps - 1) * a.dx.row;
     T *dg = static_cast<T *>(a.d_gate.p) + s.b * a.d_gate.batch + s.c + (t0 + slot * kSteps + kSteps - 1) * a.d_gate.row;
-    const long long x_round = round_span * a.x.row, g_round = round_span * a.gate.row, dy_round = round_span * a.dy.row;
-    const auto fetch = [&](int k, int buf) {  // the round k rounds on, towards the beginning
-        const int rows = s.n - t0 + k * round_span;
+    const bool whole_strip = PAIRED && s.c0 + kWidth<T> <= a.C;
+    int ahead = t0;  // first position of the next tiles to fetch, towards the beginning
+    const auto fetch = [&](int buf) {
+        const int rows = s.n - ahead;
         if (rows > 0) {
-            fetch_tile<T, CP>(sh.g[buf], g - k * g_round, a.gate.row, rows, a.C - s.c0);
-            fetch_tile<T, CP>(sh.dy[buf], dy - k * dy_round, a.dy.row, rows, a.C - s.c0);
-            if (MODE == kApply) fetch_tile<T, CP>(sh.x[buf], x - k * x_round, a.x.row, rows, a.C - s.c0);
+            g.next(sh.g[buf], rows, a.C - s.c0);
+            dy.next(sh.dy[buf], rows, a.C - s.c0);
+            if (MODE == kApply) x.next(sh.x[buf], rows, a.C - s.c0);
+        } else {
+            g.skip(), dy.skip(), x.skip();
         }
         commit_copies();
+        ahead -= round_span;
     };
-    fetch(0, (round1 - 1) & 1);
-    if (round0 + 1 < round1) fetch(1, round1 & 1);
+    if (round0 < live1) fetch((live1 - 1) & 1);
     else commit_copies();
+    if (round0 + 1 < live1) fetch(live1 & 1);
+    else commit_copies();
+    if constexpr (MODE == kApply) {
+        for (int t = live1 * round_span + s.rank * kSpan + slot * kSteps, round = live1; round < round1; ++round, t += round_span)
+            for (int j = 0; j < kSteps; ++j)
+                if (t + j < a.T) {
+                    store_two<T, PAIRED>(static_cast<T *>(a.dx.p) + s.b * a.dx.batch + (t + j) * a.dx.row + s.c, Pair(0.f), s.width);
+                    store_two<T, PAIRED>(static_cast<T *>(a.d_gate.p) + s.b * a.d_gate.batch + (t + j) * a.d_gate.row + s.c, Pair(0.f),
+                                         s.width);
+                }
+    }
 
     const Pair bias = mul(load_two(a.gate_bias + s.c, s.width), Pair(-kLog2E));
     Pair carry(0.f), sum(0.f), next_kept(0.f);
@@ -366,7 +415,7 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
             next_kept = load_two(a.states_in + ((long long)s.b * a.keep + at / WTCONV_SCAN_KEEP) * a.C + s.c, s.width);
     };
     if constexpr (MODE == kApply) {
-        kept_state(t0);
+        if (round0 < live1) kept_state(t0);
         if (a.dh_last != nullptr) carry = load_two(a.dh_last + (long long)s.b * a.C + s.c, s.width);
         if (s.seg < p.segments - 1)
             fold_segments<T, true>(maps + s.unit * kLanes<T>, s.seg + 1, p.segments, sh.maps, slot, lane, carry);
@@ -374,7 +423,7 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
     wait_copies<1>();
     if (p.cluster > 1) cg::this_cluster().sync();  // the others' shared memory is there
     else __syncthreads();
-    for (int round = round1 - 1; round >= round0; --round) {
+    for (int round = live1 - 1; round >= round0; --round) {
         const int t = t0 + slot * kSteps, live = s.n - t, buf = round & 1;
         const Pair kept = next_kept;
         Pair av[kSteps], bv[kSteps], dyv[kSteps], diff[kSteps];
@@ -395,7 +444,7 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
         wait_copies<0>();
         if constexpr (MODE == kReduce) {
             reduce_round<T, true>(back, sh.maps, buf, slot, lane, whole);
-            if (round - 2 >= round0) fetch(2, buf);
+            if (round - 2 >= round0) fetch(buf);
         } else {
             // h is scanned forward within the CTA's positions from the kept state; dh comes backward
             Map fwd = {back.a, Pair(0.f)};
@@ -403,7 +452,7 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
             for (int j = 0; j < kSteps; ++j) fwd.u = fma(av[j], fwd.u, mul(bv[j], diff[j]));
             store_map(&sh.forward[buf][slot][lane], fwd);
             Pair flow = exchange<T, true>(back, sh.maps, buf, slot, lane, p.cluster, s.rank, carry);
-            if (round - 2 >= round0) fetch(2, buf);
+            if (round - 2 >= round0) fetch(buf);
             if (round > round0) kept_state(t0 - round_span);
             Pair h = kept;
             for (int i = 0; i < slot; ++i) h = load_map(&sh.forward[buf][i][lane]).of(h);
@@ -414,20 +463,26 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
                 h = fma(av[j], h, mul(bv[j], xv));
             }
             T *to_x = dx, *to_g = dg;
+            const auto positions = [&](auto store) {
 #pragma unroll
-            for (int j = kSteps - 1; j >= 0; --j, to_x -= a.dx.row, to_g -= a.d_gate.row) {
-                const Pair dh = add(dyv[j], flow);
-                const Pair dgv = mul(mul(dh, diff[j]), mul(av[j], bv[j]));
-                sum = add(sum, dgv);
-                flow = mul(av[j], dh);
-                if (live >= kSteps || t + j < a.T) {
-                    store_two<T, PAIRED>(to_x, mul(bv[j], dh), s.width);
-                    store_two<T, PAIRED>(to_g, dgv, s.width);
+                for (int j = kSteps - 1; j >= 0; --j, to_x -= a.dx.row, to_g -= a.d_gate.row) {
+                    const Pair dh = add(dyv[j], flow);
+                    const Pair dgv = mul(mul(dh, diff[j]), mul(av[j], bv[j]));
+                    sum = add(sum, dgv);
+                    flow = mul(av[j], dh);
+                    store(j, mul(bv[j], dh), dgv);
                 }
+            };
+            if (whole_strip && live >= kSteps) {
+                positions([&](int, Pair dxv, Pair dgv) { store_pair(to_x, dxv), store_pair(to_g, dgv); });
+            } else {
+                positions([&](int j, Pair dxv, Pair dgv) {
+                    if (t + j < a.T) store_two<T, PAIRED>(to_x, dxv, s.width), store_two<T, PAIRED>(to_g, dgv, s.width);
+                });
             }
             dx -= round_span * a.dx.row, dg -= round_span * a.d_gate.row;
         }
-        t0 -= round_span, x -= x_round, g -= g_round, dy -= dy_round;
+        t0 -= round_span;
     }
     if constexpr (MODE == kReduce) {
         if (slot == 0) store_map(maps + (s.unit + s.seg) * kLanes<T> + lane, whole);
@@ -468,7 +523,8 @@ __global__ void __launch_bounds__(256) scan_tokens_bias_kernel(const float *part
     }
 }
 
-// Chains (strips of sequences) that do not give every SM `per_sm` CTAs are shared by clusters; where
+// Chains (strips of sequences) are shared by clusters as large as `per_sm` CTAs on every SM allow (one
+// more doubling left a second, mostly idle wave: 8x4096x1024 bf16 forward 70 us against 58); where
 // even full clusters give less than one CTA to every second SM, sequences are cut into segments.
 TokenPlan plan_of(const ScanArgs &a, int per_sm) {
     TokenPlan p;
@@ -478,7 +534,7 @@ TokenPlan plan_of(const ScanArgs &a, int per_sm) {
     const int rounds = (a.T + kSpan - 1) / kSpan;
     p.cluster = p.segments = 1;
     if (chains * kMaxCluster * 2 >= sms) {
-        while (p.cluster < kMaxCluster && chains * p.cluster < want && p.cluster < rounds) p.cluster *= 2;
+        while (p.cluster < kMaxCluster && chains * p.cluster * 2 <= want && p.cluster < rounds) p.cluster *= 2;
     } else {
         p.segments = (int)((want + chains - 1) / chains);
         if (p.segments > rounds) p.segments = rounds;
