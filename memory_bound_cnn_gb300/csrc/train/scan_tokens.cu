@@ -5,14 +5,14 @@
 // asynchronous copies two rounds ahead.  A thread owns two neighbouring channels (packed fp32
 // arithmetic: one instruction for both) and eight consecutive positions, which it reduces to the map
 // h -> a h + u of the state before them; the threads of a position group (a slot: a warp of 16-bit
-// strips, half a warp of fp32 ones) cover the strip.  The eight slots exchange their maps through
-// shared memory, and every thread runs its eight positions again from the state that reaches it, out
-// of registers: x, gate and (backward) dy are read once.
+// strips, half a warp of fp32 ones) cover the strip.  The slots leave their maps in shared memory, one
+// of them runs the state through all eight and leaves each slot's start, and every thread runs its
+// eight positions again from there, out of registers: x, gate and (backward) dy are read once.  (With
+// every slot folding the maps before its own, that fold was half of all instructions.)
 //
 // A strip of a sequence is a chain along time.  Where there are too few of them to fill the GPU, R
-// CTAs of a cluster share one: in a round CTA r takes the r-th 64 positions, the last slot pushes the
-// CTA's map into the shared memory of the others, and after the cluster's barrier each folds the maps
-// before its own.  Where even that leaves most SMs idle, the sequence is cut into segments whose maps
+// CTAs of a cluster share one: in a round CTA r takes the r-th 64 positions, pushes its map into the
+// shared memory of the others, and after the cluster's barrier each folds the maps before its own.  Where even that leaves most SMs idle, the sequence is cut into segments whose maps
 // a first kernel reduces (reading two inputs twice, the second time mostly from L2).
 #include <cooperative_groups.h>
 
@@ -86,7 +86,6 @@ template <typename T, int CP> struct Loader {
         }
         p += round;
     }
-    __device__ __forceinline__ void skip() { p += round; }
 };
 
 // Two channels of one row.  PAIRED: the address allows one store of both.
@@ -139,61 +138,81 @@ __device__ __forceinline__ Map load_map(const ulonglong2 *p) {
 __device__ __forceinline__ void store_map(ulonglong2 *p, const Map &m) { *p = make_ulonglong2(m.a.q, m.u.q); }
 
 template <typename T> struct Maps {
-    ulonglong2 slot[2][kSlots][kLanes<T>];
+    ulonglong2 slot[kSlots][kLanes<T>];          // this round's maps,
+    unsigned long long start[kSlots][kLanes<T>];  // and the state that reaches each slot
     ulonglong2 cta[2][kMaxCluster][kLanes<T>];
 };
 
-// Exchange of one round.  mine: the slot's map.  Returns the state before this slot's positions and
-// moves carry past the round.  BACKWARD: the last slot and CTA come first.
+// Runs carry (the state before the round) through the round: start[] of every slot, and carry after
+// the whole cluster's round.  By the kLanes threads of one slot, between two barriers; `lane` is the
+// thread's place among them.  BACKWARD: the last slot and CTA come first.
 template <typename T, bool BACKWARD>
-__device__ __forceinline__ Pair exchange(const Map &mine, Maps<T> &sh, int parity, int slot, int lane, int cluster, int rank,
-                                         Pair &carry) {
-    store_map(&sh.slot[parity][slot][lane], mine);
-    __syncthreads();
-    const int place = BACKWARD ? kSlots - 1 - slot : slot;  // in the order of the scan
-    const auto slot_map = [&](int i) { return load_map(&sh.slot[parity][BACKWARD ? kSlots - 1 - i : i][lane]); };
-    if (cluster == 1) {
-        Pair before = carry;
+__device__ __forceinline__ void run_chain(Maps<T> &sh, int lane, Pair &carry) {
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
-            carry = slot_map(i).of(carry);
-            if (i + 1 == place) before = carry;
-        }
-        return before;
+    for (int i = 0; i < kSlots; ++i) {
+        const int slot = BACKWARD ? kSlots - 1 - i : i;
+        sh.start[slot][lane] = carry.q;
+        carry = load_map(&sh.slot[slot][lane]).of(carry);
     }
-    Map pre = identity();
-    for (int i = 0; i < place; ++i) pre = pre.then(slot_map(i));
-    // Only the pushing warp orders its stores before the barrier: a release by every thread would wait
-    // for the outputs of the round before, too.
-    if (place == kSlots - 1) {  // the last slot knows the CTA's map
-        const Map all = pre.then(mine);
-        for (int r = 0; r < cluster; ++r)
-            store_map(&cg::this_cluster().map_shared_rank(&sh, r)->cta[parity][rank][lane], all);
-    }
-    __syncwarp();
-    if (__any_sync(0xffffffffu, place == kSlots - 1)) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    else asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    Pair start = carry;
+}
+// The CTA's map, pushed to every CTA of the cluster.
+template <typename T, bool BACKWARD>
+__device__ __forceinline__ void push_map(Maps<T> &sh, int lane, int parity, int cluster, int rank) {
+    Map all = load_map(&sh.slot[BACKWARD ? kSlots - 1 : 0][lane]);
+#pragma unroll
+    for (int i = 1; i < kSlots; ++i) all = all.then(load_map(&sh.slot[BACKWARD ? kSlots - 1 - i : i][lane]));
+    for (int r = 0; r < cluster; ++r) store_map(&cg::this_cluster().map_shared_rank(&sh, r)->cta[parity][rank][lane], all);
+}
+template <typename T, bool BACKWARD>
+__device__ __forceinline__ void run_cluster(Maps<T> &sh, int lane, int parity, int cluster, int rank, Pair &carry) {
+    Pair mine = carry;
     for (int i = 0; i < cluster; ++i) {
         const int r = BACKWARD ? cluster - 1 - i : i;
-        if (r == rank) start = carry;
+        if (r == rank) mine = carry;
         carry = load_map(&sh.cta[parity][r][lane]).of(carry);
     }
-    return pre.of(start);
+    run_chain<T, BACKWARD>(sh, lane, mine);
 }
-
-// A round of a segment's reduction: every slot appends all slots' maps to whole.
-template <typename T, bool BACKWARD>
-__device__ __forceinline__ void reduce_round(const Map &mine, Maps<T> &sh, int parity, int slot, int lane, Map &whole) {
-    store_map(&sh.slot[parity][slot][lane], mine);
+// One round's exchange: from the maps in sh.slot to the states in sh.start.  Threads below kLanes hold
+// the carry.  `beside`: work of another slot's threads, between the barriers.
+template <typename T, bool BACKWARD, typename F>
+__device__ __forceinline__ void exchange(Maps<T> &sh, int parity, int cluster, int rank, Pair &carry, F beside) {
+    const bool leads = threadIdx.x < kLanes<T>;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) whole = whole.then(load_map(&sh.slot[parity][BACKWARD ? kSlots - 1 - i : i][lane]));
+    if (cluster == 1) {
+        if (leads) run_chain<T, BACKWARD>(sh, threadIdx.x, carry);
+        else beside();
+        __syncthreads();
+        return;
+    }
+    // Only the pushing warp orders its stores before the barrier: a release by every thread would wait
+    // for the outputs of the round before, too.
+    if (threadIdx.x < 32) {
+        if (leads) push_map<T, BACKWARD>(sh, threadIdx.x, parity, cluster, rank);
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    } else {
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+        beside();
+        __syncwarp();
+    }
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (leads) run_cluster<T, BACKWARD>(sh, threadIdx.x, parity, cluster, rank, carry);
+    __syncthreads();
 }
 
-// State that the segments before (after, if BACKWARD) this one leave, from carry: their maps are
-// folded by the slots in parallel, then as in a round.
+// A round of a segment's reduction: the leading slot appends the round's maps to whole.
+template <typename T, bool BACKWARD> __device__ __forceinline__ void reduce_round(Maps<T> &sh, Map &whole) {
+    __syncthreads();
+    if (threadIdx.x < kLanes<T>) {
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) whole = whole.then(load_map(&sh.slot[BACKWARD ? kSlots - 1 - i : i][threadIdx.x]));
+    }
+    __syncthreads();
+}
+
+// State that the segments before (after, if BACKWARD) this one leave, from carry (of the leading
+// slot): their maps are folded by the slots in parallel, then as in a round.
 template <typename T, bool BACKWARD>
 __device__ __forceinline__ void fold_segments(const ulonglong2 *maps, int first, int last, Maps<T> &sh, int slot, int lane,
                                               Pair &carry) {
@@ -202,8 +221,8 @@ __device__ __forceinline__ void fold_segments(const ulonglong2 *maps, int first,
     const int place = BACKWARD ? kSlots - 1 - slot : slot;
     for (int i = place * per; i < min((place + 1) * per, count); ++i)
         mine = mine.then(load_map(maps + (long long)(BACKWARD ? last - 1 - i : first + i) * kLanes<T> + lane));
-    exchange<T, BACKWARD>(mine, sh, 0, slot, lane, 1, 0, carry);
-    __syncthreads();
+    store_map(&sh.slot[slot][lane], mine);
+    exchange<T, BACKWARD>(sh, 0, 1, 0, carry, [] {});
 }
 
 struct Place {
@@ -268,11 +287,8 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
     const bool whole_strip = PAIRED && s.c0 + kWidth<T> <= a.C;
     int ahead = t0;  // first position of the next tiles to fetch
     const auto fetch = [&](int buf) {
-        const int rows = s.n - ahead;
-        if (rows > 0) {
-            x.next(sh.x[buf], rows, a.C - s.c0);
-            g.next(sh.g[buf], rows, a.C - s.c0);
-        }
+        x.next(sh.x[buf], s.n - ahead, a.C - s.c0);
+        g.next(sh.g[buf], s.n - ahead, a.C - s.c0);
         commit_copies();
         ahead += round_span;
     };
@@ -296,26 +312,23 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
         const int t = t0 + slot * kSteps;
         Pair av[kSteps], uv[kSteps];
         Map mine = identity();
-        if (t0 < s.n) {
-            read_gates(sh.g[round & 1], slot, lane, bias, s.n - t, av, uv);
+        read_gates(sh.g[round & 1], slot, lane, bias, s.n - t, av, uv);
 #pragma unroll
-            for (int j = 0; j < kSteps; ++j) {
-                // (beyond the length the tile holds zeros)
-                uv[j] = mul(uv[j], sh.x[round & 1].read(slot * kSteps + j, lane));
-                mine = mine.then({av[j], uv[j]});
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < kSteps; ++j) av[j] = Pair(1.f), uv[j] = Pair(0.f);
+        for (int j = 0; j < kSteps; ++j) {
+            uv[j] = mul(uv[j], sh.x[round & 1].read(slot * kSteps + j, lane));  // (x is 0 beyond the length)
+            mine = mine.then({av[j], uv[j]});
         }
-        // the barrier inside the exchange ends all reading of this round's tiles and shows the next's
+        store_map(&sh.maps.slot[slot][lane], mine);
+        // the exchange's barriers end all reading of this round's tiles and show the next's
         wait_copies<0>();
         if constexpr (MODE == kReduce) {
-            reduce_round<T, false>(mine, sh.maps, round & 1, slot, lane, whole);
+            reduce_round<T, false>(sh.maps, whole);
             if (round + 2 < live1) fetch(round & 1);
         } else {
-            Pair h = exchange<T, false>(mine, sh.maps, round & 1, slot, lane, p.cluster, s.rank, carry);
+            exchange<T, false>(sh.maps, round & 1, p.cluster, s.rank, carry, [] {});
             if (round + 2 < live1) fetch(round & 1);
+            Pair h;
+            h.q = sh.maps.start[slot][lane];
             if (a.states_out != nullptr && slot == 0 && t0 < a.T)
                 store_state(a.states_out + ((long long)s.b * a.keep + t0 / WTCONV_SCAN_KEEP) * a.C + s.c, h, s.width);
             T *to = y;
@@ -357,7 +370,9 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
 template <typename T> struct BackwardShared {
     Tile<T> x[2], g[2], dy[2];
     Maps<T> maps;
-    ulonglong2 forward[2][kSlots][kLanes<T>];
+    // h within the CTA's positions, from the kept state: as slot and start of Maps
+    ulonglong2 forward[kSlots][kLanes<T>];
+    unsigned long long forward_start[kSlots][kLanes<T>];
 };
 
 // bias_part: one float per (unit, segment, rank, channel of the strip)
@@ -382,14 +397,9 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
     const bool whole_strip = PAIRED && s.c0 + kWidth<T> <= a.C;
     int ahead = t0;  // first position of the next tiles to fetch, towards the beginning
     const auto fetch = [&](int buf) {
-        const int rows = s.n - ahead;
-        if (rows > 0) {
-            g.next(sh.g[buf], rows, a.C - s.c0);
-            dy.next(sh.dy[buf], rows, a.C - s.c0);
-            if (MODE == kApply) x.next(sh.x[buf], rows, a.C - s.c0);
-        } else {
-            g.skip(), dy.skip(), x.skip();
-        }
+        g.next(sh.g[buf], s.n - ahead, a.C - s.c0);
+        dy.next(sh.dy[buf], s.n - ahead, a.C - s.c0);
+        if (MODE == kApply) x.next(sh.x[buf], s.n - ahead, a.C - s.c0);
         commit_copies();
         ahead -= round_span;
     };
@@ -414,8 +424,9 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
         if (at < a.T)
             next_kept = load_two(a.states_in + ((long long)s.b * a.keep + at / WTCONV_SCAN_KEEP) * a.C + s.c, s.width);
     };
+    const bool runs_h = threadIdx.x - 32u < (unsigned)kLanes<T>;  // a slot's threads in the second warp
     if constexpr (MODE == kApply) {
-        if (round0 < live1) kept_state(t0);
+        if (round0 < live1 && runs_h) kept_state(t0);
         if (a.dh_last != nullptr) carry = load_two(a.dh_last + (long long)s.b * a.C + s.c, s.width);
         if (s.seg < p.segments - 1)
             fold_segments<T, true>(maps + s.unit * kLanes<T>, s.seg + 1, p.segments, sh.maps, slot, lane, carry);
@@ -425,37 +436,42 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
     else __syncthreads();
     for (int round = live1 - 1; round >= round0; --round) {
         const int t = t0 + slot * kSteps, live = s.n - t, buf = round & 1;
-        const Pair kept = next_kept;
         Pair av[kSteps], bv[kSteps], dyv[kSteps], diff[kSteps];
         Map back = identity();
-        if (t0 < s.n) {
-            read_gates(sh.g[buf], slot, lane, bias, live, av, bv);
+        read_gates(sh.g[buf], slot, lane, bias, live, av, bv);
 #pragma unroll
-            for (int j = kSteps - 1; j >= 0; --j) {
-                dyv[j] = sh.dy[buf].read(slot * kSteps + j, lane);  // (zeros beyond the length)
-                back.u = mul(av[j], add(dyv[j], back.u));
-                back.a = mul(back.a, av[j]);
-                if (MODE == kApply) diff[j] = sh.x[buf].read(slot * kSteps + j, lane);  // x, until h is known
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < kSteps; ++j) av[j] = Pair(1.f), bv[j] = dyv[j] = diff[j] = Pair(0.f);
+        for (int j = kSteps - 1; j >= 0; --j) {
+            dyv[j] = sh.dy[buf].read(slot * kSteps + j, lane);  // (dy and x are 0 beyond the length)
+            back.u = mul(av[j], add(dyv[j], back.u));
+            back.a = mul(back.a, av[j]);
+            if (MODE == kApply) diff[j] = sh.x[buf].read(slot * kSteps + j, lane);  // x, until h is known
         }
-        wait_copies<0>();
+        store_map(&sh.maps.slot[slot][lane], back);
         if constexpr (MODE == kReduce) {
-            reduce_round<T, true>(back, sh.maps, buf, slot, lane, whole);
+            wait_copies<0>();
+            reduce_round<T, true>(sh.maps, whole);
             if (round - 2 >= round0) fetch(buf);
         } else {
             // h is scanned forward within the CTA's positions from the kept state; dh comes backward
             Map fwd = {back.a, Pair(0.f)};
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) fwd.u = fma(av[j], fwd.u, mul(bv[j], diff[j]));
-            store_map(&sh.forward[buf][slot][lane], fwd);
-            Pair flow = exchange<T, true>(back, sh.maps, buf, slot, lane, p.cluster, s.rank, carry);
+            store_map(&sh.forward[slot][lane], fwd);
+            wait_copies<0>();
+            exchange<T, true>(sh.maps, buf, p.cluster, s.rank, carry, [&] {
+                if (!runs_h) return;
+                Pair h = next_kept;
+#pragma unroll
+                for (int i = 0; i < kSlots; ++i) {
+                    sh.forward_start[i][lane] = h.q;
+                    h = load_map(&sh.forward[i][lane]).of(h);
+                }
+                if (round > round0) kept_state(t0 - round_span);
+            });
             if (round - 2 >= round0) fetch(buf);
-            if (round > round0) kept_state(t0 - round_span);
-            Pair h = kept;
-            for (int i = 0; i < slot; ++i) h = load_map(&sh.forward[buf][i][lane]).of(h);
+            Pair flow, h;
+            flow.q = sh.maps.start[slot][lane];
+            h.q = sh.forward_start[slot][lane];
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) {
                 const Pair xv = diff[j];
