@@ -54,6 +54,13 @@ enum wtconv_scan_op { WTCONV_SCAN_OP_FORWARD = 0, WTCONV_SCAN_OP_BACKWARD = 1 };
  * for an invalid shape). */
 size_t wtconv_scan_workspace_size(int op, int B, int T, int C, int layout, int dtype);
 
+/* Device-side status of the scans run so far on the current device.  The CTAs of a cluster that share
+ * a sequence wait for one another's part of a round, each time at most half a second; a wait that
+ * gives up (never expected) raises a sticky flag, and what follows of that sequence comes out as NaN.
+ * Synchronises the device; WTCONV_ERR_DEVICE_TIMEOUT if the flag was raised (and clears it),
+ * WTCONV_ERR_CUDA if the synchronisation or the read failed, else WTCONV_OK. */
+int wtconv_scan_status(void);
+
 /* y and the optional outputs h_last [B][C] and states (NULL: not wanted).  h0 NULL: zeros.
  * lengths NULL: every sequence has T positions. */
 int wtconv_scan_forward(int B, int T, int C, int layout, int dtype, const void *x, long long x_batch,

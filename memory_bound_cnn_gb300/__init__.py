@@ -12,6 +12,7 @@ from .scan import (  # noqa: F401
     gated_scan,
     wtconv_scan_backward,
     wtconv_scan_forward,
+    wtconv_scan_status,
     wtconv_scan_step,
     wtconv_scan_workspace_size,
 )

@@ -61,6 +61,13 @@ size_t wtconv_scan_workspace_size(int op, int B, int T, int C, int layout, int d
     return scan_workspace(op, shape_args(B, T, C, layout, dtype));
 }
 
+int wtconv_scan_status(void) {
+    if (cudaDeviceSynchronize() != cudaSuccess) return WTCONV_ERR_CUDA;
+    int raised = 0;
+    if (take_scan_timeout(&raised) != cudaSuccess) return WTCONV_ERR_CUDA;
+    return raised ? WTCONV_ERR_DEVICE_TIMEOUT : WTCONV_OK;
+}
+
 int wtconv_scan_forward(int B, int T, int C, int layout, int dtype, const void *x, long long x_batch, long long x_row,
                         const void *gate, long long gate_batch, long long gate_row, const float *gate_bias,
                         const float *h0, const int *lengths, void *y, long long y_batch, long long y_row,

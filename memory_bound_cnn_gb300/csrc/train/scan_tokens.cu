@@ -11,8 +11,10 @@
 // every slot folding the maps before its own, that fold was half of all instructions.)
 //
 // A strip of a sequence is a chain along time.  Where there are too few of them to fill the GPU, R
-// CTAs of a cluster share one: in a round CTA r takes the r-th 64 positions, pushes its map into the
-// shared memory of the others, and after the cluster's barrier each folds the maps before its own.  Where even that leaves most SMs idle, the sequence is cut into segments whose maps
+// CTAs of a cluster share one: in a round CTA r takes the r-th 64 positions and pushes its map into the
+// shared memory of all, where it counts towards an mbarrier; when that has all of a round's maps, each
+// CTA folds those before its own.  (A cluster barrier instead waits for every thread of every CTA, and
+// its release for the outputs of the round before: 8x4096x1024 bf16 forward 61 us, 56 so.)  Where even that leaves most SMs idle, the sequence is cut into segments whose maps
 // a first kernel reduces (reading two inputs twice, the second time mostly from L2).
 #include <cooperative_groups.h>
 
@@ -140,7 +142,54 @@ __device__ __forceinline__ void store_map(ulonglong2 *p, const Map &m) { *p = ma
 template <typename T> struct Maps {
     ulonglong2 slot[kSlots][kLanes<T>];          // this round's maps,
     unsigned long long start[kSlots][kLanes<T>];  // and the state that reaches each slot
-    ulonglong2 cta[2][kMaxCluster][kLanes<T>];
+    ulonglong2 cta[2][kMaxCluster][kLanes<T>];   // the CTAs' maps of this round and the next,
+    unsigned long long arrived[2];               // and the mbarriers that count their bytes
+};
+
+// ------------------------------------------------------------- maps of the CTAs of a cluster
+
+// Raised by a wait that gave up (never expected); read by wtconv_scan_status.
+__device__ int g_scan_timeout;
+
+constexpr unsigned kMaxTries = 1u << 20, kWaitHintNs = 20000;
+constexpr unsigned long long kMaxWaitNs = 500000000ull;
+
+__device__ __forceinline__ unsigned shared_address(const void *p) { return (unsigned)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ unsigned remote_address(unsigned local, int rank) {
+    unsigned r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ unsigned long long global_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+// Waits at most half a second for a phase of an mbarrier; false (and the flag) if it did not come.
+__device__ __forceinline__ bool wait_phase(unsigned bar, unsigned parity) {
+    unsigned long long t0 = 0;
+    for (unsigned i = 0; i < kMaxTries; ++i) {
+        unsigned done;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done) : "r"(bar), "r"(parity), "n"(kWaitHintNs) : "memory");
+        if (done) return true;
+        if ((i & 15) == 0) {
+            const unsigned long long now = global_ns();
+            if (i == 0) t0 = now;
+            else if (now - t0 > kMaxWaitNs) break;
+        }
+    }
+    atomicExch(&g_scan_timeout, 1);
+    return false;
+}
+
+// What the leading slot's threads carry from round to round.
+struct Chain {
+    Pair state;           // before the round of the whole cluster
+    unsigned phases = 0;  // bit b: phase that arrived[b] completes next
+    bool broken = false;  // a wait gave up: the rest comes out as NaN
 };
 
 // Runs carry (the state before the round) through the round: start[] of every slot, and carry after
@@ -155,50 +204,54 @@ __device__ __forceinline__ void run_chain(Maps<T> &sh, int lane, Pair &carry) {
         carry = load_map(&sh.slot[slot][lane]).of(carry);
     }
 }
-// The CTA's map, pushed to every CTA of the cluster.
+// The CTA's map to every CTA of the cluster, then the state through the maps of all.
+//
+// Two buffers are enough: a CTA pushes the maps of round k + 2 after it has those of round k + 1 from
+// all, and each of them pushed those after it had read the maps of round k.
 template <typename T, bool BACKWARD>
-__device__ __forceinline__ void push_map(Maps<T> &sh, int lane, int parity, int cluster, int rank) {
+__device__ __forceinline__ void run_cluster(Maps<T> &sh, int lane, int parity, int cluster, int rank, Chain &chain) {
     Map all = load_map(&sh.slot[BACKWARD ? kSlots - 1 : 0][lane]);
 #pragma unroll
     for (int i = 1; i < kSlots; ++i) all = all.then(load_map(&sh.slot[BACKWARD ? kSlots - 1 - i : i][lane]));
-    for (int r = 0; r < cluster; ++r) store_map(&cg::this_cluster().map_shared_rank(&sh, r)->cta[parity][rank][lane], all);
-}
-template <typename T, bool BACKWARD>
-__device__ __forceinline__ void run_cluster(Maps<T> &sh, int lane, int parity, int cluster, int rank, Pair &carry) {
-    Pair mine = carry;
+    const unsigned bar = shared_address(&sh.arrived[parity]), place = shared_address(&sh.cta[parity][rank][lane]);
+    if (lane == 0)
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(cluster * kLanes<T> * 16) : "memory");
+    for (int r = 0; r < cluster; ++r)
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                         remote_address(place, r)),
+                     "r"((unsigned)all.a.q), "r"((unsigned)(all.a.q >> 32)), "r"((unsigned)all.u.q),
+                     "r"((unsigned)(all.u.q >> 32)), "r"(remote_address(bar, r)) : "memory");
+    if (!chain.broken) chain.broken = !wait_phase(bar, chain.phases >> parity & 1);
+    chain.phases ^= 1u << parity;
+    if (chain.broken) chain.state = Pair(__int_as_float(0x7fc00000));
+    Pair mine = chain.state;
     for (int i = 0; i < cluster; ++i) {
         const int r = BACKWARD ? cluster - 1 - i : i;
-        if (r == rank) mine = carry;
-        carry = load_map(&sh.cta[parity][r][lane]).of(carry);
+        if (r == rank) mine = chain.state;
+        chain.state = load_map(&sh.cta[parity][r][lane]).of(chain.state);
     }
     run_chain<T, BACKWARD>(sh, lane, mine);
 }
 // One round's exchange: from the maps in sh.slot to the states in sh.start.  Threads below kLanes hold
-// the carry.  `beside`: work of another slot's threads, between the barriers.
+// the chain.  `beside`: work of another slot's threads, between the barriers.
 template <typename T, bool BACKWARD, typename F>
-__device__ __forceinline__ void exchange(Maps<T> &sh, int parity, int cluster, int rank, Pair &carry, F beside) {
-    const bool leads = threadIdx.x < kLanes<T>;
+__device__ __forceinline__ void exchange(Maps<T> &sh, int parity, int cluster, int rank, Chain &chain, F beside) {
     __syncthreads();
-    if (cluster == 1) {
-        if (leads) run_chain<T, BACKWARD>(sh, threadIdx.x, carry);
-        else beside();
-        __syncthreads();
-        return;
-    }
-    // Only the pushing warp orders its stores before the barrier: a release by every thread would wait
-    // for the outputs of the round before, too.
-    if (threadIdx.x < 32) {
-        if (leads) push_map<T, BACKWARD>(sh, threadIdx.x, parity, cluster, rank);
-        __syncwarp();
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (threadIdx.x < kLanes<T>) {
+        if (cluster == 1) run_chain<T, BACKWARD>(sh, threadIdx.x, chain.state);
+        else run_cluster<T, BACKWARD>(sh, threadIdx.x, parity, cluster, rank, chain);
     } else {
-        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
         beside();
-        __syncwarp();
     }
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (leads) run_cluster<T, BACKWARD>(sh, threadIdx.x, parity, cluster, rank, carry);
     __syncthreads();
+}
+// Before the first round: the cluster's mbarriers are ready, and every CTA's shared memory is there.
+template <typename T> __device__ __forceinline__ void start_cluster(Maps<T> &sh) {
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < 2; ++b) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_address(&sh.arrived[b])) : "memory");
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    cg::this_cluster().sync();
 }
 
 // A round of a segment's reduction: the leading slot appends the round's maps to whole.
@@ -211,18 +264,18 @@ template <typename T, bool BACKWARD> __device__ __forceinline__ void reduce_roun
     __syncthreads();
 }
 
-// State that the segments before (after, if BACKWARD) this one leave, from carry (of the leading
+// State that the segments before (after, if BACKWARD) this one leave, from chain (of the leading
 // slot): their maps are folded by the slots in parallel, then as in a round.
 template <typename T, bool BACKWARD>
 __device__ __forceinline__ void fold_segments(const ulonglong2 *maps, int first, int last, Maps<T> &sh, int slot, int lane,
-                                              Pair &carry) {
+                                              Chain &chain) {
     const int count = last - first, per = (count + kSlots - 1) / kSlots;
     Map mine = identity();
     const int place = BACKWARD ? kSlots - 1 - slot : slot;
     for (int i = place * per; i < min((place + 1) * per, count); ++i)
         mine = mine.then(load_map(maps + (long long)(BACKWARD ? last - 1 - i : first + i) * kLanes<T> + lane));
     store_map(&sh.slot[slot][lane], mine);
-    exchange<T, BACKWARD>(sh, 0, 1, 0, carry, [] {});
+    exchange<T, BACKWARD>(sh, 0, 1, 0, chain, [] {});
 }
 
 struct Place {
@@ -297,14 +350,15 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
     else commit_copies();
 
     const Pair bias = mul(load_two(a.gate_bias + s.c, s.width), Pair(-kLog2E));
-    Pair carry(0.f);
+    Chain chain;
+    chain.state = Pair(0.f);
     Map whole = identity();
     if constexpr (MODE == kApply) {
-        if (a.h0 != nullptr) carry = load_two(a.h0 + (long long)s.b * a.C + s.c, s.width);
-        if (s.seg > 0) fold_segments<T, false>(maps + s.unit * kLanes<T>, 0, s.seg, sh.maps, slot, lane, carry);
+        if (a.h0 != nullptr) chain.state = load_two(a.h0 + (long long)s.b * a.C + s.c, s.width);
+        if (s.seg > 0) fold_segments<T, false>(maps + s.unit * kLanes<T>, 0, s.seg, sh.maps, slot, lane, chain);
     }
     wait_copies<1>();
-    if (p.cluster > 1) cg::this_cluster().sync();  // the others' shared memory is there
+    if (p.cluster > 1) start_cluster(sh.maps);
     else __syncthreads();
     // rounds of the whole cluster up to the length; what is left after it is filled below
     const int live1 = min(round1, (s.n + round_span - 1) / round_span);
@@ -325,7 +379,7 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
             reduce_round<T, false>(sh.maps, whole);
             if (round + 2 < live1) fetch(round & 1);
         } else {
-            exchange<T, false>(sh.maps, round & 1, p.cluster, s.rank, carry, [] {});
+            exchange<T, false>(sh.maps, round & 1, p.cluster, s.rank, chain, [] {});
             if (round + 2 < live1) fetch(round & 1);
             Pair h;
             h.q = sh.maps.start[slot][lane];
@@ -352,7 +406,7 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
     if constexpr (MODE == kApply) {  // past the length the state stands still, and y is 0
         for (int round = max(live1, round0); round < round1; ++round, t0 += round_span, y += y_round) {
             if (a.states_out != nullptr && slot == 0 && t0 < a.T)
-                store_state(a.states_out + ((long long)s.b * a.keep + t0 / WTCONV_SCAN_KEEP) * a.C + s.c, carry, s.width);
+                store_state(a.states_out + ((long long)s.b * a.keep + t0 / WTCONV_SCAN_KEEP) * a.C + s.c, chain.state, s.width);
             T *to = y;
             for (int j = 0; j < kSteps; ++j, to += a.y.row)
                 if (t0 + slot * kSteps + j < a.T) store_two<T, PAIRED>(to, Pair(0.f), s.width);
@@ -361,7 +415,7 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
     if constexpr (MODE == kReduce) {
         if (slot == 0) store_map(maps + (s.unit + s.seg) * kLanes<T> + lane, whole);
     } else if (a.h_last != nullptr && s.seg == p.segments - 1 && s.rank == 0 && slot == 0) {
-        store_state(a.h_last + (long long)s.b * a.C + s.c, carry, s.width);
+        store_state(a.h_last + (long long)s.b * a.C + s.c, chain.state, s.width);
     }
 }
 
@@ -418,7 +472,9 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
     }
 
     const Pair bias = mul(load_two(a.gate_bias + s.c, s.width), Pair(-kLog2E));
-    Pair carry(0.f), sum(0.f), next_kept(0.f);
+    Chain chain;
+    chain.state = Pair(0.f);
+    Pair sum(0.f), next_kept(0.f);
     Map whole = identity();
     const auto kept_state = [&](int at) {
         if (at < a.T)
@@ -427,12 +483,12 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
     const bool runs_h = threadIdx.x - 32u < (unsigned)kLanes<T>;  // a slot's threads in the second warp
     if constexpr (MODE == kApply) {
         if (round0 < live1 && runs_h) kept_state(t0);
-        if (a.dh_last != nullptr) carry = load_two(a.dh_last + (long long)s.b * a.C + s.c, s.width);
+        if (a.dh_last != nullptr) chain.state = load_two(a.dh_last + (long long)s.b * a.C + s.c, s.width);
         if (s.seg < p.segments - 1)
-            fold_segments<T, true>(maps + s.unit * kLanes<T>, s.seg + 1, p.segments, sh.maps, slot, lane, carry);
+            fold_segments<T, true>(maps + s.unit * kLanes<T>, s.seg + 1, p.segments, sh.maps, slot, lane, chain);
     }
     wait_copies<1>();
-    if (p.cluster > 1) cg::this_cluster().sync();  // the others' shared memory is there
+    if (p.cluster > 1) start_cluster(sh.maps);
     else __syncthreads();
     for (int round = live1 - 1; round >= round0; --round) {
         const int t = t0 + slot * kSteps, live = s.n - t, buf = round & 1;
@@ -458,7 +514,7 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
             for (int j = 0; j < kSteps; ++j) fwd.u = fma(av[j], fwd.u, mul(bv[j], diff[j]));
             store_map(&sh.forward[slot][lane], fwd);
             wait_copies<0>();
-            exchange<T, true>(sh.maps, buf, p.cluster, s.rank, carry, [&] {
+            exchange<T, true>(sh.maps, buf, p.cluster, s.rank, chain, [&] {
                 if (!runs_h) return;
                 Pair h = next_kept;
 #pragma unroll
@@ -504,7 +560,7 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
         if (slot == 0) store_map(maps + (s.unit + s.seg) * kLanes<T> + lane, whole);
     } else {
         if (a.d_h0 != nullptr && s.seg == 0 && s.rank == 0 && slot == 0)
-            store_state(a.d_h0 + (long long)s.b * a.C + s.c, carry, s.width);
+            store_state(a.d_h0 + (long long)s.b * a.C + s.c, chain.state, s.width);
         __syncthreads();
         Pair *sums = reinterpret_cast<Pair *>(sh.forward);
         sums[slot * kLanes<T> + lane] = sum;
@@ -666,6 +722,12 @@ __global__ void __launch_bounds__(256) scan_step_kernel(int C, int parts, ScanTe
 }
 
 }  // namespace
+
+cudaError_t take_scan_timeout(int *raised) {
+    const cudaError_t e = cudaMemcpyFromSymbol(raised, g_scan_timeout, sizeof(int));
+    const int zero = 0;
+    return e != cudaSuccess || *raised == 0 ? e : cudaMemcpyToSymbol(g_scan_timeout, &zero, sizeof(int));
+}
 
 size_t scan_tokens_workspace(int op, const ScanArgs &a) {
     const bool back = op == WTCONV_SCAN_OP_BACKWARD;

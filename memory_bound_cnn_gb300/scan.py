@@ -17,7 +17,7 @@ from .wtconv import load, load_binding
 SCAN_KEEP = 64  # WTCONV_SCAN_KEEP
 OP_SCAN_FORWARD, OP_SCAN_BACKWARD = 0, 1
 
-EXPORTED = ("wtconv_scan_workspace_size", "wtconv_scan_forward", "wtconv_scan_backward", "wtconv_scan_step")
+EXPORTED = ("wtconv_scan_workspace_size", "wtconv_scan_status", "wtconv_scan_forward", "wtconv_scan_backward", "wtconv_scan_step")
 
 _lib = _ext = None
 
@@ -37,6 +37,8 @@ def _load() -> ctypes.CDLL:
         act = [vp, q, q]
         lib.wtconv_scan_workspace_size.restype = sz
         lib.wtconv_scan_workspace_size.argtypes = [i] * 6
+        lib.wtconv_scan_status.restype = i
+        lib.wtconv_scan_status.argtypes = []
         lib.wtconv_scan_forward.restype = i
         lib.wtconv_scan_forward.argtypes = [i] * 5 + act * 2 + [vp] * 3 + act + [vp, vp, vp, sz, vp]
         lib.wtconv_scan_backward.restype = i
@@ -49,6 +51,11 @@ def _load() -> ctypes.CDLL:
 
 def wtconv_scan_workspace_size(op: int, B: int, T: int, C: int, layout: int, dtype: int) -> int:
     return _load().wtconv_scan_workspace_size(op, B, T, C, layout, dtype)
+
+
+def wtconv_scan_status() -> int:
+    """Synchronise the device; wtconv.ERR_DEVICE_TIMEOUT if a scan's bounded wait gave up."""
+    return _load().wtconv_scan_status()
 
 
 def wtconv_scan_forward(x, gate, gate_bias, h0=None, lengths=None, layout="planes", keep_states=False, y=None,

@@ -430,3 +430,14 @@ def test_binding_refuses_on_the_gpu():
     assert e.value.status == W.ERR_WORKSPACE
     with pytest.raises(W.WTConvError):  # more sequences than rows
         S.wtconv_scan_step(d["x"][0], d["gate"][0], d["gate_bias"], torch.zeros(4, 8, device="cuda"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,C,T", [(2, 512, 1000), (3, 640, 4096), (16, 64, 777)])
+@pytest.mark.parametrize("dtype", DTYPES, ids=lambda t: str(t)[6:])
+def test_shared_sequences(dtype, B, C, T):
+    """Enough chains for clusters along time, too few to do without; no wait gives up."""
+    lengths = [T, T // 3] + [T - 70 * b for b in range(2, B)]
+    d = make(B, T, C, "tokens", dtype, seed=17, lengths=lengths)
+    check(run(d, "tokens"), reference(d, "tokens"), "tokens", dtype)
+    assert S.wtconv_scan_status() == W.OK
