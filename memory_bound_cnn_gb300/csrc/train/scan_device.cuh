@@ -62,6 +62,19 @@ __device__ __forceinline__ int scan_length(const int *lengths, int b, int T) {
     return n < 0 ? 0 : (n < T ? n : T);
 }
 
+// Asynchronous copies of 16 or 4 bytes to shared memory, of which the first `bytes` are read and the
+// rest come out as zeros.
+template <int CP> __device__ __forceinline__ void copy_async(void *to, const void *from, int bytes) {
+    const unsigned dst = (unsigned)__cvta_generic_to_shared(to);
+    if constexpr (CP == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING> __device__ __forceinline__ void wait_copies() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
 // A stretch of the recurrence as the map h -> a h + u of the state before it; `then` appends the
 // stretch that follows.
 struct Span {
@@ -70,82 +83,51 @@ struct Span {
     __device__ __forceinline__ float of(float h) const { return fmaf(a, h, u); }
 };
 
-// Inclusive scan of spans over groups of WIDTH lanes: forward (lane l ends with lanes 0..l), or
-// backward (lanes WIDTH-1 down to l).
-template <int WIDTH, bool BACKWARD> __device__ __forceinline__ Span warp_scan(Span s, int lane) {
+// s gets the span of the lane `d` before (after, if BACKWARD) in its group of lanes put before it, if
+// there is one.  The shuffle's own predicate guards the two products.  clamp: the shuffle's bounds.
+template <bool BACKWARD> __device__ __forceinline__ void scan_step(Span &s, int d, int clamp) {
+    if (BACKWARD)
+        asm volatile("{\n\t.reg .f32 a, u;\n\t.reg .pred p;\n\t"
+                     "shfl.sync.down.b32 a|p, %0, %2, %3, 0xffffffff;\n\t"
+                     "shfl.sync.down.b32 u, %1, %2, %3, 0xffffffff;\n\t"
+                     "@p fma.rn.f32 %1, %0, u, %1;\n\t@p mul.f32 %0, %0, a;\n\t}"
+                     : "+f"(s.a), "+f"(s.u) : "r"(d), "r"(clamp));
+    else
+        asm volatile("{\n\t.reg .f32 a, u;\n\t.reg .pred p;\n\t"
+                     "shfl.sync.up.b32 a|p, %0, %2, %3, 0xffffffff;\n\t"
+                     "shfl.sync.up.b32 u, %1, %2, %3, 0xffffffff;\n\t"
+                     "@p fma.rn.f32 %1, %0, u, %1;\n\t@p mul.f32 %0, %0, a;\n\t}"
+                     : "+f"(s.a), "+f"(s.u) : "r"(d), "r"(clamp));
+}
+template <bool BACKWARD> __device__ __forceinline__ int scan_clamp(int width) {
+    return (32 - width) << 8 | (BACKWARD ? 31 : 0);
+}
+// Inclusive scan of spans over groups of `width` lanes (a power of two): forward (lane l ends with
+// lanes 0..l), or backward (lanes width-1 down to l).
+template <bool BACKWARD> __device__ __forceinline__ Span warp_scan(Span s, int width) {
+    const int clamp = scan_clamp<BACKWARD>(width);
 #pragma unroll
-    for (int d = 1; d < WIDTH; d <<= 1) {
-        Span o;
-        o.a = BACKWARD ? __shfl_down_sync(0xffffffffu, s.a, d, WIDTH) : __shfl_up_sync(0xffffffffu, s.a, d, WIDTH);
-        o.u = BACKWARD ? __shfl_down_sync(0xffffffffu, s.u, d, WIDTH) : __shfl_up_sync(0xffffffffu, s.u, d, WIDTH);
-        const int l = lane & (WIDTH - 1);
-        if (BACKWARD ? l + d < WIDTH : l >= d) s = o.then(s);
-    }
+    for (int d = 1; d < 32; d <<= 1)
+        if (d < width) scan_step<BACKWARD>(s, d, clamp);
     return s;
 }
-// The scan's result of the lane before (after, if BACKWARD): the identity for the first.
-template <int WIDTH, bool BACKWARD> __device__ __forceinline__ Span lane_before(Span s, int lane) {
-    Span o;
-    o.a = BACKWARD ? __shfl_down_sync(0xffffffffu, s.a, 1, WIDTH) : __shfl_up_sync(0xffffffffu, s.a, 1, WIDTH);
-    o.u = BACKWARD ? __shfl_down_sync(0xffffffffu, s.u, 1, WIDTH) : __shfl_up_sync(0xffffffffu, s.u, 1, WIDTH);
-    const int l = lane & (WIDTH - 1);
-    if (BACKWARD ? l == WIDTH - 1 : l == 0) o = {1.f, 0.f};
+// The scan's result of the lane before (after, if BACKWARD) in the group: the identity for the first.
+template <bool BACKWARD> __device__ __forceinline__ Span lane_before(Span s, int width) {
+    Span o = {1.f, 0.f};
+    const int clamp = scan_clamp<BACKWARD>(width);
+    if (BACKWARD)
+        asm volatile("{\n\t.reg .f32 a, u;\n\t.reg .pred p;\n\t"
+                     "shfl.sync.down.b32 a|p, %2, 1, %4, 0xffffffff;\n\t"
+                     "shfl.sync.down.b32 u, %3, 1, %4, 0xffffffff;\n\t"
+                     "@p mov.f32 %0, a;\n\t@p mov.f32 %1, u;\n\t}"
+                     : "+f"(o.a), "+f"(o.u) : "f"(s.a), "f"(s.u), "r"(clamp));
+    else
+        asm volatile("{\n\t.reg .f32 a, u;\n\t.reg .pred p;\n\t"
+                     "shfl.sync.up.b32 a|p, %2, 1, %4, 0xffffffff;\n\t"
+                     "shfl.sync.up.b32 u, %3, 1, %4, 0xffffffff;\n\t"
+                     "@p mov.f32 %0, a;\n\t@p mov.f32 %1, u;\n\t}"
+                     : "+f"(o.a), "+f"(o.u) : "f"(s.a), "f"(s.u), "r"(clamp));
     return o;
 }
-
-// Eight consecutive elements as raw words, and as fp32.
-template <typename T> struct Eight {
-    uint32_t w[2 * sizeof(T)];
-    __device__ __forceinline__ float get(int j) const {
-        if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
-        else {
-            const uint16_t h = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-            return to_f32(*reinterpret_cast<const T *>(&h));
-        }
-    }
-    __device__ __forceinline__ void set(int j, float a, float b) {  // elements j (even) and j + 1
-        if constexpr (sizeof(T) == 4) {
-            w[j] = __float_as_uint(a), w[j + 1] = __float_as_uint(b);
-        } else {
-            const T lo = from_f32<T>(a), hi = from_f32<T>(b);
-            w[j >> 1] = (uint32_t)*reinterpret_cast<const uint16_t *>(&lo) |
-                        (uint32_t)*reinterpret_cast<const uint16_t *>(&hi) << 16;
-        }
-    }
-    // elements 0 .. valid-1 from p (all of them: vectors if VEC); the rest zeros
-    template <bool VEC> __device__ __forceinline__ void load(const T *p, int valid) {
-        if (VEC && valid >= 8) {
-#pragma unroll
-            for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
-                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p) + k);
-                w[4 * k] = q.x, w[4 * k + 1] = q.y, w[4 * k + 2] = q.z, w[4 * k + 3] = q.w;
-            }
-            return;
-        }
-#pragma unroll
-        for (int k = 0; k < 2 * (int)sizeof(T); ++k) w[k] = 0;
-        if (valid <= 0) return;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (j >= valid) continue;
-            if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(p[j]);
-            else w[j >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t *>(p + j) << (16 * (j & 1));
-        }
-    }
-    template <bool VEC> __device__ __forceinline__ void store(T *p, int valid) const {
-        if (VEC && valid >= 8) {
-#pragma unroll
-            for (int k = 0; k < (int)sizeof(T) / 2; ++k)
-                reinterpret_cast<uint4 *>(p)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-            return;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (j >= valid) continue;
-            if constexpr (sizeof(T) == 4) p[j] = __uint_as_float(w[j]);
-            else *reinterpret_cast<uint16_t *>(p + j) = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-        }
-    }
-};
 
 }  // namespace wtconv

@@ -1,15 +1,16 @@
-// Gated scan of planes [B][C][T] (time contiguous): one CTA per row, or per segment of a long one.
+// Gated scan of planes [B][C][T] (time contiguous).
 //
-// A warp takes 256 consecutive positions at a time, eight per lane.  A stretch of the recurrence is
-// the map h -> a h + u, and such maps compose (Span), so each lane reduces its eight positions, the
-// warp scans the lanes' maps by shuffles, the CTA's warps exchange theirs through shared memory (one
-// barrier per round of 256 positions a warp), and every lane then runs its eight positions again from
-// the state that reaches it: x, gate and (backward) dy are read once and everything stays in
-// registers.  The next round's loads are issued before the barrier.  The state that a round leaves is
-// carried to the next in a register of every thread.
+// A lane owns eight consecutive positions of a row, a warp 256 (a span).  A stretch of the recurrence is
+// the map h -> a h + u, and such maps compose (Span).  A lane takes its two halves as the two lanes of
+// packed fp32 arithmetic (one instruction for both), joins their maps, and the warp scans the lanes'
+// maps by shuffles; every lane then runs its positions again from the state that reaches it.  x, gate and (backward) dy are read once and everything stays in registers.  The backward
+// finds h again by the same scan over the few lanes between two kept states.
 //
-// Few, long rows do not fill the GPU that way: they are cut into segments, a first kernel reduces
-// each segment to its map, and the scan of a segment starts from the maps before it (after it,
+// Rows of one span or less: several rows share a warp (scan_short_*).  Longer rows: the warps of a CTA
+// take neighbouring spans of one row in rounds, exchange their maps through shared memory (one barrier
+// a round) and carry the state in a register (scan_planes_*); the next round's loads are issued before
+// the barrier.  Few, long rows do not fill the GPU that way: they are cut into segments, a first kernel
+// reduces each segment to its map, and the scan of a segment starts from the maps before it (after it,
 // backward).  That reads two of the inputs twice, the second time mostly from L2.
 #include "scan_device.cuh"
 
@@ -17,13 +18,246 @@ namespace wtconv {
 
 namespace {
 
-constexpr int kWarpSpan = 256;  // positions of a warp's round
 constexpr int kMaxWarps = 8;
-constexpr int kKeepLanes = WTCONV_SCAN_KEEP / 8;  // lanes between two kept states
+constexpr int kLane = 8, kHalf = kLane / 2;             // positions of a lane and of its halves,
+constexpr int kWarpSpan = 32 * kLane;                    // of a warp's round
+constexpr int kKeepLanes = WTCONV_SCAN_KEEP / kLane;     // lanes between two kept states
 
 enum Mode { kReduce, kApply };
+// A lane's positions as raw words; pair j holds positions j and kHalf + j.
+template <typename T> struct Strip {
+    static constexpr int words = kLane * (int)sizeof(T) / 4;
+    uint32_t w[words];
+    __device__ __forceinline__ Pair get(int j) const {
+        if constexpr (sizeof(T) == 4) return {__uint_as_float(w[j]), __uint_as_float(w[kHalf + j])};
+        else {
+            const Pair a = widen<T>(w[j >> 1]), b = widen<T>(w[(kHalf + j) >> 1]);
+            return j & 1 ? Pair(a.hi(), b.hi()) : Pair(a.lo(), b.lo());
+        }
+    }
+    __device__ __forceinline__ void set(const Pair (&v)[kHalf]) {
+#pragma unroll
+        for (int j = 0; j < kHalf; j += 2) {
+            if constexpr (sizeof(T) == 4) {
+                w[j] = __float_as_uint(v[j].lo()), w[j + 1] = __float_as_uint(v[j + 1].lo());
+                w[kHalf + j] = __float_as_uint(v[j].hi()), w[kHalf + j + 1] = __float_as_uint(v[j + 1].hi());
+            } else {
+                w[j >> 1] = narrow<T>(Pair(v[j].lo(), v[j + 1].lo()));
+                w[(kHalf + j) >> 1] = narrow<T>(Pair(v[j].hi(), v[j + 1].hi()));
+            }
+        }
+    }
+    // Straight from and to memory (short rows): positions 0 .. valid-1, as vectors where CP is 16.
+    template <int CP> __device__ __forceinline__ void load(const T *p, int valid) {
+        if (CP == 16 && valid >= kLane) {
+#pragma unroll
+            for (int k = 0; k < words; k += 4) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + k / 4);
+                w[k] = v.x, w[k + 1] = v.y, w[k + 2] = v.z, w[k + 3] = v.w;
+            }
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < words; ++k) w[k] = 0;
+#pragma unroll
+        for (int j = 0; j < kLane; ++j) {
+            if (j >= valid) continue;
+            if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(p[j]);
+            else w[j >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t *>(p + j) << (16 * (j & 1));
+        }
+    }
+    template <int CP> __device__ __forceinline__ void store(T *p, int valid) const {
+        if (CP == 16 && valid >= kLane) {
+#pragma unroll
+            for (int k = 0; k < words; k += 4)
+                reinterpret_cast<uint4 *>(p)[k / 4] = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < kLane; ++j) {
+            if (j >= valid) continue;
+            if constexpr (sizeof(T) == 4) p[j] = __uint_as_float(w[j]);
+            else *reinterpret_cast<uint16_t *>(p + j) = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+        }
+    }
+    // zeros from position `valid` on
+    __device__ __forceinline__ void cut(int valid) {
+#pragma unroll
+        for (int j = 0; j < kLane; ++j) {
+            if (j < valid) continue;
+            if constexpr (sizeof(T) == 4) w[j] = 0;
+            else w[j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
+        }
+    }
+};
 
-// Map of the segments [first, last) of a row in time order, by all lanes of a warp alike.
+// A warp's span of one tensor in shared memory, which the warp itself brings in and reads: a queue that
+// takes no registers and no barrier of the CTA.  It moves in order, CP bytes a lane at a time (16 or 4
+// asynchronously, 2 through registers), so that a warp's copies lie side by side; a lane then reads its
+// own positions.
+template <typename T> struct Cell {
+    static constexpr int bytes = kWarpSpan * (int)sizeof(T);
+    uint4 q[bytes / 16];
+    __device__ __forceinline__ char *at(int offset) { return reinterpret_cast<char *>(q) + offset; }
+    // The span from p (the warp's first position) on.  Positions from `valid` on are not read and come
+    // as zeros; anchor is an address that stands in where nothing is read.
+    template <int CP> __device__ __forceinline__ void fetch(const T *p, int valid, int lane, const void *anchor) {
+        const char *from = reinterpret_cast<const char *>(p) + lane * CP;
+        if constexpr (CP == 2) {
+#pragma unroll
+            for (int k = 0; k < bytes / 64; ++k) {
+                const uint16_t v = k * 32 + lane < valid ? *reinterpret_cast<const uint16_t *>(from + k * 64) : (uint16_t)0;
+                *reinterpret_cast<uint16_t *>(at(k * 64 + lane * 2)) = v;
+            }
+        } else if (valid >= kWarpSpan) {
+#pragma unroll
+            for (int k = 0; k < bytes / (32 * CP); ++k) copy_async<CP>(at((k * 32 + lane) * CP), from + k * 32 * CP, CP);
+        } else {
+#pragma unroll
+            for (int k = 0; k < bytes / (32 * CP); ++k) {
+                const int left = min(max(valid * (int)sizeof(T) - (k * 32 + lane) * CP, 0), CP);
+                copy_async<CP>(at((k * 32 + lane) * CP), left > 0 ? from + k * 32 * CP : anchor, left);
+            }
+        }
+    }
+    __device__ __forceinline__ Strip<T> read(int lane) const {
+        Strip<T> s;
+#pragma unroll
+        for (int k = 0; k < Strip<T>::words / 4; ++k) {
+            const uint4 v = q[lane * (Strip<T>::words / 4) + k];
+            s.w[4 * k] = v.x, s.w[4 * k + 1] = v.y, s.w[4 * k + 2] = v.z, s.w[4 * k + 3] = v.w;
+        }
+        return s;
+    }
+    // The lanes' positions to p (the warp's first position), those before `valid`: straight from the
+    // registers, or through this cell where single elements or words would lie far apart.
+    template <int CP> __device__ __forceinline__ void store(T *p, const Strip<T> &s, int valid, int lane) {
+        if (CP == 16 && valid >= kWarpSpan) {
+#pragma unroll
+            for (int k = 0; k < Strip<T>::words; k += 4)
+                reinterpret_cast<uint4 *>(p + lane * kLane)[k / 4] = make_uint4(s.w[k], s.w[k + 1], s.w[k + 2], s.w[k + 3]);
+            return;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < Strip<T>::words / 4; ++k)
+            q[lane * (Strip<T>::words / 4) + k] = make_uint4(s.w[4 * k], s.w[4 * k + 1], s.w[4 * k + 2], s.w[4 * k + 3]);
+        __syncwarp();
+        char *to = reinterpret_cast<char *>(p);
+        if (CP >= 4 && valid >= kWarpSpan) {
+#pragma unroll
+            for (int k = 0; k < bytes / 128; ++k)
+                *reinterpret_cast<uint32_t *>(to + (k * 32 + lane) * 4) = *reinterpret_cast<const uint32_t *>(at((k * 32 + lane) * 4));
+        } else {
+            constexpr int e = (int)sizeof(T);
+#pragma unroll
+            for (int k = 0; k < kLane; ++k)
+                if (k * 32 + lane < valid) *reinterpret_cast<T *>(to + (k * 32 + lane) * e) = *reinterpret_cast<const T *>(at((k * 32 + lane) * e));
+        }
+        __syncwarp();
+    }
+};
+constexpr int kStages = 3;
+
+// A lane's two halves as maps (Span of positions in time order: lo then hi).
+struct Halves {
+    Pair a, u;
+    __device__ __forceinline__ Span lo() const { return {a.lo(), u.lo()}; }
+    __device__ __forceinline__ Span hi() const { return {a.hi(), u.hi()}; }
+};
+
+// Gates of a lane's positions; those at or past `live` hold the state (a = 1, b = 0).
+template <typename T>
+__device__ __forceinline__ void lane_gates(const Strip<T> &g, Pair bias, int live, Pair (&av)[kHalf], Pair (&bv)[kHalf]) {
+#pragma unroll
+    for (int j = 0; j < kHalf; ++j) {
+        const Gates q = gates_of(g.get(j), bias);
+        av[j] = q.a, bv[j] = q.b;
+    }
+    if (live < kLane) {
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) {
+            if (j >= live) av[j] = Pair(1.f, av[j].hi()), bv[j] = Pair(0.f, bv[j].hi());
+            if (kHalf + j >= live) av[j] = Pair(av[j].lo(), 1.f), bv[j] = Pair(bv[j].lo(), 0.f);
+        }
+    }
+}
+
+// The forward of a lane: its map, then its outputs from the state before it.
+template <typename T> struct LaneForward {
+    Pair av[kHalf], uv[kHalf];
+    Halves halves;
+    __device__ __forceinline__ Span reduce(const Strip<T> &x, const Strip<T> &g, Pair bias, int live) {
+        lane_gates(g, bias, live, av, uv);
+        halves = {Pair(1.f), Pair(0.f)};
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) {
+            uv[j] = mul(uv[j], x.get(j));  // (x is 0 beyond the length)
+            halves.u = fma(av[j], halves.u, uv[j]);
+            halves.a = mul(halves.a, av[j]);
+        }
+        return halves.lo().then(halves.hi());
+    }
+    __device__ __forceinline__ Strip<T> outputs(float before, int live) {
+        Pair h(before, halves.lo().of(before)), out[kHalf];
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) out[j] = h = fma(av[j], h, uv[j]);
+        Strip<T> y;
+        y.set(out);
+        if (live < kLane) y.cut(live);  // past the length the state stands still, and y is 0
+        return y;
+    }
+};
+
+// The backward of a lane: the maps of dh (backward) and of h (forward), then its gradients.  x and dy
+// are taken from their cells again rather than kept.
+template <typename T> struct LaneBackward {
+    Pair av[kHalf], bv[kHalf];
+    Halves back, fwd;
+    __device__ __forceinline__ Span reduce(const Strip<T> &g, const Strip<T> &dy, Pair bias, int live) {
+        lane_gates(g, bias, live, av, bv);
+        back = {Pair(1.f), Pair(0.f)};
+#pragma unroll
+        for (int j = kHalf - 1; j >= 0; --j) {
+            back.u = mul(av[j], add(dy.get(j), back.u));
+            back.a = mul(back.a, av[j]);
+        }
+        return back.hi().then(back.lo());
+    }
+    __device__ __forceinline__ Span reduce_h(const Strip<T> &x) {
+        fwd = {back.a, Pair(0.f)};
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) fwd.u = fma(av[j], fwd.u, mul(bv[j], x.get(j)));
+        return fwd.lo().then(fwd.hi());
+    }
+    // h: the state before the lane; flow: a dh of the position after it
+    __device__ __forceinline__ void gradients(float h_before, float flow_after, const Strip<T> &x, const Strip<T> &dy, int live,
+                                              Strip<T> &dx, Strip<T> &dg, Pair &sum) {
+        Pair h(h_before, fwd.lo().of(h_before)), diff[kHalf];
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) {
+            const Pair xv = x.get(j);
+            diff[j] = sub(h, xv);  // h_{t-1} - x_t
+            h = fma(av[j], h, mul(bv[j], xv));
+        }
+        Pair flow(back.hi().of(flow_after), flow_after);
+#pragma unroll
+        for (int j = kHalf - 1; j >= 0; --j) {
+            const Pair dh = add(dy.get(j), flow);
+            diff[j] = mul(mul(dh, diff[j]), mul(av[j], bv[j]));
+            sum = add(sum, diff[j]);
+            bv[j] = mul(bv[j], dh);
+            flow = mul(av[j], dh);
+        }
+        dx.set(bv);
+        dg.set(diff);
+        if (live < kLane) dx.cut(live), dg.cut(live);
+    }
+};
+
+// ------------------------------------------------------------------------- rows of several spans
+
+// Map of the segments [first, last) of a row in the scan's order, by all lanes of a warp alike.
 __device__ __forceinline__ Span fold_segments(const float2 *maps, int first, int last, bool backward, int lane) {
     const int count = last - first, per = (count + 31) / 32;
     Span s = {1.f, 0.f};
@@ -34,16 +268,17 @@ __device__ __forceinline__ Span fold_segments(const float2 *maps, int first, int
             s = s.then({m.x, m.y});
         }
     }
-    s = warp_scan<32, false>(s, lane);
+    s = warp_scan<false>(s, 32);
     s.a = __shfl_sync(0xffffffffu, s.a, 31);
     s.u = __shfl_sync(0xffffffffu, s.u, 31);
     return s;
 }
 
-// One round's exchange between the CTA's warps.  mine: the warp's whole map (any lane: lane `from`
-// holds it).  Returns the state before this warp's stretch and moves carry past the round.
-__device__ __forceinline__ float exchange(Span mine, int from, float2 *slots, int warp, int warps, int lane, bool backward,
-                                          float &carry) {
+// One round's exchange between the CTA's warps.  mine: the warp's whole map in lane `from`.  Returns
+// the state before this warp's span and moves carry past the round.
+template <bool BACKWARD>
+__device__ __forceinline__ float exchange(Span mine, float2 *slots, int warp, int warps, int lane, float &carry) {
+    constexpr int from = BACKWARD ? 0 : 31;
     if (warps == 1) {
         const float before = carry;
         const Span whole = {__shfl_sync(0xffffffffu, mine.a, from), __shfl_sync(0xffffffffu, mine.u, from)};
@@ -54,7 +289,7 @@ __device__ __forceinline__ float exchange(Span mine, int from, float2 *slots, in
     __syncthreads();
     float before = 0.f;
     for (int i = 0; i < warps; ++i) {
-        const int w = backward ? warps - 1 - i : i;
+        const int w = BACKWARD ? warps - 1 - i : i;
         if (w == warp) before = carry;
         const float2 m = slots[w];
         carry = fmaf(m.x, carry, m.y);
@@ -63,9 +298,9 @@ __device__ __forceinline__ float exchange(Span mine, int from, float2 *slots, in
 }
 
 struct Segment {
-    int b, c, seg, n;              // n: length of the sequence
-    long long row;                 // b * C + c
-    int round0, round1;            // rounds of this segment
+    int b, c, seg, n;    // n: length of the sequence
+    long long row;       // b * C + c
+    int round0, round1;  // rounds of this segment
 };
 __device__ __forceinline__ Segment segment_of(const ScanArgs &a, int segments, int rounds_per, int round_span) {
     Segment s;
@@ -79,19 +314,42 @@ __device__ __forceinline__ Segment segment_of(const ScanArgs &a, int segments, i
     s.round1 = min(s.round0 + rounds_per, rounds);
     return s;
 }
+template <typename T> __device__ __forceinline__ T *row_of(const ScanTensor &t, int b, int c) {
+    return static_cast<T *>(t.p) + b * t.batch + c * t.row;
+}
 
-// ---------------------------------------------------------------------------------------- forward
+// Shared memory of a kernel: kStages cells of each of TENSORS per warp.
+template <typename T, int TENSORS> using Ring = Cell<T>[kStages][TENSORS];
+template <typename T, int TENSORS> __device__ __forceinline__ Ring<T, TENSORS> &ring_of(unsigned char *raw, int warp) {
+    return reinterpret_cast<Ring<T, TENSORS> *>(raw)[warp];
+}
+__device__ __forceinline__ int next_stage(int s) { return s + 1 == kStages ? 0 : s + 1; }
 
-template <typename T, bool VEC, Mode MODE>
+template <typename T, int CP, Mode MODE>
 __global__ void __launch_bounds__(kMaxWarps * 32) scan_planes_forward_kernel(const ScanArgs a, int segments, int rounds_per,
                                                                              float2 *maps) {
+    extern __shared__ __align__(16) unsigned char raw[];
     __shared__ float2 slots[2][kMaxWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int round_span = warps * kWarpSpan;
     const Segment s = segment_of(a, segments, rounds_per, round_span);
-    const T *x = static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c * a.x.row;
-    const T *g = static_cast<const T *>(a.gate.p) + s.b * a.gate.batch + s.c * a.gate.row;
-    T *y = static_cast<T *>(a.y.p) + s.b * a.y.batch + s.c * a.y.row;
+    auto &ring = ring_of<T, 2>(raw, warp);
+    int t0 = s.round0 * round_span + warp * kWarpSpan;  // the warp's first position
+    const T *x = row_of<T>(a.x, s.b, s.c) + t0, *g = row_of<T>(a.gate, s.b, s.c) + t0;
+    T *y = row_of<T>(a.y, s.b, s.c) + t0;
+    int ahead = s.n - t0;  // valid positions of the next cells
+    const auto fetch = [&](int stage) {
+        ring[stage][0].template fetch<CP>(x, ahead, lane, a.x.p);
+        ring[stage][1].template fetch<CP>(g, ahead, lane, a.gate.p);
+        commit_copies();
+        x += round_span, g += round_span, ahead -= round_span;
+    };
+    int left = s.round1 - s.round0;  // rounds that are not fetched yet
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) {
+        if (left > 0) fetch(k), --left;
+        else commit_copies();
+    }
     const Pair bias(-kLog2E * a.gate_bias[s.c]);
 
     float carry = 0.f;
@@ -100,57 +358,32 @@ __global__ void __launch_bounds__(kMaxWarps * 32) scan_planes_forward_kernel(con
         carry = a.h0 != nullptr ? a.h0[s.row] : 0.f;
         if (s.seg > 0) carry = fold_segments(maps + s.row * segments, 0, s.seg, false, lane).of(carry);
     }
-    int t = s.round0 * round_span + warp * kWarpSpan + lane * 8;
-    Eight<T> nx, ng;
-    nx.template load<VEC>(x + t, s.n - t);
-    ng.template load<VEC>(g + t, s.n - t);
-    for (int round = s.round0; round < s.round1; ++round, t += round_span) {
-        const Eight<T> ex = nx, eg = ng;
-        float av[8], uv[8];
-        Span span = {1.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            const Gates q = gates_of(Pair(eg.get(j), eg.get(j + 1)), bias);
-            const Pair u = mul(q.b, Pair(ex.get(j), ex.get(j + 1)));
-            av[j] = q.a.lo(), av[j + 1] = q.a.hi();
-            uv[j] = u.lo(), uv[j + 1] = u.hi();
-        }
-        if (t + 8 > s.n) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (t + j >= s.n) av[j] = 1.f, uv[j] = 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) span = span.then({av[j], uv[j]});
-        if (round + 1 < s.round1) {
-            nx.template load<VEC>(x + t + round_span, s.n - t - round_span);
-            ng.template load<VEC>(g + t + round_span, s.n - t - round_span);
-        }
-        span = warp_scan<32, false>(span, lane);
-        const Span before = lane_before<32, false>(span, lane);
+    int stage = 0, free_stage = kStages - 1;
+    for (int round = s.round0; round < s.round1; ++round, t0 += round_span) {
+        wait_copies<kStages - 2>();
+        __syncwarp();
+        LaneForward<T> f;
+        const int t = t0 + lane * kLane, live = s.n - t;
+        Span span = f.reduce(ring[stage][0].read(lane), ring[stage][1].read(lane), bias, live);
+        if (left > 0) fetch(free_stage), --left;
+        else commit_copies();
+        Cell<T> &out = ring[stage][0];  // read already
+        stage = next_stage(stage), free_stage = next_stage(free_stage);
+        span = warp_scan<false>(span, 32);
+        float2 *slot = slots[round & 1];
         if (MODE == kReduce) {
             // every warp folds the whole round, so that all end with the segment's map
-            float2 *slot = slots[round & 1];
             if (lane == 31) slot[warp] = make_float2(span.a, span.u);
             __syncthreads();
             for (int w = 0; w < warps; ++w) whole = whole.then({slot[w].x, slot[w].y});
             continue;
         }
-        float h = before.of(exchange(span, 31, slots[round & 1], warp, warps, lane, false, carry));
-        if (a.states_out != nullptr && (lane & (kKeepLanes - 1)) == 0 && t < a.T) a.states_out[s.row * a.keep + t / WTCONV_SCAN_KEEP] = h;
-        Eight<T> out;
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            const float h0 = fmaf(av[j], h, uv[j]);
-            h = fmaf(av[j + 1], h0, uv[j + 1]);
-            out.set(j, h0, h);
-        }
-        if (t + 8 > s.n) {  // past the length the state stands still, and y is 0
-#pragma unroll
-            for (int j = 0; j < 8; j += 2)
-                out.set(j, t + j < s.n ? out.get(j) : 0.f, t + j + 1 < s.n ? out.get(j + 1) : 0.f);
-        }
-        out.template store<VEC>(y + t, a.T - t);
+        const Span before = lane_before<false>(span, 32);
+        const float h = before.of(exchange<false>(span, slot, warp, warps, lane, carry));
+        if (a.states_out != nullptr && (lane & (kKeepLanes - 1)) == 0 && t < a.T)
+            a.states_out[s.row * a.keep + t / WTCONV_SCAN_KEEP] = h;
+        out.template store<CP>(y, f.outputs(h, live), a.T - t0, lane);
+        y += round_span;
     }
     if (MODE == kReduce) {
         if (threadIdx.x == 0) maps[blockIdx.x] = make_float2(whole.a, whole.u);
@@ -159,120 +392,158 @@ __global__ void __launch_bounds__(kMaxWarps * 32) scan_planes_forward_kernel(con
     }
 }
 
-// --------------------------------------------------------------------------------------- backward
-
-template <typename T, bool VEC, Mode MODE>
-__global__ void __launch_bounds__(kMaxWarps * 32) scan_planes_backward_kernel(const ScanArgs a, int segments, int rounds_per,
-                                                                              float2 *maps, float *bias_part) {
+template <typename T, int CP, Mode MODE>
+__global__ void __launch_bounds__(kMaxWarps * 32, 4)
+    scan_planes_backward_kernel(const ScanArgs a, int segments, int rounds_per, float2 *maps, float *bias_part) {
+    extern __shared__ __align__(16) unsigned char raw[];
     __shared__ float2 slots[2][kMaxWarps];
     __shared__ float sums[kMaxWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int round_span = warps * kWarpSpan;
     const Segment s = segment_of(a, segments, rounds_per, round_span);
-    const T *x = static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c * a.x.row;
-    const T *g = static_cast<const T *>(a.gate.p) + s.b * a.gate.batch + s.c * a.gate.row;
-    const T *dy = static_cast<const T *>(a.dy.p) + s.b * a.dy.batch + s.c * a.dy.row;
-    T *dx = static_cast<T *>(a.dx.p) + s.b * a.dx.batch + s.c * a.dx.row;
-    T *dg = static_cast<T *>(a.d_gate.p) + s.b * a.d_gate.batch + s.c * a.d_gate.row;
+    auto &ring = ring_of<T, 3>(raw, warp);
+    int t0 = (s.round1 - 1) * round_span + warp * kWarpSpan;  // the warp's first position
+    const T *x = row_of<T>(a.x, s.b, s.c) + t0, *g = row_of<T>(a.gate, s.b, s.c) + t0, *dy = row_of<T>(a.dy, s.b, s.c) + t0;
+    T *dx = row_of<T>(a.dx, s.b, s.c) + t0, *dg = row_of<T>(a.d_gate, s.b, s.c) + t0;
+    int ahead = s.n - t0;  // valid positions of the next cells
+    const auto fetch = [&](int stage) {
+        ring[stage][0].template fetch<CP>(g, ahead, lane, a.gate.p);
+        ring[stage][1].template fetch<CP>(dy, ahead, lane, a.dy.p);
+        if (MODE == kApply) ring[stage][2].template fetch<CP>(x, ahead, lane, a.x.p);
+        commit_copies();
+        x -= round_span, g -= round_span, dy -= round_span, ahead += round_span;
+    };
+    int left = s.round1 - s.round0;  // rounds that are not fetched yet
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) {
+        if (left > 0) fetch(k), --left;
+        else commit_copies();
+    }
+    const auto kept_at = [&](int at) {
+        return MODE == kApply && at < a.T ? a.states_in[s.row * a.keep + at / WTCONV_SCAN_KEEP] : 0.f;
+    };
+    float next_kept = kept_at(t0 + lane * kLane);
     const Pair bias(-kLog2E * a.gate_bias[s.c]);
 
-    float carry = 0.f, sum = 0.f;  // carry: a_{t+1} dh_{t+1} of the position after this round
+    float carry = 0.f;  // a dh of the position after this round
+    Pair sum(0.f);
     Span whole = {1.f, 0.f};
     if (MODE == kApply) {
         carry = a.dh_last != nullptr ? a.dh_last[s.row] : 0.f;
         if (s.seg < segments - 1)
             carry = fold_segments(maps + s.row * segments, s.seg + 1, segments, true, lane).of(carry);
     }
-    int t = (s.round1 - 1) * round_span + warp * kWarpSpan + lane * 8;
-    Eight<T> nx, ng, ndy;
-    float nh = 0.f;
-    const auto fetch = [&](int at) {
-        ng.template load<VEC>(g + at, s.n - at);
-        ndy.template load<VEC>(dy + at, s.n - at);
-        if (MODE == kApply) {
-            nx.template load<VEC>(x + at, s.n - at);
-            nh = at < a.T ? a.states_in[s.row * a.keep + at / WTCONV_SCAN_KEEP] : 0.f;
-        }
-    };
-    fetch(t);
-    for (int round = s.round1 - 1; round >= s.round0; --round, t -= round_span) {
-        const Eight<T> ex = nx, eg = ng, edy = ndy;
-        const float kept = nh;
-        float av[8], bv[8];
-        Span span = {1.f, 0.f};
-        float flow = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            const Gates q = gates_of(Pair(eg.get(j), eg.get(j + 1)), bias);
-            av[j] = q.a.lo(), av[j + 1] = q.a.hi();
-            bv[j] = q.b.lo(), bv[j + 1] = q.b.hi();
-        }
-        if (t + 8 > s.n) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (t + j >= s.n) av[j] = 1.f, bv[j] = 0.f;
-        }
-#pragma unroll
-        for (int j = 7; j >= 0; --j) {
-            flow = av[j] * (edy.get(j) + flow);
-            span.a *= av[j];
-        }
-        span.u = flow;
-        if (round > s.round0) fetch(t - round_span);
-        float diff[8];  // h_{t-1} - x_t
-        if (MODE == kApply) {
-            // h again, by groups of lanes: a kept state stands before each
-            Span fwd = {span.a, 0.f};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) fwd.u = fmaf(av[j], fwd.u, bv[j] * ex.get(j));
-            float h = lane_before<kKeepLanes, false>(warp_scan<kKeepLanes, false>(fwd, lane), lane).of(kept);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float xv = ex.get(j);
-                diff[j] = h - xv;
-                h = fmaf(av[j], h, bv[j] * xv);
-            }
-        }
-        span = warp_scan<32, true>(span, lane);
-        const Span after = lane_before<32, true>(span, lane);
+    int stage = 0, free_stage = kStages - 1;
+    for (int round = s.round1 - 1; round >= s.round0; --round, t0 -= round_span) {
+        wait_copies<kStages - 2>();
+        __syncwarp();
+        LaneBackward<T> f;
+        const float kept = next_kept;
+        const int t = t0 + lane * kLane, live = s.n - t;
+        Span span = f.reduce(ring[stage][0].read(lane), ring[stage][1].read(lane), bias, live);
+        if (left > 0) fetch(free_stage), --left;
+        else commit_copies();
+        if (round > s.round0) next_kept = kept_at(t - round_span);
+        span = warp_scan<true>(span, 32);
+        float2 *slot = slots[round & 1];
         if (MODE == kReduce) {
-            float2 *slot = slots[round & 1];
+            stage = next_stage(stage), free_stage = next_stage(free_stage);
             if (lane == 0) slot[warp] = make_float2(span.a, span.u);
             __syncthreads();
             for (int w = warps - 1; w >= 0; --w) whole = whole.then({slot[w].x, slot[w].y});
             continue;
         }
-        flow = after.of(exchange(span, 0, slots[round & 1], warp, warps, lane, true, carry));
-        Eight<T> odx, odg;
-#pragma unroll
-        for (int j = 7; j > 0; j -= 2) {
-            float dxv[2], dgv[2];
-#pragma unroll
-            for (int k = 1; k >= 0; --k) {
-                const int i = j - 1 + k;
-                const float dh = edy.get(i) + flow;
-                dxv[k] = bv[i] * dh;
-                dgv[k] = dh * diff[i] * (av[i] * bv[i]);
-                sum += dgv[k];
-                flow = av[i] * dh;
-            }
-            odx.set(j - 1, dxv[0], dxv[1]);
-            odg.set(j - 1, dgv[0], dgv[1]);
-        }
-        odx.template store<VEC>(dx + t, a.T - t);
-        odg.template store<VEC>(dg + t, a.T - t);
+        const Span fwd = warp_scan<false>(f.reduce_h(ring[stage][2].read(lane)), kKeepLanes);
+        const float h = lane_before<false>(fwd, kKeepLanes).of(kept);
+        const Span after = lane_before<true>(span, 32);
+        const float flow = after.of(exchange<true>(span, slot, warp, warps, lane, carry));
+        Strip<T> odx, odg;
+        f.gradients(h, flow, ring[stage][2].read(lane), ring[stage][1].read(lane), live, odx, odg, sum);
+        ring[stage][0].template store<CP>(dx, odx, a.T - t0, lane);
+        ring[stage][0].template store<CP>(dg, odg, a.T - t0, lane);
+        stage = next_stage(stage), free_stage = next_stage(free_stage);
+        dx -= round_span, dg -= round_span;
     }
     if (MODE == kReduce) {
         if (threadIdx.x == 0) maps[blockIdx.x] = make_float2(whole.a, whole.u);
         return;
     }
-    sum = warp_sum(sum);
-    if (lane == 0) sums[warp] = sum;
+    float total = warp_sum(sum.lo() + sum.hi());
+    if (lane == 0) sums[warp] = total;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 1; w < warps; ++w) sum += sums[w];
-        bias_part[blockIdx.x] = sum;
+        for (int w = 1; w < warps; ++w) total += sums[w];
+        bias_part[blockIdx.x] = total;
         if (a.d_h0 != nullptr && s.seg == 0) a.d_h0[s.row] = carry;
+    }
+}
+
+// --------------------------------------------------------------------- rows of one span or less
+
+constexpr int kShortThreads = 128;
+
+struct ShortRow {
+    int b, c, n, t, group;  // t: the lane's first position; group: its place among the row's lanes
+    long long row;          // past the last row: no position is live or stored
+    bool any;
+};
+template <typename T> __device__ __forceinline__ ShortRow short_row(const ScanArgs &a, int lanes) {
+    ShortRow s;
+    const unsigned per_cta = kShortThreads / lanes;
+    s.group = threadIdx.x & (lanes - 1);
+    s.row = (long long)blockIdx.x * per_cta + threadIdx.x / lanes;
+    s.any = s.row < (long long)a.B * a.C;
+    if (!s.any) s.row = 0;
+    s.b = (int)(s.row / a.C);
+    s.c = (int)(s.row - (long long)s.b * a.C);
+    s.n = s.any ? scan_length(a.lengths, s.b, a.T) : 0;
+    s.t = s.group * kLane;
+    return s;
+}
+
+template <typename T, int CP> __global__ void __launch_bounds__(kShortThreads) scan_short_forward_kernel(const ScanArgs a, int lanes) {
+    const ShortRow s = short_row<T>(a, lanes);
+    Strip<T> x, g;
+    x.template load<CP>(row_of<T>(a.x, s.b, s.c) + s.t, s.n - s.t);
+    g.template load<CP>(row_of<T>(a.gate, s.b, s.c) + s.t, s.n - s.t);
+    const Pair bias(-kLog2E * a.gate_bias[s.c]);
+    const float h0 = a.h0 != nullptr ? a.h0[s.row] : 0.f;
+    LaneForward<T> f;
+    const Span span = warp_scan<false>(f.reduce(x, g, bias, s.n - s.t), lanes);
+    const float h = lane_before<false>(span, lanes).of(h0);
+    if (!s.any) return;
+    if (a.states_out != nullptr && s.t % WTCONV_SCAN_KEEP == 0 && s.t < a.T)
+        a.states_out[s.row * a.keep + s.t / WTCONV_SCAN_KEEP] = h;
+    f.outputs(h, s.n - s.t).template store<CP>(row_of<T>(a.y, s.b, s.c) + s.t, a.T - s.t);
+    if (a.h_last != nullptr && s.group == lanes - 1) a.h_last[s.row] = span.of(h0);
+}
+
+template <typename T, int CP>
+__global__ void __launch_bounds__(kShortThreads) scan_short_backward_kernel(const ScanArgs a, int lanes, float *bias_part) {
+    const ShortRow s = short_row<T>(a, lanes);
+    Strip<T> x, g, dy;
+    x.template load<CP>(row_of<T>(a.x, s.b, s.c) + s.t, s.n - s.t);
+    g.template load<CP>(row_of<T>(a.gate, s.b, s.c) + s.t, s.n - s.t);
+    dy.template load<CP>(row_of<T>(a.dy, s.b, s.c) + s.t, s.n - s.t);
+    const Pair bias(-kLog2E * a.gate_bias[s.c]);
+    const float dh_last = a.dh_last != nullptr ? a.dh_last[s.row] : 0.f;
+    const float kept = a.states_in[s.row * a.keep];  // the state before the row
+    LaneBackward<T> f;
+    const Span back = warp_scan<true>(f.reduce(g, dy, bias, s.n - s.t), lanes);
+    const Span fwd = warp_scan<false>(f.reduce_h(x), lanes);
+    const float h = lane_before<false>(fwd, lanes).of(kept);
+    const float flow = lane_before<true>(back, lanes).of(dh_last);
+    Strip<T> dx, dg;
+    Pair sum(0.f);
+    f.gradients(h, flow, x, dy, s.n - s.t, dx, dg, sum);
+    float total = sum.lo() + sum.hi();
+    for (int d = lanes >> 1; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+    if (!s.any) return;
+    dx.template store<CP>(row_of<T>(a.dx, s.b, s.c) + s.t, a.T - s.t);
+    dg.template store<CP>(row_of<T>(a.d_gate, s.b, s.c) + s.t, a.T - s.t);
+    if (s.group == 0) {
+        bias_part[s.row] = total;
+        if (a.d_h0 != nullptr) a.d_h0[s.row] = back.of(dh_last);
     }
 }
 
@@ -290,52 +561,93 @@ __global__ void __launch_bounds__(128) scan_planes_bias_kernel(const float *part
     if (lane == 0) out[c] = sum;
 }
 
-// How rows are cut.  warps: 256 positions each; as many as a row has work for, at most eight (four
-// where rows alone fill the GPU).  segments > 1 only where the rows leave most of the GPU idle.
+// ------------------------------------------------------------------------------------------- host
+
+// How rows are cut.  lanes > 0: one span or less, that many lanes a row.  Else CTAs of `warps` warps,
+// as many as a row has spans for and as leave every row resident at once (`per_sm` warps fit an SM);
+// where rows exceed that anyway, four.  segments > 1 only where rows leave half the GPU idle.
 struct Plan {
-    int warps, segments, rounds_per;
+    int lanes, warps, segments, rounds_per;
 };
-Plan plan_of(const ScanArgs &a) {
-    Plan p;
+Plan plan_of(const ScanArgs &a, int per_sm) {
+    Plan p = {0, 1, 1, 1};
     const long long rows = (long long)a.B * a.C;
-    const int spans = (a.T + kWarpSpan - 1) / kWarpSpan, sms = sm_count();
-    p.warps = rows >= 4ll * sms ? 4 : kMaxWarps;
+    const int sms = sm_count();
+    if (a.T <= kWarpSpan) {
+        for (p.lanes = 1; p.lanes * kLane < a.T;) p.lanes *= 2;
+        return p;
+    }
+    const int spans = (a.T + kWarpSpan - 1) / kWarpSpan;
+    const long long fit = (long long)per_sm * sms;
+    p.warps = rows > fit ? 4 : 1;
+    while (p.warps < kMaxWarps && rows * p.warps * 2 <= fit) p.warps *= 2;
     while (p.warps > 1 && p.warps / 2 >= spans) p.warps /= 2;
     const int rounds = (spans + p.warps - 1) / p.warps;
-    const long long want = 4ll * sms;
-    p.segments = 1;
-    if (rows * 2 < want) p.segments = (int)((want + rows - 1) / rows);
+    if (rows * p.warps * 2 < fit) p.segments = (int)(fit / (rows * p.warps));
     if (p.segments > rounds) p.segments = rounds;
     p.rounds_per = (rounds + p.segments - 1) / p.segments;
     p.segments = (rounds + p.rounds_per - 1) / p.rounds_per;
     return p;
 }
+// warps that fit an SM: by registers, and in fp32 by the rings
+int forward_warps(const ScanArgs &) { return 36; }
+int backward_warps(const ScanArgs &a) { return a.dtype == WTCONV_F32 ? 24 : 32; }
 
-bool rows_aligned(const ScanTensor &s, const ScanArgs &a) {
-    const int per = 16 / elem_bytes_of(a.dtype);
-    return aligned_to(s.p, 16) && (a.B == 1 || s.batch % per == 0) && (a.C == 1 || s.row % per == 0);
+bool rows_at(const ScanTensor &s, const ScanArgs &a, int bytes) {
+    const int per = bytes / elem_bytes_of(a.dtype);
+    return aligned_to(s.p, bytes) && (a.B == 1 || s.batch % per == 0) && (a.C == 1 || s.row % per == 0);
 }
 
 size_t map_bytes(const ScanArgs &a, const Plan &p) {
     return p.segments > 1 ? ((size_t)a.B * a.C * p.segments * sizeof(float2) + 255) / 256 * 256 : 0;
 }
+unsigned short_grid(const ScanArgs &a, const Plan &p) {
+    const long long per_cta = kShortThreads / p.lanes;
+    return (unsigned)(((long long)a.B * a.C + per_cta - 1) / per_cta);
+}
 
-template <typename T, bool VEC> cudaError_t forward_typed(const ScanArgs &a, const Plan &p, cudaStream_t st) {
-    const unsigned grid = (unsigned)((long long)a.B * a.C * p.segments);
-    float2 *maps = static_cast<float2 *>(a.workspace);
-    if (p.segments > 1)
-        scan_planes_forward_kernel<T, VEC, kReduce><<<grid, p.warps * 32, 0, st>>>(a, p.segments, p.rounds_per, maps);
-    scan_planes_forward_kernel<T, VEC, kApply><<<grid, p.warps * 32, 0, st>>>(a, p.segments, p.rounds_per, maps);
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), unsigned grid, const Plan &p, size_t per_warp, cudaStream_t st, A... args) {
+    const size_t shared = p.warps * per_warp;
+    if (shared > 40 * 1024) {  // (the static part counts towards the default 48 KB, too)
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<grid, p.warps * 32, shared, st>>>(args...);
     return cudaGetLastError();
 }
 
-template <typename T, bool VEC> cudaError_t backward_typed(const ScanArgs &a, const Plan &p, cudaStream_t st) {
+template <typename T, int CP> cudaError_t forward_typed(const ScanArgs &a, cudaStream_t st) {
+    const Plan p = plan_of(a, forward_warps(a));
+    if (p.lanes > 0) {
+        scan_short_forward_kernel<T, CP><<<short_grid(a, p), kShortThreads, 0, st>>>(a, p.lanes);
+        return cudaGetLastError();
+    }
     const unsigned grid = (unsigned)((long long)a.B * a.C * p.segments);
+    const size_t ring = sizeof(Ring<T, 2>);
+    float2 *maps = static_cast<float2 *>(a.workspace);
+    if (p.segments > 1) {
+        const cudaError_t e = launch(scan_planes_forward_kernel<T, CP, kReduce>, grid, p, ring, st, a, p.segments, p.rounds_per, maps);
+        if (e != cudaSuccess) return e;
+    }
+    return launch(scan_planes_forward_kernel<T, CP, kApply>, grid, p, ring, st, a, p.segments, p.rounds_per, maps);
+}
+
+template <typename T, int CP> cudaError_t backward_typed(const ScanArgs &a, cudaStream_t st) {
+    const Plan p = plan_of(a, backward_warps(a));
+    const unsigned grid = (unsigned)((long long)a.B * a.C * p.segments);
+    const size_t ring = sizeof(Ring<T, 3>);
     float2 *maps = static_cast<float2 *>(a.workspace);
     float *part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + map_bytes(a, p));
-    if (p.segments > 1)
-        scan_planes_backward_kernel<T, VEC, kReduce><<<grid, p.warps * 32, 0, st>>>(a, p.segments, p.rounds_per, maps, part);
-    scan_planes_backward_kernel<T, VEC, kApply><<<grid, p.warps * 32, 0, st>>>(a, p.segments, p.rounds_per, maps, part);
+    cudaError_t e = cudaSuccess;
+    if (p.lanes > 0) {
+        scan_short_backward_kernel<T, CP><<<short_grid(a, p), kShortThreads, 0, st>>>(a, p.lanes, part);
+        e = cudaGetLastError();
+    } else {
+        if (p.segments > 1) e = launch(scan_planes_backward_kernel<T, CP, kReduce>, grid, p, ring, st, a, p.segments, p.rounds_per, maps, part);
+        if (e == cudaSuccess) e = launch(scan_planes_backward_kernel<T, CP, kApply>, grid, p, ring, st, a, p.segments, p.rounds_per, maps, part);
+    }
+    if (e != cudaSuccess) return e;
     scan_planes_bias_kernel<<<(a.C + 3) / 4, 128, 0, st>>>(part, a.d_gate_bias, a.B, a.C, p.segments);
     return cudaGetLastError();
 }
@@ -343,28 +655,41 @@ template <typename T, bool VEC> cudaError_t backward_typed(const ScanArgs &a, co
 }  // namespace
 
 size_t scan_planes_workspace(int op, const ScanArgs &a) {
-    const Plan p = plan_of(a);
-    const size_t part = op == WTCONV_SCAN_OP_BACKWARD ? (size_t)a.B * a.C * p.segments * sizeof(float) : 0;
+    const bool back = op == WTCONV_SCAN_OP_BACKWARD;
+    const Plan p = plan_of(a, back ? backward_warps(a) : forward_warps(a));
+    const size_t part = back ? (size_t)a.B * a.C * p.segments * sizeof(float) : 0;
     return map_bytes(a, p) + (part + 255) / 256 * 256;
 }
 
+namespace {
+
+// by the widest copies that every row's address allows
+template <typename T> cudaError_t forward_any(const ScanArgs &a, cudaStream_t st) {
+    const auto all = [&](int bytes) { return rows_at(a.x, a, bytes) && rows_at(a.gate, a, bytes) && rows_at(a.y, a, bytes); };
+    if (all(16)) return forward_typed<T, 16>(a, st);
+    if constexpr (sizeof(T) == 4) return forward_typed<T, 4>(a, st);
+    else return all(4) ? forward_typed<T, 4>(a, st) : forward_typed<T, 2>(a, st);
+}
+template <typename T> cudaError_t backward_any(const ScanArgs &a, cudaStream_t st) {
+    const auto all = [&](int bytes) {
+        return rows_at(a.x, a, bytes) && rows_at(a.gate, a, bytes) && rows_at(a.dy, a, bytes) && rows_at(a.dx, a, bytes) &&
+               rows_at(a.d_gate, a, bytes);
+    };
+    if (all(16)) return backward_typed<T, 16>(a, st);
+    if constexpr (sizeof(T) == 4) return backward_typed<T, 4>(a, st);
+    else return all(4) ? backward_typed<T, 4>(a, st) : backward_typed<T, 2>(a, st);
+}
+
+}  // namespace
+
 cudaError_t launch_scan_planes_forward(const ScanArgs &a, cudaStream_t st) {
-    const Plan p = plan_of(a);
-    const bool vec = rows_aligned(a.x, a) && rows_aligned(a.gate, a) && rows_aligned(a.y, a);
-    if (a.dtype == WTCONV_F32) return vec ? forward_typed<float, true>(a, p, st) : forward_typed<float, false>(a, p, st);
-    if (a.dtype == WTCONV_BF16)
-        return vec ? forward_typed<__nv_bfloat16, true>(a, p, st) : forward_typed<__nv_bfloat16, false>(a, p, st);
-    return vec ? forward_typed<__half, true>(a, p, st) : forward_typed<__half, false>(a, p, st);
+    if (a.dtype == WTCONV_F32) return forward_any<float>(a, st);
+    return a.dtype == WTCONV_BF16 ? forward_any<__nv_bfloat16>(a, st) : forward_any<__half>(a, st);
 }
 
 cudaError_t launch_scan_planes_backward(const ScanArgs &a, cudaStream_t st) {
-    const Plan p = plan_of(a);
-    const bool vec = rows_aligned(a.x, a) && rows_aligned(a.gate, a) && rows_aligned(a.dy, a) && rows_aligned(a.dx, a) &&
-                     rows_aligned(a.d_gate, a);
-    if (a.dtype == WTCONV_F32) return vec ? backward_typed<float, true>(a, p, st) : backward_typed<float, false>(a, p, st);
-    if (a.dtype == WTCONV_BF16)
-        return vec ? backward_typed<__nv_bfloat16, true>(a, p, st) : backward_typed<__nv_bfloat16, false>(a, p, st);
-    return vec ? backward_typed<__half, true>(a, p, st) : backward_typed<__half, false>(a, p, st);
+    if (a.dtype == WTCONV_F32) return backward_any<float>(a, st);
+    return a.dtype == WTCONV_BF16 ? backward_any<__nv_bfloat16>(a, st) : backward_any<__half>(a, st);
 }
 
 }  // namespace wtconv

@@ -55,25 +55,16 @@ template <typename T> struct Tile {
 
 // Copies of CP bytes: 16 or 4 asynchronously (what is past the length or the last channel reads as
 // zeros and is not touched), 2 through registers.
-template <int CP> __device__ __forceinline__ void copy_async(void *to, const void *from, int bytes) {
-    const unsigned dst = (unsigned)__cvta_generic_to_shared(to);
-    if constexpr (CP == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int PENDING> __device__ __forceinline__ void wait_copies() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
-}
 // A thread's share of the copies of one tensor's tiles: column `c` of every `rows_at_once`-th row.
 template <typename T, int CP> struct Loader {
     static constexpr int per_row = kRowBytes / CP, elems = CP / (int)sizeof(T), rows_at_once = kThreads<T> / per_row;
     static_assert(kThreads<T> % per_row == 0 && kSpan % rows_at_once == 0, "");
-    const T *p;           // the thread's element of the next tile
+    const T *p, *anchor;  // the thread's element of the next tile; an address that stands in where nothing is read
     long long round, stride;
     // from: the strip's first channel at the CTA's first position; round: elements between its tiles
-    __device__ __forceinline__ Loader(const T *from, long long row, long long round_)
-        : p(from + (threadIdx.x / per_row) * row + (threadIdx.x % per_row) * elems), round(round_), stride(rows_at_once * row) {}
+    __device__ __forceinline__ Loader(const T *base, const T *from, long long row, long long round_)
+        : p(from + (threadIdx.x / per_row) * row + (threadIdx.x % per_row) * elems), anchor(base), round(round_),
+          stride(rows_at_once * row) {}
     // rows: valid positions of the tile; width: valid channels of the strip
     __device__ __forceinline__ void next(Tile<T> &tile, int rows, int width) {
         const int r0 = threadIdx.x / per_row, c = (threadIdx.x % per_row) * elems, left = width - c;
@@ -84,7 +75,7 @@ template <typename T, int CP> struct Loader {
         for (int k = 0; k < kSpan; k += rows_at_once, from += stride) {
             const bool valid = r0 + k < rows && bytes > 0;
             if constexpr (CP == 2) to[k * kWidth<T>] = valid ? *from : from_f32<T>(0.f);
-            else copy_async<CP>(to + k * kWidth<T>, from, valid ? bytes : 0);  // of 0 bytes: the address is not read
+            else copy_async<CP>(to + k * kWidth<T>, valid ? from : anchor, valid ? bytes : 0);
         }
         p += round;
     }
@@ -332,8 +323,8 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
     const int round_span = p.cluster * kSpan, rounds = (a.T + round_span - 1) / round_span;
     const int round0 = s.seg * p.rounds_per, round1 = min(round0 + p.rounds_per, rounds);
     int t0 = round0 * round_span + s.rank * kSpan;  // the CTA's first position of the round
-    Loader<T, CP> x(static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c0 + t0 * a.x.row, a.x.row, round_span * a.x.row);
-    Loader<T, CP> g(static_cast<const T *>(a.gate.p) + s.b * a.gate.batch + s.c0 + t0 * a.gate.row, a.gate.row,
+    Loader<T, CP> x(static_cast<const T *>(a.x.p), static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c0 + t0 * a.x.row, a.x.row, round_span * a.x.row);
+    Loader<T, CP> g(static_cast<const T *>(a.gate.p), static_cast<const T *>(a.gate.p) + s.b * a.gate.batch + s.c0 + t0 * a.gate.row, a.gate.row,
                     round_span * a.gate.row);
     T *y = static_cast<T *>(a.y.p) + s.b * a.y.batch + s.c + (t0 + slot * kSteps) * a.y.row;
     const long long y_round = round_span * a.y.row;
@@ -442,10 +433,10 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
     // the rounds past the length come first: no gradient passes them, dx and d_gate are 0
     const int live1 = max(round0, min(round1, (s.n + round_span - 1) / round_span));
     int t0 = (live1 - 1) * round_span + s.rank * kSpan;
-    Loader<T, CP> x(static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c0 + t0 * a.x.row, a.x.row, -round_span * a.x.row);
-    Loader<T, CP> g(static_cast<const T *>(a.gate.p) + s.b * a.gate.batch + s.c0 + t0 * a.gate.row, a.gate.row,
+    Loader<T, CP> x(static_cast<const T *>(a.x.p), static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c0 + t0 * a.x.row, a.x.row, -round_span * a.x.row);
+    Loader<T, CP> g(static_cast<const T *>(a.gate.p), static_cast<const T *>(a.gate.p) + s.b * a.gate.batch + s.c0 + t0 * a.gate.row, a.gate.row,
                     -round_span * a.gate.row);
-    Loader<T, CP> dy(static_cast<const T *>(a.dy.p) + s.b * a.dy.batch + s.c0 + t0 * a.dy.row, a.dy.row, -round_span * a.dy.row);
+    Loader<T, CP> dy(static_cast<const T *>(a.dy.p), static_cast<const T *>(a.dy.p) + s.b * a.dy.batch + s.c0 + t0 * a.dy.row, a.dy.row, -round_span * a.dy.row);
     T *dx = static_cast<T *>(a.dx.p) + s.b * a.dx.batch + s.c + (t0 + slot * kSteps + kSteps - 1) * a.dx.row;
     T *dg = static_cast<T *>(a.d_gate.p) + s.b * a.d_gate.batch + s.c + (t0 + slot * kSteps + kSteps - 1) * a.d_gate.row;
     const bool whole_strip = PAIRED && s.c0 + kWidth<T> <= a.C;
