@@ -1,6 +1,6 @@
 // Gated scan of planes [B][C][T] (time contiguous).
 //
-// A lane owns eight consecutive positions of a row, a warp 256 (a span).  A stretch of the recurrence is
+// A lane owns 32 consecutive bytes of a row (16 or 8 positions), a warp 1024 (a span).  A stretch of the recurrence is
 // the map h -> a h + u, and such maps compose (Span).  A lane takes its two halves as the two lanes of
 // packed fp32 arithmetic (one instruction for both), joins their maps, and the warp scans the lanes'
 // maps by shuffles; every lane then runs its positions again from the state that reaches it.  x, gate and (backward) dy are read once and everything stays in registers.  The backward
@@ -19,37 +19,38 @@ namespace wtconv {
 namespace {
 
 constexpr int kMaxWarps = 8;
-constexpr int kLane = 8, kHalf = kLane / 2;             // positions of a lane and of its halves,
-constexpr int kWarpSpan = 32 * kLane;                    // of a warp's round
-constexpr int kKeepLanes = WTCONV_SCAN_KEEP / kLane;     // lanes between two kept states
+template <typename T> constexpr int kLane = 32 / (int)sizeof(T);                // positions of a lane,
+template <typename T> constexpr int kHalf = kLane<T> / 2;                       // of its halves,
+template <typename T> constexpr int kWarpSpan = 32 * kLane<T>;                  // of a warp's round
+template <typename T> constexpr int kKeepLanes = WTCONV_SCAN_KEEP / kLane<T>;   // lanes between two kept states
 
 enum Mode { kReduce, kApply };
-// A lane's positions as raw words; pair j holds positions j and kHalf + j.
+// A lane's positions as raw words; pair j holds positions j and kHalf<T> + j.
 template <typename T> struct Strip {
-    static constexpr int words = kLane * (int)sizeof(T) / 4;
+    static constexpr int words = kLane<T> * (int)sizeof(T) / 4;
     uint32_t w[words];
     __device__ __forceinline__ Pair get(int j) const {
-        if constexpr (sizeof(T) == 4) return {__uint_as_float(w[j]), __uint_as_float(w[kHalf + j])};
+        if constexpr (sizeof(T) == 4) return {__uint_as_float(w[j]), __uint_as_float(w[kHalf<T> + j])};
         else {
-            const Pair a = widen<T>(w[j >> 1]), b = widen<T>(w[(kHalf + j) >> 1]);
+            const Pair a = widen<T>(w[j >> 1]), b = widen<T>(w[(kHalf<T> + j) >> 1]);
             return j & 1 ? Pair(a.hi(), b.hi()) : Pair(a.lo(), b.lo());
         }
     }
-    __device__ __forceinline__ void set(const Pair (&v)[kHalf]) {
+    __device__ __forceinline__ void set(const Pair (&v)[kHalf<T>]) {
 #pragma unroll
-        for (int j = 0; j < kHalf; j += 2) {
+        for (int j = 0; j < kHalf<T>; j += 2) {
             if constexpr (sizeof(T) == 4) {
                 w[j] = __float_as_uint(v[j].lo()), w[j + 1] = __float_as_uint(v[j + 1].lo());
-                w[kHalf + j] = __float_as_uint(v[j].hi()), w[kHalf + j + 1] = __float_as_uint(v[j + 1].hi());
+                w[kHalf<T> + j] = __float_as_uint(v[j].hi()), w[kHalf<T> + j + 1] = __float_as_uint(v[j + 1].hi());
             } else {
                 w[j >> 1] = narrow<T>(Pair(v[j].lo(), v[j + 1].lo()));
-                w[(kHalf + j) >> 1] = narrow<T>(Pair(v[j].hi(), v[j + 1].hi()));
+                w[(kHalf<T> + j) >> 1] = narrow<T>(Pair(v[j].hi(), v[j + 1].hi()));
             }
         }
     }
     // Straight from and to memory (short rows): positions 0 .. valid-1, as vectors where CP is 16.
     template <int CP> __device__ __forceinline__ void load(const T *p, int valid) {
-        if (CP == 16 && valid >= kLane) {
+        if (CP == 16 && valid >= kLane<T>) {
 #pragma unroll
             for (int k = 0; k < words; k += 4) {
                 const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + k / 4);
@@ -60,21 +61,21 @@ template <typename T> struct Strip {
 #pragma unroll
         for (int k = 0; k < words; ++k) w[k] = 0;
 #pragma unroll
-        for (int j = 0; j < kLane; ++j) {
+        for (int j = 0; j < kLane<T>; ++j) {
             if (j >= valid) continue;
             if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(p[j]);
             else w[j >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t *>(p + j) << (16 * (j & 1));
         }
     }
     template <int CP> __device__ __forceinline__ void store(T *p, int valid) const {
-        if (CP == 16 && valid >= kLane) {
+        if (CP == 16 && valid >= kLane<T>) {
 #pragma unroll
             for (int k = 0; k < words; k += 4)
                 reinterpret_cast<uint4 *>(p)[k / 4] = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
             return;
         }
 #pragma unroll
-        for (int j = 0; j < kLane; ++j) {
+        for (int j = 0; j < kLane<T>; ++j) {
             if (j >= valid) continue;
             if constexpr (sizeof(T) == 4) p[j] = __uint_as_float(w[j]);
             else *reinterpret_cast<uint16_t *>(p + j) = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
@@ -83,7 +84,7 @@ template <typename T> struct Strip {
     // zeros from position `valid` on
     __device__ __forceinline__ void cut(int valid) {
 #pragma unroll
-        for (int j = 0; j < kLane; ++j) {
+        for (int j = 0; j < kLane<T>; ++j) {
             if (j < valid) continue;
             if constexpr (sizeof(T) == 4) w[j] = 0;
             else w[j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
@@ -96,7 +97,7 @@ template <typename T> struct Strip {
 // asynchronously, 2 through registers), so that a warp's copies lie side by side; a lane then reads its
 // own positions.
 template <typename T> struct Cell {
-    static constexpr int bytes = kWarpSpan * (int)sizeof(T);
+    static constexpr int bytes = kWarpSpan<T> * (int)sizeof(T);
     uint4 q[bytes / 16];
     __device__ __forceinline__ char *at(int offset) { return reinterpret_cast<char *>(q) + offset; }
     // The span from p (the warp's first position) on.  Positions from `valid` on are not read and come
@@ -109,7 +110,7 @@ template <typename T> struct Cell {
                 const uint16_t v = k * 32 + lane < valid ? *reinterpret_cast<const uint16_t *>(from + k * 64) : (uint16_t)0;
                 *reinterpret_cast<uint16_t *>(at(k * 64 + lane * 2)) = v;
             }
-        } else if (valid >= kWarpSpan) {
+        } else if (valid >= kWarpSpan<T>) {
 #pragma unroll
             for (int k = 0; k < bytes / (32 * CP); ++k) copy_async<CP>(at((k * 32 + lane) * CP), from + k * 32 * CP, CP);
         } else {
@@ -132,10 +133,10 @@ template <typename T> struct Cell {
     // The lanes' positions to p (the warp's first position), those before `valid`: straight from the
     // registers, or through this cell where single elements or words would lie far apart.
     template <int CP> __device__ __forceinline__ void store(T *p, const Strip<T> &s, int valid, int lane) {
-        if (CP == 16 && valid >= kWarpSpan) {
+        if (CP == 16 && valid >= kWarpSpan<T>) {
 #pragma unroll
             for (int k = 0; k < Strip<T>::words; k += 4)
-                reinterpret_cast<uint4 *>(p + lane * kLane)[k / 4] = make_uint4(s.w[k], s.w[k + 1], s.w[k + 2], s.w[k + 3]);
+                reinterpret_cast<uint4 *>(p + lane * kLane<T>)[k / 4] = make_uint4(s.w[k], s.w[k + 1], s.w[k + 2], s.w[k + 3]);
             return;
         }
         __syncwarp();
@@ -144,20 +145,20 @@ template <typename T> struct Cell {
             q[lane * (Strip<T>::words / 4) + k] = make_uint4(s.w[4 * k], s.w[4 * k + 1], s.w[4 * k + 2], s.w[4 * k + 3]);
         __syncwarp();
         char *to = reinterpret_cast<char *>(p);
-        if (CP >= 4 && valid >= kWarpSpan) {
+        if (CP >= 4 && valid >= kWarpSpan<T>) {
 #pragma unroll
             for (int k = 0; k < bytes / 128; ++k)
                 *reinterpret_cast<uint32_t *>(to + (k * 32 + lane) * 4) = *reinterpret_cast<const uint32_t *>(at((k * 32 + lane) * 4));
         } else {
             constexpr int e = (int)sizeof(T);
 #pragma unroll
-            for (int k = 0; k < kLane; ++k)
+            for (int k = 0; k < kLane<T>; ++k)
                 if (k * 32 + lane < valid) *reinterpret_cast<T *>(to + (k * 32 + lane) * e) = *reinterpret_cast<const T *>(at((k * 32 + lane) * e));
         }
         __syncwarp();
     }
 };
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 
 // A lane's two halves as maps (Span of positions in time order: lo then hi).
 struct Halves {
@@ -168,30 +169,30 @@ struct Halves {
 
 // Gates of a lane's positions; those at or past `live` hold the state (a = 1, b = 0).
 template <typename T>
-__device__ __forceinline__ void lane_gates(const Strip<T> &g, Pair bias, int live, Pair (&av)[kHalf], Pair (&bv)[kHalf]) {
+__device__ __forceinline__ void lane_gates(const Strip<T> &g, Pair bias, int live, Pair (&av)[kHalf<T>], Pair (&bv)[kHalf<T>]) {
 #pragma unroll
-    for (int j = 0; j < kHalf; ++j) {
+    for (int j = 0; j < kHalf<T>; ++j) {
         const Gates q = gates_of(g.get(j), bias);
         av[j] = q.a, bv[j] = q.b;
     }
-    if (live < kLane) {
+    if (live < kLane<T>) {
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j) {
+        for (int j = 0; j < kHalf<T>; ++j) {
             if (j >= live) av[j] = Pair(1.f, av[j].hi()), bv[j] = Pair(0.f, bv[j].hi());
-            if (kHalf + j >= live) av[j] = Pair(av[j].lo(), 1.f), bv[j] = Pair(bv[j].lo(), 0.f);
+            if (kHalf<T> + j >= live) av[j] = Pair(av[j].lo(), 1.f), bv[j] = Pair(bv[j].lo(), 0.f);
         }
     }
 }
 
 // The forward of a lane: its map, then its outputs from the state before it.
 template <typename T> struct LaneForward {
-    Pair av[kHalf], uv[kHalf];
+    Pair av[kHalf<T>], uv[kHalf<T>];
     Halves halves;
     __device__ __forceinline__ Span reduce(const Strip<T> &x, const Strip<T> &g, Pair bias, int live) {
         lane_gates(g, bias, live, av, uv);
         halves = {Pair(1.f), Pair(0.f)};
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j) {
+        for (int j = 0; j < kHalf<T>; ++j) {
             uv[j] = mul(uv[j], x.get(j));  // (x is 0 beyond the length)
             halves.u = fma(av[j], halves.u, uv[j]);
             halves.a = mul(halves.a, av[j]);
@@ -199,12 +200,12 @@ template <typename T> struct LaneForward {
         return halves.lo().then(halves.hi());
     }
     __device__ __forceinline__ Strip<T> outputs(float before, int live) {
-        Pair h(before, halves.lo().of(before)), out[kHalf];
+        Pair h(before, halves.lo().of(before)), out[kHalf<T>];
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j) out[j] = h = fma(av[j], h, uv[j]);
+        for (int j = 0; j < kHalf<T>; ++j) out[j] = h = fma(av[j], h, uv[j]);
         Strip<T> y;
         y.set(out);
-        if (live < kLane) y.cut(live);  // past the length the state stands still, and y is 0
+        if (live < kLane<T>) y.cut(live);  // past the length the state stands still, and y is 0
         return y;
     }
 };
@@ -212,13 +213,13 @@ template <typename T> struct LaneForward {
 // The backward of a lane: the maps of dh (backward) and of h (forward), then its gradients.  x and dy
 // are taken from their cells again rather than kept.
 template <typename T> struct LaneBackward {
-    Pair av[kHalf], bv[kHalf];
+    Pair av[kHalf<T>], bv[kHalf<T>];
     Halves back, fwd;
     __device__ __forceinline__ Span reduce(const Strip<T> &g, const Strip<T> &dy, Pair bias, int live) {
         lane_gates(g, bias, live, av, bv);
         back = {Pair(1.f), Pair(0.f)};
 #pragma unroll
-        for (int j = kHalf - 1; j >= 0; --j) {
+        for (int j = kHalf<T> - 1; j >= 0; --j) {
             back.u = mul(av[j], add(dy.get(j), back.u));
             back.a = mul(back.a, av[j]);
         }
@@ -227,22 +228,22 @@ template <typename T> struct LaneBackward {
     __device__ __forceinline__ Span reduce_h(const Strip<T> &x) {
         fwd = {back.a, Pair(0.f)};
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j) fwd.u = fma(av[j], fwd.u, mul(bv[j], x.get(j)));
+        for (int j = 0; j < kHalf<T>; ++j) fwd.u = fma(av[j], fwd.u, mul(bv[j], x.get(j)));
         return fwd.lo().then(fwd.hi());
     }
     // h: the state before the lane; flow: a dh of the position after it
     __device__ __forceinline__ void gradients(float h_before, float flow_after, const Strip<T> &x, const Strip<T> &dy, int live,
                                               Strip<T> &dx, Strip<T> &dg, Pair &sum) {
-        Pair h(h_before, fwd.lo().of(h_before)), diff[kHalf];
+        Pair h(h_before, fwd.lo().of(h_before)), diff[kHalf<T>];
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j) {
+        for (int j = 0; j < kHalf<T>; ++j) {
             const Pair xv = x.get(j);
             diff[j] = sub(h, xv);  // h_{t-1} - x_t
             h = fma(av[j], h, mul(bv[j], xv));
         }
         Pair flow(back.hi().of(flow_after), flow_after);
 #pragma unroll
-        for (int j = kHalf - 1; j >= 0; --j) {
+        for (int j = kHalf<T> - 1; j >= 0; --j) {
             const Pair dh = add(dy.get(j), flow);
             diff[j] = mul(mul(dh, diff[j]), mul(av[j], bv[j]));
             sum = add(sum, diff[j]);
@@ -251,7 +252,7 @@ template <typename T> struct LaneBackward {
         }
         dx.set(bv);
         dg.set(diff);
-        if (live < kLane) dx.cut(live), dg.cut(live);
+        if (live < kLane<T>) dx.cut(live), dg.cut(live);
     }
 };
 
@@ -325,16 +326,16 @@ template <typename T, int TENSORS> __device__ __forceinline__ Ring<T, TENSORS> &
 }
 __device__ __forceinline__ int next_stage(int s) { return s + 1 == kStages ? 0 : s + 1; }
 
+// (72 registers leave room for 28 warps an SM: every row of 1024 at once, four warps each)
 template <typename T, int CP, Mode MODE>
-__global__ void __launch_bounds__(kMaxWarps * 32) scan_planes_forward_kernel(const ScanArgs a, int segments, int rounds_per,
-                                                                             float2 *maps) {
+__global__ void __maxnreg__(72) scan_planes_forward_kernel(const ScanArgs a, int segments, int rounds_per, float2 *maps) {
     extern __shared__ __align__(16) unsigned char raw[];
     __shared__ float2 slots[2][kMaxWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int round_span = warps * kWarpSpan;
+    const int round_span = warps * kWarpSpan<T>;
     const Segment s = segment_of(a, segments, rounds_per, round_span);
     auto &ring = ring_of<T, 2>(raw, warp);
-    int t0 = s.round0 * round_span + warp * kWarpSpan;  // the warp's first position
+    int t0 = s.round0 * round_span + warp * kWarpSpan<T>;  // the warp's first position
     const T *x = row_of<T>(a.x, s.b, s.c) + t0, *g = row_of<T>(a.gate, s.b, s.c) + t0;
     T *y = row_of<T>(a.y, s.b, s.c) + t0;
     int ahead = s.n - t0;  // valid positions of the next cells
@@ -363,13 +364,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32) scan_planes_forward_kernel(con
         wait_copies<kStages - 2>();
         __syncwarp();
         LaneForward<T> f;
-        const int t = t0 + lane * kLane, live = s.n - t;
-        Span span = f.reduce(ring[stage][0].read(lane), ring[stage][1].read(lane), bias, live);
+        const int t = t0 + lane * kLane<T>, live = s.n - t;
+        Span span = {1.f, 0.f};
+        if (t0 < a.T) span = f.reduce(ring[stage][0].read(lane), ring[stage][1].read(lane), bias, live);
         if (left > 0) fetch(free_stage), --left;
         else commit_copies();
         Cell<T> &out = ring[stage][0];  // read already
         stage = next_stage(stage), free_stage = next_stage(free_stage);
-        span = warp_scan<false>(span, 32);
+        if (t0 < a.T) span = warp_scan<false>(span, 32);
         float2 *slot = slots[round & 1];
         if (MODE == kReduce) {
             // every warp folds the whole round, so that all end with the segment's map
@@ -380,7 +382,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) scan_planes_forward_kernel(con
         }
         const Span before = lane_before<false>(span, 32);
         const float h = before.of(exchange<false>(span, slot, warp, warps, lane, carry));
-        if (a.states_out != nullptr && (lane & (kKeepLanes - 1)) == 0 && t < a.T)
+        if (t0 >= a.T) break;  // the row's last round, and nothing of it for this warp
+        if (a.states_out != nullptr && (lane & (kKeepLanes<T> - 1)) == 0 && t < a.T)
             a.states_out[s.row * a.keep + t / WTCONV_SCAN_KEEP] = h;
         out.template store<CP>(y, f.outputs(h, live), a.T - t0, lane);
         y += round_span;
@@ -393,16 +396,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32) scan_planes_forward_kernel(con
 }
 
 template <typename T, int CP, Mode MODE>
-__global__ void __launch_bounds__(kMaxWarps * 32, 4)
+__global__ void __launch_bounds__(kMaxWarps * 32, sizeof(T) == 4 ? 4 : 2)
     scan_planes_backward_kernel(const ScanArgs a, int segments, int rounds_per, float2 *maps, float *bias_part) {
     extern __shared__ __align__(16) unsigned char raw[];
     __shared__ float2 slots[2][kMaxWarps];
     __shared__ float sums[kMaxWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int round_span = warps * kWarpSpan;
+    const int round_span = warps * kWarpSpan<T>;
     const Segment s = segment_of(a, segments, rounds_per, round_span);
     auto &ring = ring_of<T, 3>(raw, warp);
-    int t0 = (s.round1 - 1) * round_span + warp * kWarpSpan;  // the warp's first position
+    int t0 = (s.round1 - 1) * round_span + warp * kWarpSpan<T>;  // the warp's first position
     const T *x = row_of<T>(a.x, s.b, s.c) + t0, *g = row_of<T>(a.gate, s.b, s.c) + t0, *dy = row_of<T>(a.dy, s.b, s.c) + t0;
     T *dx = row_of<T>(a.dx, s.b, s.c) + t0, *dg = row_of<T>(a.d_gate, s.b, s.c) + t0;
     int ahead = s.n - t0;  // valid positions of the next cells
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4)
     const auto kept_at = [&](int at) {
         return MODE == kApply && at < a.T ? a.states_in[s.row * a.keep + at / WTCONV_SCAN_KEEP] : 0.f;
     };
-    float next_kept = kept_at(t0 + lane * kLane);
+    float next_kept = kept_at(t0 + lane * kLane<T>);
     const Pair bias(-kLog2E * a.gate_bias[s.c]);
 
     float carry = 0.f;  // a dh of the position after this round
@@ -439,12 +442,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4)
         __syncwarp();
         LaneBackward<T> f;
         const float kept = next_kept;
-        const int t = t0 + lane * kLane, live = s.n - t;
-        Span span = f.reduce(ring[stage][0].read(lane), ring[stage][1].read(lane), bias, live);
+        const int t = t0 + lane * kLane<T>, live = s.n - t;
+        Span span = {1.f, 0.f};
+        if (t0 < a.T) span = f.reduce(ring[stage][0].read(lane), ring[stage][1].read(lane), bias, live);
         if (left > 0) fetch(free_stage), --left;
         else commit_copies();
         if (round > s.round0) next_kept = kept_at(t - round_span);
-        span = warp_scan<true>(span, 32);
+        if (t0 < a.T) span = warp_scan<true>(span, 32);
         float2 *slot = slots[round & 1];
         if (MODE == kReduce) {
             stage = next_stage(stage), free_stage = next_stage(free_stage);
@@ -453,8 +457,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4)
             for (int w = warps - 1; w >= 0; --w) whole = whole.then({slot[w].x, slot[w].y});
             continue;
         }
-        const Span fwd = warp_scan<false>(f.reduce_h(ring[stage][2].read(lane)), kKeepLanes);
-        const float h = lane_before<false>(fwd, kKeepLanes).of(kept);
+        if (t0 >= a.T) {  // the row's last round, and nothing of it for this warp
+            exchange<true>(span, slot, warp, warps, lane, carry);
+            stage = next_stage(stage), free_stage = next_stage(free_stage);
+            dx -= round_span, dg -= round_span;
+            continue;
+        }
+        const Span fwd = warp_scan<false>(f.reduce_h(ring[stage][2].read(lane)), kKeepLanes<T>);
+        const float h = lane_before<false>(fwd, kKeepLanes<T>).of(kept);
         const Span after = lane_before<true>(span, 32);
         const float flow = after.of(exchange<true>(span, slot, warp, warps, lane, carry));
         Strip<T> odx, odg;
@@ -497,7 +507,7 @@ template <typename T> __device__ __forceinline__ ShortRow short_row(const ScanAr
     s.b = (int)(s.row / a.C);
     s.c = (int)(s.row - (long long)s.b * a.C);
     s.n = s.any ? scan_length(a.lengths, s.b, a.T) : 0;
-    s.t = s.group * kLane;
+    s.t = s.group * kLane<T>;
     return s;
 }
 
@@ -572,16 +582,19 @@ struct Plan {
 Plan plan_of(const ScanArgs &a, int per_sm) {
     Plan p = {0, 1, 1, 1};
     const long long rows = (long long)a.B * a.C;
-    const int sms = sm_count();
-    if (a.T <= kWarpSpan) {
-        for (p.lanes = 1; p.lanes * kLane < a.T;) p.lanes *= 2;
+    const int lane = 32 / elem_bytes_of(a.dtype), span = 32 * lane, sms = sm_count();
+    if (a.T <= span) {
+        for (p.lanes = 1; p.lanes * lane < a.T;) p.lanes *= 2;
         return p;
     }
-    const int spans = (a.T + kWarpSpan - 1) / kWarpSpan;
+    const int spans = (a.T + span - 1) / span;
     const long long fit = (long long)per_sm * sms;
     p.warps = rows > fit ? 4 : 1;
     while (p.warps < kMaxWarps && rows * p.warps * 2 <= fit) p.warps *= 2;
     while (p.warps > 1 && p.warps / 2 >= spans) p.warps /= 2;
+    // (fewer warps where that wastes less of the last round)
+    for (int w = p.warps / 2; w > 1; w /= 2)
+        if ((spans + w - 1) / w * w < (spans + p.warps - 1) / p.warps * p.warps) p.warps = w;
     const int rounds = (spans + p.warps - 1) / p.warps;
     if (rows * p.warps * 2 < fit) p.segments = (int)(fit / (rows * p.warps));
     if (p.segments > rounds) p.segments = rounds;
@@ -590,8 +603,8 @@ Plan plan_of(const ScanArgs &a, int per_sm) {
     return p;
 }
 // warps that fit an SM: by registers, and in fp32 by the rings
-int forward_warps(const ScanArgs &) { return 36; }
-int backward_warps(const ScanArgs &a) { return a.dtype == WTCONV_F32 ? 24 : 32; }
+int forward_warps(const ScanArgs &) { return 28; }
+int backward_warps(const ScanArgs &a) { return a.dtype == WTCONV_F32 ? 32 : 20; }
 
 bool rows_at(const ScanTensor &s, const ScanArgs &a, int bytes) {
     const int per = bytes / elem_bytes_of(a.dtype);
