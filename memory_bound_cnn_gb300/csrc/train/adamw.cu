@@ -293,6 +293,7 @@ __device__ __forceinline__ bool vector_ok(const wtconv_optim_tensor &t) {
 template <typename G, int BITS, int CAP>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ TensorTable<CAP> table, StepScalars s,
                                                          const float *clip) {
+    begin_kernel();
     const float scale = clip != nullptr ? *clip : 1.f;
     const int which = find_tensor(table, blockIdx.x);
     const wtconv_optim_tensor &t = table.t[which];
@@ -331,6 +332,7 @@ template <bool VEC> __device__ __forceinline__ void write_values(const wtconv_op
 }
 
 template <int CAP> __global__ void __launch_bounds__(kThreads) state_values_kernel(const __grid_constant__ TensorTable<CAP> table) {
+    begin_kernel();
     const int which = find_tensor(table, blockIdx.x);
     const wtconv_optim_tensor &t = table.t[which];
     const long long start = (long long)(blockIdx.x - table.first[which]) * kChunk;
@@ -390,6 +392,7 @@ template <typename G, int CAP>
 __global__ void __launch_bounds__(kThreads) norm_part_kernel(const __grid_constant__ TensorTable<CAP> table, double *part) {
     __shared__ double scratch[kThreads / 32];
     constexpr int kRun = 64 * kChunk;
+    begin_kernel();
     double sum = 0.0;
     const int chunks = table.first[table.count];
     int chunk = (int)((long long)chunks * blockIdx.x / gridDim.x);
@@ -410,6 +413,7 @@ __global__ void __launch_bounds__(kThreads) norm_part_kernel(const __grid_consta
 
 __global__ void __launch_bounds__(kThreads) norm_final_kernel(const double *part, int count, double max_norm, float *out) {
     __shared__ double scratch[kThreads / 32];
+    begin_kernel();
     double sum = 0.0;
     for (int i = threadIdx.x; i < count; i += kThreads) sum += part[i];
     sum = block_sum(sum, scratch);
@@ -423,9 +427,8 @@ __global__ void __launch_bounds__(kThreads) norm_final_kernel(const double *part
 template <typename G, int CAP>
 cudaError_t launch_adamw_typed(const TensorTable<CAP> &table, const StepScalars &s, const float *clip, cudaStream_t st) {
     const unsigned grid = (unsigned)table.first[table.count];
-    if (s.state_bits == 32) adamw_kernel<G, 32, CAP><<<grid, kThreads, 0, st>>>(table, s, clip);
-    else adamw_kernel<G, 8, CAP><<<grid, kThreads, 0, st>>>(table, s, clip);
-    return cudaGetLastError();
+    return launch_kernel(s.state_bits == 32 ? adamw_kernel<G, 32, CAP> : adamw_kernel<G, 8, CAP>, grid, kThreads, 0, st, 1, table, s,
+                         clip);
 }
 
 }  // namespace
@@ -443,20 +446,17 @@ template <int CAP> cudaError_t launch_adamw(const TensorTable<CAP> &table, const
 
 template <int CAP>
 cudaError_t launch_norm_part(const TensorTable<CAP> &table, int grad_dtype, double *part, int blocks, cudaStream_t st) {
-    if (grad_dtype == WTCONV_F32) norm_part_kernel<float><<<blocks, kThreads, 0, st>>>(table, part);
-    else if (grad_dtype == WTCONV_BF16) norm_part_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(table, part);
-    else norm_part_kernel<__half><<<blocks, kThreads, 0, st>>>(table, part);
-    return cudaGetLastError();
+    const auto kernel = grad_dtype == WTCONV_F32 ? norm_part_kernel<float, CAP>
+                        : grad_dtype == WTCONV_BF16 ? norm_part_kernel<__nv_bfloat16, CAP> : norm_part_kernel<__half, CAP>;
+    return launch_kernel(kernel, blocks, kThreads, 0, st, 1, table, part);
 }
 
 cudaError_t launch_norm_final(const double *part, int count, double max_norm, float *out, cudaStream_t st) {
-    norm_final_kernel<<<1, kThreads, 0, st>>>(part, count, max_norm, out);
-    return cudaGetLastError();
+    return launch_kernel(norm_final_kernel, 1, kThreads, 0, st, 1, part, count, max_norm, out);
 }
 
 template <int CAP> cudaError_t launch_state_values(const TensorTable<CAP> &table, cudaStream_t st) {
-    state_values_kernel<<<(unsigned)table.first[table.count], kThreads, 0, st>>>(table);
-    return cudaGetLastError();
+    return launch_kernel(state_values_kernel<CAP>, (unsigned)table.first[table.count], kThreads, 0, st, 1, table);
 }
 
 template cudaError_t launch_adamw<kSmallTable>(const TensorTable<kSmallTable> &, const StepScalars &, const float *, cudaStream_t);

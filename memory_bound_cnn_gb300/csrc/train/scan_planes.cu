@@ -18,7 +18,7 @@ namespace wtconv {
 
 namespace {
 
-constexpr int kMaxWarps = 8;
+constexpr int kMaxWarps = 4;
 template <typename T> constexpr int kLane = 32 / (int)sizeof(T);                // positions of a lane,
 template <typename T> constexpr int kHalf = kLane<T> / 2;                       // of its halves,
 template <typename T> constexpr int kWarpSpan = 32 * kLane<T>;                  // of a warp's round
@@ -331,6 +331,7 @@ template <typename T, int CP, Mode MODE>
 __global__ void __maxnreg__(72) scan_planes_forward_kernel(const ScanArgs a, int segments, int rounds_per, float2 *maps) {
     extern __shared__ __align__(16) unsigned char raw[];
     __shared__ float2 slots[2][kMaxWarps];
+    begin_kernel();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int round_span = warps * kWarpSpan<T>;
     const Segment s = segment_of(a, segments, rounds_per, round_span);
@@ -396,11 +397,12 @@ __global__ void __maxnreg__(72) scan_planes_forward_kernel(const ScanArgs a, int
 }
 
 template <typename T, int CP, Mode MODE>
-__global__ void __launch_bounds__(kMaxWarps * 32, sizeof(T) == 4 ? 4 : 2)
+__global__ void __launch_bounds__(kMaxWarps * 32, sizeof(T) == 4 ? 6 : 4)
     scan_planes_backward_kernel(const ScanArgs a, int segments, int rounds_per, float2 *maps, float *bias_part) {
     extern __shared__ __align__(16) unsigned char raw[];
     __shared__ float2 slots[2][kMaxWarps];
     __shared__ float sums[kMaxWarps];
+    begin_kernel();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int round_span = warps * kWarpSpan<T>;
     const Segment s = segment_of(a, segments, rounds_per, round_span);
@@ -512,6 +514,7 @@ template <typename T> __device__ __forceinline__ ShortRow short_row(const ScanAr
 }
 
 template <typename T, int CP> __global__ void __launch_bounds__(kShortThreads) scan_short_forward_kernel(const ScanArgs a, int lanes) {
+    begin_kernel();
     const ShortRow s = short_row<T>(a, lanes);
     Strip<T> x, g;
     x.template load<CP>(row_of<T>(a.x, s.b, s.c) + s.t, s.n - s.t);
@@ -530,6 +533,7 @@ template <typename T, int CP> __global__ void __launch_bounds__(kShortThreads) s
 
 template <typename T, int CP>
 __global__ void __launch_bounds__(kShortThreads) scan_short_backward_kernel(const ScanArgs a, int lanes, float *bias_part) {
+    begin_kernel();
     const ShortRow s = short_row<T>(a, lanes);
     Strip<T> x, g, dy;
     x.template load<CP>(row_of<T>(a.x, s.b, s.c) + s.t, s.n - s.t);
@@ -559,6 +563,7 @@ __global__ void __launch_bounds__(kShortThreads) scan_short_backward_kernel(cons
 
 // d_gate_bias_c = sum over sequences and segments of the parts, in a fixed order: one warp per channel.
 __global__ void __launch_bounds__(128) scan_planes_bias_kernel(const float *part, float *out, int B, int C, int segments) {
+    begin_kernel();
     const int c = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (c >= C) return;
     float sum = 0.f;
@@ -574,8 +579,9 @@ __global__ void __launch_bounds__(128) scan_planes_bias_kernel(const float *part
 // ------------------------------------------------------------------------------------------- host
 
 // How rows are cut.  lanes > 0: one span or less, that many lanes a row.  Else CTAs of `warps` warps,
-// as many as a row has spans for and as leave every row resident at once (`per_sm` warps fit an SM);
-// where rows exceed that anyway, four.  segments > 1 only where rows leave half the GPU idle.
+// as many as a row has spans for and as leave every row resident at once (`per_sm` warps fit an SM, a
+// multiple of kMaxWarps); where rows exceed that anyway, four.  segments > 1 only where rows leave half
+// the GPU idle.
 struct Plan {
     int lanes, warps, segments, rounds_per;
 };
@@ -604,7 +610,7 @@ Plan plan_of(const ScanArgs &a, int per_sm) {
 }
 // warps that fit an SM: by registers, and in fp32 by the rings
 int forward_warps(const ScanArgs &) { return 28; }
-int backward_warps(const ScanArgs &a) { return a.dtype == WTCONV_F32 ? 32 : 20; }
+int backward_warps(const ScanArgs &a) { return a.dtype == WTCONV_F32 ? 24 : 16; }
 
 bool rows_at(const ScanTensor &s, const ScanArgs &a, int bytes) {
     const int per = bytes / elem_bytes_of(a.dtype);
@@ -626,15 +632,13 @@ cudaError_t launch(void (*kernel)(P...), unsigned grid, const Plan &p, size_t pe
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
         if (e != cudaSuccess) return e;
     }
-    kernel<<<grid, p.warps * 32, shared, st>>>(args...);
-    return cudaGetLastError();
+    return launch_kernel(kernel, grid, p.warps * 32, shared, st, 1, args...);
 }
 
 template <typename T, int CP> cudaError_t forward_typed(const ScanArgs &a, cudaStream_t st) {
     const Plan p = plan_of(a, forward_warps(a));
     if (p.lanes > 0) {
-        scan_short_forward_kernel<T, CP><<<short_grid(a, p), kShortThreads, 0, st>>>(a, p.lanes);
-        return cudaGetLastError();
+        return launch_kernel(scan_short_forward_kernel<T, CP>, short_grid(a, p), kShortThreads, 0, st, 1, a, p.lanes);
     }
     const unsigned grid = (unsigned)((long long)a.B * a.C * p.segments);
     const size_t ring = sizeof(Ring<T, 2>);
@@ -654,15 +658,13 @@ template <typename T, int CP> cudaError_t backward_typed(const ScanArgs &a, cuda
     float *part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + map_bytes(a, p));
     cudaError_t e = cudaSuccess;
     if (p.lanes > 0) {
-        scan_short_backward_kernel<T, CP><<<short_grid(a, p), kShortThreads, 0, st>>>(a, p.lanes, part);
-        e = cudaGetLastError();
+        e = launch_kernel(scan_short_backward_kernel<T, CP>, short_grid(a, p), kShortThreads, 0, st, 1, a, p.lanes, part);
     } else {
         if (p.segments > 1) e = launch(scan_planes_backward_kernel<T, CP, kReduce>, grid, p, ring, st, a, p.segments, p.rounds_per, maps, part);
         if (e == cudaSuccess) e = launch(scan_planes_backward_kernel<T, CP, kApply>, grid, p, ring, st, a, p.segments, p.rounds_per, maps, part);
     }
     if (e != cudaSuccess) return e;
-    scan_planes_bias_kernel<<<(a.C + 3) / 4, 128, 0, st>>>(part, a.d_gate_bias, a.B, a.C, p.segments);
-    return cudaGetLastError();
+    return launch_kernel(scan_planes_bias_kernel, (a.C + 3) / 4, 128, 0, st, 1, part, a.d_gate_bias, a.B, a.C, p.segments);
 }
 
 }  // namespace

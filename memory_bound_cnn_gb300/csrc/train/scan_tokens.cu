@@ -317,6 +317,7 @@ template <typename T> struct ForwardShared {
 template <typename T, int CP, bool PAIRED, Mode MODE>
 __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(const ScanArgs a, const TokenPlan p, ulonglong2 *maps) {
     extern __shared__ __align__(16) unsigned char raw[];
+    begin_kernel();
     ForwardShared<T> &sh = *reinterpret_cast<ForwardShared<T> *>(raw);
     const int lane = threadIdx.x % kLanes<T>, slot = threadIdx.x / kLanes<T>;
     const Place s = place_of<T>(a, p, lane);
@@ -425,6 +426,7 @@ template <typename T, int CP, bool PAIRED, Mode MODE>
 __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
     scan_tokens_backward_kernel(const ScanArgs a, const TokenPlan p, ulonglong2 *maps, float *bias_part) {
     extern __shared__ __align__(16) unsigned char raw[];
+    begin_kernel();
     BackwardShared<T> &sh = *reinterpret_cast<BackwardShared<T> *>(raw);
     const int lane = threadIdx.x % kLanes<T>, slot = threadIdx.x / kLanes<T>;
     const Place s = place_of<T>(a, p, lane);
@@ -568,6 +570,7 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
 __global__ void __launch_bounds__(256) scan_tokens_bias_kernel(const float *part, float *out, int B, int C, int strips,
                                                                int per_unit, int width) {
     __shared__ float sums[8][32];
+    begin_kernel();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float sum = 0.f;
@@ -623,17 +626,8 @@ cudaError_t launch(void (*kernel)(P...), int threads, size_t shared, const ScanA
                    A... args) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t config = {};
-    config.gridDim = dim3((unsigned)((long long)a.B * p.strips * p.segments * p.cluster));
-    config.blockDim = dim3(threads);
-    config.dynamicSmemBytes = shared;
-    config.stream = st;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = p.cluster, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    config.attrs = &attr;
-    config.numAttrs = p.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&config, kernel, a, p, args...);
+    return launch_kernel(kernel, (unsigned)((long long)a.B * p.strips * p.segments * p.cluster), threads, shared, st, p.cluster, a, p,
+                         args...);
 }
 
 // Whether every row of a tensor starts at a multiple of `bytes`.
@@ -662,9 +656,8 @@ template <typename T, int CP, bool PAIRED> cudaError_t backward_typed(const Scan
     if (p.segments > 1) e = launch(scan_tokens_backward_kernel<T, CP, PAIRED, kReduce>, kThreads<T>, shared, a, p, st, maps, part);
     if (e == cudaSuccess) e = launch(scan_tokens_backward_kernel<T, CP, PAIRED, kApply>, kThreads<T>, shared, a, p, st, maps, part);
     if (e != cudaSuccess) return e;
-    scan_tokens_bias_kernel<<<(a.C + 31) / 32, 256, 0, st>>>(part, a.d_gate_bias, a.B, a.C, p.strips,
-                                                            p.segments * p.cluster, kWidth<T>);
-    return cudaGetLastError();
+    return launch_kernel(scan_tokens_bias_kernel, (a.C + 31) / 32, 256, 0, st, 1, part, a.d_gate_bias, a.B, a.C, p.strips,
+                         p.segments * p.cluster, kWidth<T>);
 }
 
 // How wide rows can be copied in, and whether outputs can be stored two channels at a time.  The
@@ -699,6 +692,7 @@ template <typename T> cudaError_t backward_any(const ScanArgs &a, cudaStream_t s
 template <typename T>
 __global__ void __launch_bounds__(256) scan_step_kernel(int C, int parts, ScanTensor x, ScanTensor gate, const float *gate_bias,
                                                         float *pool, int n_states, const int *slots, ScanTensor y) {
+    begin_kernel();
     const int b = blockIdx.x / parts, c = (blockIdx.x - b * parts) * 256 + threadIdx.x;
     if (c >= C) return;
     const int slot = slots != nullptr ? slots[b] : b;
@@ -740,11 +734,9 @@ cudaError_t launch_scan_step(int B, int C, int dtype, const ScanTensor &x, const
                              float *pool, int n_states, const int *slots, const ScanTensor &y, cudaStream_t st) {
     const int parts = (C + 255) / 256;
     const unsigned grid = (unsigned)B * parts;
-    if (dtype == WTCONV_F32) scan_step_kernel<float><<<grid, 256, 0, st>>>(C, parts, x, gate, gate_bias, pool, n_states, slots, y);
-    else if (dtype == WTCONV_BF16)
-        scan_step_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(C, parts, x, gate, gate_bias, pool, n_states, slots, y);
-    else scan_step_kernel<__half><<<grid, 256, 0, st>>>(C, parts, x, gate, gate_bias, pool, n_states, slots, y);
-    return cudaGetLastError();
+    const auto kernel = dtype == WTCONV_F32 ? scan_step_kernel<float>
+                        : dtype == WTCONV_BF16 ? scan_step_kernel<__nv_bfloat16> : scan_step_kernel<__half>;
+    return launch_kernel(kernel, grid, 256, 0, st, 1, C, parts, x, gate, gate_bias, pool, n_states, slots, y);
 }
 
 }  // namespace wtconv

@@ -29,4 +29,25 @@ inline int sm_count() {
     return sms;
 }
 
+// Launches a kernel that may be set up while the one before it on the stream still runs: every kernel
+// of these operators waits for that one's end by itself (begin_kernel in train_device.cuh).  Between
+// the two kernels of a short call that is most of the gap.  cluster: CTAs that share a cluster.
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*kernel)(P...), unsigned grid, unsigned threads, size_t shared, cudaStream_t st, unsigned cluster,
+                          const A &...args) {
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(grid);
+    config.blockDim = dim3(threads);
+    config.dynamicSmemBytes = shared;
+    config.stream = st;
+    cudaLaunchAttribute attrs[2] = {};
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = cluster, attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    config.attrs = attrs;
+    config.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&config, kernel, args...);
+}
+
 }  // namespace wtconv

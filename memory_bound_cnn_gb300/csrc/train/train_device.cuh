@@ -80,6 +80,13 @@ __device__ __forceinline__ float root_of(float v) {  // the same; below the leas
     return r;
 }
 
+// First of all in every kernel: lets the next launch of the stream be set up, and waits until the one
+// before has ended and its memory is visible.
+__device__ __forceinline__ void begin_kernel() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 template <typename V> __device__ __forceinline__ V warp_sum(V v) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
