@@ -24,9 +24,12 @@ __device__ __forceinline__ float capped(float e) {  // min(e, 2^100), or NaN
     return r;
 }
 __device__ __forceinline__ Gates gates_of_exp(Pair e) {
-    const Pair d = add(e, Pair(1.f));
+    const Pair d = fma(e, Pair(-1.f), Pair(-1.f));  // -(1 + e)
     Gates g;
-    g.a = Pair(reciprocal(d.lo()), reciprocal(d.hi()));
+    g.a = Pair(reciprocal(-d.lo()), reciprocal(-d.hi()));
+    // one Newton step: a bias of the approximation would grow with the hundreds of positions that a
+    // state remembers (a^n)
+    g.a = fma(g.a, fma(d, g.a, Pair(1.f)), g.a);
     g.b = mul(e, g.a);
     return g;
 }

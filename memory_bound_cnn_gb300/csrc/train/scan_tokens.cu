@@ -511,9 +511,15 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
                 if (!runs_h) return;
                 Pair h = next_kept;
 #pragma unroll
-                for (int i = 0; i < kSlots; ++i) {
-                    sh.forward_start[i][lane] = h.q;
-                    h = load_map(&sh.forward[i][lane]).of(h);
+                for (int i = 0; i < kSlots; i += 4) {
+                    Map m[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) m[k] = load_map(&sh.forward[i + k][lane]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        sh.forward_start[i + k][lane] = h.q;
+                        h = m[k].of(h);
+                    }
                 }
                 if (round > round0) kept_state(t0 - round_span);
             });
