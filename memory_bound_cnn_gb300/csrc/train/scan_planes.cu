@@ -93,40 +93,61 @@ template <typename T> struct Strip {
 };
 
 // A warp's span of one tensor in shared memory, which the warp itself brings in and reads: a queue that
-// takes no registers and no barrier of the CTA.  It moves in order, CP bytes a lane at a time (16 or 4
-// asynchronously, 2 through registers), so that a warp's copies lie side by side; a lane then reads its
-// own positions.
+// takes no registers and no barrier of the CTA.  It moves in order, CP bytes a lane at a time, so that a
+// warp's copies lie side by side; a lane then reads its own positions.  CP 2: rows that start at any
+// 16-bit element are copied by whole words, from the one that holds the span's first position on, and
+// lie one element further (`shift`) where that is not a multiple of 4.
 template <typename T> struct Cell {
     static constexpr int bytes = kWarpSpan<T> * (int)sizeof(T);
-    uint4 q[bytes / 16];
+    uint4 q[bytes / 16 + 1];
     __device__ __forceinline__ char *at(int offset) { return reinterpret_cast<char *>(q) + offset; }
     // The span from p (the warp's first position) on.  Positions from `valid` on are not read and come
-    // as zeros; anchor is an address that stands in where nothing is read.
-    template <int CP> __device__ __forceinline__ void fetch(const T *p, int valid, int lane, const void *anchor) {
-        const char *from = reinterpret_cast<const char *>(p) + lane * CP;
+    // as zeros; base is the tensor's first element, an address that stands in where nothing is read.
+    template <int CP> __device__ __forceinline__ void fetch(const T *p, int valid, int lane, const void *base) {
         if constexpr (CP == 2) {
+            const int shift = (int)(reinterpret_cast<uintptr_t>(p) >> 1 & 1);
+            const void *anchor = reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(base) + 2 & ~(uintptr_t)3);
 #pragma unroll
-            for (int k = 0; k < bytes / 64; ++k) {
-                const uint16_t v = k * 32 + lane < valid ? *reinterpret_cast<const uint16_t *>(from + k * 64) : (uint16_t)0;
-                *reinterpret_cast<uint16_t *>(at(k * 64 + lane * 2)) = v;
+            for (int k = 0; k <= bytes / 128; ++k) {
+                if (k == bytes / 128 && lane > 0) continue;  // one word more
+                const int t = (k * 32 + lane) * 2 - shift;   // the word's first position
+                const T *from = p + t;
+                const int left = min(max(valid - t, 0), 2) * 2;
+                if (t < 0 && from < base) {  // before the tensor: its first element alone
+                    const uint16_t v = valid > 0 ? *reinterpret_cast<const uint16_t *>(from + 1) : (uint16_t)0;
+                    *reinterpret_cast<uint32_t *>(at(0)) = (uint32_t)v << 16;
+                } else {
+                    copy_async<4>(at((k * 32 + lane) * 4), left > 0 ? static_cast<const void *>(from) : anchor, left);
+                }
             }
-        } else if (valid >= kWarpSpan<T>) {
-#pragma unroll
-            for (int k = 0; k < bytes / (32 * CP); ++k) copy_async<CP>(at((k * 32 + lane) * CP), from + k * 32 * CP, CP);
+            return;
         } else {
+            const char *from = reinterpret_cast<const char *>(p) + lane * CP;
+            if (valid >= kWarpSpan<T>) {
 #pragma unroll
-            for (int k = 0; k < bytes / (32 * CP); ++k) {
-                const int left = min(max(valid * (int)sizeof(T) - (k * 32 + lane) * CP, 0), CP);
-                copy_async<CP>(at((k * 32 + lane) * CP), left > 0 ? from + k * 32 * CP : anchor, left);
+                for (int k = 0; k < bytes / (32 * CP); ++k) copy_async<CP>(at((k * 32 + lane) * CP), from + k * 32 * CP, CP);
+            } else {
+#pragma unroll
+                for (int k = 0; k < bytes / (32 * CP); ++k) {
+                    const int left = min(max(valid * (int)sizeof(T) - (k * 32 + lane) * CP, 0), CP);
+                    copy_async<CP>(at((k * 32 + lane) * CP), left > 0 ? from + k * 32 * CP : base, left);
+                }
             }
         }
     }
-    __device__ __forceinline__ Strip<T> read(int lane) const {
+    // shift: of the span that was fetched (0 unless CP is 2)
+    template <int CP> __device__ __forceinline__ Strip<T> read(int lane, int shift) const {
         Strip<T> s;
 #pragma unroll
         for (int k = 0; k < Strip<T>::words / 4; ++k) {
             const uint4 v = q[lane * (Strip<T>::words / 4) + k];
             s.w[4 * k] = v.x, s.w[4 * k + 1] = v.y, s.w[4 * k + 2] = v.z, s.w[4 * k + 3] = v.w;
+        }
+        if constexpr (CP == 2) {
+            const uint32_t last = q[(lane + 1) * (Strip<T>::words / 4)].x;
+#pragma unroll
+            for (int k = 0; k < Strip<T>::words; ++k)
+                s.w[k] = __funnelshift_r(s.w[k], k + 1 < Strip<T>::words ? s.w[k + 1] : last, 16 * shift);
         }
         return s;
     }
@@ -315,6 +336,10 @@ __device__ __forceinline__ Segment segment_of(const ScanArgs &a, int segments, i
     s.round1 = min(s.round0 + rounds_per, rounds);
     return s;
 }
+// Elements that a span from p on lies further in its cell (CP 2).
+template <int CP, typename T> __device__ __forceinline__ int shift_of(const T *p) {
+    return CP == 2 ? (int)(reinterpret_cast<uintptr_t>(p) >> 1 & 1) : 0;
+}
 template <typename T> __device__ __forceinline__ T *row_of(const ScanTensor &t, int b, int c) {
     return static_cast<T *>(t.p) + b * t.batch + c * t.row;
 }
@@ -339,6 +364,7 @@ __global__ void __maxnreg__(72) scan_planes_forward_kernel(const ScanArgs a, int
     int t0 = s.round0 * round_span + warp * kWarpSpan<T>;  // the warp's first position
     const T *x = row_of<T>(a.x, s.b, s.c) + t0, *g = row_of<T>(a.gate, s.b, s.c) + t0;
     T *y = row_of<T>(a.y, s.b, s.c) + t0;
+    const int shift_x = shift_of<CP>(x), shift_g = shift_of<CP>(g);  // (a span is an even number of positions)
     int ahead = s.n - t0;  // valid positions of the next cells
     const auto fetch = [&](int stage) {
         ring[stage][0].template fetch<CP>(x, ahead, lane, a.x.p);
@@ -367,7 +393,7 @@ __global__ void __maxnreg__(72) scan_planes_forward_kernel(const ScanArgs a, int
         LaneForward<T> f;
         const int t = t0 + lane * kLane<T>, live = s.n - t;
         Span span = {1.f, 0.f};
-        if (t0 < a.T) span = f.reduce(ring[stage][0].read(lane), ring[stage][1].read(lane), bias, live);
+        if (t0 < a.T) span = f.reduce(ring[stage][0].template read<CP>(lane, shift_x), ring[stage][1].template read<CP>(lane, shift_g), bias, live);
         if (left > 0) fetch(free_stage), --left;
         else commit_copies();
         Cell<T> &out = ring[stage][0];  // read already
@@ -410,6 +436,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, sizeof(T) == 4 ? 6 : 4)
     int t0 = (s.round1 - 1) * round_span + warp * kWarpSpan<T>;  // the warp's first position
     const T *x = row_of<T>(a.x, s.b, s.c) + t0, *g = row_of<T>(a.gate, s.b, s.c) + t0, *dy = row_of<T>(a.dy, s.b, s.c) + t0;
     T *dx = row_of<T>(a.dx, s.b, s.c) + t0, *dg = row_of<T>(a.d_gate, s.b, s.c) + t0;
+    const int shift_x = shift_of<CP>(x), shift_g = shift_of<CP>(g), shift_dy = shift_of<CP>(dy);
     int ahead = s.n - t0;  // valid positions of the next cells
     const auto fetch = [&](int stage) {
         ring[stage][0].template fetch<CP>(g, ahead, lane, a.gate.p);
@@ -446,7 +473,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, sizeof(T) == 4 ? 6 : 4)
         const float kept = next_kept;
         const int t = t0 + lane * kLane<T>, live = s.n - t;
         Span span = {1.f, 0.f};
-        if (t0 < a.T) span = f.reduce(ring[stage][0].read(lane), ring[stage][1].read(lane), bias, live);
+        if (t0 < a.T) span = f.reduce(ring[stage][0].template read<CP>(lane, shift_g), ring[stage][1].template read<CP>(lane, shift_dy), bias, live);
         if (left > 0) fetch(free_stage), --left;
         else commit_copies();
         if (round > s.round0) next_kept = kept_at(t - round_span);
@@ -465,12 +492,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, sizeof(T) == 4 ? 6 : 4)
             dx -= round_span, dg -= round_span;
             continue;
         }
-        const Span fwd = warp_scan<false>(f.reduce_h(ring[stage][2].read(lane)), kKeepLanes<T>);
+        const Span fwd = warp_scan<false>(f.reduce_h(ring[stage][2].template read<CP>(lane, shift_x)), kKeepLanes<T>);
         const float h = lane_before<false>(fwd, kKeepLanes<T>).of(kept);
         const Span after = lane_before<true>(span, 32);
         const float flow = after.of(exchange<true>(span, slot, warp, warps, lane, carry));
         Strip<T> odx, odg;
-        f.gradients(h, flow, ring[stage][2].read(lane), ring[stage][1].read(lane), live, odx, odg, sum);
+        f.gradients(h, flow, ring[stage][2].template read<CP>(lane, shift_x), ring[stage][1].template read<CP>(lane, shift_dy), live, odx, odg,
+                    sum);
         ring[stage][0].template store<CP>(dx, odx, a.T - t0, lane);
         ring[stage][0].template store<CP>(dg, odg, a.T - t0, lane);
         stage = next_stage(stage), free_stage = next_stage(free_stage);

@@ -40,22 +40,43 @@ template <typename T> constexpr int kWidth = kRowBytes / (int)sizeof(T);  // cha
 template <typename T> constexpr int kLanes = kWidth<T> / 2;               // threads of a slot
 template <typename T> constexpr int kThreads = kSlots * kLanes<T>;
 
+// Two channels of one position as they lie in memory, and as fp32.
+template <typename T> struct Two {
+    uint32_t w;
+    __device__ __forceinline__ Pair wide() const { return widen<T>(w); }
+};
+template <> struct Two<float> {
+    Pair v;
+    __device__ __forceinline__ Pair wide() const { return v; }
+};
+
 // kSpan positions of a strip of one tensor.
-template <typename T> struct Tile {
+template <typename T, int CP> struct Tile {
     T v[kSpan][kWidth<T>];
-    __device__ __forceinline__ Pair read(int r, int lane) const {
+    __device__ __forceinline__ Two<T> raw(int r, int lane) const {
         if constexpr (sizeof(T) == 4) {
             const float2 f = *reinterpret_cast<const float2 *>(&v[r][lane * 2]);
-            return {f.x, f.y};
+            return {Pair(f.x, f.y)};
         } else {
-            return widen<T>(*reinterpret_cast<const uint32_t *>(&v[r][lane * 2]));
+            return {*reinterpret_cast<const uint32_t *>(&v[r][lane * 2])};
         }
     }
 };
+// The same where rows start at any 16-bit element: whole words are copied, from the one that holds a
+// row's first channel on, so that the channels of a row lie one element further where its address is
+// not a multiple of 4.  `first` is that offset in row 0, `step` (0 or 1) whether it alternates.
+template <typename T> struct Tile<T, 2> {
+    static constexpr int words = kWidth<T> / 2 + 1;
+    uint32_t w[kSpan][words];
+    int first, step;
+    __device__ __forceinline__ Two<T> raw(int r, int lane) const {
+        const uint16_t *h = reinterpret_cast<const uint16_t *>(w[r]) + ((first + r * step) & 1) + lane * 2;
+        return {(uint32_t)h[0] | (uint32_t)h[1] << 16};
+    }
+};
 
-// Copies of CP bytes: 16 or 4 asynchronously (what is past the length or the last channel reads as
-// zeros and is not touched), 2 through registers.
-// A thread's share of the copies of one tensor's tiles: column `c` of every `rows_at_once`-th row.
+// A thread's share of the copies of one tensor's tiles, CP bytes each: column `c` of every
+// `rows_at_once`-th row.  What is past the length or the last channel reads as zeros and is not touched.
 template <typename T, int CP> struct Loader {
     static constexpr int per_row = kRowBytes / CP, elems = CP / (int)sizeof(T), rows_at_once = kThreads<T> / per_row;
     static_assert(kThreads<T> % per_row == 0 && kSpan % rows_at_once == 0, "");
@@ -66,7 +87,7 @@ template <typename T, int CP> struct Loader {
         : p(from + (threadIdx.x / per_row) * row + (threadIdx.x % per_row) * elems), anchor(base), round(round_),
           stride(rows_at_once * row) {}
     // rows: valid positions of the tile; width: valid channels of the strip
-    __device__ __forceinline__ void next(Tile<T> &tile, int rows, int width) {
+    __device__ __forceinline__ void next(Tile<T, CP> &tile, int rows, int width) {
         const int r0 = threadIdx.x / per_row, c = (threadIdx.x % per_row) * elems, left = width - c;
         const int bytes = left <= 0 ? 0 : left >= elems ? CP : left * (int)sizeof(T);
         T *to = &tile.v[r0][c];
@@ -74,8 +95,46 @@ template <typename T, int CP> struct Loader {
 #pragma unroll
         for (int k = 0; k < kSpan; k += rows_at_once, from += stride) {
             const bool valid = r0 + k < rows && bytes > 0;
-            if constexpr (CP == 2) to[k * kWidth<T>] = valid ? *from : from_f32<T>(0.f);
-            else copy_async<CP>(to + k * kWidth<T>, valid ? from : anchor, valid ? bytes : 0);
+            copy_async<CP>(to + k * kWidth<T>, valid ? from : anchor, valid ? bytes : 0);
+        }
+        p += round;
+    }
+};
+template <typename T> struct Loader<T, 2> {
+    // A thread copies word k of every eighth row, whose offset is the same in all of them, and the first
+    // 64 threads the last word of one row each.
+    static constexpr int per_row = kWidth<T> / 2, rows_at_once = kThreads<T> / per_row;
+    static_assert(rows_at_once % 2 == 0 && kSpan <= kThreads<T>, "");
+    const T *p, *anchor;  // the strip's first channel of the next tile's first row; the tensor's first element
+    long long round, row;
+    int first, step;
+    __device__ __forceinline__ Loader(const T *base, const T *from, long long row_, long long round_)
+        : p(from), anchor(base), round(round_), row(row_), first((int)(reinterpret_cast<uintptr_t>(from) >> 1 & 1)),
+          step((int)(row_ & 1)) {}
+    __device__ __forceinline__ void next(Tile<T, 2> &tile, int rows, int width) {
+        if (threadIdx.x == 0) tile.first = first, tile.step = step;
+        const void *none = reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(anchor) + 2 & ~(uintptr_t)3);
+        const int have = min(width, kWidth<T>);
+        {
+            const int r0 = threadIdx.x / per_row, k = threadIdx.x % per_row;
+            const int c = 2 * k - ((first + r0 * step) & 1);  // the word's first channel; -1: the element before the strip
+            const int bytes = min(max(have - c, 0), 2) * 2;
+            const T *from = p + r0 * row + c;
+            uint32_t *to = &tile.w[r0][k];
+#pragma unroll
+            for (int j = 0; j < kSpan; j += rows_at_once, from += rows_at_once * row) {
+                const bool valid = r0 + j < rows && bytes > 0;
+                if (j == 0 && from < anchor) {  // before the tensor: its first element alone
+                    *to = valid ? (uint32_t)*reinterpret_cast<const uint16_t *>(from + 1) << 16 : 0u;
+                } else {
+                    copy_async<4>(to + j * Tile<T, 2>::words, valid ? from : none, valid ? bytes : 0);
+                }
+            }
+        }
+        if (threadIdx.x < kSpan) {
+            const int r = threadIdx.x, c = kWidth<T> - ((first + r * step) & 1);
+            const bool valid = r < rows && c < have;
+            copy_async<4>(&tile.w[r][per_row], valid ? p + r * row + c : none, valid ? 2 : 0);
         }
         p += round;
     }
@@ -291,12 +350,12 @@ template <typename T> __device__ __forceinline__ Place place_of(const ScanArgs &
 }
 
 // Gates of a thread's positions; those at or past `live` hold the state (a = 1, b = 0).
-template <typename T>
-__device__ __forceinline__ void read_gates(const Tile<T> &tile, int slot, int lane, Pair bias, int live, Pair (&av)[kSteps],
+template <typename T, int CP>
+__device__ __forceinline__ void read_gates(const Tile<T, CP> &tile, int slot, int lane, Pair bias, int live, Pair (&av)[kSteps],
                                            Pair (&bv)[kSteps]) {
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
-        const Gates q = gates_of(tile.read(slot * kSteps + j, lane), bias);
+        const Gates q = gates_of(tile.raw(slot * kSteps + j, lane).wide(), bias);
         av[j] = q.a, bv[j] = q.b;
     }
     if (live < kSteps) {
@@ -308,8 +367,8 @@ __device__ __forceinline__ void read_gates(const Tile<T> &tile, int slot, int la
 
 // ---------------------------------------------------------------------------------------- forward
 
-template <typename T> struct ForwardShared {
-    Tile<T> x[2], g[2];
+template <typename T, int CP> struct ForwardShared {
+    Tile<T, CP> x[2], g[2];
     Maps<T> maps;
 };
 
@@ -318,7 +377,7 @@ template <typename T, int CP, bool PAIRED, Mode MODE>
 __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(const ScanArgs a, const TokenPlan p, ulonglong2 *maps) {
     extern __shared__ __align__(16) unsigned char raw[];
     begin_kernel();
-    ForwardShared<T> &sh = *reinterpret_cast<ForwardShared<T> *>(raw);
+    ForwardShared<T, CP> &sh = *reinterpret_cast<ForwardShared<T, CP> *>(raw);
     const int lane = threadIdx.x % kLanes<T>, slot = threadIdx.x / kLanes<T>;
     const Place s = place_of<T>(a, p, lane);
     const int round_span = p.cluster * kSpan, rounds = (a.T + round_span - 1) / round_span;
@@ -361,7 +420,7 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
         read_gates(sh.g[round & 1], slot, lane, bias, s.n - t, av, uv);
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
-            uv[j] = mul(uv[j], sh.x[round & 1].read(slot * kSteps + j, lane));  // (x is 0 beyond the length)
+            uv[j] = mul(uv[j], sh.x[round & 1].raw(slot * kSteps + j, lane).wide());  // (x is 0 beyond the length)
             mine = mine.then({av[j], uv[j]});
         }
         store_map(&sh.maps.slot[slot][lane], mine);
@@ -413,8 +472,8 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
 
 // --------------------------------------------------------------------------------------- backward
 
-template <typename T> struct BackwardShared {
-    Tile<T> x[2], g[2], dy[2];
+template <typename T, int CP> struct BackwardShared {
+    Tile<T, CP> x[2], g[2], dy[2];
     Maps<T> maps;
     // h within the CTA's positions, from the kept state: as slot and start of Maps
     ulonglong2 forward[kSlots][kLanes<T>];
@@ -427,7 +486,7 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
     scan_tokens_backward_kernel(const ScanArgs a, const TokenPlan p, ulonglong2 *maps, float *bias_part) {
     extern __shared__ __align__(16) unsigned char raw[];
     begin_kernel();
-    BackwardShared<T> &sh = *reinterpret_cast<BackwardShared<T> *>(raw);
+    BackwardShared<T, CP> &sh = *reinterpret_cast<BackwardShared<T, CP> *>(raw);
     const int lane = threadIdx.x % kLanes<T>, slot = threadIdx.x / kLanes<T>;
     const Place s = place_of<T>(a, p, lane);
     const int round_span = p.cluster * kSpan, rounds = (a.T + round_span - 1) / round_span;
@@ -485,15 +544,16 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
     else __syncthreads();
     for (int round = live1 - 1; round >= round0; --round) {
         const int t = t0 + slot * kSteps, live = s.n - t, buf = round & 1;
-        Pair av[kSteps], bv[kSteps], dyv[kSteps], diff[kSteps];
+        Pair av[kSteps], bv[kSteps];
+        Two<T> dyv[kSteps], xv[kSteps];  // kept as they lie: half the registers in 16 bits
         Map back = identity();
         read_gates(sh.g[buf], slot, lane, bias, live, av, bv);
 #pragma unroll
         for (int j = kSteps - 1; j >= 0; --j) {
-            dyv[j] = sh.dy[buf].read(slot * kSteps + j, lane);  // (dy and x are 0 beyond the length)
-            back.u = mul(av[j], add(dyv[j], back.u));
+            dyv[j] = sh.dy[buf].raw(slot * kSteps + j, lane);  // (dy and x are 0 beyond the length)
+            back.u = mul(av[j], add(dyv[j].wide(), back.u));
             back.a = mul(back.a, av[j]);
-            if (MODE == kApply) diff[j] = sh.x[buf].read(slot * kSteps + j, lane);  // x, until h is known
+            if (MODE == kApply) xv[j] = sh.x[buf].raw(slot * kSteps + j, lane);
         }
         store_map(&sh.maps.slot[slot][lane], back);
         if constexpr (MODE == kReduce) {
@@ -504,7 +564,7 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
             // h is scanned forward within the CTA's positions from the kept state; dh comes backward
             Map fwd = {back.a, Pair(0.f)};
 #pragma unroll
-            for (int j = 0; j < kSteps; ++j) fwd.u = fma(av[j], fwd.u, mul(bv[j], diff[j]));
+            for (int j = 0; j < kSteps; ++j) fwd.u = fma(av[j], fwd.u, mul(bv[j], xv[j].wide()));
             store_map(&sh.forward[slot][lane], fwd);
             wait_copies<0>();
             exchange<T, true>(sh.maps, buf, p.cluster, s.rank, chain, [&] {
@@ -527,17 +587,18 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
             Pair flow, h;
             flow.q = sh.maps.start[slot][lane];
             h.q = sh.forward_start[slot][lane];
+            Pair diff[kSteps];  // h_{t-1} - x_t
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) {
-                const Pair xv = diff[j];
-                diff[j] = sub(h, xv);
-                h = fma(av[j], h, mul(bv[j], xv));
+                const Pair x_t = xv[j].wide();
+                diff[j] = sub(h, x_t);
+                h = fma(av[j], h, mul(bv[j], x_t));
             }
             T *to_x = dx, *to_g = dg;
             const auto positions = [&](auto store) {
 #pragma unroll
                 for (int j = kSteps - 1; j >= 0; --j, to_x -= a.dx.row, to_g -= a.d_gate.row) {
-                    const Pair dh = add(dyv[j], flow);
+                    const Pair dh = add(dyv[j].wide(), flow);
                     const Pair dgv = mul(mul(dh, diff[j]), mul(av[j], bv[j]));
                     sum = add(sum, dgv);
                     flow = mul(av[j], dh);
@@ -644,7 +705,7 @@ bool rows_at(const ScanTensor &s, const ScanArgs &a, int bytes) {
 
 template <typename T, int CP, bool PAIRED> cudaError_t forward_typed(const ScanArgs &a, cudaStream_t st) {
     const TokenPlan p = plan_of(a, kForwardPerSm);
-    const size_t shared = sizeof(ForwardShared<T>);
+    const size_t shared = sizeof(ForwardShared<T, CP>);
     ulonglong2 *maps = static_cast<ulonglong2 *>(a.workspace);
     if (p.segments > 1) {
         const cudaError_t e = launch(scan_tokens_forward_kernel<T, CP, PAIRED, kReduce>, kThreads<T>, shared, a, p, st, maps);
@@ -655,7 +716,7 @@ template <typename T, int CP, bool PAIRED> cudaError_t forward_typed(const ScanA
 
 template <typename T, int CP, bool PAIRED> cudaError_t backward_typed(const ScanArgs &a, cudaStream_t st) {
     const TokenPlan p = plan_of(a, kBackwardPerSm);
-    const size_t shared = sizeof(BackwardShared<T>);
+    const size_t shared = sizeof(BackwardShared<T, CP>);
     ulonglong2 *maps = static_cast<ulonglong2 *>(a.workspace);
     float *part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + map_bytes(a, p));
     cudaError_t e = cudaSuccess;
@@ -667,7 +728,7 @@ template <typename T, int CP, bool PAIRED> cudaError_t backward_typed(const Scan
 }
 
 // How wide rows can be copied in, and whether outputs can be stored two channels at a time.  The
-// narrow combinations share one kernel: rows of single elements are rare and a quarter as fast.
+// narrow combinations share one kernel.
 template <typename T, typename F16, typename F4, typename FS>
 cudaError_t by_access(const ScanArgs &a, std::initializer_list<const ScanTensor *> in,
                       std::initializer_list<const ScanTensor *> out, F16 wide, F4 words, FS single) {
