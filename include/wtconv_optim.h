@@ -76,7 +76,8 @@ int wtconv_adamw_step(int n_tensors, const wtconv_optim_tensor *tensors,
 int wtconv_adamw_state_values(int n_tensors, const wtconv_optim_tensor *tensors,
                               float *const *m_out, float *const *v_out, wtconv_stream_t stream);
 
-/* Bytes of device workspace wtconv_grad_norm needs (16-byte aligned). */
+/* Bytes of device workspace wtconv_grad_norm needs (16-byte aligned; 0 for few elements, which one
+ * launch sums). */
 size_t wtconv_grad_norm_workspace_size(int n_tensors, const wtconv_optim_tensor *tensors);
 
 /* out[0] = norm = sqrt(sum of squares of every gradient), out[1] = the factor that limits it to

@@ -2,6 +2,7 @@
 // checks tensors, allocates outputs and scratch from PyTorch's caching allocator, and calls the C ABI
 // on the current stream.  Compiled, because these calls are short: a decoding step takes 4.5 us of
 // host time here and took 23 us through ctypes.
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/extension.h>
@@ -92,7 +93,7 @@ V *array(const optional<Tensor> &t, const char *name, c10::IntArrayRef shape, c1
 }
 
 Tensor empty(c10::IntArrayRef shape, at::ScalarType dtype, c10::Device device) {
-    return at::empty(shape, at::TensorOptions().dtype(dtype).device(device));
+    return at::detail::empty_cuda(shape, dtype, device, c10::nullopt);
 }
 
 // The caller's scratch or a new one of `need` bytes.
@@ -211,6 +212,7 @@ Tensor grad_norm(int n, uintptr_t tensors, int grad_dtype, const c10::Device &de
     float *out_p = array<float>(out, "out", {2}, dev);
     const c10::cuda::CUDAGuard guard(dev);
     const Scratch ws = scratch(workspace, workspace_bytes, dev);
+    // (scratch: none for few elements)
     check_status(wtconv_grad_norm(n, table(tensors), grad_dtype, max_norm, out_p, ws.p, ws.bytes, stream_on(stream, dev)),
                  "wtconv_grad_norm");
     return out;

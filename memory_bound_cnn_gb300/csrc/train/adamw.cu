@@ -3,6 +3,7 @@
 // One CTA per chunk of 2048 elements of one tensor, one warp per 256 of them (a block of the 8-bit
 // states), eight elements per lane in registers between the one read and the one write of each
 // array.  Bound by HBM.
+#include <cooperative_groups.h>
 #include <float.h>
 
 #include "optim.h"
@@ -12,7 +13,9 @@ namespace wtconv {
 
 namespace {
 
-constexpr int kThreads = 256;
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 256, kNormCluster = 8;
 constexpr uint32_t kIndexStride = 3242174889u;  // 2^32 / p, p^3 = p + 1
 constexpr float kLeastMax = 8.077935669463161e-28f;  // 2^-90
 
@@ -388,16 +391,13 @@ template <typename G> __device__ __forceinline__ float squares(const G *g, long 
 
 // A CTA takes a run of chunks, through one tensor after the other.  A thread's fp32 sum covers at
 // most kRun elements' share before it moves to fp64.
-template <typename G, int CAP>
-__global__ void __launch_bounds__(kThreads) norm_part_kernel(const __grid_constant__ TensorTable<CAP> table, double *part) {
-    __shared__ double scratch[kThreads / 32];
+template <typename G, int CAP> __device__ __forceinline__ double run_of_squares(const TensorTable<CAP> &table) {
     constexpr int kRun = 64 * kChunk;
-    begin_kernel();
     double sum = 0.0;
     const int chunks = table.first[table.count];
     int chunk = (int)((long long)chunks * blockIdx.x / gridDim.x);
     const int end = (int)((long long)chunks * (blockIdx.x + 1) / gridDim.x);
-    int which = find_tensor(table, chunk);
+    int which = chunk < end ? find_tensor(table, chunk) : 0;
     while (chunk < end) {
         const wtconv_optim_tensor &t = table.t[which];
         const int upto = min(end, table.first[which + 1]);
@@ -407,8 +407,20 @@ __global__ void __launch_bounds__(kThreads) norm_part_kernel(const __grid_consta
         chunk = upto;
         ++which;
     }
-    sum = block_sum(sum, scratch);
+    return sum;
+}
+template <typename G, int CAP>
+__global__ void __launch_bounds__(kThreads) norm_part_kernel(const __grid_constant__ TensorTable<CAP> table, double *part) {
+    __shared__ double scratch[kThreads / 32];
+    begin_kernel();
+    const double sum = block_sum(run_of_squares<G>(table), scratch);
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
+}
+
+__device__ __forceinline__ void write_norm(double sum, double max_norm, float *out) {
+    const double norm = sqrt(sum);
+    out[0] = (float)norm;
+    out[1] = norm <= (double)FLT_MAX ? (float)fmin(1.0, max_norm / (norm + 1e-6)) : __int_as_float(0x7fc00000);
 }
 
 __global__ void __launch_bounds__(kThreads) norm_final_kernel(const double *part, int count, double max_norm, float *out) {
@@ -417,10 +429,23 @@ __global__ void __launch_bounds__(kThreads) norm_final_kernel(const double *part
     double sum = 0.0;
     for (int i = threadIdx.x; i < count; i += kThreads) sum += part[i];
     sum = block_sum(sum, scratch);
-    if (threadIdx.x == 0) {
-        const double norm = sqrt(sum);
-        out[0] = (float)norm;
-        out[1] = norm <= (double)FLT_MAX ? (float)fmin(1.0, max_norm / (norm + 1e-6)) : __int_as_float(0x7fc00000);
+    if (threadIdx.x == 0) write_norm(sum, max_norm, out);
+}
+
+// Few chunks: one cluster sums them all, its CTAs leaving their sums with the first one.
+template <typename G, int CAP>
+__global__ void __launch_bounds__(kThreads) norm_small_kernel(const __grid_constant__ TensorTable<CAP> table, double max_norm, float *out) {
+    __shared__ double scratch[kThreads / 32], sums[kNormCluster];
+    begin_kernel();
+    cg::cluster_group cluster = cg::this_cluster();
+    const double sum = block_sum(run_of_squares<G>(table), scratch);
+    cluster.sync();  // the first CTA's shared memory is there
+    if (threadIdx.x == 0) cluster.map_shared_rank(sums, 0)[blockIdx.x] = sum;
+    cluster.sync();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        double total = 0.0;
+        for (int i = 0; i < kNormCluster; ++i) total += sums[i];
+        write_norm(total, max_norm, out);
     }
 }
 
@@ -451,6 +476,13 @@ cudaError_t launch_norm_part(const TensorTable<CAP> &table, int grad_dtype, doub
     return launch_kernel(kernel, blocks, kThreads, 0, st, 1, table, part);
 }
 
+template <int CAP>
+cudaError_t launch_norm_small(const TensorTable<CAP> &table, int grad_dtype, double max_norm, float *out, cudaStream_t st) {
+    const auto kernel = grad_dtype == WTCONV_F32 ? norm_small_kernel<float, CAP>
+                        : grad_dtype == WTCONV_BF16 ? norm_small_kernel<__nv_bfloat16, CAP> : norm_small_kernel<__half, CAP>;
+    return launch_kernel(kernel, kNormCluster, kThreads, 0, st, kNormCluster, table, max_norm, out);
+}
+
 cudaError_t launch_norm_final(const double *part, int count, double max_norm, float *out, cudaStream_t st) {
     return launch_kernel(norm_final_kernel, 1, kThreads, 0, st, 1, part, count, max_norm, out);
 }
@@ -463,6 +495,8 @@ template cudaError_t launch_adamw<kSmallTable>(const TensorTable<kSmallTable> &,
 template cudaError_t launch_adamw<kLargeTable>(const TensorTable<kLargeTable> &, const StepScalars &, const float *, cudaStream_t);
 template cudaError_t launch_norm_part<kSmallTable>(const TensorTable<kSmallTable> &, int, double *, int, cudaStream_t);
 template cudaError_t launch_norm_part<kLargeTable>(const TensorTable<kLargeTable> &, int, double *, int, cudaStream_t);
+template cudaError_t launch_norm_small<kSmallTable>(const TensorTable<kSmallTable> &, int, double, float *, cudaStream_t);
+template cudaError_t launch_norm_small<kLargeTable>(const TensorTable<kLargeTable> &, int, double, float *, cudaStream_t);
 template cudaError_t launch_state_values<kSmallTable>(const TensorTable<kSmallTable> &, cudaStream_t);
 template cudaError_t launch_state_values<kLargeTable>(const TensorTable<kLargeTable> &, cudaStream_t);
 

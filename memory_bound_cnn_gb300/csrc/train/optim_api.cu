@@ -69,6 +69,11 @@ bool list_ok(int n_tensors, const wtconv_optim_tensor *t) {
         if (t[i].n < 0 || t[i].n > kMostElements) return false;
     return true;
 }
+// one launch sums every gradient
+bool small_norm(int n_tensors, const wtconv_optim_tensor *t) {
+    const Batch b = next_batch(n_tensors, t, 0);
+    return b.end == n_tensors && b.count > 0 && b.chunks <= kSmallNorm;
+}
 bool f32_ok(const void *p) { return p != nullptr && aligned_to(p, 4); }
 bool state8_ok(const wtconv_optim_tensor &t) {
     return t.m != nullptr && t.v != nullptr && f32_ok(t.m_max) && f32_ok(t.v_max);
@@ -131,7 +136,7 @@ int wtconv_adamw_state_values(int n_tensors, const wtconv_optim_tensor *tensors,
 }
 
 size_t wtconv_grad_norm_workspace_size(int n_tensors, const wtconv_optim_tensor *tensors) {
-    if (!list_ok(n_tensors, tensors)) return 0;
+    if (!list_ok(n_tensors, tensors) || small_norm(n_tensors, tensors)) return 0;
     size_t blocks = 0;
     for (int at = 0; at < n_tensors;) {
         const Batch b = next_batch(n_tensors, tensors, at);
@@ -153,6 +158,10 @@ int wtconv_grad_norm(int n_tensors, const wtconv_optim_tensor *tensors, int grad
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return WTCONV_ERR_WORKSPACE;
     if (fault_injected()) return WTCONV_ERR_INJECTED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (small_norm(n_tensors, tensors))
+        return for_each_table(n_tensors, tensors, [&](const auto &table, const Batch &) {
+            return launch_norm_small(table, grad_dtype, max_norm, out, st);
+        });
     double *part = static_cast<double *>(workspace);
     int used = 0;
     const int rc = for_each_table(n_tensors, tensors, [&](const auto &table, const Batch &b) {

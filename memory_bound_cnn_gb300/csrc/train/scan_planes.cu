@@ -657,7 +657,7 @@ template <typename... P, typename... A>
 cudaError_t launch(void (*kernel)(P...), unsigned grid, const Plan &p, size_t per_warp, cudaStream_t st, A... args) {
     const size_t shared = p.warps * per_warp;
     if (shared > 40 * 1024) {  // (the static part counts towards the default 48 KB, too)
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+        const cudaError_t e = allow_shared(kernel, shared);
         if (e != cudaSuccess) return e;
     }
     return launch_kernel(kernel, grid, p.warps * 32, shared, st, 1, args...);

@@ -691,7 +691,7 @@ size_t part_bytes(const ScanArgs &a, const TokenPlan &p) {
 template <typename... P, typename... A>
 cudaError_t launch(void (*kernel)(P...), int threads, size_t shared, const ScanArgs &a, const TokenPlan &p, cudaStream_t st,
                    A... args) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+    const cudaError_t e = allow_shared(kernel, shared);
     if (e != cudaSuccess) return e;
     return launch_kernel(kernel, (unsigned)((long long)a.B * p.strips * p.segments * p.cluster), threads, shared, st, p.cluster, a, p,
                          args...);

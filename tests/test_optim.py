@@ -166,14 +166,18 @@ def test_norm_and_values_refuse(monkeypatch):
     assert adamw(tensors(copy=256), copy_dtype=0) == W.ERR_UNSUPPORTED
     assert adamw(None) == W.ERR_INVALID_ARG
 
-    def norm(t=tensors(), dtype=0, most=1.0, out=fake, ws=fake, nbytes=1 << 16):
+    many = 10_000_000  # more elements than one launch sums: a workspace is needed
+
+    def norm(t=tensors(n=many), dtype=0, most=1.0, out=fake, ws=fake, nbytes=1 << 16):
         return lib.wtconv_grad_norm(1, t, dtype, most, out, ws, nbytes, None)
 
     assert norm(out=None) == W.ERR_INVALID_ARG
     assert norm(most=0.0) == W.ERR_INVALID_ARG
     assert norm(most=float("nan")) == W.ERR_INVALID_ARG
     assert norm(dtype=4) == W.ERR_UNSUPPORTED
-    assert norm(t=tensors(grad=None)) == W.ERR_INVALID_ARG
+    assert norm(t=tensors(grad=None, n=many)) == W.ERR_INVALID_ARG
+    assert lib.wtconv_grad_norm_workspace_size(1, tensors(n=many)) > 0
+    assert lib.wtconv_grad_norm_workspace_size(1, tensors(n=-1)) == 0
     assert norm(ws=ctypes.c_void_p(264)) == W.ERR_INVALID_ARG
     assert norm(ws=None) == W.ERR_WORKSPACE
     assert norm(nbytes=7) == W.ERR_WORKSPACE
