@@ -1,7 +1,7 @@
 // Gated scan of tokens [B][T][C] (channels contiguous): one CTA per strip of channels of a sequence,
 // or a cluster of CTAs along its time.
 //
-// A strip is 128 bytes of every row, a round 64 positions of it, brought into shared memory by
+// A strip is 128 bytes of every row (32 where there are few channels), a round 64 positions of it, brought into shared memory by
 // asynchronous copies two rounds ahead.  A thread owns two neighbouring channels (packed fp32
 // arithmetic: one instruction for both) and eight consecutive positions, which it reduces to the map
 // h -> a h + u of the state before them; the threads of a position group (a slot: a warp of 16-bit
@@ -32,13 +32,17 @@ constexpr int kSlots = 8, kSteps = 8;
 constexpr int kSpan = kSlots * kSteps;  // positions of a CTA's round
 static_assert(kSpan == WTCONV_SCAN_KEEP, "a round starts at a kept state");
 constexpr int kMaxCluster = 8;
-constexpr int kRowBytes = 128;  // of a strip
+// R: bytes of a strip's rows, 128, or 32 where few channels would leave most of such a strip empty.
 
 enum Mode { kReduce, kApply };
 
-template <typename T> constexpr int kWidth = kRowBytes / (int)sizeof(T);  // channels of a strip
-template <typename T> constexpr int kLanes = kWidth<T> / 2;               // threads of a slot
-template <typename T> constexpr int kThreads = kSlots * kLanes<T>;
+// CTAs that an SM is to hold
+template <int R> constexpr int kForwardPerSm = 4 * 128 / R;
+template <int R> constexpr int kBackwardPerSm = 2 * 128 / R;
+
+template <typename T, int R> constexpr int kWidth = R / (int)sizeof(T);  // channels of a strip
+template <typename T, int R> constexpr int kLanes = kWidth<T, R> / 2;    // threads of a slot
+template <typename T, int R> constexpr int kThreads = kSlots * kLanes<T, R>;
 
 // Two channels of one position as they lie in memory, and as fp32.
 template <typename T> struct Two {
@@ -51,8 +55,8 @@ template <> struct Two<float> {
 };
 
 // kSpan positions of a strip of one tensor.
-template <typename T, int CP> struct Tile {
-    T v[kSpan][kWidth<T>];
+template <typename T, int CP, int R> struct Tile {
+    T v[kSpan][kWidth<T, R>];
     __device__ __forceinline__ Two<T> raw(int r, int lane) const {
         if constexpr (sizeof(T) == 4) {
             const float2 f = *reinterpret_cast<const float2 *>(&v[r][lane * 2]);
@@ -65,8 +69,8 @@ template <typename T, int CP> struct Tile {
 // The same where rows start at any 16-bit element: whole words are copied, from the one that holds a
 // row's first channel on, so that the channels of a row lie one element further where its address is
 // not a multiple of 4.  `first` is that offset in row 0, `step` (0 or 1) whether it alternates.
-template <typename T> struct Tile<T, 2> {
-    static constexpr int words = kWidth<T> / 2 + 1;
+template <typename T, int R> struct Tile<T, 2, R> {
+    static constexpr int words = kWidth<T, R> / 2 + 1;
     uint32_t w[kSpan][words];
     int first, step;
     __device__ __forceinline__ Two<T> raw(int r, int lane) const {
@@ -77,9 +81,9 @@ template <typename T> struct Tile<T, 2> {
 
 // A thread's share of the copies of one tensor's tiles, CP bytes each: column `c` of every
 // `rows_at_once`-th row.  What is past the length or the last channel reads as zeros and is not touched.
-template <typename T, int CP> struct Loader {
-    static constexpr int per_row = kRowBytes / CP, elems = CP / (int)sizeof(T), rows_at_once = kThreads<T> / per_row;
-    static_assert(kThreads<T> % per_row == 0 && kSpan % rows_at_once == 0, "");
+template <typename T, int CP, int R> struct Loader {
+    static constexpr int per_row = R / CP, elems = CP / (int)sizeof(T), rows_at_once = kThreads<T, R> / per_row;
+    static_assert(kThreads<T, R> % per_row == 0 && kSpan % rows_at_once == 0, "");
     const T *p, *anchor;  // the thread's element of the next tile; an address that stands in where nothing is read
     long long round, stride;
     // from: the strip's first channel at the CTA's first position; round: elements between its tiles
@@ -87,7 +91,7 @@ template <typename T, int CP> struct Loader {
         : p(from + (threadIdx.x / per_row) * row + (threadIdx.x % per_row) * elems), anchor(base), round(round_),
           stride(rows_at_once * row) {}
     // rows: valid positions of the tile; width: valid channels of the strip
-    __device__ __forceinline__ void next(Tile<T, CP> &tile, int rows, int width) {
+    __device__ __forceinline__ void next(Tile<T, CP, R> &tile, int rows, int width) {
         const int r0 = threadIdx.x / per_row, c = (threadIdx.x % per_row) * elems, left = width - c;
         const int bytes = left <= 0 ? 0 : left >= elems ? CP : left * (int)sizeof(T);
         T *to = &tile.v[r0][c];
@@ -95,26 +99,26 @@ template <typename T, int CP> struct Loader {
 #pragma unroll
         for (int k = 0; k < kSpan; k += rows_at_once, from += stride) {
             const bool valid = r0 + k < rows && bytes > 0;
-            copy_async<CP>(to + k * kWidth<T>, valid ? from : anchor, valid ? bytes : 0);
+            copy_async<CP>(to + k * kWidth<T, R>, valid ? from : anchor, valid ? bytes : 0);
         }
         p += round;
     }
 };
-template <typename T> struct Loader<T, 2> {
+template <typename T, int R> struct Loader<T, 2, R> {
     // A thread copies word k of every eighth row, whose offset is the same in all of them, and the first
     // 64 threads the last word of one row each.
-    static constexpr int per_row = kWidth<T> / 2, rows_at_once = kThreads<T> / per_row;
-    static_assert(rows_at_once % 2 == 0 && kSpan <= kThreads<T>, "");
+    static constexpr int per_row = kWidth<T, R> / 2, rows_at_once = kThreads<T, R> / per_row;
+    static_assert(rows_at_once % 2 == 0 && kSpan <= kThreads<T, R>, "");
     const T *p, *anchor;  // the strip's first channel of the next tile's first row; the tensor's first element
     long long round, row;
     int first, step;
     __device__ __forceinline__ Loader(const T *base, const T *from, long long row_, long long round_)
         : p(from), anchor(base), round(round_), row(row_), first((int)(reinterpret_cast<uintptr_t>(from) >> 1 & 1)),
           step((int)(row_ & 1)) {}
-    __device__ __forceinline__ void next(Tile<T, 2> &tile, int rows, int width) {
+    __device__ __forceinline__ void next(Tile<T, 2, R> &tile, int rows, int width) {
         if (threadIdx.x == 0) tile.first = first, tile.step = step;
         const void *none = reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(anchor) + 2 & ~(uintptr_t)3);
-        const int have = min(width, kWidth<T>);
+        const int have = min(width, kWidth<T, R>);
         {
             const int r0 = threadIdx.x / per_row, k = threadIdx.x % per_row;
             const int c = 2 * k - ((first + r0 * step) & 1);  // the word's first channel; -1: the element before the strip
@@ -127,12 +131,12 @@ template <typename T> struct Loader<T, 2> {
                 if (j == 0 && from < anchor) {  // before the tensor: its first element alone
                     *to = valid ? (uint32_t)*reinterpret_cast<const uint16_t *>(from + 1) << 16 : 0u;
                 } else {
-                    copy_async<4>(to + j * Tile<T, 2>::words, valid ? from : none, valid ? bytes : 0);
+                    copy_async<4>(to + j * Tile<T, 2, R>::words, valid ? from : none, valid ? bytes : 0);
                 }
             }
         }
         if (threadIdx.x < kSpan) {
-            const int r = threadIdx.x, c = kWidth<T> - ((first + r * step) & 1);
+            const int r = threadIdx.x, c = kWidth<T, R> - ((first + r * step) & 1);
             const bool valid = r < rows && c < have;
             copy_async<4>(&tile.w[r][per_row], valid ? p + r * row + c : none, valid ? 2 : 0);
         }
@@ -189,10 +193,10 @@ __device__ __forceinline__ Map load_map(const ulonglong2 *p) {
 }
 __device__ __forceinline__ void store_map(ulonglong2 *p, const Map &m) { *p = make_ulonglong2(m.a.q, m.u.q); }
 
-template <typename T> struct Maps {
-    ulonglong2 slot[kSlots][kLanes<T>];          // this round's maps,
-    unsigned long long start[kSlots][kLanes<T>];  // and the state that reaches each slot
-    ulonglong2 cta[2][kMaxCluster][kLanes<T>];   // the CTAs' maps of this round and the next,
+template <typename T, int R> struct Maps {
+    ulonglong2 slot[kSlots][kLanes<T, R>];          // this round's maps,
+    unsigned long long start[kSlots][kLanes<T, R>];  // and the state that reaches each slot
+    ulonglong2 cta[2][kMaxCluster][kLanes<T, R>];   // the CTAs' maps of this round and the next,
     unsigned long long arrived[2];               // and the mbarriers that count their bytes
 };
 
@@ -245,8 +249,8 @@ struct Chain {
 // Runs carry (the state before the round) through the round: start[] of every slot, and carry after
 // the whole cluster's round.  By the kLanes threads of one slot, between two barriers; `lane` is the
 // thread's place among them.  BACKWARD: the last slot and CTA come first.
-template <typename T, bool BACKWARD>
-__device__ __forceinline__ void run_chain(Maps<T> &sh, int lane, Pair &carry) {
+template <typename T, int R, bool BACKWARD>
+__device__ __forceinline__ void run_chain(Maps<T, R> &sh, int lane, Pair &carry) {
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
         const int slot = BACKWARD ? kSlots - 1 - i : i;
@@ -258,14 +262,14 @@ __device__ __forceinline__ void run_chain(Maps<T> &sh, int lane, Pair &carry) {
 //
 // Two buffers are enough: a CTA pushes the maps of round k + 2 after it has those of round k + 1 from
 // all, and each of them pushed those after it had read the maps of round k.
-template <typename T, bool BACKWARD>
-__device__ __forceinline__ void run_cluster(Maps<T> &sh, int lane, int parity, int cluster, int rank, Chain &chain) {
+template <typename T, int R, bool BACKWARD>
+__device__ __forceinline__ void run_cluster(Maps<T, R> &sh, int lane, int parity, int cluster, int rank, Chain &chain) {
     Map all = load_map(&sh.slot[BACKWARD ? kSlots - 1 : 0][lane]);
 #pragma unroll
     for (int i = 1; i < kSlots; ++i) all = all.then(load_map(&sh.slot[BACKWARD ? kSlots - 1 - i : i][lane]));
     const unsigned bar = shared_address(&sh.arrived[parity]), place = shared_address(&sh.cta[parity][rank][lane]);
     if (lane == 0)
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(cluster * kLanes<T> * 16) : "memory");
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(cluster * kLanes<T, R> * 16) : "memory");
     for (int r = 0; r < cluster; ++r)
         asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
                          remote_address(place, r)),
@@ -280,23 +284,23 @@ __device__ __forceinline__ void run_cluster(Maps<T> &sh, int lane, int parity, i
         if (r == rank) mine = chain.state;
         chain.state = load_map(&sh.cta[parity][r][lane]).of(chain.state);
     }
-    run_chain<T, BACKWARD>(sh, lane, mine);
+    run_chain<T, R, BACKWARD>(sh, lane, mine);
 }
 // One round's exchange: from the maps in sh.slot to the states in sh.start.  Threads below kLanes hold
 // the chain.  `beside`: work of another slot's threads, between the barriers.
-template <typename T, bool BACKWARD, typename F>
-__device__ __forceinline__ void exchange(Maps<T> &sh, int parity, int cluster, int rank, Chain &chain, F beside) {
+template <typename T, int R, bool BACKWARD, typename F>
+__device__ __forceinline__ void exchange(Maps<T, R> &sh, int parity, int cluster, int rank, Chain &chain, F beside) {
     __syncthreads();
-    if (threadIdx.x < kLanes<T>) {
-        if (cluster == 1) run_chain<T, BACKWARD>(sh, threadIdx.x, chain.state);
-        else run_cluster<T, BACKWARD>(sh, threadIdx.x, parity, cluster, rank, chain);
+    if (threadIdx.x < kLanes<T, R>) {
+        if (cluster == 1) run_chain<T, R, BACKWARD>(sh, threadIdx.x, chain.state);
+        else run_cluster<T, R, BACKWARD>(sh, threadIdx.x, parity, cluster, rank, chain);
     } else {
         beside();
     }
     __syncthreads();
 }
 // Before the first round: the cluster's mbarriers are ready, and every CTA's shared memory is there.
-template <typename T> __device__ __forceinline__ void start_cluster(Maps<T> &sh) {
+template <typename T, int R> __device__ __forceinline__ void start_cluster(Maps<T, R> &sh) {
     if (threadIdx.x == 0) {
         for (int b = 0; b < 2; ++b) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_address(&sh.arrived[b])) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -305,9 +309,9 @@ template <typename T> __device__ __forceinline__ void start_cluster(Maps<T> &sh)
 }
 
 // A round of a segment's reduction: the leading slot appends the round's maps to whole.
-template <typename T, bool BACKWARD> __device__ __forceinline__ void reduce_round(Maps<T> &sh, Map &whole) {
+template <typename T, int R, bool BACKWARD> __device__ __forceinline__ void reduce_round(Maps<T, R> &sh, Map &whole) {
     __syncthreads();
-    if (threadIdx.x < kLanes<T>) {
+    if (threadIdx.x < kLanes<T, R>) {
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) whole = whole.then(load_map(&sh.slot[BACKWARD ? kSlots - 1 - i : i][threadIdx.x]));
     }
@@ -316,16 +320,16 @@ template <typename T, bool BACKWARD> __device__ __forceinline__ void reduce_roun
 
 // State that the segments before (after, if BACKWARD) this one leave, from chain (of the leading
 // slot): their maps are folded by the slots in parallel, then as in a round.
-template <typename T, bool BACKWARD>
-__device__ __forceinline__ void fold_segments(const ulonglong2 *maps, int first, int last, Maps<T> &sh, int slot, int lane,
+template <typename T, int R, bool BACKWARD>
+__device__ __forceinline__ void fold_segments(const ulonglong2 *maps, int first, int last, Maps<T, R> &sh, int slot, int lane,
                                               Chain &chain) {
     const int count = last - first, per = (count + kSlots - 1) / kSlots;
     Map mine = identity();
     const int place = BACKWARD ? kSlots - 1 - slot : slot;
     for (int i = place * per; i < min((place + 1) * per, count); ++i)
-        mine = mine.then(load_map(maps + (long long)(BACKWARD ? last - 1 - i : first + i) * kLanes<T> + lane));
+        mine = mine.then(load_map(maps + (long long)(BACKWARD ? last - 1 - i : first + i) * kLanes<T, R> + lane));
     store_map(&sh.slot[slot][lane], mine);
-    exchange<T, BACKWARD>(sh, 0, 1, 0, chain, [] {});
+    exchange<T, R, BACKWARD>(sh, 0, 1, 0, chain, [] {});
 }
 
 struct Place {
@@ -333,7 +337,7 @@ struct Place {
     int width;                   // channels that the thread has (2, fewer at the end, or <= 0)
     long long unit;              // (b * strips + strip) * segments
 };
-template <typename T> __device__ __forceinline__ Place place_of(const ScanArgs &a, const TokenPlan &p, int lane) {
+template <typename T, int R> __device__ __forceinline__ Place place_of(const ScanArgs &a, const TokenPlan &p, int lane) {
     Place s;
     s.rank = blockIdx.x % p.cluster;
     unsigned i = blockIdx.x / p.cluster;
@@ -342,7 +346,7 @@ template <typename T> __device__ __forceinline__ Place place_of(const ScanArgs &
     s.unit = (long long)i * p.segments;
     const int strip = i % p.strips;
     s.b = i / p.strips;
-    s.c0 = strip * kWidth<T>;
+    s.c0 = strip * kWidth<T, R>;
     s.c = s.c0 + lane * 2;
     s.width = a.C - s.c;
     s.n = scan_length(a.lengths, s.b, a.T);
@@ -350,8 +354,8 @@ template <typename T> __device__ __forceinline__ Place place_of(const ScanArgs &
 }
 
 // Gates of a thread's positions; those at or past `live` hold the state (a = 1, b = 0).
-template <typename T, int CP>
-__device__ __forceinline__ void read_gates(const Tile<T, CP> &tile, int slot, int lane, Pair bias, int live, Pair (&av)[kSteps],
+template <typename T, int CP, int R>
+__device__ __forceinline__ void read_gates(const Tile<T, CP, R> &tile, int slot, int lane, Pair bias, int live, Pair (&av)[kSteps],
                                            Pair (&bv)[kSteps]) {
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
@@ -367,28 +371,28 @@ __device__ __forceinline__ void read_gates(const Tile<T, CP> &tile, int slot, in
 
 // ---------------------------------------------------------------------------------------- forward
 
-template <typename T, int CP> struct ForwardShared {
-    Tile<T, CP> x[2], g[2];
-    Maps<T> maps;
+template <typename T, int CP, int R> struct ForwardShared {
+    Tile<T, CP, R> x[2], g[2];
+    Maps<T, R> maps;
 };
 
 // CP: bytes of a copy; PAIRED: the outputs' rows allow stores of two channels
-template <typename T, int CP, bool PAIRED, Mode MODE>
-__global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(const ScanArgs a, const TokenPlan p, ulonglong2 *maps) {
+template <typename T, int CP, int R, bool PAIRED, Mode MODE>
+__global__ void __launch_bounds__(kThreads<T, R>, kForwardPerSm<R>) scan_tokens_forward_kernel(const ScanArgs a, const TokenPlan p, ulonglong2 *maps) {
     extern __shared__ __align__(16) unsigned char raw[];
     begin_kernel();
-    ForwardShared<T, CP> &sh = *reinterpret_cast<ForwardShared<T, CP> *>(raw);
-    const int lane = threadIdx.x % kLanes<T>, slot = threadIdx.x / kLanes<T>;
-    const Place s = place_of<T>(a, p, lane);
+    ForwardShared<T, CP, R> &sh = *reinterpret_cast<ForwardShared<T, CP, R> *>(raw);
+    const int lane = threadIdx.x % kLanes<T, R>, slot = threadIdx.x / kLanes<T, R>;
+    const Place s = place_of<T, R>(a, p, lane);
     const int round_span = p.cluster * kSpan, rounds = (a.T + round_span - 1) / round_span;
     const int round0 = s.seg * p.rounds_per, round1 = min(round0 + p.rounds_per, rounds);
     int t0 = round0 * round_span + s.rank * kSpan;  // the CTA's first position of the round
-    Loader<T, CP> x(static_cast<const T *>(a.x.p), static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c0 + t0 * a.x.row, a.x.row, round_span * a.x.row);
-    Loader<T, CP> g(static_cast<const T *>(a.gate.p), static_cast<const T *>(a.gate.p) + s.b * a.gate.batch + s.c0 + t0 * a.gate.row, a.gate.row,
+    Loader<T, CP, R> x(static_cast<const T *>(a.x.p), static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c0 + t0 * a.x.row, a.x.row, round_span * a.x.row);
+    Loader<T, CP, R> g(static_cast<const T *>(a.gate.p), static_cast<const T *>(a.gate.p) + s.b * a.gate.batch + s.c0 + t0 * a.gate.row, a.gate.row,
                     round_span * a.gate.row);
     T *y = static_cast<T *>(a.y.p) + s.b * a.y.batch + s.c + (t0 + slot * kSteps) * a.y.row;
     const long long y_round = round_span * a.y.row;
-    const bool whole_strip = PAIRED && s.c0 + kWidth<T> <= a.C;
+    const bool whole_strip = PAIRED && s.c0 + kWidth<T, R> <= a.C;
     int ahead = t0;  // first position of the next tiles to fetch
     const auto fetch = [&](int buf) {
         x.next(sh.x[buf], s.n - ahead, a.C - s.c0);
@@ -406,7 +410,7 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
     Map whole = identity();
     if constexpr (MODE == kApply) {
         if (a.h0 != nullptr) chain.state = load_two(a.h0 + (long long)s.b * a.C + s.c, s.width);
-        if (s.seg > 0) fold_segments<T, false>(maps + s.unit * kLanes<T>, 0, s.seg, sh.maps, slot, lane, chain);
+        if (s.seg > 0) fold_segments<T, R, false>(maps + s.unit * kLanes<T, R>, 0, s.seg, sh.maps, slot, lane, chain);
     }
     wait_copies<1>();
     if (p.cluster > 1) start_cluster(sh.maps);
@@ -427,10 +431,10 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
         // the exchange's barriers end all reading of this round's tiles and show the next's
         wait_copies<0>();
         if constexpr (MODE == kReduce) {
-            reduce_round<T, false>(sh.maps, whole);
+            reduce_round<T, R, false>(sh.maps, whole);
             if (round + 2 < live1) fetch(round & 1);
         } else {
-            exchange<T, false>(sh.maps, round & 1, p.cluster, s.rank, chain, [] {});
+            exchange<T, R, false>(sh.maps, round & 1, p.cluster, s.rank, chain, [] {});
             if (round + 2 < live1) fetch(round & 1);
             Pair h;
             h.q = sh.maps.start[slot][lane];
@@ -464,7 +468,7 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
         }
     }
     if constexpr (MODE == kReduce) {
-        if (slot == 0) store_map(maps + (s.unit + s.seg) * kLanes<T> + lane, whole);
+        if (slot == 0) store_map(maps + (s.unit + s.seg) * kLanes<T, R> + lane, whole);
     } else if (a.h_last != nullptr && s.seg == p.segments - 1 && s.rank == 0 && slot == 0) {
         store_state(a.h_last + (long long)s.b * a.C + s.c, chain.state, s.width);
     }
@@ -472,35 +476,35 @@ __global__ void __launch_bounds__(kThreads<T>, 4) scan_tokens_forward_kernel(con
 
 // --------------------------------------------------------------------------------------- backward
 
-template <typename T, int CP> struct BackwardShared {
-    Tile<T, CP> x[2], g[2], dy[2];
-    Maps<T> maps;
+template <typename T, int CP, int R> struct BackwardShared {
+    Tile<T, CP, R> x[2], g[2], dy[2];
+    Maps<T, R> maps;
     // h within the CTA's positions, from the kept state: as slot and start of Maps
-    ulonglong2 forward[kSlots][kLanes<T>];
-    unsigned long long forward_start[kSlots][kLanes<T>];
+    ulonglong2 forward[kSlots][kLanes<T, R>];
+    unsigned long long forward_start[kSlots][kLanes<T, R>];
 };
 
 // bias_part: one float per (unit, segment, rank, channel of the strip)
-template <typename T, int CP, bool PAIRED, Mode MODE>
-__global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
+template <typename T, int CP, int R, bool PAIRED, Mode MODE>
+__global__ void __launch_bounds__(kThreads<T, R>, sizeof(T) == 4 ? kBackwardPerSm<R> * 3 / 2 : kBackwardPerSm<R>)
     scan_tokens_backward_kernel(const ScanArgs a, const TokenPlan p, ulonglong2 *maps, float *bias_part) {
     extern __shared__ __align__(16) unsigned char raw[];
     begin_kernel();
-    BackwardShared<T, CP> &sh = *reinterpret_cast<BackwardShared<T, CP> *>(raw);
-    const int lane = threadIdx.x % kLanes<T>, slot = threadIdx.x / kLanes<T>;
-    const Place s = place_of<T>(a, p, lane);
+    BackwardShared<T, CP, R> &sh = *reinterpret_cast<BackwardShared<T, CP, R> *>(raw);
+    const int lane = threadIdx.x % kLanes<T, R>, slot = threadIdx.x / kLanes<T, R>;
+    const Place s = place_of<T, R>(a, p, lane);
     const int round_span = p.cluster * kSpan, rounds = (a.T + round_span - 1) / round_span;
     const int round0 = s.seg * p.rounds_per, round1 = min(round0 + p.rounds_per, rounds);
     // the rounds past the length come first: no gradient passes them, dx and d_gate are 0
     const int live1 = max(round0, min(round1, (s.n + round_span - 1) / round_span));
     int t0 = (live1 - 1) * round_span + s.rank * kSpan;
-    Loader<T, CP> x(static_cast<const T *>(a.x.p), static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c0 + t0 * a.x.row, a.x.row, -round_span * a.x.row);
-    Loader<T, CP> g(static_cast<const T *>(a.gate.p), static_cast<const T *>(a.gate.p) + s.b * a.gate.batch + s.c0 + t0 * a.gate.row, a.gate.row,
+    Loader<T, CP, R> x(static_cast<const T *>(a.x.p), static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c0 + t0 * a.x.row, a.x.row, -round_span * a.x.row);
+    Loader<T, CP, R> g(static_cast<const T *>(a.gate.p), static_cast<const T *>(a.gate.p) + s.b * a.gate.batch + s.c0 + t0 * a.gate.row, a.gate.row,
                     -round_span * a.gate.row);
-    Loader<T, CP> dy(static_cast<const T *>(a.dy.p), static_cast<const T *>(a.dy.p) + s.b * a.dy.batch + s.c0 + t0 * a.dy.row, a.dy.row, -round_span * a.dy.row);
+    Loader<T, CP, R> dy(static_cast<const T *>(a.dy.p), static_cast<const T *>(a.dy.p) + s.b * a.dy.batch + s.c0 + t0 * a.dy.row, a.dy.row, -round_span * a.dy.row);
     T *dx = static_cast<T *>(a.dx.p) + s.b * a.dx.batch + s.c + (t0 + slot * kSteps + kSteps - 1) * a.dx.row;
     T *dg = static_cast<T *>(a.d_gate.p) + s.b * a.d_gate.batch + s.c + (t0 + slot * kSteps + kSteps - 1) * a.d_gate.row;
-    const bool whole_strip = PAIRED && s.c0 + kWidth<T> <= a.C;
+    const bool whole_strip = PAIRED && s.c0 + kWidth<T, R> <= a.C;
     int ahead = t0;  // first position of the next tiles to fetch, towards the beginning
     const auto fetch = [&](int buf) {
         g.next(sh.g[buf], s.n - ahead, a.C - s.c0);
@@ -532,12 +536,13 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
         if (at < a.T)
             next_kept = load_two(a.states_in + ((long long)s.b * a.keep + at / WTCONV_SCAN_KEEP) * a.C + s.c, s.width);
     };
-    const bool runs_h = threadIdx.x - 32u < (unsigned)kLanes<T>;  // a slot's threads in the second warp
+    // the slot that runs h: in another warp than the leading one, if there is one
+    const bool runs_h = slot == (kThreads<T, R> > 32 ? 32 / kLanes<T, R> : 1);
     if constexpr (MODE == kApply) {
         if (round0 < live1 && runs_h) kept_state(t0);
         if (a.dh_last != nullptr) chain.state = load_two(a.dh_last + (long long)s.b * a.C + s.c, s.width);
         if (s.seg < p.segments - 1)
-            fold_segments<T, true>(maps + s.unit * kLanes<T>, s.seg + 1, p.segments, sh.maps, slot, lane, chain);
+            fold_segments<T, R, true>(maps + s.unit * kLanes<T, R>, s.seg + 1, p.segments, sh.maps, slot, lane, chain);
     }
     wait_copies<1>();
     if (p.cluster > 1) start_cluster(sh.maps);
@@ -558,7 +563,7 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
         store_map(&sh.maps.slot[slot][lane], back);
         if constexpr (MODE == kReduce) {
             wait_copies<0>();
-            reduce_round<T, true>(sh.maps, whole);
+            reduce_round<T, R, true>(sh.maps, whole);
             if (round - 2 >= round0) fetch(buf);
         } else {
             // h is scanned forward within the CTA's positions from the kept state; dh comes backward
@@ -567,7 +572,7 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
             for (int j = 0; j < kSteps; ++j) fwd.u = fma(av[j], fwd.u, mul(bv[j], xv[j].wide()));
             store_map(&sh.forward[slot][lane], fwd);
             wait_copies<0>();
-            exchange<T, true>(sh.maps, buf, p.cluster, s.rank, chain, [&] {
+            exchange<T, R, true>(sh.maps, buf, p.cluster, s.rank, chain, [&] {
                 if (!runs_h) return;
                 Pair h = next_kept;
 #pragma unroll
@@ -617,17 +622,17 @@ __global__ void __launch_bounds__(kThreads<T>, sizeof(T) == 4 ? 3 : 2)
         t0 -= round_span;
     }
     if constexpr (MODE == kReduce) {
-        if (slot == 0) store_map(maps + (s.unit + s.seg) * kLanes<T> + lane, whole);
+        if (slot == 0) store_map(maps + (s.unit + s.seg) * kLanes<T, R> + lane, whole);
     } else {
         if (a.d_h0 != nullptr && s.seg == 0 && s.rank == 0 && slot == 0)
             store_state(a.d_h0 + (long long)s.b * a.C + s.c, chain.state, s.width);
         __syncthreads();
         Pair *sums = reinterpret_cast<Pair *>(sh.forward);
-        sums[slot * kLanes<T> + lane] = sum;
+        sums[slot * kLanes<T, R> + lane] = sum;
         __syncthreads();
         if (slot == 0) {
-            for (int i = 1; i < kSlots; ++i) sum = add(sum, sums[i * kLanes<T> + lane]);
-            float *to = bias_part + ((s.unit + s.seg) * p.cluster + s.rank) * kWidth<T> + lane * 2;
+            for (int i = 1; i < kSlots; ++i) sum = add(sum, sums[i * kLanes<T, R> + lane]);
+            float *to = bias_part + ((s.unit + s.seg) * p.cluster + s.rank) * kWidth<T, R> + lane * 2;
             to[0] = sum.lo(), to[1] = sum.hi();
         }
     }
@@ -656,17 +661,26 @@ __global__ void __launch_bounds__(256) scan_tokens_bias_kernel(const float *part
     }
 }
 
-// Chains (strips of sequences) are shared by clusters as large as `per_sm` CTAs on every SM allow (one
-// more doubling left a second, mostly idle wave: 8x4096x1024 bf16 forward 70 us against 58); where
-// even full clusters give less than one CTA to every second SM, sequences are cut into segments.
-TokenPlan plan_of(const ScanArgs &a, int per_sm) {
+// Rows of 32 bytes where that takes at most two thirds of the lanes (104x40909x5 fp16 forward 634 us
+// with 128, 271 with 32; 64x8192x24 and wider do as well with either).
+int row_bytes(const ScanArgs &a) {
+    const long long wide = 128 / elem_bytes_of(a.dtype), slim = wide / 4;
+    return (a.C + slim - 1) / slim * slim * 3 <= (a.C + wide - 1) / wide * wide * 2 ? 32 : 128;
+}
+
+// Chains (strips of sequences) are shared by clusters as large as the CTAs that fit the GPU allow (one
+// more doubling left a second, mostly idle wave: 8x4096x1024 bf16 forward 70 us against 67).  Where even
+// full clusters make less than half of those, sequences are cut into segments: 1x10634x1158 fp16 forward,
+// 19 chains, took 76 us in clusters and 52 in segments; 2x30730x303, 10 chains, forward + backward 561
+// and 194.
+TokenPlan plan_of(const ScanArgs &a, bool backward) {
     TokenPlan p;
-    const int width = kRowBytes / elem_bytes_of(a.dtype);
+    const int row = row_bytes(a), width = row / elem_bytes_of(a.dtype), per_sm = (backward ? 2 : 4) * 128 / row;
     p.strips = (a.C + width - 1) / width;
-    const long long sms = sm_count(), chains = (long long)a.B * p.strips, want = per_sm * sms;
+    const long long chains = (long long)a.B * p.strips, want = (long long)per_sm * sm_count();
     const int rounds = (a.T + kSpan - 1) / kSpan;
     p.cluster = p.segments = 1;
-    if (chains * kMaxCluster * 2 >= sms) {
+    if (chains * kMaxCluster * 2 >= want || rounds <= kMaxCluster) {
         while (p.cluster < kMaxCluster && chains * p.cluster * 2 <= want && p.cluster < rounds) p.cluster *= 2;
     } else {
         p.segments = (int)((want + chains - 1) / chains);
@@ -677,15 +691,14 @@ TokenPlan plan_of(const ScanArgs &a, int per_sm) {
     p.segments = (cluster_rounds + p.rounds_per - 1) / p.rounds_per;
     return p;
 }
-constexpr int kForwardPerSm = 4, kBackwardPerSm = 2;
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 size_t map_bytes(const ScanArgs &a, const TokenPlan &p) {
-    const size_t lanes = kRowBytes / elem_bytes_of(a.dtype) / 2;
+    const size_t lanes = row_bytes(a) / elem_bytes_of(a.dtype) / 2;
     return p.segments > 1 ? round256((size_t)a.B * p.strips * p.segments * lanes * sizeof(ulonglong2)) : 0;
 }
 size_t part_bytes(const ScanArgs &a, const TokenPlan &p) {
-    return round256((size_t)a.B * p.strips * p.segments * p.cluster * (kRowBytes / elem_bytes_of(a.dtype)) * sizeof(float));
+    return round256((size_t)a.B * p.strips * p.segments * p.cluster * (row_bytes(a) / elem_bytes_of(a.dtype)) * sizeof(float));
 }
 
 template <typename... P, typename... A>
@@ -703,28 +716,28 @@ bool rows_at(const ScanTensor &s, const ScanArgs &a, int bytes) {
     return aligned_to(s.p, bytes) && (a.B == 1 || s.batch % per == 0) && (a.T == 1 || s.row % per == 0);
 }
 
-template <typename T, int CP, bool PAIRED> cudaError_t forward_typed(const ScanArgs &a, cudaStream_t st) {
-    const TokenPlan p = plan_of(a, kForwardPerSm);
-    const size_t shared = sizeof(ForwardShared<T, CP>);
+template <typename T, int CP, int R, bool PAIRED> cudaError_t forward_typed(const ScanArgs &a, cudaStream_t st) {
+    const TokenPlan p = plan_of(a, false);
+    const size_t shared = sizeof(ForwardShared<T, CP, R>);
     ulonglong2 *maps = static_cast<ulonglong2 *>(a.workspace);
     if (p.segments > 1) {
-        const cudaError_t e = launch(scan_tokens_forward_kernel<T, CP, PAIRED, kReduce>, kThreads<T>, shared, a, p, st, maps);
+        const cudaError_t e = launch(scan_tokens_forward_kernel<T, CP, R, PAIRED, kReduce>, kThreads<T, R>, shared, a, p, st, maps);
         if (e != cudaSuccess) return e;
     }
-    return launch(scan_tokens_forward_kernel<T, CP, PAIRED, kApply>, kThreads<T>, shared, a, p, st, maps);
+    return launch(scan_tokens_forward_kernel<T, CP, R, PAIRED, kApply>, kThreads<T, R>, shared, a, p, st, maps);
 }
 
-template <typename T, int CP, bool PAIRED> cudaError_t backward_typed(const ScanArgs &a, cudaStream_t st) {
-    const TokenPlan p = plan_of(a, kBackwardPerSm);
-    const size_t shared = sizeof(BackwardShared<T, CP>);
+template <typename T, int CP, int R, bool PAIRED> cudaError_t backward_typed(const ScanArgs &a, cudaStream_t st) {
+    const TokenPlan p = plan_of(a, true);
+    const size_t shared = sizeof(BackwardShared<T, CP, R>);
     ulonglong2 *maps = static_cast<ulonglong2 *>(a.workspace);
     float *part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + map_bytes(a, p));
     cudaError_t e = cudaSuccess;
-    if (p.segments > 1) e = launch(scan_tokens_backward_kernel<T, CP, PAIRED, kReduce>, kThreads<T>, shared, a, p, st, maps, part);
-    if (e == cudaSuccess) e = launch(scan_tokens_backward_kernel<T, CP, PAIRED, kApply>, kThreads<T>, shared, a, p, st, maps, part);
+    if (p.segments > 1) e = launch(scan_tokens_backward_kernel<T, CP, R, PAIRED, kReduce>, kThreads<T, R>, shared, a, p, st, maps, part);
+    if (e == cudaSuccess) e = launch(scan_tokens_backward_kernel<T, CP, R, PAIRED, kApply>, kThreads<T, R>, shared, a, p, st, maps, part);
     if (e != cudaSuccess) return e;
     return launch_kernel(scan_tokens_bias_kernel, (a.C + 31) / 32, 256, 0, st, 1, part, a.d_gate_bias, a.B, a.C, p.strips,
-                         p.segments * p.cluster, kWidth<T>);
+                         p.segments * p.cluster, kWidth<T, R>);
 }
 
 // How wide rows can be copied in, and whether outputs can be stored two channels at a time.  The
@@ -743,15 +756,21 @@ cudaError_t by_access(const ScanArgs &a, std::initializer_list<const ScanTensor 
 }
 template <typename T> constexpr int kNarrowest = sizeof(T) == 4 ? 4 : 2;
 
+template <typename T, int R> cudaError_t forward_rows(const ScanArgs &a, cudaStream_t st) {
+    return by_access<T>(a, {&a.x, &a.gate}, {&a.y}, [&] { return forward_typed<T, 16, R, true>(a, st); },
+                        [&] { return forward_typed<T, 4, R, true>(a, st); },
+                        [&] { return forward_typed<T, kNarrowest<T>, R, false>(a, st); });
+}
+template <typename T, int R> cudaError_t backward_rows(const ScanArgs &a, cudaStream_t st) {
+    return by_access<T>(a, {&a.x, &a.gate, &a.dy}, {&a.dx, &a.d_gate}, [&] { return backward_typed<T, 16, R, true>(a, st); },
+                        [&] { return backward_typed<T, 4, R, true>(a, st); },
+                        [&] { return backward_typed<T, kNarrowest<T>, R, false>(a, st); });
+}
 template <typename T> cudaError_t forward_any(const ScanArgs &a, cudaStream_t st) {
-    return by_access<T>(a, {&a.x, &a.gate}, {&a.y}, [&] { return forward_typed<T, 16, true>(a, st); },
-                        [&] { return forward_typed<T, 4, true>(a, st); },
-                        [&] { return forward_typed<T, kNarrowest<T>, false>(a, st); });
+    return row_bytes(a) == 32 ? forward_rows<T, 32>(a, st) : forward_rows<T, 128>(a, st);
 }
 template <typename T> cudaError_t backward_any(const ScanArgs &a, cudaStream_t st) {
-    return by_access<T>(a, {&a.x, &a.gate, &a.dy}, {&a.dx, &a.d_gate}, [&] { return backward_typed<T, 16, true>(a, st); },
-                        [&] { return backward_typed<T, 4, true>(a, st); },
-                        [&] { return backward_typed<T, kNarrowest<T>, false>(a, st); });
+    return row_bytes(a) == 32 ? backward_rows<T, 32>(a, st) : backward_rows<T, 128>(a, st);
 }
 
 // ------------------------------------------------------------------------------------------- step
@@ -783,7 +802,7 @@ cudaError_t take_scan_timeout(int *raised) {
 
 size_t scan_tokens_workspace(int op, const ScanArgs &a) {
     const bool back = op == WTCONV_SCAN_OP_BACKWARD;
-    const TokenPlan p = plan_of(a, back ? kBackwardPerSm : kForwardPerSm);
+    const TokenPlan p = plan_of(a, back);
     return map_bytes(a, p) + (back ? part_bytes(a, p) : 0);
 }
 
