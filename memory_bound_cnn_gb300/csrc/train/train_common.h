@@ -35,18 +35,22 @@ inline int sm_count() {
 
 // Lets a kernel have `shared` bytes of dynamic shared memory on the current device.  Asked of the
 // runtime once per kernel and device: it takes a microsecond.
-template <typename... P> cudaError_t allow_shared(void (*kernel)(P...), size_t shared) {
+template <typename... P> cudaError_t allow_shared(void (*kernel)(P...), size_t shared) noexcept {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    static std::mutex lock;
-    static std::map<std::pair<void (*)(P...), int>, size_t> allowed;
-    std::lock_guard<std::mutex> guard(lock);
-    size_t &have = allowed[{kernel, dev}];
-    if (have >= shared) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
-    if (e == cudaSuccess) have = shared;
-    return e;
+    try {
+        static std::mutex lock;
+        static std::map<std::pair<void (*)(P...), int>, size_t> allowed;
+        std::lock_guard<std::mutex> guard(lock);
+        size_t &have = allowed[{kernel, dev}];
+        if (have >= shared) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+        if (e == cudaSuccess) have = shared;
+        return e;
+    } catch (...) {  // no memory for the entry: nothing leaves through the C entry point
+        return cudaErrorMemoryAllocation;
+    }
 }
 
 // Launches a kernel that may be set up while the one before it on the stream still runs: every kernel

@@ -71,7 +71,7 @@ class AdamW:
             raise ValueError("no parameters")
         if state_bits not in (32, 8):
             raise ValueError(f"state_bits must be 32 or 8, not {state_bits}")
-        self.state_bits, self.count = state_bits, int(count)
+        self.state_bits, self.count, self.lr = state_bits, int(count), lr
         self.device = self.params[0].device
         n = len(self.params)
         self._tensors = (OptimTensor * n)()
@@ -147,13 +147,12 @@ class AdamW:
 
     def step(self, clip=None, lr=None, count=None, stream=None) -> None:
         """One update of every parameter.  clip: what ``grad_norm`` returned (a factor that is not
-        finite leaves everything as it is).  count: the step's number, from 1 (default: the next)."""
+        finite leaves everything as it is).  lr: the rate from this step on.  count: the step's number, from 1 (default: the next)."""
         config = self._config
-        if lr is not None:
-            config.lr = lr
+        config.lr = self.lr if lr is None else lr
         config.step = self.count + 1 if count is None else count
         self._ext.adamw_step(len(self.params), self._table, self._scalars, self.device, clip, stream)
-        self.count = config.step
+        self.count, self.lr = config.step, config.lr
 
     def state_values(self, m_out=None, v_out=None, stream=None):
         """The averages (m, v) as lists of fp32 tensors: the states themselves in 32 bits, else what

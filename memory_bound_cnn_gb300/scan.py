@@ -87,7 +87,8 @@ class WTConvScanFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, gate, gate_bias, h0, lengths, layout):
-        y, h_last, states = wtconv_scan_forward(x, gate, gate_bias, h0, lengths, layout, keep_states=True)
+        y, h_last, states = wtconv_scan_forward(x, gate, gate_bias, h0, lengths, layout,
+                                                keep_states=any(ctx.needs_input_grad))
         ctx.save_for_backward(x, gate, gate_bias, states, lengths)
         ctx.layout, ctx.has_h0 = layout, h0 is not None
         ctx.set_materialize_grads(False)

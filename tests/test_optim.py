@@ -426,6 +426,7 @@ def test_binding_refuses_on_the_gpu():
         opt.step(count=0)
     with pytest.raises(W.WTConvError):
         opt.step(lr=-1.0)
+    assert opt.lr == 1e-3
     with pytest.raises(ValueError, match="clip"):
         opt.step(clip=torch.ones(1, device="cuda"))
     with pytest.raises(W.WTConvError):

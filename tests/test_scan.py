@@ -441,3 +441,38 @@ def test_shared_sequences(dtype, B, C, T):
     d = make(B, T, C, "tokens", dtype, seed=17, lengths=lengths)
     check(run(d, "tokens"), reference(d, "tokens"), "tokens", dtype)
     assert S.wtconv_scan_status() == W.OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["planes", "tokens"])
+def test_given_stream_and_workspace(layout):
+    """An explicit stream and a caller's scratch of the size that is asked for, larger or misplaced."""
+    d = make(2, 5000, 8, layout, torch.bfloat16, seed=18)
+    want = run(d, layout)
+    dims = (2, 5000, 8, {"planes": 0, "tokens": 1}[layout], 1)
+    ws = [torch.empty(S.wtconv_scan_workspace_size(op, *dims) + 64, dtype=torch.uint8, device="cuda") for op in (0, 1)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y, h, states = S.wtconv_scan_forward(d["x"], d["gate"], d["gate_bias"], d["h0"], None, layout, True, workspace=ws[0],
+                                         stream=side)
+    dx, dg, db, dh0 = S.wtconv_scan_backward(d["x"], d["gate"], d["gate_bias"], states, d["dy"], d["dh_last"], None, layout,
+                                             workspace=ws[1], stream=side)
+    side.synchronize()
+    for k, t in (("y", y), ("h_last", h), ("states", states), ("dx", dx), ("d_gate", dg), ("d_gate_bias", db), ("d_h0", dh0)):
+        assert torch.equal(t, want[k]), k
+    with pytest.raises(ValueError, match="workspace"):
+        S.wtconv_scan_forward(d["x"], d["gate"], d["gate_bias"], layout=layout, workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    if ws[1].numel() > 64:
+        with pytest.raises(W.WTConvError):
+            S.wtconv_scan_backward(d["x"], d["gate"], d["gate_bias"], states, d["dy"], layout=layout, workspace=ws[1][8:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["planes", "tokens"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("C", [4, 5, 12, 16, 17, 31, 67])
+def test_few_channels_and_long_sequences(C, dtype, layout):
+    """Narrow strips of tokens, segments of long rows, ragged ends in each of them."""
+    T = 3000 + C
+    d = make(3, T, C, layout, dtype, seed=C, lengths=[T, 1777, 63])
+    check(run(d, layout), reference(d, layout), layout, dtype)
