@@ -206,6 +206,28 @@ Tensor scan_step(const Tensor &x, const Tensor &gate, const Tensor &gate_bias, c
 
 const wtconv_optim_tensor *table(uintptr_t address) { return reinterpret_cast<const wtconv_optim_tensor *>(address); }
 
+// Checks one tensor per descriptor and writes its address into the field at `offset`.  The tensor has
+// one element for every `per` of the parameter's (which `params` sets the number of); None is allowed
+// where `optional` says so.
+void fill_field(int n, uintptr_t tensors, const std::vector<optional<Tensor>> &ts, size_t offset, at::ScalarType dtype, int64_t per,
+                const c10::Device &dev, const std::string &name, bool params, bool may_be_none) {
+    if ((int)ts.size() != n) refuse(std::to_string(ts.size()) + " tensors in " + name + " for " + std::to_string(n) + " parameters");
+    wtconv_optim_tensor *const list = reinterpret_cast<wtconv_optim_tensor *>(tensors);
+    for (int i = 0; i < n; ++i) {
+        const optional<Tensor> &t = ts[i];
+        if (!t.has_value() && may_be_none) continue;
+        const int64_t want = params && t.has_value() ? t->numel() : (list[i].n + per - 1) / per;
+        if (!t.has_value() || !t->is_cuda() || t->device() != dev || t->scalar_type() != dtype || t->numel() != want || !t->is_contiguous())
+            refuse(name + "[" + std::to_string(i) + "] must be a contiguous " + c10::toString(dtype) + " tensor of " +
+                   std::to_string(want) + " elements on " + dev.str());
+    }
+    for (int i = 0; i < n; ++i) {  // (only once all of them are right)
+        if (!ts[i].has_value()) continue;
+        if (params) list[i].n = ts[i]->numel();
+        *reinterpret_cast<void **>(reinterpret_cast<char *>(&list[i]) + offset) = ts[i]->data_ptr();
+    }
+}
+
 Tensor grad_norm(int n, uintptr_t tensors, int grad_dtype, const c10::Device &dev, double max_norm, const optional<Tensor> &out_given,
                  const optional<Tensor> &workspace, size_t workspace_bytes, const py::object &stream) {
     const Tensor out = out_given.has_value() ? *out_given : empty({2}, at::kFloat, dev);
@@ -254,6 +276,7 @@ PYBIND11_MODULE(_binding, m) {
     m.def("scan_forward", &scan_forward);
     m.def("scan_backward", &scan_backward);
     m.def("scan_step", &scan_step);
+    m.def("fill_field", &fill_field);
     m.def("grad_norm", &grad_norm);
     m.def("adamw_step", &adamw_step);
     m.def("state_values", &state_values);

@@ -2,7 +2,9 @@
 //
 // One CTA per chunk of 2048 elements of one tensor, one warp per 256 of them (a block of the 8-bit
 // states), eight elements per lane in registers between the one read and the one write of each
-// array.  Bound by HBM.
+// array.  With 32-bit states the step runs at the rate of a copy (100 M elements with bf16 gradients and
+// a bf16 copy, 28 bytes each: 409 us, 6.8 TB/s).  With 8-bit states it is bound by the issue of
+// instructions (102 an element at 77 % of the issue slots; 130 M elements 451 us, 4.6 TB/s).
 #include <cooperative_groups.h>
 #include <float.h>
 
@@ -354,7 +356,8 @@ template <typename V> __device__ __forceinline__ V block_sum(V v, V *scratch) { 
     return v;
 }
 
-// Sum of squares of g[first..last), by the CTA: sixteen bytes a load, four loads in flight.
+// Sum of squares of g[first..last), by the CTA: sixteen bytes a load, four loads in flight (130 M fp32
+// elements 94 us, 5.5 TB/s, bound by HBM; with one load in flight and a search per chunk 114).
 template <typename G> __device__ __forceinline__ float squares(const G *g, long long first, long long last) {
     constexpr int per = 16 / sizeof(G);
     float mine[4] = {0.f, 0.f, 0.f, 0.f};

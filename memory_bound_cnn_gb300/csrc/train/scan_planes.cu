@@ -1,17 +1,24 @@
 // Gated scan of planes [B][C][T] (time contiguous).
 //
-// A lane owns 32 consecutive bytes of a row (16 or 8 positions), a warp 1024 (a span).  A stretch of the recurrence is
-// the map h -> a h + u, and such maps compose (Span).  A lane takes its two halves as the two lanes of
-// packed fp32 arithmetic (one instruction for both), joins their maps, and the warp scans the lanes'
-// maps by shuffles; every lane then runs its positions again from the state that reaches it.  x, gate and (backward) dy are read once and everything stays in registers.  The backward
-// finds h again by the same scan over the few lanes between two kept states.
+// A lane owns 32 consecutive bytes of a row (16 or 8 positions), a warp 1024 (a span).  A stretch of the
+// recurrence is the map h -> a h + u, and such maps compose (Span).  A lane takes its two halves as the
+// two lanes of packed fp32 arithmetic (one instruction for both), joins their maps, and the warp scans
+// the lanes' maps by shuffles; every lane then runs its positions again from the state that reaches it.
+// The backward finds h again by the same scan over the few lanes between two kept states.  x, gate and
+// (backward) dy are read once, through a ring of asynchronous copies that each warp keeps for itself
+// (Cell): a queue in registers left the backward of 16-bit planes 72 registers too many.
 //
 // Rows of one span or less: several rows share a warp (scan_short_*).  Longer rows: the warps of a CTA
 // take neighbouring spans of one row in rounds, exchange their maps through shared memory (one barrier
-// a round) and carry the state in a register (scan_planes_*); the next round's loads are issued before
-// the barrier.  Few, long rows do not fill the GPU that way: they are cut into segments, a first kernel
-// reduces each segment to its map, and the scan of a segment starts from the maps before it (after it,
-// backward).  That reads two of the inputs twice, the second time mostly from L2.
+// a round) and carry the state in a register (scan_planes_*).  Few, long rows do not fill the GPU that
+// way: they are cut into segments, a first kernel reduces each segment to its map, and the scan of a
+// segment starts from the maps before it (after it, backward).  That reads two of the inputs twice, the
+// second time mostly from L2.
+//
+// Bound by HBM, closely followed by the issue of instructions (25 an element forward, 34 backward, at
+// 65 % and 51 % of the issue slots).  Alone, with cold caches: 16x64x65536 bf16 forward 74 us (5.4 TB/s,
+// 81 % of a copy), backward 129 us (5.2 TB/s, 78 %); 64x96x3136 fp32 48 us (72 %) and 74 us (78 %).
+// With eight positions a lane the shuffles and the exchange weighed twice as much (83 and 146 us).
 #include "scan_device.cuh"
 
 namespace wtconv {
@@ -25,6 +32,7 @@ template <typename T> constexpr int kWarpSpan = 32 * kLane<T>;                  
 template <typename T> constexpr int kKeepLanes = WTCONV_SCAN_KEEP / kLane<T>;   // lanes between two kept states
 
 enum Mode { kReduce, kApply };
+
 // A lane's positions as raw words; pair j holds positions j and kHalf<T> + j.
 template <typename T> struct Strip {
     static constexpr int words = kLane<T> * (int)sizeof(T) / 4;

@@ -1,8 +1,8 @@
 // Gated scan of tokens [B][T][C] (channels contiguous): one CTA per strip of channels of a sequence,
 // or a cluster of CTAs along its time.
 //
-// A strip is 128 bytes of every row (32 where there are few channels), a round 64 positions of it, brought into shared memory by
-// asynchronous copies two rounds ahead.  A thread owns two neighbouring channels (packed fp32
+// A strip is 128 bytes of every row (32 where there are few channels), a round 64 positions of it,
+// brought into shared memory by asynchronous copies two rounds ahead.  A thread owns two neighbouring channels (packed fp32
 // arithmetic: one instruction for both) and eight consecutive positions, which it reduces to the map
 // h -> a h + u of the state before them; the threads of a position group (a slot: a warp of 16-bit
 // strips, half a warp of fp32 ones) cover the strip.  The slots leave their maps in shared memory, one
@@ -14,8 +14,14 @@
 // CTAs of a cluster share one: in a round CTA r takes the r-th 64 positions and pushes its map into the
 // shared memory of all, where it counts towards an mbarrier; when that has all of a round's maps, each
 // CTA folds those before its own.  (A cluster barrier instead waits for every thread of every CTA, and
-// its release for the outputs of the round before: 8x4096x1024 bf16 forward 61 us, 56 so.)  Where even that leaves most SMs idle, the sequence is cut into segments whose maps
-// a first kernel reduces (reading two inputs twice, the second time mostly from L2).
+// its release for the outputs of the round before: 8x4096x1024 bf16 forward 61 us, 54 so.)  Where even
+// that leaves most SMs idle, the sequence is cut into segments whose maps a first kernel reduces
+// (reading two inputs twice, the second time mostly from L2).
+//
+// Bound by the latency of a round's exchange and, after it, by the issue of instructions (25 an element
+// forward, 34 backward): the four (backward two) CTAs that fit an SM overlap their rounds only so far.
+// Alone, with cold caches: 32x2048x768 bf16 ragged forward 59 us (5.1 TB/s, 77 % of a copy, padding
+// counted), 8x4096x1024 bf16 forward 54 us and backward 92 us (3.7 TB/s, 55 %).
 #include <cooperative_groups.h>
 
 #include <initializer_list>

@@ -75,19 +75,15 @@ class AdamW:
         self.device = self.params[0].device
         n = len(self.params)
         self._tensors = (OptimTensor * n)()
-        for k, p in enumerate(self.params):
-            self._check(p, f"params[{k}]", torch.float32, p.numel())
-            self._tensors[k].param, self._tensors[k].n = p.data_ptr(), p.numel()
+        self._ext = load_binding()
+        self._table = ctypes.addressof(self._tensors)
+        self._fill("param", self.params, torch.float32, "params", params=True)
         self.copies = [None] * n if copies is None else list(copies)
-        if len(self.copies) != n:
-            raise ValueError(f"{len(self.copies)} copies for {n} parameters")
         kinds = {c.dtype for c in self.copies if c is not None}
         if len(kinds) > 1 or kinds - {torch.bfloat16, torch.float16}:
             raise ValueError(f"copies must all be bf16 or all fp16, not {kinds}")
-        for k, c in enumerate(self.copies):
-            if c is not None:
-                self._check(c, f"copies[{k}]", c.dtype, self.params[k].numel())
-                self._tensors[k].copy = c.data_ptr()
+        copy_dtype = kinds.pop() if kinds else torch.bfloat16
+        self._fill("copy", self.copies, copy_dtype, "copies", may_be_none=True)
         if states is None:
             states = self._new_states()
         self.states = {name: list(ts) for name, ts in states.items()}
@@ -95,20 +91,14 @@ class AdamW:
         if set(self.states) != set(want):
             raise ValueError(f"states hold {sorted(self.states)}, expected {sorted(want)}")
         for name, (dtype, per) in want.items():
-            if len(self.states[name]) != n:
-                raise ValueError(f"{len(self.states[name])} states {name} for {n} parameters")
-            for k, t in enumerate(self.states[name]):
-                self._check(t, f"states[{name!r}][{k}]", dtype, -(-self.params[k].numel() // per))
-                setattr(self._tensors[k], name, t.data_ptr())
-        copy_dtype = DTYPE_CODE[kinds.pop()] if kinds else 0
-        self._config = AdamWConfig(lr, betas[0], betas[1], eps, weight_decay, 0, state_bits, 0, copy_dtype)
-        self._ext = load_binding()
-        self._table, self._scalars = ctypes.addressof(self._tensors), ctypes.addressof(self._config)
+            self._fill(name, self.states[name], dtype, f"states[{name!r}]", per)
+        self._config = AdamWConfig(lr, betas[0], betas[1], eps, weight_decay, 0, state_bits, 0, DTYPE_CODE[copy_dtype])
+        self._scalars = ctypes.addressof(self._config)
         self.set_grads(grads)
 
-    def _check(self, t, name, dtype, numel):
-        if not t.is_cuda or t.device != self.device or t.dtype != dtype or t.numel() != numel or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements on {self.device}")
+    def _fill(self, field, tensors, dtype, name, per=1, params=False, may_be_none=False):
+        self._ext.fill_field(len(self.params), self._table, tensors, getattr(OptimTensor, field).offset, dtype, per, self.device,
+                             name, params, may_be_none)
 
     def _state_layout(self):
         if self.state_bits == 32:
@@ -128,10 +118,7 @@ class AdamW:
         dtype = grads[0].dtype
         if dtype not in DTYPE_CODE:
             raise ValueError(f"gradients have unsupported dtype {dtype}")
-        for k, g in enumerate(grads):
-            self._check(g, f"grads[{k}]", dtype, self.params[k].numel())
-        for k, g in enumerate(grads):
-            self._tensors[k].grad = g.data_ptr()
+        self._fill("grad", grads, dtype, "grads")
         self.grads = grads
         self._config.grad_dtype = DTYPE_CODE[dtype]
         self._norm_bytes = _load().wtconv_grad_norm_workspace_size(len(self.params), self._tensors)
@@ -147,7 +134,8 @@ class AdamW:
 
     def step(self, clip=None, lr=None, count=None, stream=None) -> None:
         """One update of every parameter.  clip: what ``grad_norm`` returned (a factor that is not
-        finite leaves everything as it is).  lr: the rate from this step on.  count: the step's number, from 1 (default: the next)."""
+        finite leaves everything as it is).  lr: the rate from this step on.  count: the step's
+        number, from 1 (default: the next).  A captured graph replays this step's number."""
         config = self._config
         config.lr = self.lr if lr is None else lr
         config.step = self.count + 1 if count is None else count

@@ -421,7 +421,11 @@ def test_binding_refuses_on_the_gpu():
         O.AdamW([p], [g], states={"m": [p]})
     with pytest.raises(ValueError, match=r"states\['m'\]"):
         O.AdamW([p], [g], state_bits=8, states={k: [p] for k in ("m", "v", "m_max", "v_max")})
-    opt = O.AdamW([p], [g])
+    opt = O.AdamW([p, p.clone()], [g, g.clone()])
+    before = bytes(opt._tensors)
+    with pytest.raises(ValueError, match=r"grads\[1\]"):  # a refused list leaves the old one in place
+        opt.set_grads([g.clone(), g[:4]])
+    assert bytes(opt._tensors) == before
     with pytest.raises(W.WTConvError):
         opt.step(count=0)
     with pytest.raises(W.WTConvError):
