@@ -38,8 +38,9 @@ int norm_blocks(long long chunks);
 template <int CAP> cudaError_t launch_adamw(const TensorTable<CAP> &table, const StepScalars &s, const float *clip, cudaStream_t st);
 template <int CAP>
 cudaError_t launch_norm_part(const TensorTable<CAP> &table, int grad_dtype, double *part, int blocks, cudaStream_t st);
-// The whole norm in one launch, for one table of at most kSmallNorm chunks: twenty tensors of 190 K
-// elements, norm and step, take 13.0 us a pass with two launches for the norm, 11.8 with one.
+// The whole norm in one launch, for one table of at most kSmallNorm chunks: 255 fp32 tensors of 1500
+// elements 7.5 us with one launch, 300 of them 8.0 with two; one tensor of 522,240 elements 5.5 us with
+// one, of 524,289 6.7 with two.
 constexpr int kSmallNorm = 256;
 template <int CAP>
 cudaError_t launch_norm_small(const TensorTable<CAP> &table, int grad_dtype, double max_norm, float *out, cudaStream_t st);

@@ -287,6 +287,28 @@ def test_norm(sizes, grad, odd):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("grad", DTYPES, ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("odd", [0, 1])
+@pytest.mark.parametrize("sizes", [[1], [7] * 20, [8, 31, 33, 255, 257, 1023, 1025, 2047, 2048, 2049, 4095], [2048 * 256],
+                                   [2049] * 120, [1500] * 256, [1500] * 257], ids=lambda s: f"{len(s)}x{s[0]}")
+def test_norm_of_few_chunks(sizes, grad, odd):
+    """One launch (up to 256 chunks of 2048 elements) sums what 64 bits do, wherever chunks end.  A
+    lane rounds 16 products and 2 sums before it moves to fp64, half of which reaches the root, and
+    the root is rounded once."""
+    g = torch.Generator().manual_seed(len(sizes))
+    flat = [torch.randn(n + odd, generator=g).to(grad).cuda() for n in sizes]
+    grads = [f[odd:] for f in flat]
+    opt = O.AdamW([torch.zeros(n, device="cuda") for n in sizes], grads)
+    want = float(np.sqrt(sum((t.double() ** 2).sum().item() for t in grads)))
+    got = float(opt.grad_norm()[0])
+    assert abs(got - want) <= (18 / 2 + 1) * 2.0**-24 * want
+    for i in {0, len(sizes) // 2, len(sizes) - 1}:  # the last element counts
+        grads[i][-1] = 1000.0
+    want = float(np.sqrt(sum((t.double() ** 2).sum().item() for t in grads)))
+    assert abs(float(opt.grad_norm()[0]) - want) <= (18 / 2 + 1) * 2.0**-24 * want
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 1e25])
 @pytest.mark.parametrize("bits", [32, 8])
 def test_a_step_without_a_norm_changes_nothing(bad, bits):
