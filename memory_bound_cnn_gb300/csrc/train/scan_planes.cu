@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, sizeof(T) == 4 ? 6 : 4)
     float next_kept = kept_at(t0 + lane * kLane<T>);
     const Pair bias(-kLog2E * a.gate_bias[s.c]);
 
-    float carry = 0.f;  // a dh of the position after this round
+    float carry = 0.f;  // a dh of the position after the round
     Pair sum(0.f);
     Span whole = {1.f, 0.f};
     if (MODE == kApply) {

@@ -200,9 +200,9 @@ __device__ __forceinline__ Map load_map(const ulonglong2 *p) {
 __device__ __forceinline__ void store_map(ulonglong2 *p, const Map &m) { *p = make_ulonglong2(m.a.q, m.u.q); }
 
 template <typename T, int R> struct Maps {
-    ulonglong2 slot[kSlots][kLanes<T, R>];          // this round's maps,
+    ulonglong2 slot[kSlots][kLanes<T, R>];          // a round's maps,
     unsigned long long start[kSlots][kLanes<T, R>];  // and the state that reaches each slot
-    ulonglong2 cta[2][kMaxCluster][kLanes<T, R>];   // the CTAs' maps of this round and the next,
+    ulonglong2 cta[2][kMaxCluster][kLanes<T, R>];   // the CTAs' maps of a round and the next,
     unsigned long long arrived[2];               // and the mbarriers that count their bytes
 };
 
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kThreads<T, R>, kForwardPerSm<R>) scan_tokens_
             mine = mine.then({av[j], uv[j]});
         }
         store_map(&sh.maps.slot[slot][lane], mine);
-        // the exchange's barriers end all reading of this round's tiles and show the next's
+        // the exchange's barriers end all reading of a round's tiles and show the next's
         wait_copies<0>();
         if constexpr (MODE == kReduce) {
             reduce_round<T, R, false>(sh.maps, whole);
