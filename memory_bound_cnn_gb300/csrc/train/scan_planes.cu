@@ -135,9 +135,10 @@ template <typename T> struct Cell {
 #pragma unroll
                 for (int k = 0; k < bytes / (32 * CP); ++k) copy_async<CP>(at((k * 32 + lane) * CP), from + k * 32 * CP, CP);
             } else {
+                const int have = max(valid, 0) * (int)sizeof(T);  // (valid may be as low as -2^30)
 #pragma unroll
                 for (int k = 0; k < bytes / (32 * CP); ++k) {
-                    const int left = min(max(valid * (int)sizeof(T) - (k * 32 + lane) * CP, 0), CP);
+                    const int left = min(max(have - (k * 32 + lane) * CP, 0), CP);
                     copy_async<CP>(at((k * 32 + lane) * CP), left > 0 ? from + k * 32 * CP : base, left);
                 }
             }
