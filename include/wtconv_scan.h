@@ -56,10 +56,16 @@ size_t wtconv_scan_workspace_size(int op, int B, int T, int C, int layout, int d
 
 /* Device-side status of the scans run so far on the current device.  The CTAs of a cluster that share
  * a sequence wait for one another's part of a round, each time at most half a second; a wait that
- * gives up (never expected) raises a sticky flag, and what follows of that sequence comes out as NaN.
+ * gives up (never expected) raises a sticky flag, and what follows of that sequence comes out as NaN
+ * (the others that share it give up too, within half a second).
  * Synchronises the device; WTCONV_ERR_DEVICE_TIMEOUT if the flag was raised (and clears it),
  * WTCONV_ERR_CUDA if the synchronisation or the read failed, else WTCONV_OK. */
 int wtconv_scan_status(void);
+
+/* Diagnostic of that failure path, with no fault: one thread waits for an arrival that never comes.
+ * The wait gives up after half a second, so the next wtconv_scan_status() returns
+ * WTCONV_ERR_DEVICE_TIMEOUT (and clears it). */
+int wtconv_scan_selftest_wait_timeout(wtconv_stream_t stream);
 
 /* y and the optional outputs h_last [B][C] and states (NULL: not wanted).  h0 NULL: zeros.
  * lengths NULL: every sequence has T positions. */

@@ -32,6 +32,8 @@ cudaError_t launch_scan_planes_forward(const ScanArgs &a, cudaStream_t st);
 cudaError_t launch_scan_planes_backward(const ScanArgs &a, cudaStream_t st);
 // whether a bounded wait gave up on the current device since the last call; clears it
 cudaError_t take_scan_timeout(int *raised);
+// a bounded wait that gives up
+cudaError_t launch_scan_wait_selftest(cudaStream_t st);
 size_t scan_tokens_workspace(int op, const ScanArgs &a);
 cudaError_t launch_scan_tokens_forward(const ScanArgs &a, cudaStream_t st);
 cudaError_t launch_scan_tokens_backward(const ScanArgs &a, cudaStream_t st);

@@ -68,6 +68,10 @@ int wtconv_scan_status(void) {
     return raised ? WTCONV_ERR_DEVICE_TIMEOUT : WTCONV_OK;
 }
 
+int wtconv_scan_selftest_wait_timeout(wtconv_stream_t stream) {
+    return status_of(launch_scan_wait_selftest(reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int wtconv_scan_forward(int B, int T, int C, int layout, int dtype, const void *x, long long x_batch, long long x_row,
                         const void *gate, long long gate_batch, long long gate_row, const float *gate_bias,
                         const float *h0, const int *lengths, void *y, long long y_batch, long long y_row,

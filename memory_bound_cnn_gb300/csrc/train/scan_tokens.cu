@@ -267,22 +267,26 @@ __device__ __forceinline__ void run_chain(Maps<T, R> &sh, int lane, Pair &carry)
 // The CTA's map to every CTA of the cluster, then the state through the maps of all.
 //
 // Two buffers are enough: a CTA pushes the maps of round k + 2 after it has those of round k + 1 from
-// all, and each of them pushed those after it had read the maps of round k.
+// all, and each of them pushed those after it had read the maps of round k.  A thread that gave up takes
+// no further part (its bytes would count towards a phase that is not over, and an arrival would be one
+// too many), so the others give up in the same round or the next: all of a strip's later results are NaN.
 template <typename T, int R, bool BACKWARD>
 __device__ __forceinline__ void run_cluster(Maps<T, R> &sh, int lane, int parity, int cluster, int rank, Chain &chain) {
     Map all = load_map(&sh.slot[BACKWARD ? kSlots - 1 : 0][lane]);
 #pragma unroll
     for (int i = 1; i < kSlots; ++i) all = all.then(load_map(&sh.slot[BACKWARD ? kSlots - 1 - i : i][lane]));
-    const unsigned bar = shared_address(&sh.arrived[parity]), place = shared_address(&sh.cta[parity][rank][lane]);
-    if (lane == 0)
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(cluster * kLanes<T, R> * 16) : "memory");
-    for (int r = 0; r < cluster; ++r)
-        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
-                         remote_address(place, r)),
-                     "r"((unsigned)all.a.q), "r"((unsigned)(all.a.q >> 32)), "r"((unsigned)all.u.q),
-                     "r"((unsigned)(all.u.q >> 32)), "r"(remote_address(bar, r)) : "memory");
-    if (!chain.broken) chain.broken = !wait_phase(bar, chain.phases >> parity & 1);
-    chain.phases ^= 1u << parity;
+    if (!chain.broken) {
+        const unsigned bar = shared_address(&sh.arrived[parity]), place = shared_address(&sh.cta[parity][rank][lane]);
+        if (lane == 0)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(cluster * kLanes<T, R> * 16) : "memory");
+        for (int r = 0; r < cluster; ++r)
+            asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                             remote_address(place, r)),
+                         "r"((unsigned)all.a.q), "r"((unsigned)(all.a.q >> 32)), "r"((unsigned)all.u.q),
+                         "r"((unsigned)(all.u.q >> 32)), "r"(remote_address(bar, r)) : "memory");
+        chain.broken = !wait_phase(bar, chain.phases >> parity & 1);
+        chain.phases ^= 1u << parity;
+    }
     if (chain.broken) chain.state = Pair(__int_as_float(0x7fc00000));
     Pair mine = chain.state;
     for (int i = 0; i < cluster; ++i) {
@@ -291,6 +295,13 @@ __device__ __forceinline__ void run_cluster(Maps<T, R> &sh, int lane, int parity
         chain.state = load_map(&sh.cta[parity][r][lane]).of(chain.state);
     }
     run_chain<T, R, BACKWARD>(sh, lane, mine);
+}
+// Last of all in a kernel with clusters.  Where every wait ended well, every push to this CTA has arrived.
+// After one that gave up pushes may still be under way: the thread keeps the CTA, and so its shared
+// memory, until all other threads of the cluster have come here too or have exited.
+__device__ __forceinline__ void leave_cluster(const Chain &chain) {
+    if (chain.broken)
+        asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 // One round's exchange: from the maps in sh.slot to the states in sh.start.  Threads below kLanes hold
 // the chain.  `beside`: work of another slot's threads, between the barriers.
@@ -478,6 +489,7 @@ __global__ void __launch_bounds__(kThreads<T, R>, kForwardPerSm<R>) scan_tokens_
     } else if (a.h_last != nullptr && s.seg == p.segments - 1 && s.rank == 0 && slot == 0) {
         store_state(a.h_last + (long long)s.b * a.C + s.c, chain.state, s.width);
     }
+    leave_cluster(chain);
 }
 
 // --------------------------------------------------------------------------------------- backward
@@ -642,6 +654,7 @@ __global__ void __launch_bounds__(kThreads<T, R>, sizeof(T) == 4 ? kBackwardPerS
             to[0] = sum.lo(), to[1] = sum.hi();
         }
     }
+    leave_cluster(chain);
 }
 
 // d_gate_bias_c = sum of the parts over sequences, segments and ranks, in a fixed order.
@@ -779,6 +792,15 @@ template <typename T> cudaError_t backward_any(const ScanArgs &a, cudaStream_t s
     return row_bytes(a) == 32 ? backward_rows<T, 32>(a, st) : backward_rows<T, 128>(a, st);
 }
 
+// Diagnostic: a wait for an arrival that never comes.
+__global__ void __launch_bounds__(32) scan_wait_selftest_kernel() {
+    __shared__ unsigned long long bar;
+    begin_kernel();
+    if (threadIdx.x != 0) return;
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_address(&bar)) : "memory");
+    wait_phase(shared_address(&bar), 0);
+}
+
 // ------------------------------------------------------------------------------------------- step
 
 template <typename T>
@@ -805,6 +827,8 @@ cudaError_t take_scan_timeout(int *raised) {
     const int zero = 0;
     return e != cudaSuccess || *raised == 0 ? e : cudaMemcpyToSymbol(g_scan_timeout, &zero, sizeof(int));
 }
+
+cudaError_t launch_scan_wait_selftest(cudaStream_t st) { return launch_kernel(scan_wait_selftest_kernel, 1, 32, 0, st, 1); }
 
 size_t scan_tokens_workspace(int op, const ScanArgs &a) {
     const bool back = op == WTCONV_SCAN_OP_BACKWARD;

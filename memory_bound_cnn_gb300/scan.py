@@ -12,12 +12,13 @@ import ctypes
 
 import torch
 
-from .wtconv import load, load_binding
+from .wtconv import _raise, _stream, load, load_binding
 
 SCAN_KEEP = 64  # WTCONV_SCAN_KEEP
 OP_SCAN_FORWARD, OP_SCAN_BACKWARD = 0, 1
 
-EXPORTED = ("wtconv_scan_workspace_size", "wtconv_scan_status", "wtconv_scan_forward", "wtconv_scan_backward", "wtconv_scan_step")
+EXPORTED = ("wtconv_scan_workspace_size", "wtconv_scan_status", "wtconv_scan_selftest_wait_timeout", "wtconv_scan_forward",
+            "wtconv_scan_backward", "wtconv_scan_step")
 
 _lib = _ext = None
 
@@ -39,6 +40,8 @@ def _load() -> ctypes.CDLL:
         lib.wtconv_scan_workspace_size.argtypes = [i] * 6
         lib.wtconv_scan_status.restype = i
         lib.wtconv_scan_status.argtypes = []
+        lib.wtconv_scan_selftest_wait_timeout.restype = i
+        lib.wtconv_scan_selftest_wait_timeout.argtypes = [vp]
         lib.wtconv_scan_forward.restype = i
         lib.wtconv_scan_forward.argtypes = [i] * 5 + act * 2 + [vp] * 3 + act + [vp, vp, vp, sz, vp]
         lib.wtconv_scan_backward.restype = i
@@ -56,6 +59,12 @@ def wtconv_scan_workspace_size(op: int, B: int, T: int, C: int, layout: int, dty
 def wtconv_scan_status() -> int:
     """Synchronise the device; wtconv.ERR_DEVICE_TIMEOUT if a scan's bounded wait gave up."""
     return _load().wtconv_scan_status()
+
+
+def wtconv_scan_selftest_wait_timeout(stream=None) -> None:
+    """Launch the diagnostic whose one bounded wait is never completed: the next
+    wtconv_scan_status() then returns wtconv.ERR_DEVICE_TIMEOUT."""
+    _raise(_load().wtconv_scan_selftest_wait_timeout(_stream(stream)), "wtconv_scan_selftest_wait_timeout")
 
 
 def wtconv_scan_forward(x, gate, gate_bias, h0=None, lengths=None, layout="planes", keep_states=False, y=None,

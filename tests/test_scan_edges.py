@@ -3,8 +3,10 @@ import numpy as np
 import pytest
 import scan_reference as R
 import torch
+from test_scan import make, run
 
 from memory_bound_cnn_gb300 import scan as S
+from memory_bound_cnn_gb300 import wtconv as W
 
 
 @pytest.mark.gpu
@@ -30,3 +32,19 @@ def test_short_lengths_of_very_long_rows(extra):
     R.assert_near("h_last", h_last.double().cpu().numpy(), want_h)
     R.assert_near("d_h0", dh0.double().cpu().numpy(), want["d_h0"])
     R.assert_near("d_gate_bias", db.double().cpu().numpy(), want["d_gate_bias"], scale=want["abs"].max())
+
+
+@pytest.mark.gpu
+def test_a_wait_that_gives_up_is_reported_once():
+    """A bounded wait that nothing completes raises the flag; the host reads it once, and scans whose
+    sequences are shared by clusters go on as before."""
+    d = make(2, 1000, 512, "tokens", torch.bfloat16, seed=27)
+    before = run(d, "tokens")
+    assert S.wtconv_scan_status() == W.OK
+    S.wtconv_scan_selftest_wait_timeout()
+    assert S.wtconv_scan_status() == W.ERR_DEVICE_TIMEOUT
+    assert S.wtconv_scan_status() == W.OK
+    after = run(d, "tokens")
+    for k in before:
+        assert torch.equal(before[k], after[k]), k
+    assert S.wtconv_scan_status() == W.OK
