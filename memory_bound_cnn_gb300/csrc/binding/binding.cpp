@@ -3,6 +3,7 @@
 // on the current stream.  Compiled, because these calls are short: a decoding step takes 4.5 us of
 // host time here and took 23 us through ctypes.
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/extension.h>
@@ -41,13 +42,52 @@ std::string text(c10::IntArrayRef shape) {
     return s + ")";
 }
 
-// The caller's stream, or the tensors' device's current one.
-wtconv_stream_t stream_on(const py::object &stream, c10::Device device) {
-    if (stream.is_none()) return reinterpret_cast<wtconv_stream_t>(c10::cuda::getCurrentCUDAStream(device.index()).stream());
-    const py::object where = py::getattr(stream, "device", py::none());
-    if (!where.is_none() && py::cast<c10::Device>(where) != device) refuse("stream is on another device than the tensors");
-    return reinterpret_cast<wtconv_stream_t>(py::cast<uintptr_t>(stream.attr("cuda_stream")));
-}
+// Where a call runs: on the tensors' device, on its current stream or on the one that the caller gives.
+// There the call's scratch and new tensors are allocated under that stream, so that no other stream's
+// earlier or later use of their memory meets this one, and every tensor is recorded on the stream that it
+// does not belong to: memory that the caller lets go of is not used again before the work has ended.  (Not on
+// an ExternalStream, which may end before the tensors do: its owner keeps them.)
+class Call {
+  public:
+    Call(const py::object &stream, c10::Device device)
+        : device_(device), guard_(device), current_(c10::cuda::getCurrentCUDAStream(device.index())), stream_(current_) {
+        if (stream.is_none()) return;
+        const py::object where = py::getattr(stream, "device", py::none());
+        if (!where.is_none() && py::cast<c10::Device>(where) != device) refuse("stream is on another device than the tensors");
+        stream_ = c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(py::cast<uintptr_t>(stream.attr("cuda_stream"))),
+                                                   device.index());
+        if (stream_.stream() == current_.stream()) return;
+        under_.reset_stream(stream_);
+        const py::object cuda = py::module_::import("torch.cuda");
+        records_ = py::isinstance(stream, cuda.attr("Stream")) && !py::isinstance(stream, cuda.attr("ExternalStream"));
+    }
+    wtconv_stream_t stream() const { return reinterpret_cast<wtconv_stream_t>(stream_.stream()); }
+    // The caller's tensors that the work reads or writes.
+    template <typename... Ts> void uses(const Ts &...ts) const {
+        if (records_) (record(ts, stream_), ...);
+    }
+    // A new tensor that the caller gets.
+    Tensor empty(c10::IntArrayRef shape, at::ScalarType dtype) const {
+        Tensor t = at::detail::empty_cuda(shape, dtype, device_, c10::nullopt);
+        if (records_) record(t, current_);
+        return t;
+    }
+    // Scratch that ends with the call.
+    Tensor scratch(size_t bytes) const { return at::detail::empty_cuda({(int64_t)bytes}, at::kByte, device_, c10::nullopt); }
+
+  private:
+    static void record(const Tensor &t, const c10::cuda::CUDAStream &stream) {
+        c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), stream);
+    }
+    static void record(const optional<Tensor> &t, const c10::cuda::CUDAStream &stream) {
+        if (t.has_value()) record(*t, stream);
+    }
+    c10::Device device_;
+    c10::cuda::CUDAGuard guard_;
+    c10::cuda::OptionalCUDAStreamGuard under_;
+    c10::cuda::CUDAStream current_, stream_;
+    bool records_ = false;
+};
 
 // One activation of the scan as strides of its batch and row axes.
 struct Act {
@@ -92,24 +132,21 @@ V *array(const optional<Tensor> &t, const char *name, c10::IntArrayRef shape, c1
     return static_cast<V *>(t->data_ptr());
 }
 
-Tensor empty(c10::IntArrayRef shape, at::ScalarType dtype, c10::Device device) {
-    return at::detail::empty_cuda(shape, dtype, device, c10::nullopt);
-}
-
 // The caller's scratch or a new one of `need` bytes.
 struct Scratch {
     Tensor t;
     void *p = nullptr;
     size_t bytes = 0;
 };
-Scratch scratch(const optional<Tensor> &given, size_t need, c10::Device device) {
+Scratch scratch(const optional<Tensor> &given, size_t need, c10::Device device, const Call &call) {
     Scratch s;
     if (given.has_value()) {
         if (given->device() != device) refuse("workspace is on " + given->device().str() + ", the tensors on " + device.str());
         if (!given->is_contiguous()) refuse("workspace must be contiguous");
         s.t = *given;
+        call.uses(s.t);
     } else if (need > 0) {
-        s.t = empty({(int64_t)need}, at::kByte, device);
+        s.t = call.scratch(need);
     }
     if (s.t.defined()) s.p = s.t.data_ptr(), s.bytes = s.t.nbytes();
     return s;
@@ -133,16 +170,17 @@ py::tuple scan_forward(const Tensor &x, const Tensor &gate, const Tensor &gate_b
     const float *bias_p = array<float>(gate_bias, "gate_bias", {d.C}, dev);
     const float *h0_p = array<float>(h0, "h0", {d.B, d.C}, dev);
     const int *len_p = array<int>(lengths, "lengths", {d.B}, dev);
-    const Tensor y = y_given.has_value() ? *y_given : empty(x.sizes(), x.scalar_type(), dev);
+    const Call call(stream, dev);
+    const Tensor y = y_given.has_value() ? *y_given : call.empty(x.sizes(), x.scalar_type());
     const Act ay = activation(y, "y", planes, &x);
-    const Tensor h_last = empty({d.B, d.C}, at::kFloat, dev);
+    const Tensor h_last = call.empty({d.B, d.C}, at::kFloat);
     Tensor states;
-    if (keep_states) states = empty(states_shape(d), at::kFloat, dev);
-    const c10::cuda::CUDAGuard guard(dev);
-    const Scratch ws = scratch(workspace, wtconv_scan_workspace_size(WTCONV_SCAN_OP_FORWARD, d.B, d.T, d.C, d.layout, d.dtype), dev);
+    if (keep_states) states = call.empty(states_shape(d), at::kFloat);
+    const Scratch ws = scratch(workspace, wtconv_scan_workspace_size(WTCONV_SCAN_OP_FORWARD, d.B, d.T, d.C, d.layout, d.dtype), dev, call);
+    call.uses(x, gate, gate_bias, h0, lengths, y_given);
     check_status(wtconv_scan_forward(d.B, d.T, d.C, d.layout, d.dtype, ax.p, ax.batch, ax.row, ag.p, ag.batch, ag.row, bias_p,
                                      h0_p, len_p, ay.p, ay.batch, ay.row, h_last.data_ptr<float>(),
-                                     keep_states ? states.data_ptr<float>() : nullptr, ws.p, ws.bytes, stream_on(stream, dev)),
+                                     keep_states ? states.data_ptr<float>() : nullptr, ws.p, ws.bytes, call.stream()),
                  "wtconv_scan_forward");
     return py::make_tuple(y, h_last, keep_states ? py::cast(states) : py::none());
 }
@@ -160,16 +198,17 @@ py::tuple scan_backward(const Tensor &x, const Tensor &gate, const Tensor &gate_
     const float *states_p = array<float>(states, "states", states_shape(d), dev);
     const float *dh_p = array<float>(dh_last, "dh_last", {d.B, d.C}, dev);
     const int *len_p = array<int>(lengths, "lengths", {d.B}, dev);
-    const Tensor dx = dx_given.has_value() ? *dx_given : empty(x.sizes(), x.scalar_type(), dev);
-    const Tensor d_gate = d_gate_given.has_value() ? *d_gate_given : empty(x.sizes(), x.scalar_type(), dev);
+    const Call call(stream, dev);
+    const Tensor dx = dx_given.has_value() ? *dx_given : call.empty(x.sizes(), x.scalar_type());
+    const Tensor d_gate = d_gate_given.has_value() ? *d_gate_given : call.empty(x.sizes(), x.scalar_type());
     const Act adx = activation(dx, "dx", planes, &x), adg = activation(d_gate, "d_gate", planes, &x);
-    const Tensor d_bias = empty({d.C}, at::kFloat, dev), d_h0 = empty({d.B, d.C}, at::kFloat, dev);
-    const c10::cuda::CUDAGuard guard(dev);
-    const Scratch ws = scratch(workspace, wtconv_scan_workspace_size(WTCONV_SCAN_OP_BACKWARD, d.B, d.T, d.C, d.layout, d.dtype), dev);
+    const Tensor d_bias = call.empty({d.C}, at::kFloat), d_h0 = call.empty({d.B, d.C}, at::kFloat);
+    const Scratch ws = scratch(workspace, wtconv_scan_workspace_size(WTCONV_SCAN_OP_BACKWARD, d.B, d.T, d.C, d.layout, d.dtype), dev, call);
+    call.uses(x, gate, gate_bias, states, dy, dh_last, lengths, dx_given, d_gate_given);
     check_status(wtconv_scan_backward(d.B, d.T, d.C, d.layout, d.dtype, ax.p, ax.batch, ax.row, ag.p, ag.batch, ag.row, bias_p,
                                       states_p, len_p, ady.p, ady.batch, ady.row, dh_p, adx.p, adx.batch, adx.row, adg.p,
                                       adg.batch, adg.row, d_bias.data_ptr<float>(), d_h0.data_ptr<float>(), ws.p, ws.bytes,
-                                      stream_on(stream, dev)),
+                                      call.stream()),
                  "wtconv_scan_backward");
     return py::make_tuple(dx, d_gate, d_bias, d_h0);
 }
@@ -181,7 +220,8 @@ Tensor scan_step(const Tensor &x, const Tensor &gate, const Tensor &gate_bias, c
         refuse("x must be a non-empty (B, C) CUDA tensor of fp32, bf16 or fp16");
     const int64_t B = x.size(0), C = x.size(1);
     const c10::Device dev = x.device();
-    const Tensor y = y_given.has_value() ? *y_given : empty({B, C}, x.scalar_type(), dev);
+    const Call call(stream, dev);
+    const Tensor y = y_given.has_value() ? *y_given : call.empty({B, C}, x.scalar_type());
     const auto check = [&](const Tensor &t, const char *name) {
         if (t.sizes() != x.sizes() || t.scalar_type() != x.scalar_type() || t.device() != dev || (t.stride(1) != 1 && C > 1))
             refuse(std::string(name) + " must match x's shape, dtype and device and be contiguous along C");
@@ -192,10 +232,10 @@ Tensor scan_step(const Tensor &x, const Tensor &gate, const Tensor &gate_bias, c
     const float *bias_p = array<float>(gate_bias, "gate_bias", {C}, dev);
     float *pool_p = array<float>(pool, "pool", pool.sizes(), dev);
     const int *slots_p = array<int>(slots, "slots", {B}, dev);
-    const c10::cuda::CUDAGuard guard(dev);
+    call.uses(x, gate, gate_bias, pool, slots, y_given);
     check_status(wtconv_scan_step((int)B, (int)C, dtype_code(x.scalar_type()), x.data_ptr(), x.stride(0), gate.data_ptr(),
                                   gate.stride(0), bias_p, pool_p, (int)pool.size(0), slots_p, y.data_ptr(), y.stride(0),
-                                  stream_on(stream, dev)),
+                                  call.stream()),
                  "wtconv_scan_step");
     return y;
 }
@@ -230,12 +270,13 @@ void fill_field(int n, uintptr_t tensors, const std::vector<optional<Tensor>> &t
 
 Tensor grad_norm(int n, uintptr_t tensors, int grad_dtype, const c10::Device &dev, double max_norm, const optional<Tensor> &out_given,
                  const optional<Tensor> &workspace, size_t workspace_bytes, const py::object &stream) {
-    const Tensor out = out_given.has_value() ? *out_given : empty({2}, at::kFloat, dev);
+    const Call call(stream, dev);
+    const Tensor out = out_given.has_value() ? *out_given : call.empty({2}, at::kFloat);
     float *out_p = array<float>(out, "out", {2}, dev);
-    const c10::cuda::CUDAGuard guard(dev);
-    const Scratch ws = scratch(workspace, workspace_bytes, dev);
+    const Scratch ws = scratch(workspace, workspace_bytes, dev, call);
+    call.uses(out_given);
     // (scratch: none for few elements)
-    check_status(wtconv_grad_norm(n, table(tensors), grad_dtype, max_norm, out_p, ws.p, ws.bytes, stream_on(stream, dev)),
+    check_status(wtconv_grad_norm(n, table(tensors), grad_dtype, max_norm, out_p, ws.p, ws.bytes, call.stream()),
                  "wtconv_grad_norm");
     return out;
 }
@@ -243,14 +284,23 @@ Tensor grad_norm(int n, uintptr_t tensors, int grad_dtype, const c10::Device &de
 void adamw_step(int n, uintptr_t tensors, uintptr_t config, const c10::Device &dev, const optional<Tensor> &clip,
                 const py::object &stream) {
     const float *clip_p = array<float>(clip, "clip", {2}, dev);
-    const c10::cuda::CUDAGuard guard(dev);
+    const Call call(stream, dev);
+    call.uses(clip);
     check_status(wtconv_adamw_step(n, table(tensors), reinterpret_cast<const wtconv_adamw_config *>(config),
-                                   clip_p != nullptr ? clip_p + 1 : nullptr, stream_on(stream, dev)),
+                                   clip_p != nullptr ? clip_p + 1 : nullptr, call.stream()),
                  "wtconv_adamw_step");
 }
 
-void state_values(int n, uintptr_t tensors, const c10::Device &dev, const std::vector<Tensor> &m_out,
-                  const std::vector<Tensor> &v_out, const py::object &stream) {
+// The lists (m, v): the caller's, or new ones.
+py::tuple state_values(int n, uintptr_t tensors, const c10::Device &dev, const optional<std::vector<Tensor>> &m_given,
+                       const optional<std::vector<Tensor>> &v_given, const py::object &stream) {
+    const Call call(stream, dev);
+    const auto outputs = [&](const optional<std::vector<Tensor>> &given) {
+        if (given.has_value()) return *given;
+        std::vector<Tensor> ts;
+        for (int i = 0; i < n; ++i) ts.push_back(call.empty({(int64_t)table(tensors)[i].n}, at::kFloat));
+        return ts;
+    };
     const auto pointers = [&](const std::vector<Tensor> &ts, const char *name) {
         if ((int)ts.size() != n)
             refuse(std::to_string(ts.size()) + " tensors in " + name + " for " + std::to_string(n) + " parameters");
@@ -260,14 +310,15 @@ void state_values(int n, uintptr_t tensors, const c10::Device &dev, const std::v
             if (t.device() != dev || t.scalar_type() != at::kFloat || t.numel() != table(tensors)[i].n || !t.is_contiguous())
                 refuse(std::string(name) + "[" + std::to_string(i) + "] must be a contiguous fp32 tensor of " +
                        std::to_string(table(tensors)[i].n) + " elements on " + dev.str());
+            call.uses(t);
             p[i] = static_cast<float *>(t.data_ptr());
         }
         return p;
     };
+    const std::vector<Tensor> m_out = outputs(m_given), v_out = outputs(v_given);
     const std::vector<float *> m = pointers(m_out, "m_out"), v = pointers(v_out, "v_out");
-    const c10::cuda::CUDAGuard guard(dev);
-    check_status(wtconv_adamw_state_values(n, table(tensors), m.data(), v.data(), stream_on(stream, dev)),
-                 "wtconv_adamw_state_values");
+    check_status(wtconv_adamw_state_values(n, table(tensors), m.data(), v.data(), call.stream()), "wtconv_adamw_state_values");
+    return py::make_tuple(m_out, v_out);
 }
 
 }  // namespace

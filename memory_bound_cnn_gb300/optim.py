@@ -62,6 +62,9 @@ class AdamW:
     parameters, rewritten by each step (None entries: no copy).  state_bits: 32 or 8.
     states: adopt existing ones, as ``state_dict`` gives them (they are used in place), ``count``
     steps having been taken.
+
+    A method's ``stream`` (default: the current one) is where its work is queued.  The caller orders it
+    after the work that writes the gradients, and keeps this object until that work has ended.
     """
 
     def __init__(self, params, grads, state_bits=32, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
@@ -148,7 +151,4 @@ class AdamW:
         not given)."""
         if self.state_bits == 32:
             return self.states["m"], self.states["v"]
-        outs = [[torch.empty(p.numel(), dtype=torch.float32, device=self.device) for p in self.params]
-                if given is None else given for given in (m_out, v_out)]
-        self._ext.state_values(len(self.params), self._table, self.device, *outs, stream)
-        return outs[0], outs[1]
+        return self._ext.state_values(len(self.params), self._table, self.device, m_out, v_out, stream)

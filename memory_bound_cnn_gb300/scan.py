@@ -5,6 +5,11 @@ work on CUDA tensors; ``WTConvScanFunction`` (and ``gated_scan`` around it) make
 differentiable.  Activations are planes (B, C, T) or (B, C, H, W) with ``layout="planes"``, or
 tokens (B, T, C) with ``layout="tokens"``; the innermost axis must be contiguous, the others may
 have any strides (one half of a projection's output, a slice of a batch).
+
+``stream`` (default: the current one) is where a call's work is queued, and new tensors are allocated
+for it.  The caller orders it after the work that makes the inputs and before what reads the outputs;
+memory of a tensor that is let go of meanwhile is not used again before the work has ended, except with
+an ``ExternalStream``, whose owner keeps the tensors.
 """
 from __future__ import annotations
 

@@ -48,3 +48,73 @@ def test_a_wait_that_gives_up_is_reported_once():
     for k in before:
         assert torch.equal(before[k], after[k]), k
     assert S.wtconv_scan_status() == W.OK
+
+
+def dirty(sizes):
+    """Blocks of these many bytes of the current stream's pool, filled with NaN or large bytes and let go."""
+    for n in sizes:
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xff)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["planes", "tokens"])
+@pytest.mark.parametrize("size", [(2, 5000, 8), (1, 40000, 16), (4, 300, 64)], ids=str)
+def test_given_stream_without_workspace(size, layout):
+    """The side stream is held up, so that the call's work runs after the current stream has used whatever
+    memory it could get again: the call's scratch, and inputs that the caller has let go of.  Then the current
+    stream is held up with writes to blocks that it has let go of, which a new output must not be put in."""
+    B, T, C = size
+    d = make(B, T, C, layout, torch.bfloat16, seed=28)
+    want = run(d, layout)
+    order = {"planes": 0, "tokens": 1}[layout]
+    scratch = [S.wtconv_scan_workspace_size(op, B, T, C, order, 1) for op in (0, 1)]
+    sizes = [n for n in (*scratch, d["x"].nbytes, d["h0"].nbytes, want["states"].nbytes, 4 * C) if n > 0] * 4
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for round in range(2):
+        given = {k: v if v is None else v.clone() for k, v in d.items()}
+        side.wait_stream(torch.cuda.current_stream())
+        if round == 0:
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(100_000_000)
+        else:
+            torch.cuda._sleep(100_000_000)
+            dirty(sizes)
+        y, h, states = S.wtconv_scan_forward(given["x"], given["gate"], given["gate_bias"], given["h0"], None, layout, True,
+                                             stream=side)
+        if round == 0:
+            dirty(sizes)
+        dx, dg, db, dh0 = S.wtconv_scan_backward(given["x"], given["gate"], given["gate_bias"], states, given["dy"],
+                                                 given["dh_last"], None, layout, stream=side)
+        del given
+        if round == 0:
+            dirty(sizes)
+        torch.cuda.synchronize()
+        for k, t in (("y", y), ("h_last", h), ("states", states), ("dx", dx), ("d_gate", dg), ("d_gate_bias", db), ("d_h0", dh0)):
+            assert torch.equal(t, want[k]), (round, k)
+
+
+@pytest.mark.gpu
+def test_given_stream_step():
+    """As above for single tokens; and results that the current stream still reads when they are let go of
+    are not overwritten by the side stream's next call."""
+    g = torch.Generator(device="cuda").manual_seed(29)
+    x, gate = torch.randn(2, 64, 4096, generator=g, device="cuda").bfloat16()
+    bias, pool = torch.ones(4096, device="cuda"), torch.zeros(64, 4096, device="cuda")
+    want = S.wtconv_scan_step(x, gate, bias, pool.clone())
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    first = x.clone()
+    side.wait_stream(torch.cuda.current_stream())
+    y = S.wtconv_scan_step(first, gate, bias, pool.clone(), stream=side)
+    del first
+    dirty([x.nbytes, pool[0].nbytes * 64] * 4)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(100_000_000)
+    late = y.clone()  # runs after the sleep
+    del y
+    S.wtconv_scan_step(-x, gate, bias, pool, stream=side)  # runs at once
+    torch.cuda.synchronize()
+    assert torch.equal(late, want)
