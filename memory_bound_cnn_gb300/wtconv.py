@@ -13,6 +13,10 @@ Functions carry the C names: ``wtconv_forward``, ``wtconv_backward_input``,
 
 Every call runs with the activations' device current (the library plans, looks up its device
 symbols and launches on the current device), and rejects a stream or workspace on another device.
+With ``stream`` its new tensors are allocated for that stream; the caller orders the stream after the
+work that makes the inputs and before what reads the outputs.  Memory of a tensor that is let go of
+meanwhile is not used again before the work has ended, except with an ``ExternalStream``, whose owner
+keeps the tensors.
 """
 from __future__ import annotations
 
@@ -227,11 +231,45 @@ def check_devices(device: torch.device, stream=None, workspace: torch.Tensor | N
         raise ValueError(f"workspace is on {workspace.device}, the tensors on {device}")
 
 
+def _foreign(device: torch.device, stream) -> bool:
+    """Whether a call's stream is another than the device's current one."""
+    return stream is not None and stream.cuda_stream != torch.cuda.current_stream(device).cuda_stream
+
+
+def _under(device: torch.device, stream):
+    """Allocations within belong to the call's stream: no other stream's use of their memory meets it."""
+    if not _foreign(device, stream):
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    return torch.cuda.stream(stream)
+
+
+def _records(stream) -> bool:
+    """PyTorch's own streams outlive every tensor; an ExternalStream may not, and its owner keeps the tensors."""
+    return isinstance(stream, torch.cuda.Stream) and not isinstance(stream, torch.cuda.ExternalStream)
+
+
+def _new_like(t: torch.Tensor, stream) -> torch.Tensor:
+    """A new output of a call on `stream`; let go of, its memory waits for the current stream's reads too."""
+    check_devices(t.device, stream)
+    with _under(t.device, stream):
+        out = torch.empty_like(t)
+    if _foreign(t.device, stream) and _records(stream):
+        out.record_stream(torch.cuda.current_stream(t.device))
+    return out
+
+
 @contextlib.contextmanager
-def _on(device: torch.device, stream, workspace):
-    """The activations' device made current for the call (checked against stream and workspace)."""
+def _on(device: torch.device, stream, workspace, tensors=()):
+    """The activations' device made current for the call (checked against stream and workspace), and
+    the call's stream for its allocations; `tensors` and the workspace are used on that stream."""
     check_devices(device, stream, workspace)
-    with torch.cuda.device(device):
+    if _foreign(device, stream) and _records(stream):
+        for t in (*tensors, workspace):
+            if t is not None:
+                t.record_stream(stream)
+    with torch.cuda.device(device), _under(device, stream):
         yield
 
 
@@ -242,9 +280,9 @@ def wtconv_forward(x, base_w, base_bias, base_scale, wavelet_w, wavelet_scale, y
     shape = _shape(x, wavelet_w, base_w)
     p = _params(base_w, base_bias, base_scale, wavelet_w, wavelet_scale, x)
     if y is None:
-        y = torch.empty_like(x)
+        y = _new_like(x, stream)
     _check_out(y, "y", x)
-    with _on(x.device, stream, workspace):
+    with _on(x.device, stream, workspace, (x, y, base_w, base_bias, base_scale, wavelet_w, wavelet_scale)):
         ws, nbytes = _workspace(OP_FORWARD, shape, x.device, workspace)
         rc = load().wtconv_forward(*shape, _ptr(x), *p, _ptr(y), _ptr(ws), nbytes, _stream(stream))
     _raise(rc, "wtconv_forward")
@@ -258,21 +296,21 @@ def wtconv_backward_input(dy, base_w, base_bias, base_scale, wavelet_w, wavelet_
     shape = _shape(dy, wavelet_w, base_w)
     p = _params(base_w, base_bias, base_scale, wavelet_w, wavelet_scale, dy)
     if dx is None:
-        dx = torch.empty_like(dy)
+        dx = _new_like(dy, stream)
     _check_out(dx, "dx", dy)
-    with _on(dy.device, stream, workspace):
+    with _on(dy.device, stream, workspace, (dy, dx, base_w, base_bias, base_scale, wavelet_w, wavelet_scale)):
         ws, nbytes = _workspace(OP_BACKWARD_INPUT, shape, dy.device, workspace)
         rc = load().wtconv_backward_input(*shape, *p, _ptr(dy), _ptr(dx), _ptr(ws), nbytes, _stream(stream))
     _raise(rc, "wtconv_backward_input")
     return dx
 
 
-def _grad_buffers(base_w, base_bias, base_scale, wavelet_w, wavelet_scale, grads):
+def _grad_buffers(base_w, base_bias, base_scale, wavelet_w, wavelet_scale, grads, stream):
     if grads is None:
         grads = {
-            "d_base_w": torch.empty_like(base_w), "d_base_bias": torch.empty_like(base_bias),
-            "d_base_scale": torch.empty_like(base_scale), "d_wavelet_w": torch.empty_like(wavelet_w),
-            "d_wavelet_scale": torch.empty_like(wavelet_scale),
+            "d_base_w": _new_like(base_w, stream), "d_base_bias": _new_like(base_bias, stream),
+            "d_base_scale": _new_like(base_scale, stream), "d_wavelet_w": _new_like(wavelet_w, stream),
+            "d_wavelet_scale": _new_like(wavelet_scale, stream),
         }
     order = ("d_base_w", "d_base_bias", "d_base_scale", "d_wavelet_w", "d_wavelet_scale")
     for n, like in zip(order, (base_w, base_bias, base_scale, wavelet_w, wavelet_scale)):
@@ -290,8 +328,8 @@ def wtconv_backward_weights(x, dy, base_w, base_bias, base_scale, wavelet_w, wav
     _check_out(dy, "dy", x)
     shape = _shape(x, wavelet_w, base_w)
     p = _params(base_w, base_bias, base_scale, wavelet_w, wavelet_scale, x)
-    grads, gp = _grad_buffers(base_w, base_bias, base_scale, wavelet_w, wavelet_scale, grads)
-    with _on(x.device, stream, workspace):
+    grads, gp = _grad_buffers(base_w, base_bias, base_scale, wavelet_w, wavelet_scale, grads, stream)
+    with _on(x.device, stream, workspace, (x, dy, base_w, base_bias, base_scale, wavelet_w, wavelet_scale, *grads.values())):
         ws, nbytes = _workspace(OP_BACKWARD_WEIGHTS, shape, x.device, workspace)
         rc = load().wtconv_backward_weights(*shape, _ptr(x), _ptr(dy), *p, *gp, _ptr(ws), nbytes,
                                             _stream(stream))
@@ -312,8 +350,8 @@ def wtconv_backward_weights_noalloc(x, dy, base_w, base_bias, base_scale, wavele
     _check_out(dy, "dy", x)
     shape = _shape(x, wavelet_w, base_w)
     p = _params(base_w, base_bias, base_scale, wavelet_w, wavelet_scale, x)
-    grads, gp = _grad_buffers(base_w, base_bias, base_scale, wavelet_w, wavelet_scale, grads)
-    with _on(x.device, stream, None):
+    grads, gp = _grad_buffers(base_w, base_bias, base_scale, wavelet_w, wavelet_scale, grads, stream)
+    with _on(x.device, stream, None, (x, dy, base_w, base_bias, base_scale, wavelet_w, wavelet_scale, *grads.values())):
         rc = load().wtconv_backward_weights_noalloc(*shape, _ptr(x), _ptr(dy), *p, *gp, _stream(stream))
     _raise(rc, "wtconv_backward_weights_noalloc")
     return grads
@@ -327,11 +365,11 @@ def wtconv_backward(x, dy, base_w, base_bias, base_scale, wavelet_w, wavelet_sca
     shape = _shape(x, wavelet_w, base_w)
     p = _params(base_w, base_bias, base_scale, wavelet_w, wavelet_scale, x)
     if dx is None:
-        dx = torch.empty_like(x)
+        dx = _new_like(x, stream)
     _check_out(dx, "dx", x)
     _check_out(dy, "dy", x)
-    grads, gp = _grad_buffers(base_w, base_bias, base_scale, wavelet_w, wavelet_scale, grads)
-    with _on(x.device, stream, workspace):
+    grads, gp = _grad_buffers(base_w, base_bias, base_scale, wavelet_w, wavelet_scale, grads, stream)
+    with _on(x.device, stream, workspace, (x, dy, dx, base_w, base_bias, base_scale, wavelet_w, wavelet_scale, *grads.values())):
         ws, nbytes = _workspace(OP_BACKWARD, shape, x.device, workspace)
         rc = load().wtconv_backward(*shape, _ptr(x), _ptr(dy), *p, _ptr(dx), *gp, _ptr(ws), nbytes,
                                     _stream(stream))
