@@ -96,15 +96,30 @@ def wtconv_scan_step(x, gate, gate_bias, pool, slots=None, y=None, stream=None):
     return (_ext or _load_ext()).scan_step(x, gate, gate_bias, pool, slots, y, stream)
 
 
+class _ScanGradients(torch.autograd.Function):
+    """wtconv_scan_backward as an operation of its own, so that a second derivative meets its refusal."""
+
+    @staticmethod
+    def forward(ctx, x, gate, gate_bias, h0, states, dy, dh_last, lengths, layout):
+        ctx.set_materialize_grads(False)
+        return wtconv_scan_backward(x, gate, gate_bias, states, dy, dh_last, lengths, layout)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the gated scan has no second derivative")
+
+
 class WTConvScanFunction(torch.autograd.Function):
-    """Autograd wrapper: (y, h_last) through wtconv_scan_forward, gradients through wtconv_scan_backward."""
+    """Autograd wrapper: (y, h_last) through wtconv_scan_forward, gradients through wtconv_scan_backward.
+    A derivative of those gradients (``create_graph=True``) is refused."""
 
     @staticmethod
     def forward(ctx, x, gate, gate_bias, h0, lengths, layout):
         y, h_last, states = wtconv_scan_forward(x, gate, gate_bias, h0, lengths, layout,
                                                 keep_states=any(ctx.needs_input_grad))
         ctx.save_for_backward(x, gate, gate_bias, states, lengths)
-        ctx.layout, ctx.has_h0 = layout, h0 is not None
+        ctx.layout = layout
+        ctx.h0 = h0  # for its place in the graph only: the backward does not read it, so it may have changed
         ctx.set_materialize_grads(False)
         return y, h_last
 
@@ -113,10 +128,14 @@ class WTConvScanFunction(torch.autograd.Function):
         x, gate, gate_bias, states, lengths = ctx.saved_tensors
         dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()
         dh_last = None if dh_last is None else dh_last.contiguous()
-        dx, d_gate, d_bias, d_h0 = wtconv_scan_backward(x, gate, gate_bias, states, dy, dh_last, lengths, ctx.layout)
-        return dx, d_gate, d_bias, d_h0 if ctx.has_h0 else None, None, None
+        if torch.is_grad_enabled():  # create_graph=True
+            grads = _ScanGradients.apply(x, gate, gate_bias, ctx.h0, states, dy, dh_last, lengths, ctx.layout)
+        else:
+            grads = wtconv_scan_backward(x, gate, gate_bias, states, dy, dh_last, lengths, ctx.layout)
+        dx, d_gate, d_bias, d_h0 = grads
+        return dx, d_gate, d_bias, None if ctx.h0 is None else d_h0, None, None
 
 
 def gated_scan(x, gate, gate_bias, h0=None, lengths=None, layout="planes"):
-    """Differentiable gated scan: (y, h_last); arguments as wtconv_scan_forward's."""
+    """Differentiable gated scan: (y, h_last); arguments as wtconv_scan_forward's.  First derivatives only."""
     return WTConvScanFunction.apply(x, gate, gate_bias, h0, lengths, layout)

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import scan_reference as R
 import torch
-from test_scan import make, run
+from test_scan import make, reference, run
 
 from memory_bound_cnn_gb300 import scan as S
 from memory_bound_cnn_gb300 import wtconv as W
@@ -118,3 +118,54 @@ def test_given_stream_step():
     S.wtconv_scan_step(-x, gate, bias, pool, stream=side)  # runs at once
     torch.cuda.synchronize()
     assert torch.equal(late, want)
+
+
+def check_second_derivatives(x, gate, bias, h0, layout):
+    """First derivatives taken with create_graph are the plain ones; their derivative by any input of
+    the scan is refused, also where a loss has other parts and where dy depends on nothing."""
+    given = [t.clone().requires_grad_() for t in (x, gate, bias, h0)]
+    y, h = S.gated_scan(*given, None, layout)
+    plain = torch.autograd.grad(y.sum() + h.sum(), given, retain_graph=True)
+    kept = torch.autograd.grad(y.sum() + h.sum(), given, create_graph=True)
+    for a, b in zip(plain, kept):
+        assert torch.equal(a, b) and b.requires_grad
+    for t, g in zip(given, kept):
+        with pytest.raises(RuntimeError, match="second derivative"):
+            (g.square().sum() + t.square().sum()).backward(retain_graph=True)
+    scale = torch.ones((), requires_grad=True, device=x.device)  # dy depends on an input, the scan's inputs on none
+    y, _ = S.gated_scan(given[0], gate, bias, None, None, layout)
+    (g,) = torch.autograd.grad((y * scale).sum(), given[0], create_graph=True)
+    with pytest.raises(RuntimeError, match="second derivative"):
+        torch.autograd.grad(g.sum(), scale)
+
+
+def test_second_derivatives_refuse_without_a_gpu(monkeypatch):
+    def forward(x, gate, gate_bias, h0=None, lengths=None, layout="planes", keep_states=False):
+        return x * 2, x.sum(2), x.clone()
+
+    def backward(x, gate, gate_bias, states, dy, dh_last=None, lengths=None, layout="planes"):
+        return dy * 2, dy * 3, dy.sum((0, 2)), dy.sum(2)
+
+    monkeypatch.setattr(S, "wtconv_scan_forward", forward)
+    monkeypatch.setattr(S, "wtconv_scan_backward", backward)
+    x = torch.ones(2, 3, 4)
+    check_second_derivatives(x, x, torch.ones(3), torch.ones(2, 3), "planes")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["planes", "tokens"])
+def test_second_derivatives_refuse(layout):
+    d = make(2, 100, 8, layout, torch.float32, seed=21)
+    check_second_derivatives(d["x"], d["gate"], d["gate_bias"], d["h0"], layout)
+
+
+@pytest.mark.gpu
+def test_state_may_move_on_before_the_backward():
+    """A state that is carried from call to call in place: the backward needs only what the forward kept."""
+    d = make(2, 100, 8, "tokens", torch.float32, seed=31)
+    x, state = d["x"].clone().requires_grad_(), d["h0"].clone()
+    y, h = S.gated_scan(x, d["gate"], d["gate_bias"], state, None, "tokens")
+    state.copy_(h.detach())
+    y.backward(d["dy"])
+    want = reference({**d, "dh_last": None}, "tokens")
+    R.assert_near("dx", R.time_first(x.grad, "tokens"), want["dx"])
