@@ -119,7 +119,7 @@ class WTConvScanFunction(torch.autograd.Function):
                                                 keep_states=any(ctx.needs_input_grad))
         ctx.save_for_backward(x, gate, gate_bias, states, lengths)
         ctx.layout = layout
-        ctx.h0 = h0  # for its place in the graph only: the backward does not read it, so it may have changed
+        ctx.h0 = h0  # for its place in the graph only: the backward does not read its values, which may change
         ctx.set_materialize_grads(False)
         return y, h_last
 

@@ -377,17 +377,36 @@ def wtconv_backward(x, dy, base_w, base_bias, base_scale, wavelet_w, wavelet_sca
     return dx, grads
 
 
+class _WTConvGradients(torch.autograd.Function):
+    """wtconv_backward as an operation of its own, so that a second derivative meets its refusal."""
+
+    @staticmethod
+    def forward(ctx, origin, x, dy, *params):  # origin: what x was made contiguous from, or None
+        dx, g = wtconv_backward(x, dy, *params)
+        return dx, g["d_base_w"], g["d_base_bias"], g["d_base_scale"], g["d_wavelet_w"], g["d_wavelet_scale"]
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the WTConv layer has no second derivative")
+
+
 class WTConvFunction(torch.autograd.Function):
-    """Autograd wrapper: forward through wtconv_forward, backward through the fused wtconv_backward."""
+    """Autograd wrapper: forward through wtconv_forward, backward through the fused wtconv_backward.
+    A derivative of those gradients (``create_graph=True``) is refused."""
 
     @staticmethod
     def forward(ctx, x, base_w, base_bias, base_scale, wavelet_w, wavelet_scale):
         xc = x.contiguous()  # the backward reads the same contiguous copy
         ctx.save_for_backward(xc, base_w, base_bias, base_scale, wavelet_w, wavelet_scale)
+        # for its place in the graph only: its values may change
+        ctx.origin = x if x is not xc and x.requires_grad else None
         return wtconv_forward(xc, base_w, base_bias, base_scale, wavelet_w, wavelet_scale)
 
     @staticmethod
     def backward(ctx, dy):
-        x, base_w, base_bias, base_scale, wavelet_w, wavelet_scale = ctx.saved_tensors
-        dx, g = wtconv_backward(x, dy.contiguous(), base_w, base_bias, base_scale, wavelet_w, wavelet_scale)
+        x, *params = ctx.saved_tensors
+        dy = dy.contiguous()
+        if torch.is_grad_enabled():  # create_graph=True
+            return _WTConvGradients.apply(ctx.origin, x, dy, *params)
+        dx, g = wtconv_backward(x, dy, *params)
         return dx, g["d_base_w"], g["d_base_bias"], g["d_base_scale"], g["d_wavelet_w"], g["d_wavelet_scale"]
