@@ -26,7 +26,9 @@
  *
  * Non-finite values: where *clip is not finite (see wtconv_grad_norm) the call leaves every tensor
  * as it is.  Without clip, a non-finite gradient makes its element's p, m and v non-finite (with
- * 8-bit states: the m and v of its block).
+ * 8-bit states: the m and v of its block).  A finite one whose square passes fp32 (above 1.8e19)
+ * makes its v infinite; in 8 bits that leaves its block's v infinite or NaN, and from the next step
+ * on the parameters under a NaN are NaN.  sqrt(v') is that of at least 2^-126.
  *
  * Conventions are those of wtconv.h: device pointers in a host array of descriptors (read before
  * the call returns), asynchronous on `stream`, nothing allocated, arguments checked before any

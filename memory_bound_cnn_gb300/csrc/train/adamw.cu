@@ -128,6 +128,11 @@ __device__ __forceinline__ float block_max(uint32_t mine) { return __uint_as_flo
 __device__ __forceinline__ uint32_t larger(uint32_t most, Pair size) {
     return max(most, max(__float_as_uint(size.lo()), __float_as_uint(size.hi())));
 }
+__device__ __forceinline__ float at_least_normal(float v) {  // max(v, 2^-126), or NaN
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(FLT_MIN));
+    return r;
+}
 // levels per unit of magnitude: top^power / max (0 where the block is held as zeros)
 __device__ __forceinline__ float inverse_unit(float most, float top_power) {
     return most > 0.f ? __fmul_rn(__fdiv_rn(1.f, most), top_power) : most;
@@ -246,8 +251,8 @@ __device__ __forceinline__ void update(const wtconv_optim_tensor &t, const StepS
                 m_most = larger(m_most, abs(m[h][k]));
                 v_most = larger(v_most, v[h][k]);
             }
-            // (at least the least normal number: its root is far below any useful eps)
-            roots[h][k] = Pair(root_of(fmaxf(v[h][k].lo(), FLT_MIN)), root_of(fmaxf(v[h][k].hi(), FLT_MIN)));
+            // (at least the least normal number: its root is far below any useful eps; a NaN comes through)
+            roots[h][k] = Pair(root_of(at_least_normal(v[h][k].lo())), root_of(at_least_normal(v[h][k].hi())));
             const Pair d = fma(roots[h][k], Pair(s.root_scale), Pair(s.eps));
             const Pair step = mul(m[h][k], Pair(reciprocal(d.lo()), reciprocal(d.hi())));
             const Pair q = fma(Pair(-s.rate), step, mul(Pair(p[h][2 * k], p[h][2 * k + 1]), Pair(s.keep)));

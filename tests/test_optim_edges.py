@@ -28,3 +28,34 @@ def test_given_stream_without_workspace():
     late_m, late_v = other.state_values(stream=side)
     torch.cuda.synchronize()
     assert torch.equal(clip, late) and torch.equal(p, q) and torch.equal(m[0], late_m[0]) and torch.equal(v[0], late_v[0])
+
+
+@pytest.mark.gpu
+def test_averages_that_are_not_finite():
+    """A finite gradient whose square passes fp32 makes its 8-bit block's v infinite, and NaN where the
+    code is 0.  The parameters under a NaN become NaN at the next step: no finite step of any size."""
+    p, g = torch.ones(600, device="cuda"), torch.full((600,), 1e-3, device="cuda")
+    opt = O.AdamW([p], [g], state_bits=8)
+    opt.step()
+    g[300] = 2e19
+    opt.step()
+    bad = torch.isnan(opt.state_values()[1][0])
+    assert int(bad[256:512].sum()) == 255 and int(bad.sum()) == 255
+    g.fill_(1e-3)
+    opt.step()
+    assert torch.isnan(p[bad]).all() and torch.isfinite(p[~bad]).all() and float(p[~bad].abs().max()) < 1.01
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_nan_second_average_alone(bits):
+    """v NaN beside a finite m, as states may be adopted: p is NaN there and nowhere else."""
+    p, g = torch.ones(256, device="cuda"), torch.full((256,), 1e-3, device="cuda")
+    opt = O.AdamW([p], [g], state_bits=bits)
+    if bits == 32:
+        opt.states["v"][0][100] = float("nan")
+    else:
+        opt.states["v_max"][0][0] = float("nan")
+    opt.step()
+    bad = torch.isnan(p)
+    assert bad[100] and int(bad.sum()) == (1 if bits == 32 else 256)
