@@ -623,15 +623,20 @@ __global__ void __launch_bounds__(kThreads<T, R>, sizeof(T) == 4 ? kBackwardPerS
                 for (int j = kSteps - 1; j >= 0; --j, to_x -= a.dx.row, to_g -= a.d_gate.row) {
                     const Pair dh = add(dyv[j].wide(), flow);
                     const Pair dgv = mul(mul(dh, diff[j]), mul(av[j], bv[j]));
-                    sum = add(sum, dgv);
                     flow = mul(av[j], dh);
                     store(j, mul(bv[j], dh), dgv);
                 }
             };
             if (whole_strip && live >= kSteps) {
-                positions([&](int, Pair dxv, Pair dgv) { store_pair(to_x, dxv), store_pair(to_g, dgv); });
+                positions([&](int, Pair dxv, Pair dgv) {
+                    sum = add(sum, dgv);
+                    store_pair(to_x, dxv), store_pair(to_g, dgv);
+                });
             } else {
                 positions([&](int j, Pair dxv, Pair dgv) {
+                    // zeros past the length (b is 0 there, but a state or dh that is not finite makes b dh NaN)
+                    if (j >= live) dxv = dgv = Pair(0.f);
+                    sum = add(sum, dgv);
                     if (t + j < a.T) store_two<T, PAIRED>(to_x, dxv, s.width), store_two<T, PAIRED>(to_g, dgv, s.width);
                 });
             }

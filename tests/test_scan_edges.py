@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import scan_reference as R
 import torch
-from test_scan import make, reference, run
+from test_scan import DTYPES, make, reference, run
 
 from memory_bound_cnn_gb300 import scan as S
 from memory_bound_cnn_gb300 import wtconv as W
@@ -169,3 +169,41 @@ def test_state_may_move_on_before_the_backward():
     y.backward(d["dy"])
     want = reference({**d, "dh_last": None}, "tokens")
     R.assert_near("dx", R.time_first(x.grad, "tokens"), want["dx"])
+
+
+GARBAGE = [float("inf"), float("-inf"), float("nan")]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["planes", "tokens"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("T,C", [(37, 9), (400, 64), (2600, 20), (1000, 512)])
+@pytest.mark.parametrize("bad", GARBAGE, ids=str)
+def test_zeros_past_a_length(bad, T, C, dtype, layout):
+    """y, dx and d_gate are exact zeros from a length on, whatever states and gradients come to it."""
+    lengths = [T, T // 2 + 3, 0, 1, min(T, 63)]
+    d = make(len(lengths), T, C, layout, dtype, seed=22, lengths=lengths)
+    d["dh_last"][1], d["h0"][3], d["dh_last"][4] = bad, bad, bad
+    got = run(d, layout)
+    for k in ("y", "dx", "d_gate"):
+        v = R.time_first(got[k], layout)
+        for b, n in enumerate(lengths):
+            assert (v[n:, b] == 0).all(), (k, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["planes", "tokens"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("T,C", [(37, 9), (400, 64), (2600, 20), (1000, 512)])
+@pytest.mark.parametrize("bad", GARBAGE, ids=str)
+def test_empty_sequences_give_no_gradient(bad, T, C, dtype, layout):
+    """A sequence without positions has no part in d_gate_bias, whatever its state and dh_last hold; those
+    come out as h_last and d_h0 as they are."""
+    lengths = [T, 0, T // 2]
+    d = make(3, T, C, layout, dtype, seed=23, lengths=lengths)
+    want = reference(d, layout)
+    d["h0"][1], d["dh_last"][1] = bad, bad
+    got = run(d, layout)
+    R.assert_near("d_gate_bias", got["d_gate_bias"].double().cpu().numpy(), want["d_gate_bias"], scale=want["abs"].max())
+    for k, given in (("h_last", "h0"), ("d_h0", "dh_last")):
+        assert torch.equal(torch.nan_to_num(got[k][1], 5.0), torch.nan_to_num(d[given][1], 5.0)), k
