@@ -9,6 +9,7 @@
 #include <torch/extension.h>
 
 #include <climits>
+#include <cstddef>
 #include <string>
 #include <vector>
 
@@ -152,6 +153,14 @@ Scratch scratch(const optional<Tensor> &given, size_t need, c10::Device device, 
     return s;
 }
 
+// A tensor of the caller's that a kernel has written: autograd then sees that a value it saved has changed.
+void written(const Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(const optional<Tensor> &t) {
+    if (t.has_value()) written(*t);
+}
+
 // ------------------------------------------------------------------------------------------- scan
 
 std::vector<int64_t> states_shape(const Dims &d) {
@@ -182,6 +191,7 @@ py::tuple scan_forward(const Tensor &x, const Tensor &gate, const Tensor &gate_b
                                      h0_p, len_p, ay.p, ay.batch, ay.row, h_last.data_ptr<float>(),
                                      keep_states ? states.data_ptr<float>() : nullptr, ws.p, ws.bytes, call.stream()),
                  "wtconv_scan_forward");
+    written(y_given);
     return py::make_tuple(y, h_last, keep_states ? py::cast(states) : py::none());
 }
 
@@ -210,6 +220,7 @@ py::tuple scan_backward(const Tensor &x, const Tensor &gate, const Tensor &gate_
                                       adg.batch, adg.row, d_bias.data_ptr<float>(), d_h0.data_ptr<float>(), ws.p, ws.bytes,
                                       call.stream()),
                  "wtconv_scan_backward");
+    written(dx_given), written(d_gate_given);
     return py::make_tuple(dx, d_gate, d_bias, d_h0);
 }
 
@@ -237,68 +248,93 @@ Tensor scan_step(const Tensor &x, const Tensor &gate, const Tensor &gate_bias, c
                                   gate.stride(0), bias_p, pool_p, (int)pool.size(0), slots_p, y.data_ptr(), y.stride(0),
                                   call.stream()),
                  "wtconv_scan_step");
+    written(pool), written(y_given);
     return y;
 }
 
 // ------------------------------------------------------------------------------------------ AdamW
-// `tensors` and `config` are addresses of the optimiser's wtconv_optim_tensor and
-// wtconv_adamw_config, checked when it was built.
 
-const wtconv_optim_tensor *table(uintptr_t address) { return reinterpret_cast<const wtconv_optim_tensor *>(address); }
+// The tensors behind an optimiser's descriptors, which lie at `address` in its own memory: field by field,
+// checked when they are filled in.
+class TensorTable {
+  public:
+    TensorTable(int n, uintptr_t address, const c10::Device &device)
+        : list(reinterpret_cast<wtconv_optim_tensor *>(address)), n(n), device(device) {}
 
-// Checks one tensor per descriptor and writes its address into the field at `offset`.  The tensor has
-// one element for every `per` of the parameter's (which `params` sets the number of); None is allowed
-// where `optional` says so.
-void fill_field(int n, uintptr_t tensors, const std::vector<optional<Tensor>> &ts, size_t offset, at::ScalarType dtype, int64_t per,
-                const c10::Device &dev, const std::string &name, bool params, bool may_be_none) {
-    if ((int)ts.size() != n) refuse(std::to_string(ts.size()) + " tensors in " + name + " for " + std::to_string(n) + " parameters");
-    wtconv_optim_tensor *const list = reinterpret_cast<wtconv_optim_tensor *>(tensors);
-    for (int i = 0; i < n; ++i) {
-        const optional<Tensor> &t = ts[i];
-        if (!t.has_value() && may_be_none) continue;
-        const int64_t want = params && t.has_value() ? t->numel() : (list[i].n + per - 1) / per;
-        if (!t.has_value() || !t->is_cuda() || t->device() != dev || t->scalar_type() != dtype || t->numel() != want || !t->is_contiguous())
-            refuse(name + "[" + std::to_string(i) + "] must be a contiguous " + c10::toString(dtype) + " tensor of " +
-                   std::to_string(want) + " elements on " + dev.str());
+    // One tensor per descriptor, whose addresses go to the field at `offset`.  The tensor has one element
+    // for every `per` of the parameter's (which `params` sets the number of); None is allowed where
+    // `may_be_none` says so.
+    void fill(const std::vector<optional<Tensor>> &ts, size_t offset, at::ScalarType dtype, int64_t per, const std::string &name,
+              bool params, bool may_be_none) {
+        if ((int)ts.size() != n) refuse(std::to_string(ts.size()) + " tensors in " + name + " for " + std::to_string(n) + " parameters");
+        for (int i = 0; i < n; ++i) {
+            const optional<Tensor> &t = ts[i];
+            if (!t.has_value() && may_be_none) continue;
+            const int64_t want = params && t.has_value() ? t->numel() : (list[i].n + per - 1) / per;
+            if (!t.has_value() || !t->is_cuda() || t->device() != device || t->scalar_type() != dtype || t->numel() != want ||
+                !t->is_contiguous())
+                refuse(name + "[" + std::to_string(i) + "] must be a contiguous " + c10::toString(dtype) + " tensor of " +
+                       std::to_string(want) + " elements on " + device.str());
+        }
+        for (int i = 0; i < n; ++i) {  // (only once all of them are right)
+            if (!ts[i].has_value()) continue;
+            if (params) list[i].n = ts[i]->numel();
+            *reinterpret_cast<void **>(reinterpret_cast<char *>(&list[i]) + offset) = ts[i]->data_ptr();
+        }
+        if (params) params_ = ts;
+        if (offset == offsetof(wtconv_optim_tensor, copy)) copies_ = ts;
     }
-    for (int i = 0; i < n; ++i) {  // (only once all of them are right)
-        if (!ts[i].has_value()) continue;
-        if (params) list[i].n = ts[i]->numel();
-        *reinterpret_cast<void **>(reinterpret_cast<char *>(&list[i]) + offset) = ts[i]->data_ptr();
+    // After a step: the parameters and their copies have changed.
+    void stepped() const {
+        for (const auto *ts : {&params_, &copies_})
+            for (const optional<Tensor> &t : *ts) written(t);
     }
-}
 
-Tensor grad_norm(int n, uintptr_t tensors, int grad_dtype, const c10::Device &dev, double max_norm, const optional<Tensor> &out_given,
+    wtconv_optim_tensor *const list;
+    const int n;
+    const c10::Device device;
+
+  private:
+    std::vector<optional<Tensor>> params_, copies_;
+};
+
+Tensor grad_norm(const TensorTable &table, int grad_dtype, double max_norm, const optional<Tensor> &out_given,
                  const optional<Tensor> &workspace, size_t workspace_bytes, const py::object &stream) {
+    const c10::Device dev = table.device;
     const Call call(stream, dev);
     const Tensor out = out_given.has_value() ? *out_given : call.empty({2}, at::kFloat);
     float *out_p = array<float>(out, "out", {2}, dev);
     const Scratch ws = scratch(workspace, workspace_bytes, dev, call);
     call.uses(out_given);
     // (scratch: none for few elements)
-    check_status(wtconv_grad_norm(n, table(tensors), grad_dtype, max_norm, out_p, ws.p, ws.bytes, call.stream()),
+    check_status(wtconv_grad_norm(table.n, table.list, grad_dtype, max_norm, out_p, ws.p, ws.bytes, call.stream()),
                  "wtconv_grad_norm");
+    written(out_given);
     return out;
 }
 
-void adamw_step(int n, uintptr_t tensors, uintptr_t config, const c10::Device &dev, const optional<Tensor> &clip,
-                const py::object &stream) {
+// config: address of the optimiser's wtconv_adamw_config.
+void adamw_step(const TensorTable &table, uintptr_t config, const optional<Tensor> &clip, const py::object &stream) {
+    const c10::Device dev = table.device;
     const float *clip_p = array<float>(clip, "clip", {2}, dev);
     const Call call(stream, dev);
     call.uses(clip);
-    check_status(wtconv_adamw_step(n, table(tensors), reinterpret_cast<const wtconv_adamw_config *>(config),
+    check_status(wtconv_adamw_step(table.n, table.list, reinterpret_cast<const wtconv_adamw_config *>(config),
                                    clip_p != nullptr ? clip_p + 1 : nullptr, call.stream()),
                  "wtconv_adamw_step");
+    table.stepped();
 }
 
 // The lists (m, v): the caller's, or new ones.
-py::tuple state_values(int n, uintptr_t tensors, const c10::Device &dev, const optional<std::vector<Tensor>> &m_given,
+py::tuple state_values(const TensorTable &table, const optional<std::vector<Tensor>> &m_given,
                        const optional<std::vector<Tensor>> &v_given, const py::object &stream) {
+    const int n = table.n;
+    const c10::Device dev = table.device;
     const Call call(stream, dev);
     const auto outputs = [&](const optional<std::vector<Tensor>> &given) {
         if (given.has_value()) return *given;
         std::vector<Tensor> ts;
-        for (int i = 0; i < n; ++i) ts.push_back(call.empty({(int64_t)table(tensors)[i].n}, at::kFloat));
+        for (int i = 0; i < n; ++i) ts.push_back(call.empty({(int64_t)table.list[i].n}, at::kFloat));
         return ts;
     };
     const auto pointers = [&](const std::vector<Tensor> &ts, const char *name) {
@@ -307,9 +343,9 @@ py::tuple state_values(int n, uintptr_t tensors, const c10::Device &dev, const o
         std::vector<float *> p(n);
         for (int i = 0; i < n; ++i) {
             const Tensor &t = ts[i];
-            if (t.device() != dev || t.scalar_type() != at::kFloat || t.numel() != table(tensors)[i].n || !t.is_contiguous())
+            if (t.device() != dev || t.scalar_type() != at::kFloat || t.numel() != table.list[i].n || !t.is_contiguous())
                 refuse(std::string(name) + "[" + std::to_string(i) + "] must be a contiguous fp32 tensor of " +
-                       std::to_string(table(tensors)[i].n) + " elements on " + dev.str());
+                       std::to_string(table.list[i].n) + " elements on " + dev.str());
             call.uses(t);
             p[i] = static_cast<float *>(t.data_ptr());
         }
@@ -317,7 +353,10 @@ py::tuple state_values(int n, uintptr_t tensors, const c10::Device &dev, const o
     };
     const std::vector<Tensor> m_out = outputs(m_given), v_out = outputs(v_given);
     const std::vector<float *> m = pointers(m_out, "m_out"), v = pointers(v_out, "v_out");
-    check_status(wtconv_adamw_state_values(n, table(tensors), m.data(), v.data(), call.stream()), "wtconv_adamw_state_values");
+    check_status(wtconv_adamw_state_values(n, table.list, m.data(), v.data(), call.stream()), "wtconv_adamw_state_values");
+    for (const auto *given : {&m_given, &v_given})
+        if (given->has_value())
+            for (const Tensor &t : **given) written(t);
     return py::make_tuple(m_out, v_out);
 }
 
@@ -327,7 +366,7 @@ PYBIND11_MODULE(_binding, m) {
     m.def("scan_forward", &scan_forward);
     m.def("scan_backward", &scan_backward);
     m.def("scan_step", &scan_step);
-    m.def("fill_field", &fill_field);
+    py::class_<TensorTable>(m, "TensorTable").def(py::init<int, uintptr_t, const c10::Device &>()).def("fill", &TensorTable::fill);
     m.def("grad_norm", &grad_norm);
     m.def("adamw_step", &adamw_step);
     m.def("state_values", &state_values);

@@ -79,7 +79,7 @@ class AdamW:
         n = len(self.params)
         self._tensors = (OptimTensor * n)()
         self._ext = load_binding()
-        self._table = ctypes.addressof(self._tensors)
+        self._table = self._ext.TensorTable(n, ctypes.addressof(self._tensors), self.device)
         self._fill("param", self.params, torch.float32, "params", params=True)
         self.copies = [None] * n if copies is None else list(copies)
         kinds = {c.dtype for c in self.copies if c is not None}
@@ -100,8 +100,7 @@ class AdamW:
         self.set_grads(grads)
 
     def _fill(self, field, tensors, dtype, name, per=1, params=False, may_be_none=False):
-        self._ext.fill_field(len(self.params), self._table, tensors, getattr(OptimTensor, field).offset, dtype, per, self.device,
-                             name, params, may_be_none)
+        self._table.fill(tensors, getattr(OptimTensor, field).offset, dtype, per, name, params, may_be_none)
 
     def _state_layout(self):
         if self.state_bits == 32:
@@ -132,8 +131,7 @@ class AdamW:
     def grad_norm(self, max_norm=float("inf"), out=None, workspace=None, stream=None) -> torch.Tensor:
         """Device tensor (norm, factor): the norm over every gradient and the factor that limits it
         to max_norm (NaN where the norm is not finite), for ``step(clip=...)``."""
-        return self._ext.grad_norm(len(self.params), self._table, self._config.grad_dtype, self.device, max_norm, out,
-                                   workspace, self._norm_bytes, stream)
+        return self._ext.grad_norm(self._table, self._config.grad_dtype, max_norm, out, workspace, self._norm_bytes, stream)
 
     def step(self, clip=None, lr=None, count=None, stream=None) -> None:
         """One update of every parameter.  clip: what ``grad_norm`` returned (a factor that is not
@@ -142,7 +140,7 @@ class AdamW:
         config = self._config
         config.lr = self.lr if lr is None else lr
         config.step = self.count + 1 if count is None else count
-        self._ext.adamw_step(len(self.params), self._table, self._scalars, self.device, clip, stream)
+        self._ext.adamw_step(self._table, self._scalars, clip, stream)
         self.count, self.lr = config.step, config.lr
 
     def state_values(self, m_out=None, v_out=None, stream=None):
@@ -151,4 +149,4 @@ class AdamW:
         not given)."""
         if self.state_bits == 32:
             return self.states["m"], self.states["v"]
-        return self._ext.state_values(len(self.params), self._table, self.device, m_out, v_out, stream)
+        return self._ext.state_values(self._table, m_out, v_out, stream)

@@ -59,3 +59,24 @@ def test_nan_second_average_alone(bits):
     opt.step()
     bad = torch.isnan(p)
     assert bad[100] and int(bad.sum()) == (1 if bits == 32 else 256)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_autograd_sees_a_step(bits):
+    """A graph that saved a parameter, its working copy or a state before they were updated is refused."""
+    p = torch.ones(600, device="cuda", requires_grad=True)
+    copy = torch.ones(600, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(600, device="cuda", requires_grad=True)
+    opt = O.AdamW([p.detach()], [torch.ones(600, device="cuda")], state_bits=bits, copies=[copy])
+    losses = [(p * p).sum(), (copy * w).sum()]
+    opt.step(clip=opt.grad_norm(1.0))
+    for loss in losses:
+        with pytest.raises(RuntimeError, match="modified by an inplace"):
+            loss.backward()
+    (p * p).sum().backward()  # a graph over the new values is as good as ever
+    assert torch.equal(p.grad, 2 * p.detach())
+    with torch.inference_mode():
+        q = torch.ones(4, device="cuda")
+        O.AdamW([q], [torch.ones(4, device="cuda")], state_bits=bits).step()
+        assert (q < 1).all()

@@ -207,3 +207,18 @@ def test_empty_sequences_give_no_gradient(bad, T, C, dtype, layout):
     R.assert_near("d_gate_bias", got["d_gate_bias"].double().cpu().numpy(), want["d_gate_bias"], scale=want["abs"].max())
     for k, given in (("h_last", "h0"), ("d_h0", "dh_last")):
         assert torch.equal(torch.nan_to_num(got[k][1], 5.0), torch.nan_to_num(d[given][1], 5.0)), k
+
+
+@pytest.mark.gpu
+def test_autograd_sees_what_is_written():
+    """A graph that saved the pool or an output's buffer before a call wrote it is refused."""
+    d = make(2, 20, 8, "tokens", torch.float32, seed=25)
+    w = torch.ones(8, device="cuda", requires_grad=True)
+    pool, y, dx, dg = (torch.zeros(s, device="cuda") for s in ((4, 8), (2, 20, 8), (2, 20, 8), (2, 20, 8)))
+    losses = [(t * w).sum() for t in (pool, y, dx, dg)]
+    S.wtconv_scan_step(d["x"][:, 0], d["gate"][:, 0], d["gate_bias"], pool)
+    _, _, states = S.wtconv_scan_forward(d["x"], d["gate"], d["gate_bias"], layout="tokens", keep_states=True, y=y)
+    S.wtconv_scan_backward(d["x"], d["gate"], d["gate_bias"], states, d["dy"], layout="tokens", dx=dx, d_gate=dg)
+    for loss in losses:
+        with pytest.raises(RuntimeError, match="modified by an inplace"):
+            loss.backward()
