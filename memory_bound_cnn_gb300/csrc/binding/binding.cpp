@@ -267,27 +267,25 @@ class TensorTable {
     void fill(const std::vector<optional<Tensor>> &ts, size_t offset, at::ScalarType dtype, int64_t per, const std::string &name,
               bool params, bool may_be_none) {
         if ((int)ts.size() != n) refuse(std::to_string(ts.size()) + " tensors in " + name + " for " + std::to_string(n) + " parameters");
-        for (int i = 0; i < n; ++i) {
-            const optional<Tensor> &t = ts[i];
-            if (!t.has_value() && may_be_none) continue;
-            const int64_t want = params && t.has_value() ? t->numel() : (list[i].n + per - 1) / per;
-            if (!t.has_value() || !t->is_cuda() || t->device() != device || t->scalar_type() != dtype || t->numel() != want ||
-                !t->is_contiguous())
-                refuse(name + "[" + std::to_string(i) + "] must be a contiguous " + c10::toString(dtype) + " tensor of " +
-                       std::to_string(want) + " elements on " + device.str());
-        }
+        const Field f = {ts, offset, dtype, name, may_be_none};
+        for (int i = 0; i < n; ++i) f.check(i, params && ts[i].has_value() ? ts[i]->numel() : (list[i].n + per - 1) / per, device);
         for (int i = 0; i < n; ++i) {  // (only once all of them are right)
             if (!ts[i].has_value()) continue;
             if (params) list[i].n = ts[i]->numel();
-            *reinterpret_cast<void **>(reinterpret_cast<char *>(&list[i]) + offset) = ts[i]->data_ptr();
+            f.address(list[i]) = ts[i]->data_ptr();
         }
-        if (params) params_ = ts;
-        if (offset == offsetof(wtconv_optim_tensor, copy)) copies_ = ts;
+        if (params) params_ = f;
+        else if (offset == offsetof(wtconv_optim_tensor, grad)) grads_ = f;
+        else if (offset == offsetof(wtconv_optim_tensor, copy)) copies_ = f;
     }
+    // Before every use: tensors whose memory is another by now (`p.data = ...` gives one a new storage)
+    // are checked again and followed.
+    void follow_grads() { follow(grads_); }
+    void follow() { follow(params_), follow(grads_), follow(copies_); }
     // After a step: the parameters and their copies have changed.
     void stepped() const {
-        for (const auto *ts : {&params_, &copies_})
-            for (const optional<Tensor> &t : *ts) written(t);
+        for (const Field *f : {&params_, &copies_})
+            for (const optional<Tensor> &t : f->ts) written(t);
     }
 
     wtconv_optim_tensor *const list;
@@ -295,12 +293,37 @@ class TensorTable {
     const c10::Device device;
 
   private:
-    std::vector<optional<Tensor>> params_, copies_;
+    struct Field {
+        std::vector<optional<Tensor>> ts;
+        size_t offset;
+        at::ScalarType dtype;
+        std::string name;
+        bool may_be_none;
+        void *&address(wtconv_optim_tensor &t) const { return *reinterpret_cast<void **>(reinterpret_cast<char *>(&t) + offset); }
+        void check(int i, int64_t want, const c10::Device &device) const {
+            const optional<Tensor> &t = ts[i];
+            if (!t.has_value() && may_be_none) return;
+            if (!t.has_value() || !t->is_cuda() || t->device() != device || t->scalar_type() != dtype || t->numel() != want ||
+                !t->is_contiguous())
+                refuse(name + "[" + std::to_string(i) + "] must be a contiguous " + c10::toString(dtype) + " tensor of " +
+                       std::to_string(want) + " elements on " + device.str());
+        }
+    };
+    void follow(const Field &f) {
+        for (int i = 0; i < (int)f.ts.size(); ++i) {
+            const optional<Tensor> &t = f.ts[i];
+            if (!t.has_value() || (t->const_data_ptr() == f.address(list[i]) && t->numel() == list[i].n)) continue;
+            f.check(i, list[i].n, device);
+            f.address(list[i]) = t->data_ptr();
+        }
+    }
+    Field params_, grads_, copies_;
 };
 
-Tensor grad_norm(const TensorTable &table, int grad_dtype, double max_norm, const optional<Tensor> &out_given,
+Tensor grad_norm(TensorTable &table, int grad_dtype, double max_norm, const optional<Tensor> &out_given,
                  const optional<Tensor> &workspace, size_t workspace_bytes, const py::object &stream) {
     const c10::Device dev = table.device;
+    table.follow_grads();
     const Call call(stream, dev);
     const Tensor out = out_given.has_value() ? *out_given : call.empty({2}, at::kFloat);
     float *out_p = array<float>(out, "out", {2}, dev);
@@ -314,9 +337,10 @@ Tensor grad_norm(const TensorTable &table, int grad_dtype, double max_norm, cons
 }
 
 // config: address of the optimiser's wtconv_adamw_config.
-void adamw_step(const TensorTable &table, uintptr_t config, const optional<Tensor> &clip, const py::object &stream) {
+void adamw_step(TensorTable &table, uintptr_t config, const optional<Tensor> &clip, const py::object &stream) {
     const c10::Device dev = table.device;
     const float *clip_p = array<float>(clip, "clip", {2}, dev);
+    table.follow();
     const Call call(stream, dev);
     call.uses(clip);
     check_status(wtconv_adamw_step(table.n, table.list, reinterpret_cast<const wtconv_adamw_config *>(config),

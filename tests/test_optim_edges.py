@@ -80,3 +80,36 @@ def test_autograd_sees_a_step(bits):
         q = torch.ones(4, device="cuda")
         O.AdamW([q], [torch.ones(4, device="cuda")], state_bits=bits).step()
         assert (q < 1).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_tensors_that_move(bits):
+    """Parameters, gradients and copies that are given other memory are followed there; where that does not
+    fit, the step is refused and nothing changes."""
+    n = 3000
+    p, other = torch.ones(n, device="cuda"), torch.full((n,), 7.0, device="cuda")
+    g, copy = torch.full((n,), 0.5, device="cuda"), torch.ones(n, device="cuda").half()
+    opt = O.AdamW([p], [g], state_bits=bits, copies=[copy])
+    old = [t.data for t in (p, g, copy)]
+    opt.step(clip=opt.grad_norm())
+    p.data, other.data = other.data, p.data  # as a program that swaps averaged weights in does
+    g.data, copy.data = torch.full((n,), -0.25, device="cuda"), torch.zeros(n, device="cuda").half()
+    before = [t.clone() for t in old]
+    clip = opt.grad_norm()
+    assert abs(float(clip[0]) - 0.25 * n ** 0.5) < 1e-4
+    opt.step(clip=clip)
+    for a, b in zip(old, before):  # the memory that they had is left alone
+        assert torch.equal(a, b)
+    assert torch.equal(copy, p.half()) and (p != 7).all() and (p > 6.9).all()
+    kept = p.clone()
+    for t, bad in ((p, torch.ones(n + 1, device="cuda")), (g, torch.ones(n, device="cuda").bfloat16()), (p, torch.ones(n)),
+                   (p, torch.ones(2 * n, device="cuda")[::2])):
+        good = t.data
+        t.data = bad
+        with pytest.raises(ValueError, match=r"params\[0\]|grads\[0\]"):
+            opt.step()
+        t.data = good
+    assert torch.equal(p, kept) and opt.count == 2
+    opt.step()
+    assert opt.count == 3 and not torch.equal(p, kept)
