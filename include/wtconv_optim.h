@@ -33,8 +33,9 @@
  * Conventions are those of wtconv.h: device pointers in a host array of descriptors (read before
  * the call returns), asynchronous on `stream`, nothing allocated, arguments checked before any
  * launch.  Pointers need only their element's alignment; tensors whose pointers are all 16-byte
- * aligned run fastest.  Descriptors with n = 0 are skipped (their pointers may be NULL).  Results
- * do not depend on how tensors are grouped, except the last bits of the norm.
+ * aligned run fastest.  No two tensors' outputs may overlap (a shared parameter is given once).
+ * Descriptors with n = 0 are skipped (their pointers may be NULL).  Results do not depend on how
+ * tensors are grouped, except the last bits of the norm.
  */
 #ifndef WTCONV_OPTIM_H
 #define WTCONV_OPTIM_H

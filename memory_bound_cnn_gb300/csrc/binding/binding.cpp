@@ -8,6 +8,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/extension.h>
 
+#include <algorithm>
 #include <climits>
 #include <cstddef>
 #include <string>
@@ -269,6 +270,7 @@ class TensorTable {
         if ((int)ts.size() != n) refuse(std::to_string(ts.size()) + " tensors in " + name + " for " + std::to_string(n) + " parameters");
         const Field f = {ts, offset, dtype, name, may_be_none};
         for (int i = 0; i < n; ++i) f.check(i, params && ts[i].has_value() ? ts[i]->numel() : (list[i].n + per - 1) / per, device);
+        if (params) refuse_overlaps(ts, name);
         for (int i = 0; i < n; ++i) {  // (only once all of them are right)
             if (!ts[i].has_value()) continue;
             if (params) list[i].n = ts[i]->numel();
@@ -309,6 +311,23 @@ class TensorTable {
                        std::to_string(want) + " elements on " + device.str());
         }
     };
+    // Elements that two parameters share would be updated by two warps at once.
+    static void refuse_overlaps(const std::vector<optional<Tensor>> &ts, const std::string &name) {
+        struct Range {
+            const char *begin, *end;
+            int which;
+        };
+        std::vector<Range> ranges;
+        for (int i = 0; i < (int)ts.size(); ++i) {
+            const char *const p = static_cast<const char *>(ts[i]->const_data_ptr());
+            if (ts[i]->numel() > 0) ranges.push_back({p, p + ts[i]->nbytes(), i});
+        }
+        std::sort(ranges.begin(), ranges.end(), [](const Range &a, const Range &b) { return a.begin < b.begin; });
+        for (size_t i = 1; i < ranges.size(); ++i)
+            if (ranges[i].begin < ranges[i - 1].end)
+                refuse(name + "[" + std::to_string(std::min(ranges[i - 1].which, ranges[i].which)) + "] and " + name + "[" +
+                       std::to_string(std::max(ranges[i - 1].which, ranges[i].which)) + "] share memory");
+    }
     void follow(const Field &f) {
         for (int i = 0; i < (int)f.ts.size(); ++i) {
             const optional<Tensor> &t = f.ts[i];

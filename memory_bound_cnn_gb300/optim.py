@@ -56,11 +56,12 @@ def _load() -> ctypes.CDLL:
 class AdamW:
     """AdamW over many tensors in one call per step.
 
-    params: contiguous fp32 CUDA tensors, updated in place.  grads: one contiguous tensor per
-    parameter, of its size and one dtype (fp32, bf16 or fp16); the buffers that the backward
-    writes each step (``set_grads`` for other tensors).  copies: optional 16-bit working copies of the
-    parameters, rewritten by each step (None entries: no copy).  Each of these may be given other
-    memory between steps (``p.data = ...``); a ``detach()`` of it would not follow.  state_bits: 32 or 8.
+    params: contiguous fp32 CUDA tensors, updated in place; one that layers share is given once.
+    grads: one contiguous tensor per parameter, of its size and one dtype (fp32, bf16 or fp16); the
+    buffers that the backward writes each step (``set_grads`` for other tensors).  copies: optional
+    16-bit working copies of the parameters, rewritten by each step (None entries: no copy).  Each of
+    these may be given other memory between steps (``p.data = ...``); a ``detach()`` of it would not
+    follow.  state_bits: 32 or 8.
     states: adopt existing ones, as ``state_dict`` gives them (they are used in place), ``count``
     steps having been taken.
 

@@ -113,3 +113,16 @@ def test_tensors_that_move(bits):
     assert torch.equal(p, kept) and opt.count == 2
     opt.step()
     assert opt.count == 3 and not torch.equal(p, kept)
+
+
+@pytest.mark.gpu
+def test_shared_parameters_refuse():
+    """A parameter that is given twice, or that lies within another, would be updated by two warps at once."""
+    flat, grads = torch.ones(1000, device="cuda"), [torch.ones(500, device="cuda"), torch.ones(500, device="cuda")]
+    for second in (flat[:500], flat[499:999]):
+        with pytest.raises(ValueError, match=r"params\[0\] and params\[1\] share memory"):
+            O.AdamW([flat[:500], second], grads)
+    O.AdamW([flat[500:], flat[:500]], grads).step()
+    assert (flat < 1).all()
+    empty = flat[:0]
+    O.AdamW([flat, empty, empty], [torch.ones(1000, device="cuda"), empty.clone(), empty.clone()]).step()
