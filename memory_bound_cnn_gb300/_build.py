@@ -59,45 +59,29 @@ def _compile_binding() -> tuple[list[str], str]:
     return cmd, obj
 
 
+def binding_stale() -> bool:
+    """Whether the binding is missing or older than its sources."""
+    return _stale(BINDING, [BINDING_SRC, *glob.glob(os.path.join(INCLUDE, "*.h")), __file__])
+
+
 def _link_binding(obj: str) -> None:
     import torch
 
     lib_dir = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + f".{os.getpid()}.tmp"
-    subprocess.run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libwtconv.so",
+    subprocess.run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L" + os.path.dirname(LIB), "-l:libwtconv.so",
                     "-Wl,-rpath,$ORIGIN", "-L" + lib_dir, "-Wl,-rpath," + lib_dir, "-ltorch_python", "-ltorch", "-ltorch_cpu",
                     "-ltorch_cuda", "-lc10", "-lc10_cuda"], check=True)
     os.replace(tmp, BINDING)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Build what is missing or stale; returns the library's path."""
-    srcs = sources()
-    headers = [h for d in (CSRC, CSRC_TRAIN, INCLUDE) for pat in ("*.h", "*.cuh")
-               for h in glob.glob(os.path.join(d, pat))]
-    lib_stale = force or _stale(LIB, srcs + headers + [__file__])
-    binding_stale = force or _stale(BINDING, [BINDING_SRC, *glob.glob(os.path.join(INCLUDE, "*.h")), __file__])
-    if not lib_stale and not binding_stale:
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    procs = []
-    objs = []
-    if binding_stale:
-        cmd, binding_obj = _compile_binding()
-        if verbose:
-            print(" ".join(cmd), file=sys.stderr)
-        procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    for src in srcs if lib_stale else ():
-        obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-        objs.append(obj)
-        # a layer kernel uses the layer's headers, an operator of csrc/train that folder's own
-        used = [h for h in headers if os.path.dirname(h) in (INCLUDE, os.path.dirname(src))]
-        if not force and not _stale(obj, [src, *used, __file__]):
-            continue
-        cmd = [nvcc(), *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj]
-        if verbose:
-            print(" ".join(cmd), file=sys.stderr)
-        procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+def _start(cmd: list[str], verbose: bool):
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    return cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _finish(procs) -> None:
     failed = []
     for cmd, p in procs:
         out, _ = p.communicate()
@@ -106,15 +90,55 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if failed:
         msg = "\n".join(" ".join(c) + "\n" + o for c, o in failed)
         raise RuntimeError("compilation failed:\n" + msg)
-    if lib_stale:
-        tmp = LIB + f".{os.getpid()}.tmp"
-        cmd = [nvcc(), *ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-soname=libwtconv.so", "-o", tmp, *objs]
-        if verbose:
-            print(" ".join(cmd), file=sys.stderr)
-        subprocess.run(cmd, check=True)
-        os.replace(tmp, LIB)
-    if binding_stale:
-        _link_binding(binding_obj)
+
+
+def _build_library(force: bool, verbose: bool) -> None:
+    srcs = sources()
+    headers = [h for d in (CSRC, CSRC_TRAIN, INCLUDE) for pat in ("*.h", "*.cuh")
+               for h in glob.glob(os.path.join(d, pat))]
+    if not force and not _stale(LIB, srcs + headers + [__file__]):
+        return
+    procs = []
+    objs = []
+    for src in srcs:
+        obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
+        objs.append(obj)
+        # a layer kernel uses the layer's headers, an operator of csrc/train that folder's own
+        used = [h for h in headers if os.path.dirname(h) in (INCLUDE, os.path.dirname(src))]
+        if not force and not _stale(obj, [src, *used, __file__]):
+            continue
+        procs.append(_start([nvcc(), *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj], verbose))
+    _finish(procs)
+    tmp = LIB + f".{os.getpid()}.tmp"
+    cmd = [nvcc(), *ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-soname=libwtconv.so", "-o", tmp, *objs]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, LIB)
+
+
+def build(force: bool = False, verbose: bool = False, binding: bool = True) -> str:
+    """Build what is missing or stale: the library, and with ``binding`` the compiled binding beside it;
+    returns the library's path.  The library needs nothing of the binding, and is built where that fails."""
+    os.makedirs(BUILD, exist_ok=True)
+    compiling, failure = None, None
+    if binding and (force or binding_stale()):
+        cmd, obj = _compile_binding()
+        try:
+            compiling = _start(cmd, verbose)
+        except OSError as e:  # no compiler for it
+            failure = e
+    try:
+        _build_library(force, verbose)
+    except BaseException:
+        if compiling is not None:
+            compiling[1].communicate()
+        raise
+    if failure is not None:
+        raise failure
+    if compiling is not None:
+        _finish([compiling])
+        _link_binding(obj)
     return LIB
 
 

@@ -62,7 +62,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     path = library_path()
     if build_if_missing:
         try:
-            path = _build.build()
+            path = _build.build(binding=False)
         except OSError as e:  # no nvcc here: use what is built, if anything
             if not os.path.exists(path):
                 raise RuntimeError(f"libwtconv.so is not built and cannot be built: {e}") from e
@@ -105,10 +105,16 @@ _binding = None
 
 
 def load_binding():
-    """The compiled binding of the operators beside the layer (built with the library)."""
+    """The compiled binding of the operators beside the layer (built first if it is missing or stale).
+    The layer itself does without it."""
     global _binding
     if _binding is None:
         load()
+        try:
+            _build.build()
+        except OSError as e:  # no compiler here: use what is built, if anything
+            if not os.path.exists(_build.BINDING):
+                raise RuntimeError(f"_binding.so is not built and cannot be built: {e}") from e
         from . import _binding as module  # the extension module _binding.so
 
         _binding = module
