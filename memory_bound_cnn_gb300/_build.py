@@ -22,6 +22,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libwtconv.so")
 BINDING_SRC = os.path.join(CSRC, "binding", "binding.cpp")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_KEY = os.path.join(PKG, "_binding.key")  # the PyTorch and Python that _binding.so was built for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
@@ -59,9 +60,22 @@ def _compile_binding() -> tuple[list[str], str]:
     return cmd, obj
 
 
+def _binding_key() -> str:
+    import torch
+
+    return f"torch {torch.__version__} at {os.path.dirname(torch.__file__)}, C++11 ABI {torch._C._GLIBCXX_USE_CXX11_ABI}, " \
+        f"Python {sysconfig.get_config_var('SOABI')}\n"
+
+
 def binding_stale() -> bool:
-    """Whether the binding is missing or older than its sources."""
-    return _stale(BINDING, [BINDING_SRC, *glob.glob(os.path.join(INCLUDE, "*.h")), __file__])
+    """Whether the binding is missing, older than its sources, or built for another PyTorch or Python."""
+    if _stale(BINDING, [BINDING_SRC, *glob.glob(os.path.join(INCLUDE, "*.h")), __file__]):
+        return True
+    try:
+        with open(BINDING_KEY) as f:
+            return f.read() != _binding_key()
+    except FileNotFoundError:
+        return True
 
 
 def _link_binding(obj: str) -> None:
@@ -73,6 +87,9 @@ def _link_binding(obj: str) -> None:
                     "-Wl,-rpath,$ORIGIN", "-L" + lib_dir, "-Wl,-rpath," + lib_dir, "-ltorch_python", "-ltorch", "-ltorch_cpu",
                     "-ltorch_cuda", "-lc10", "-lc10_cuda"], check=True)
     os.replace(tmp, BINDING)
+    with open(BINDING_KEY + f".{os.getpid()}.tmp", "w") as f:
+        f.write(_binding_key())
+    os.replace(f.name, BINDING_KEY)
 
 
 def _start(cmd: list[str], verbose: bool):

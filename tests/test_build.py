@@ -4,6 +4,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 from memory_bound_cnn_gb300 import _build
 
@@ -45,3 +46,14 @@ except RuntimeError:
 """
     r = child(code, CXX="false")
     assert r.returncode == 0 and r.stdout.split() == ["refused", "True"], r.stdout + r.stderr
+
+
+def test_another_pytorch_makes_the_binding_stale(monkeypatch):
+    """The binding holds PyTorch's and Python's layouts: it is rebuilt when either changes, not reused."""
+    _build.build()
+    assert not _build.binding_stale()
+    for module, name, value in ((torch, "__version__", "1.0"), (torch._C, "_GLIBCXX_USE_CXX11_ABI", None)):
+        with monkeypatch.context() as m:
+            m.setattr(module, name, value)
+            assert _build.binding_stale(), name
+    assert not _build.binding_stale()
