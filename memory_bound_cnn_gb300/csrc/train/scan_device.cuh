@@ -6,9 +6,11 @@
 
 namespace wtconv {
 
-// Gates of two elements: a = sigmoid(z) and b = 1 - a, both to a few units of their own last place.
-// With e = exp(-z), a = 1 / (1 + e) and b = e a: nothing cancels.  e is held below 2^100, where a has
-// long been 0 to fp32's eyes beside any h that matters (2^-100) and b is 1.  A NaN comes through.
+// Gates of two elements: a = sigmoid(z) and b = 1 - a.  With e = exp(-z), a = 1 / (1 + e) and b = e a:
+// nothing cancels.  In units of 2^-24 of its own value e is off by up to 2.2 |z| + 4 (z is rounded, and so
+// is its product with a rounded log2 e; the exponential itself: 4), which reaches a times b and b times a;
+// the other operations add up to 4.  e is held below 2^100, where a has long been 0 to fp32's eyes beside
+// any h that matters (2^-100) and b is 1.  A NaN comes through.
 struct Gates {
     Pair a, b;
 };
@@ -33,9 +35,10 @@ __device__ __forceinline__ Gates gates_of_exp(Pair e) {
     g.b = mul(e, g.a);
     return g;
 }
-// bias: minus the channels' gate_bias, times log2 e
+// (The sum comes first: a bias scaled beforehand saves an instruction, but is rounded at its own size, the
+// same way at every position.  With gates and biases of 20 to 60 that cancel, b was off by 58 units.)
 __device__ __forceinline__ Gates gates_of(Pair gate, Pair bias) {
-    const Pair w = fma(gate, Pair(-kLog2E), bias);
+    const Pair w = mul(add(gate, bias), Pair(-kLog2E));
     return gates_of_exp(Pair(capped(exp2_of(w.lo())), capped(exp2_of(w.hi()))));
 }
 

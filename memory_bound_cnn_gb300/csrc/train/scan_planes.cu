@@ -395,7 +395,7 @@ __global__ void __maxnreg__(72) scan_planes_forward_kernel(const ScanArgs a, int
         if (left > 0) fetch(k), --left;
         else commit_copies();
     }
-    const Pair bias(-kLog2E * a.gate_bias[s.c]);
+    const Pair bias(a.gate_bias[s.c]);
 
     float carry = 0.f;
     Span whole = {1.f, 0.f};  // kReduce: the segment so far
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, sizeof(T) == 4 ? 6 : 4)
         return MODE == kApply && at < a.T ? a.states_in[s.row * a.keep + at / WTCONV_SCAN_KEEP] : 0.f;
     };
     float next_kept = kept_at(t0 + lane * kLane<T>);
-    const Pair bias(-kLog2E * a.gate_bias[s.c]);
+    const Pair bias(a.gate_bias[s.c]);
 
     float carry = 0.f;  // a dh of the position after the round
     Pair sum(0.f);
@@ -564,7 +564,7 @@ template <typename T, int CP> __global__ void __launch_bounds__(kShortThreads) s
     Strip<T> x, g;
     x.template load<CP>(row_of<T>(a.x, s.b, s.c) + s.t, s.n - s.t);
     g.template load<CP>(row_of<T>(a.gate, s.b, s.c) + s.t, s.n - s.t);
-    const Pair bias(-kLog2E * a.gate_bias[s.c]);
+    const Pair bias(a.gate_bias[s.c]);
     const float h0 = a.h0 != nullptr ? a.h0[s.row] : 0.f;
     LaneForward<T> f;
     const Span span = warp_scan<false>(f.reduce(x, g, bias, s.n - s.t), lanes);
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(kShortThreads) scan_short_backward_kernel(cons
     x.template load<CP>(row_of<T>(a.x, s.b, s.c) + s.t, s.n - s.t);
     g.template load<CP>(row_of<T>(a.gate, s.b, s.c) + s.t, s.n - s.t);
     dy.template load<CP>(row_of<T>(a.dy, s.b, s.c) + s.t, s.n - s.t);
-    const Pair bias(-kLog2E * a.gate_bias[s.c]);
+    const Pair bias(a.gate_bias[s.c]);
     const float dh_last = a.dh_last != nullptr ? a.dh_last[s.row] : 0.f;
     const float kept = a.states_in[s.row * a.keep];  // the state before the row
     LaneBackward<T> f;

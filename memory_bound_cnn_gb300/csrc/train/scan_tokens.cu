@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads<T, R>, kForwardPerSm<R>) scan_tokens_
     if (round0 + 1 < round1) fetch((round0 + 1) & 1);
     else commit_copies();
 
-    const Pair bias = mul(load_two(a.gate_bias + s.c, s.width), Pair(-kLog2E));
+    const Pair bias = load_two(a.gate_bias + s.c, s.width);
     Chain chain;
     chain.state = Pair(0.f);
     Map whole = identity();
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kThreads<T, R>, sizeof(T) == 4 ? kBackwardPerS
                 }
     }
 
-    const Pair bias = mul(load_two(a.gate_bias + s.c, s.width), Pair(-kLog2E));
+    const Pair bias = load_two(a.gate_bias + s.c, s.width);
     Chain chain;
     chain.state = Pair(0.f);
     Pair sum(0.f), next_kept(0.f);
@@ -818,7 +818,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(int C, int parts, ScanTe
     float h = 0.f;
     if (slot >= 0 && slot < n_states) {
         float *s = pool + (long long)slot * C + c;
-        const Gates q = gates_of(Pair(to_f32(static_cast<const T *>(gate.p)[b * gate.row + c])), Pair(-kLog2E * gate_bias[c]));
+        const Gates q = gates_of(Pair(to_f32(static_cast<const T *>(gate.p)[b * gate.row + c])), Pair(gate_bias[c]));
         h = fmaf(q.a.lo(), *s, q.b.lo() * to_f32(static_cast<const T *>(x.p)[b * x.row + c]));
         *s = h;
     }

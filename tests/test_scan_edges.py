@@ -222,3 +222,26 @@ def test_autograd_sees_what_is_written():
     for loss in losses:
         with pytest.raises(RuntimeError, match="modified by an inplace"):
             loss.backward()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["planes", "tokens"])
+def test_gates_that_cancel(layout):
+    """a and b = 1 - a to a few units of their own value where a large gate and a large bias nearly cancel.
+    Over one position of dy = 1 and no dh: dx = b and d_h0 = a exactly.  Units of 2^-24: z is rounded
+    (|z|), its product with log2 e too (|z|), which is itself off by 0.23; these move e by 2.23 |z|, the
+    exponential by 4, and e's error reaches b times a and a times b.  1 + e, its reciprocal and e a round
+    once each; one more is left for the terms of second order."""
+    g = torch.Generator(device="cuda").manual_seed(24)
+    B, C = 512, 256
+    z = torch.rand(B, C, generator=g, device="cuda") * 30 - 10
+    bias = torch.rand(C, generator=g, device="cuda") * 40 + 20
+    shape = (B, 1, C) if layout == "tokens" else (B, C, 1)
+    gate, one = (z - bias).view(shape), torch.ones(shape, device="cuda")
+    _, _, states = S.wtconv_scan_forward(one, gate, bias, layout=layout, keep_states=True)
+    dx, _, _, d_h0 = S.wtconv_scan_backward(one, gate, bias, states, one, layout=layout)
+    z = gate.view(B, C).double() + bias.double()
+    a, b = 1 / (1 + torch.exp(-z)), 1 / (1 + torch.exp(z))
+    for name, got, want, rest in (("a", d_h0, a, b), ("b", dx.view(B, C), b, a)):
+        units = (got.double() - want).abs() / want * 2.0 ** 24
+        assert (units <= (2.23 * z.abs() + 4) * rest + 4).all(), (name, float(units.max()))
