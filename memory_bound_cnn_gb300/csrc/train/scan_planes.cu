@@ -272,25 +272,27 @@ template <typename T> struct LaneBackward {
             h = fma(av[j], h, mul(bv[j], xv));
         }
         Pair flow(back.hi().of(flow_after), flow_after);
+        const Pair before = sum;
 #pragma unroll
         for (int j = kHalf<T> - 1; j >= 0; --j) {
             const Pair dh = add(dy.get(j), flow);
             diff[j] = mul(mul(dh, diff[j]), mul(av[j], bv[j]));
+            sum = add(sum, diff[j]);
             bv[j] = mul(bv[j], dh);
             flow = mul(av[j], dh);
         }
-        if (live < kLane<T>) {
-            // nothing past the length (b is 0 there, but a state or dh that is not finite makes b dh NaN)
-#pragma unroll
-            for (int j = 0; j < kHalf<T>; ++j) {
-                if (j >= live) diff[j] = Pair(0.f, diff[j].hi()), bv[j] = Pair(0.f, bv[j].hi());
-                if (kHalf<T> + j >= live) diff[j] = Pair(diff[j].lo(), 0.f), bv[j] = Pair(bv[j].lo(), 0.f);
-            }
-        }
-#pragma unroll
-        for (int j = kHalf<T> - 1; j >= 0; --j) sum = add(sum, diff[j]);
         dx.set(bv);
         dg.set(diff);
+        if (live < kLane<T>) {
+            // Nothing past the length: 1 - a is 0 there, but a state or dh that is not finite makes its
+            // products NaN.  (Apart from the loop, and the sum formed again: with every lane's sum after the
+            // loop 16x64x65536 bf16 forward + backward took 209 us, with selections in it 200, so 193.)
+            dx.cut(live), dg.cut(live);
+            sum = before;
+#pragma unroll
+            for (int j = kHalf<T> - 1; j >= 0; --j)
+                sum = add(sum, Pair(j < live ? diff[j].lo() : 0.f, kHalf<T> + j < live ? diff[j].hi() : 0.f));
+        }
     }
 };
 
