@@ -10,7 +10,7 @@ import ctypes
 
 import torch
 
-from .wtconv import DTYPE_CODE, load, load_binding
+from .wtconv import DTYPE_CODE, _on, load, load_binding
 
 ADAMW_BLOCK = 256  # WTCONV_ADAMW_BLOCK
 
@@ -146,9 +146,23 @@ class AdamW:
         self.count, self.lr = config.step, config.lr
 
     def state_values(self, m_out=None, v_out=None, stream=None):
-        """The averages (m, v) as lists of fp32 tensors: the states themselves in 32 bits, else what
-        the 8-bit codes stand for, written to m_out and v_out (lists of fp32 tensors; new ones if
-        not given)."""
-        if self.state_bits == 32:
-            return self.states["m"], self.states["v"]
-        return self._ext.state_values(self._table, m_out, v_out, stream)
+        """The averages (m, v) as lists of fp32 tensors.  m_out, v_out: lists of fp32 tensors to write
+        them to.  Where a list is not given, the states themselves in 32 bits, in 8 new tensors of what
+        the codes stand for."""
+        if self.state_bits == 8:
+            return self._ext.state_values(self._table, m_out, v_out, stream)
+        lists = []
+        for name, kind, out in (("m_out", "m", m_out), ("v_out", "v", v_out)):
+            states = self.states[kind]
+            if out is not None and len(out) != len(states):
+                raise ValueError(f"{len(out)} tensors in {name} for {len(states)} parameters")
+            for i, (t, s) in enumerate(zip(out or (), states)):
+                if t.dtype != torch.float32 or t.device != self.device or t.numel() != s.numel() or not t.is_contiguous():
+                    raise ValueError(f"{name}[{i}] must be a contiguous fp32 tensor of {s.numel()} elements on {self.device}")
+            lists.append(states if out is None else out)
+        with _on(self.device, stream, None, [t for out in (m_out, v_out) for t in out or ()]):
+            for out, kind in zip(lists, "mv"):
+                for t, s in zip(out, self.states[kind]):
+                    if t is not s:
+                        t.view(-1).copy_(s.view(-1))
+        return tuple(lists)

@@ -126,3 +126,26 @@ def test_shared_parameters_refuse():
     assert (flat < 1).all()
     empty = flat[:0]
     O.AdamW([flat, empty, empty], [torch.ones(1000, device="cuda"), empty.clone(), empty.clone()]).step()
+
+
+@pytest.mark.gpu
+def test_values_of_32_bit_states():
+    """Given lists are written in 32 bits as in 8; one that is not given is the states themselves."""
+    p, g = torch.ones(30, 20, device="cuda"), torch.ones(600, device="cuda")
+    opt = O.AdamW([p], [g])
+    opt.step()
+    m, v = [torch.zeros(600, device="cuda")], [torch.zeros(600, device="cuda")]
+    got = opt.state_values(m, v)
+    assert got[0] is m and got[1] is v
+    assert torch.equal(m[0], opt.states["m"][0].view(-1)) and torch.equal(v[0], opt.states["v"][0].view(-1))
+    assert float(m[0][0]) == pytest.approx(0.1) and opt.state_values(m)[1] is opt.states["v"]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    opt.step(stream=side)
+    opt.state_values(m, stream=side)
+    side.synchronize()
+    assert torch.equal(m[0], opt.states["m"][0].view(-1))
+    for bad in ([], [g[:1]], [g.half()], [torch.zeros(600)], [torch.zeros(1200, device="cuda")[::2]]):
+        for bits in (32, 8):
+            with pytest.raises(ValueError, match="v_out"):
+                O.AdamW([p], [g], state_bits=bits).state_values(v_out=bad)
