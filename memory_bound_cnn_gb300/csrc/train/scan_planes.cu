@@ -711,7 +711,7 @@ template <typename T, int CP> cudaError_t backward_typed(const ScanArgs &a, cuda
         if (e == cudaSuccess) e = launch(scan_planes_backward_kernel<T, CP, kApply>, grid, p, ring, st, a, p.segments, p.rounds_per, maps, part);
     }
     if (e != cudaSuccess) return e;
-    return launch_kernel(scan_planes_bias_kernel, (a.C + 3) / 4, 128, 0, st, 1, part, a.d_gate_bias, a.B, a.C, p.segments);
+    return launch_kernel(scan_planes_bias_kernel, ceil_div(a.C, 4), 128, 0, st, 1, part, a.d_gate_bias, a.B, a.C, p.segments);
 }
 
 }  // namespace

@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads<T, R>, kForwardPerSm<R>) scan_tokens_
                     round_span * a.gate.row);
     T *y = static_cast<T *>(a.y.p) + s.b * a.y.batch + s.c + (t0 + slot * kSteps) * a.y.row;
     const long long y_round = round_span * a.y.row;
-    const bool whole_strip = PAIRED && s.c0 + kWidth<T, R> <= a.C;
+    const bool whole_strip = PAIRED && a.C - s.c0 >= kWidth<T, R>;
     int ahead = t0;  // first position of the next tiles to fetch
     const auto fetch = [&](int buf) {
         x.next(sh.x[buf], s.n - ahead, a.C - s.c0);
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kThreads<T, R>, sizeof(T) == 4 ? kBackwardPerS
     Loader<T, CP, R> dy(static_cast<const T *>(a.dy.p), static_cast<const T *>(a.dy.p) + s.b * a.dy.batch + s.c0 + t0 * a.dy.row, a.dy.row, -round_span * a.dy.row);
     T *dx = static_cast<T *>(a.dx.p) + s.b * a.dx.batch + s.c + (t0 + slot * kSteps + kSteps - 1) * a.dx.row;
     T *dg = static_cast<T *>(a.d_gate.p) + s.b * a.d_gate.batch + s.c + (t0 + slot * kSteps + kSteps - 1) * a.d_gate.row;
-    const bool whole_strip = PAIRED && s.c0 + kWidth<T, R> <= a.C;
+    const bool whole_strip = PAIRED && a.C - s.c0 >= kWidth<T, R>;
     int ahead = t0;  // first position of the next tiles to fetch, towards the beginning
     const auto fetch = [&](int buf) {
         g.next(sh.g[buf], s.n - ahead, a.C - s.c0);
@@ -700,7 +700,7 @@ int row_bytes(const ScanArgs &a) {
 TokenPlan plan_of(const ScanArgs &a, bool backward) {
     TokenPlan p;
     const int row = row_bytes(a), width = row / elem_bytes_of(a.dtype), per_sm = (backward ? 2 : 4) * 128 / row;
-    p.strips = (a.C + width - 1) / width;
+    p.strips = ceil_div(a.C, width);
     const long long chains = (long long)a.B * p.strips, want = (long long)per_sm * sm_count();
     const int rounds = (a.T + kSpan - 1) / kSpan;
     p.cluster = p.segments = 1;
@@ -760,7 +760,7 @@ template <typename T, int CP, int R, bool PAIRED> cudaError_t backward_typed(con
     if (p.segments > 1) e = launch(scan_tokens_backward_kernel<T, CP, R, PAIRED, kReduce>, kThreads<T, R>, shared, a, p, st, maps, part);
     if (e == cudaSuccess) e = launch(scan_tokens_backward_kernel<T, CP, R, PAIRED, kApply>, kThreads<T, R>, shared, a, p, st, maps, part);
     if (e != cudaSuccess) return e;
-    return launch_kernel(scan_tokens_bias_kernel, (a.C + 31) / 32, 256, 0, st, 1, part, a.d_gate_bias, a.B, a.C, p.strips,
+    return launch_kernel(scan_tokens_bias_kernel, ceil_div(a.C, 32), 256, 0, st, 1, part, a.d_gate_bias, a.B, a.C, p.strips,
                          p.segments * p.cluster, kWidth<T, R>);
 }
 
@@ -853,7 +853,7 @@ cudaError_t launch_scan_tokens_backward(const ScanArgs &a, cudaStream_t st) {
 
 cudaError_t launch_scan_step(int B, int C, int dtype, const ScanTensor &x, const ScanTensor &gate, const float *gate_bias,
                              float *pool, int n_states, const int *slots, const ScanTensor &y, cudaStream_t st) {
-    const int parts = (C + 255) / 256;
+    const int parts = ceil_div(C, 256);
     const unsigned grid = (unsigned)B * parts;
     const auto kernel = dtype == WTCONV_F32 ? scan_step_kernel<float>
                         : dtype == WTCONV_BF16 ? scan_step_kernel<__nv_bfloat16> : scan_step_kernel<__half>;

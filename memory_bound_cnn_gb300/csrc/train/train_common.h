@@ -14,6 +14,8 @@
 namespace wtconv {
 
 inline int elem_bytes_of(int dtype) { return dtype == WTCONV_F32 ? 4 : 2; }
+// (n > 0, up to the largest int)
+inline int ceil_div(int n, int d) { return (n - 1) / d + 1; }
 inline bool dtype_ok(int dtype) { return dtype == WTCONV_F32 || dtype == WTCONV_BF16 || dtype == WTCONV_F16; }
 inline bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline bool fault_injected() {

@@ -245,3 +245,28 @@ def test_gates_that_cancel(layout):
     for name, got, want, rest in (("a", d_h0, a, b), ("b", dx.view(B, C), b, a)):
         units = (got.double() - want).abs() / want * 2.0 ** 24
         assert (units <= (2.23 * z.abs() + 4) * rest + 4).all(), (name, float(units.max()))
+
+
+@pytest.mark.parametrize("layout,C", [(layout, (1 << 31) - k) for layout in (0, 1) for k in (1, 2, 31, 32, 33, 256)])
+def test_workspace_of_the_most_channels(layout, C):
+    """B*C < 2^31: numbers of strips next to that limit are not formed past it.  One float a channel of
+    every strip is what the sums of d_gate_bias take."""
+    for dtype, width in ((W.F32, 32), (W.BF16, 64)):
+        want = 4 * C if layout == 0 else 4 * (-(-C // width) * width)
+        got = S.wtconv_scan_workspace_size(S.OP_SCAN_BACKWARD, 1, 1, C, layout, dtype)
+        assert got == -(-want // 256) * 256
+        assert S.wtconv_scan_workspace_size(S.OP_SCAN_FORWARD, 1, 1, C, layout, dtype) == 0
+
+
+@pytest.mark.gpu
+def test_step_of_the_most_channels():
+    """One sequence of 2^31 - 1 channels: the first and the last are updated like any other."""
+    C = (1 << 31) - 1
+    x = torch.ones(1, C, dtype=torch.bfloat16, device="cuda")
+    bias, pool = torch.zeros(C, device="cuda"), torch.zeros(1, C, device="cuda")
+    y = S.wtconv_scan_step(x, x, bias, pool)
+    want = 1 / (1 + np.exp(1.0))
+    for at in (slice(0, 300), slice(C - 300, C)):
+        R.assert_near("pool", pool[0, at].double().cpu().numpy(), np.full(300, want))
+        R.assert_near("y", y[0, at].double().cpu().numpy(), np.full(300, want), torch.bfloat16)
+    assert float((pool - pool[0, 0]).abs().max()) == 0
