@@ -368,9 +368,13 @@ template <typename T, int TENSORS> using Ring = Cell<T>[kStages][TENSORS];
 template <typename T, int TENSORS> __device__ __forceinline__ Ring<T, TENSORS> &ring_of(unsigned char *raw, int warp) {
     return reinterpret_cast<Ring<T, TENSORS> *>(raw)[warp];
 }
+static_assert(kMaxWarps * sizeof(Ring<float, 3>) <= 40 * 1024 && kMaxWarps * sizeof(Ring<__half, 3>) <= 40 * 1024,
+              "with its static part a CTA stays within the 48 KB that need no permission");
 __device__ __forceinline__ int next_stage(int s) { return s + 1 == kStages ? 0 : s + 1; }
 
-// (72 registers leave room for 28 warps an SM: every row of 1024 at once, four warps each)
+// 72 registers leave room for 28 warps an SM (forward_warps).  Forward, cold caches: 16x64x65536 bf16 74 us,
+// 64x96x3136 fp32 48, 4x300x40000 fp16 68, 2x400x100000 fp32 167.  Capped at 64, for 32 warps: 76, 50, 59 and
+// 167; at 80, for 24: 93, 52, 68 and 165.
 template <typename T, int CP, Mode MODE>
 __global__ void __maxnreg__(72) scan_planes_forward_kernel(const ScanArgs a, int segments, int rounds_per, float2 *maps) {
     extern __shared__ __align__(16) unsigned char raw[];
@@ -674,12 +678,7 @@ unsigned short_grid(const ScanArgs &a, const Plan &p) {
 
 template <typename... P, typename... A>
 cudaError_t launch(void (*kernel)(P...), unsigned grid, const Plan &p, size_t per_warp, cudaStream_t st, A... args) {
-    const size_t shared = p.warps * per_warp;
-    if (shared > 40 * 1024) {  // (the static part counts towards the default 48 KB, too)
-        const cudaError_t e = allow_shared(kernel, shared);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_kernel(kernel, grid, p.warps * 32, shared, st, 1, args...);
+    return launch_kernel(kernel, grid, p.warps * 32, p.warps * per_warp, st, 1, args...);
 }
 
 template <typename T, int CP> cudaError_t forward_typed(const ScanArgs &a, cudaStream_t st) {
