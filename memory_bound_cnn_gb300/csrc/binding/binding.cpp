@@ -355,30 +355,33 @@ Tensor grad_norm(TensorTable &table, int grad_dtype, double max_norm, const opti
     return out;
 }
 
-// config: address of the optimiser's wtconv_adamw_config.
-void adamw_step(TensorTable &table, uintptr_t config, const optional<Tensor> &clip, const py::object &stream) {
+// config: address of the optimiser's wtconv_adamw_config, which takes the step's rate and number.
+void adamw_step(TensorTable &table, uintptr_t config_address, double lr, long long step, const optional<Tensor> &clip,
+                const py::object &stream) {
+    wtconv_adamw_config *const config = reinterpret_cast<wtconv_adamw_config *>(config_address);
+    config->lr = lr, config->step = step;
     const c10::Device dev = table.device;
     const float *clip_p = array<float>(clip, "clip", {2}, dev);
     table.follow();
     const Call call(stream, dev);
     call.uses(clip);
-    check_status(wtconv_adamw_step(table.n, table.list, reinterpret_cast<const wtconv_adamw_config *>(config),
+    check_status(wtconv_adamw_step(table.n, table.list, config,
                                    clip_p != nullptr ? clip_p + 1 : nullptr, call.stream()),
                  "wtconv_adamw_step");
     table.stepped();
 }
 
-// The lists (m, v): the caller's, or new ones.
+// The lists (m, v) where they are new, None for one that the caller gave.
 py::tuple state_values(const TensorTable &table, const optional<std::vector<Tensor>> &m_given,
                        const optional<std::vector<Tensor>> &v_given, const py::object &stream) {
     const int n = table.n;
     const c10::Device dev = table.device;
     const Call call(stream, dev);
-    const auto outputs = [&](const optional<std::vector<Tensor>> &given) {
+    std::vector<Tensor> m_new, v_new;
+    const auto outputs = [&](const optional<std::vector<Tensor>> &given, std::vector<Tensor> &made) -> const std::vector<Tensor> & {
         if (given.has_value()) return *given;
-        std::vector<Tensor> ts;
-        for (int i = 0; i < n; ++i) ts.push_back(call.empty({(int64_t)table.list[i].n}, at::kFloat));
-        return ts;
+        for (int i = 0; i < n; ++i) made.push_back(call.empty({(int64_t)table.list[i].n}, at::kFloat));
+        return made;
     };
     const auto pointers = [&](const std::vector<Tensor> &ts, const char *name) {
         if ((int)ts.size() != n)
@@ -394,13 +397,12 @@ py::tuple state_values(const TensorTable &table, const optional<std::vector<Tens
         }
         return p;
     };
-    const std::vector<Tensor> m_out = outputs(m_given), v_out = outputs(v_given);
-    const std::vector<float *> m = pointers(m_out, "m_out"), v = pointers(v_out, "v_out");
+    const std::vector<float *> m = pointers(outputs(m_given, m_new), "m_out"), v = pointers(outputs(v_given, v_new), "v_out");
     check_status(wtconv_adamw_state_values(n, table.list, m.data(), v.data(), call.stream()), "wtconv_adamw_state_values");
     for (const auto *given : {&m_given, &v_given})
         if (given->has_value())
             for (const Tensor &t : **given) written(t);
-    return py::make_tuple(m_out, v_out);
+    return py::make_tuple(m_given.has_value() ? py::none() : py::cast(m_new), v_given.has_value() ? py::none() : py::cast(v_new));
 }
 
 }  // namespace

@@ -124,7 +124,7 @@ class AdamW:
             raise ValueError(f"gradients have unsupported dtype {dtype}")
         self._fill("grad", grads, dtype, "grads")
         self.grads = grads
-        self._config.grad_dtype = DTYPE_CODE[dtype]
+        self._config.grad_dtype = self._grad_dtype = DTYPE_CODE[dtype]
         self._norm_bytes = _load().wtconv_grad_norm_workspace_size(len(self.params), self._tensors)
 
     def state_dict(self):
@@ -133,24 +133,24 @@ class AdamW:
     def grad_norm(self, max_norm=float("inf"), out=None, workspace=None, stream=None) -> torch.Tensor:
         """Device tensor (norm, factor): the norm over every gradient and the factor that limits it
         to max_norm (NaN where the norm is not finite), for ``step(clip=...)``."""
-        return self._ext.grad_norm(self._table, self._config.grad_dtype, max_norm, out, workspace, self._norm_bytes, stream)
+        return self._ext.grad_norm(self._table, self._grad_dtype, max_norm, out, workspace, self._norm_bytes, stream)
 
     def step(self, clip=None, lr=None, count=None, stream=None) -> None:
         """One update of every parameter.  clip: what ``grad_norm`` returned (a factor that is not
         finite leaves everything as it is).  lr: the rate from this step on.  count: the step's
         number, from 1 (default: the next).  A captured graph replays this step's number."""
-        config = self._config
-        config.lr = self.lr if lr is None else lr
-        config.step = self.count + 1 if count is None else count
-        self._ext.adamw_step(self._table, self._scalars, clip, stream)
-        self.count, self.lr = config.step, config.lr
+        lr = self.lr if lr is None else lr
+        count = self.count + 1 if count is None else count
+        self._ext.adamw_step(self._table, self._scalars, lr, count, clip, stream)
+        self.count, self.lr = count, lr
 
     def state_values(self, m_out=None, v_out=None, stream=None):
         """The averages (m, v) as lists of fp32 tensors.  m_out, v_out: lists of fp32 tensors to write
         them to.  Where a list is not given, the states themselves in 32 bits, in 8 new tensors of what
         the codes stand for."""
         if self.state_bits == 8:
-            return self._ext.state_values(self._table, m_out, v_out, stream)
+            m, v = self._ext.state_values(self._table, m_out, v_out, stream)
+            return m_out if m is None else m, v_out if v is None else v
         lists = []
         for name, kind, out in (("m_out", "m", m_out), ("v_out", "v", v_out)):
             states = self.states[kind]
