@@ -87,7 +87,9 @@ size_t wtconv_grad_norm_workspace_size(int n_tensors, const wtconv_optim_tensor 
  * max_norm: min(1, max_norm / (norm + 1e-6)), or NaN where the norm is not finite.  out is device
  * memory that wtconv_adamw_step can take its clip from (out + 1), with no host in between.  Squares
  * are summed in fp32 over at most a few hundred elements of a thread and in fp64 beyond, in an order
- * that depends on the device and the tensors' sizes only.  max_norm > 0 (infinity: the factor is 1).  Reads only grad and n of each descriptor. */
+ * that depends on the device and on the tensors' sizes and 16-byte alignment only; a gradient above
+ * 1.8e19, whose square passes fp32, makes the norm infinite.  max_norm > 0 (infinity: the factor is
+ * 1).  Reads only grad and n of each descriptor. */
 int wtconv_grad_norm(int n_tensors, const wtconv_optim_tensor *tensors, int grad_dtype,
                      double max_norm, float *out, void *workspace, size_t workspace_bytes,
                      wtconv_stream_t stream);

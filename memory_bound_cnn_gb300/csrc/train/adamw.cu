@@ -3,8 +3,10 @@
 // One CTA per chunk of 2048 elements of one tensor, one warp per 256 of them (a block of the 8-bit
 // states), eight elements per lane in registers between the one read and the one write of each
 // array.  With 32-bit states the step runs at the rate of a copy (100 M elements with bf16 gradients and
-// a bf16 copy, 28 bytes each: 409 us, 6.8 TB/s).  With 8-bit states it is bound by the issue of
-// instructions (102 an element at 77 % of the issue slots; 130 M elements 451 us, 4.6 TB/s).
+// a bf16 copy, 28 bytes each: 409 us, 6.8 TB/s).  With 8-bit states (130 M elements 451 us, 4.6 TB/s) neither
+// HBM nor one unit is full: 102 instructions an element take 77 % of the issue slots, and the 64 registers
+// that they need leave 45 % of an SM's warps to cover the loads, the largest stall.  A form with 88
+// instructions and the same registers took as long (454 us), so issue alone does not bound it.
 #include <cooperative_groups.h>
 #include <float.h>
 
@@ -95,11 +97,11 @@ template <bool VEC> __device__ __forceinline__ void store_codes(uint8_t *p, long
 
 // ------------------------------------------------------------------------- 8-bit states
 // Products and sums that decide a code are rounded one by one (no fused multiply-add: `product`), so
-// that a code is a function of its inputs that any fp32 program can follow.  The step is bound by the issue
-// of instructions, so elements are worked on in pairs (Pair: one instruction for two), and bytes
-// become fp32 and back through 2^23 + n, whose last bits are n: conversion instructions run at an
-// eighth of the rate of an add.  130 M elements took 787 us one by one with conversions and exact
-// square roots, 551 us without those.
+// that a code is a function of its inputs that any fp32 program can follow.  Elements are worked on in pairs
+// (Pair: one instruction for two), and bytes become fp32 and back through 2^23 + n, whose last bits are n:
+// a conversion instruction runs at an eighth of the rate of an add, and the threshold's is the one that is
+// left for an element.  130 M elements took 787 us one by one with conversions and exact square roots, 551 us
+// without those.
 
 constexpr float kTwo23 = 8388608.f;
 
@@ -283,7 +285,7 @@ __device__ __forceinline__ void update(const wtconv_optim_tensor &t, const StepS
             const long long i = first + h * 128 + lane * 4;
             const uint32_t w = (uint32_t)i * kIndexStride + s.threshold0;
             FourCodes c;
-            if (four_codes<false>(m[h], v[h], roots[h], mi, vi, v_scale, w, zero, c.m, c.v))  // one warp in some hundred
+            if (four_codes<false>(m[h], v[h], roots[h], mi, vi, v_scale, w, zero, c.m, c.v))  // (rare)
                 c = exact_codes(m[h][0], m[h][1], v[h][0], v[h][1], mi, vi, w, zero);
             store_codes<VEC>(static_cast<uint8_t *>(t.m), i, n, c.m);
             store_codes<VEC>(static_cast<uint8_t *>(t.v), i, n, c.v);
