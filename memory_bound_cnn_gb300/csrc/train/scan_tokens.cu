@@ -134,8 +134,9 @@ template <typename T, int R> struct Loader<T, 2, R> {
 #pragma unroll
             for (int j = 0; j < kSpan; j += rows_at_once, from += rows_at_once * row) {
                 const bool valid = r0 + j < rows && bytes > 0;
-                if (j == 0 && from < anchor) {  // before the tensor: its first element alone
-                    *to = valid ? (uint32_t)*reinterpret_cast<const uint16_t *>(from + 1) << 16 : 0u;
+                // before the tensor (in its first row, or in every one where all rows are the same): its first element alone
+                if ((j == 0 || row == 0) && from < anchor) {
+                    to[j * Tile<T, 2, R>::words] = valid ? (uint32_t)*reinterpret_cast<const uint16_t *>(from + 1) << 16 : 0u;
                 } else {
                     copy_async<4>(to + j * Tile<T, 2, R>::words, valid ? from : none, valid ? bytes : 0);
                 }

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import scan_reference as R
 import torch
-from test_scan import DTYPES, make, reference, run
+from test_scan import DTYPES, check, make, reference, run
 
 from memory_bound_cnn_gb300 import scan as S
 from memory_bound_cnn_gb300 import wtconv as W
@@ -270,3 +270,48 @@ def test_step_of_the_most_channels():
         R.assert_near("pool", pool[0, at].double().cpu().numpy(), np.full(300, want))
         R.assert_near("y", y[0, at].double().cpu().numpy(), np.full(300, want), torch.bfloat16)
     assert float((pool - pool[0, 0]).abs().max()) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["planes", "tokens"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("start", [0, 1, 3])
+def test_repeated_rows(start, dtype, layout):
+    """One row for every position of tokens, one plane for every channel: a row stride of 0, also where the
+    row starts at an odd element.  What lies before the row is NaN.  Results are those of the same rows laid out."""
+    B, T, C = 3, 200, 40
+    d = make(B, T, C, layout, dtype, seed=32)
+    laid_out = dict(d)
+    for k in ("x", "gate", "dy"):
+        n = d[k].shape[2]
+        buf = torch.full((start + n,), float("nan"), dtype=dtype, device="cuda")
+        buf[start:] = d[k][0, 0]
+        d[k] = buf[start:].expand(d[k].shape)
+        laid_out[k] = d[k].contiguous()
+    want = run(laid_out, layout)
+    for k, t in run(d, layout).items():
+        assert torch.equal(t, want[k]) and torch.isfinite(t).all(), k
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["planes", "tokens"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=lambda t: str(t)[6:])
+def test_rows_past_32_bits(dtype, layout):
+    """Rows of one sequence further apart than 2^31 elements in all, at any alignment."""
+    B, T, C = (1, 130, 24) if layout == "tokens" else (1, 700, 130)
+    d = make(B, T, C, layout, dtype, seed=26)
+    want = reference(d, layout)
+    rows, inner = d["x"].shape[1:]
+    for odd in (0, 1):
+        row = (1 << 24) + 1024 + odd
+        store = torch.empty(rows * row, dtype=dtype, device="cuda")
+
+        def far(t, k):
+            view = store.as_strided(t.shape, (rows * row, row, 1), k * 1024)
+            view.copy_(t)
+            return view
+
+        got = run({**d, "x": far(d["x"], 0), "gate": far(d["gate"], 1), "dy": far(d["dy"], 2)}, layout,
+                  dx=far(d["x"] * 0, 3), d_gate=far(d["x"] * 0, 4))
+        check(got, want, layout, dtype)
+        del got, store
