@@ -134,9 +134,11 @@ template <typename T, int R> struct Loader<T, 2, R> {
 #pragma unroll
             for (int j = 0; j < kSpan; j += rows_at_once, from += rows_at_once * row) {
                 const bool valid = r0 + j < rows && bytes > 0;
-                // before the tensor (in its first row, or in every one where all rows are the same): its first element alone
-                if ((j == 0 || row == 0) && from < anchor) {
-                    to[j * Tile<T, 2, R>::words] = valid ? (uint32_t)*reinterpret_cast<const uint16_t *>(from + 1) << 16 : 0u;
+                // Before the tensor: its first element alone.  (A row stride of 0 has more rows there, which read the
+                // whole word that holds that element: it is aligned, so all of it is memory of the same allocation,
+                // and the other half is dropped.  With the test in every row odd rows took 20 to 40 % longer.)
+                if (j == 0 && from < anchor) {
+                    *to = valid ? (uint32_t)*reinterpret_cast<const uint16_t *>(from + 1) << 16 : 0u;
                 } else {
                     copy_async<4>(to + j * Tile<T, 2, R>::words, valid ? from : none, valid ? bytes : 0);
                 }
