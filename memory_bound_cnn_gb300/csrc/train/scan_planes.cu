@@ -15,9 +15,9 @@
 // segment starts from the maps before it (after it, backward).  That reads two of the inputs twice, the
 // second time mostly from L2.
 //
-// Bound by HBM, closely followed by the issue of instructions (25 an element forward, 34 backward, at
-// 65 % and 51 % of the issue slots).  Alone, with cold caches: 16x64x65536 bf16 forward 74 us (5.4 TB/s,
-// 81 % of a copy), backward 129 us (5.2 TB/s, 78 %); 64x96x3136 fp32 48 us (72 %) and 74 us (78 %).
+// Bound by HBM, closely followed by the issue of instructions (25 an element forward, 35 backward, at
+// 67 % and 53 % of the issue slots).  Alone, with cold caches: 16x64x65536 bf16 forward 75 us (5.3 TB/s,
+// 80 % of a copy), backward 129 us (5.2 TB/s, 78 %); 64x96x3136 fp32 49 us (70 %) and 74 us (78 %).
 // With eight positions a lane the shuffles and the exchange weighed twice as much (83 and 146 us).
 #include "scan_device.cuh"
 

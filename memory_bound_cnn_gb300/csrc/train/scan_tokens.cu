@@ -20,8 +20,9 @@
 //
 // Bound by the latency of a round's exchange and, after it, by the issue of instructions (25 an element
 // forward, 34 backward): the four (backward two) CTAs that fit an SM overlap their rounds only so far.
-// Alone, with cold caches: 32x2048x768 bf16 ragged forward 59 us (5.1 TB/s, 77 % of a copy, padding
-// counted), 8x4096x1024 bf16 forward 54 us and backward 92 us (3.7 TB/s, 55 %).
+// Alone, with cold caches: 8x4096x1024 bf16 forward 55 us and backward 88 us (3.7 and 3.8 TB/s, 55 and 57 %
+// of a copy), fp32 85 and 136 us (71 and 74 %).  32x2048x768 bf16 forward of ragged sequences that fill 48 %
+// of their rows 59 us: 3.4 TB/s of what is read and written, half of a copy.
 #include <cooperative_groups.h>
 
 #include <initializer_list>
