@@ -12,6 +12,7 @@
 #include <climits>
 #include <cstddef>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "wtconv.h"
@@ -265,10 +266,11 @@ class TensorTable {
     // One tensor per descriptor, whose addresses go to the field at `offset`.  The tensor has one element
     // for every `per` of the parameter's (which `params` sets the number of); None is allowed where
     // `may_be_none` says so.
-    void fill(const std::vector<optional<Tensor>> &ts, size_t offset, at::ScalarType dtype, int64_t per, const std::string &name,
+    void fill(std::vector<optional<Tensor>> given, size_t offset, at::ScalarType dtype, int64_t per, const std::string &name,
               bool params, bool may_be_none) {
-        if ((int)ts.size() != n) refuse(std::to_string(ts.size()) + " tensors in " + name + " for " + std::to_string(n) + " parameters");
-        const Field f = {ts, offset, dtype, name, may_be_none};
+        if ((int)given.size() != n) refuse(std::to_string(given.size()) + " tensors in " + name + " for " + std::to_string(n) + " parameters");
+        Field f = {std::move(given), offset, dtype, name, may_be_none};
+        const std::vector<optional<Tensor>> &ts = f.ts;
         for (int i = 0; i < n; ++i) f.check(i, params && ts[i].has_value() ? ts[i]->numel() : (list[i].n + per - 1) / per, device);
         if (params) refuse_overlaps(ts, name);
         for (int i = 0; i < n; ++i) {  // (only once all of them are right)
@@ -276,9 +278,9 @@ class TensorTable {
             if (params) list[i].n = ts[i]->numel();
             f.address(list[i]) = ts[i]->data_ptr();
         }
-        if (params) params_ = f;
-        else if (offset == offsetof(wtconv_optim_tensor, grad)) grads_ = f;
-        else if (offset == offsetof(wtconv_optim_tensor, copy)) copies_ = f;
+        if (params) params_ = std::move(f);
+        else if (offset == offsetof(wtconv_optim_tensor, grad)) grads_ = std::move(f);
+        else if (offset == offsetof(wtconv_optim_tensor, copy)) copies_ = std::move(f);
     }
     // Before every use: tensors whose memory is another by now (`p.data = ...` gives one a new storage)
     // are checked again and followed.
@@ -318,6 +320,7 @@ class TensorTable {
             int which;
         };
         std::vector<Range> ranges;
+        ranges.reserve(ts.size());
         for (int i = 0; i < (int)ts.size(); ++i) {
             const char *const p = static_cast<const char *>(ts[i]->const_data_ptr());
             if (ts[i]->numel() > 0) ranges.push_back({p, p + ts[i]->nbytes(), i});
