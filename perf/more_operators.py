@@ -303,8 +303,9 @@ def _own_norm_train(s):
     from memory_bound_cnn_gb300 import wtconv_rms_backward, wtconv_rms_forward
 
     y, total, rstd = wtconv_rms_forward(s["x"], s["weight"], residual=s["residual"], eps=EPS)
-    dx, d_residual, d_weight = wtconv_rms_backward(s["dy"], total, s["weight"], rstd, d_total=s["d_total"])
-    return y, None if s["residual"] is None else total, dx, d_residual, d_weight
+    added = s["residual"] is not None
+    dx, d_residual, d_weight = wtconv_rms_backward(s["dy"], total, s["weight"], rstd, d_total=s["d_total"], residual=added)
+    return y, total if added else None, dx, d_residual, d_weight
 
 
 # ------------------------------------------------------------------------------- plain forms
