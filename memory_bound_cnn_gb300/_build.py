@@ -20,7 +20,7 @@ CSRC_TRAIN = os.path.join(CSRC, "train")  # operators beside the layer: gated sc
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libwtconv.so")
-BINDING_SRC = os.path.join(CSRC, "binding", "binding.cpp")
+CSRC_BINDING = os.path.join(CSRC, "binding")
 BINDING = os.path.join(PKG, "_binding.so")
 BINDING_KEY = os.path.join(PKG, "_binding.key")  # the PyTorch and Python that _binding.so was built for
 
@@ -46,18 +46,19 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _compile_binding() -> tuple[list[str], str]:
-    """Command that compiles the binding's object, and the object."""
+def _compile_binding() -> list[tuple[list[str], str]]:
+    """Commands that compile the binding's objects, each with its object."""
     import torch
 
     torch_dir = os.path.dirname(torch.__file__)
-    obj = os.path.join(BUILD, "binding.o")
     includes = [INCLUDE, os.path.join(torch_dir, "include"),
                 os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", *["-I" + d for d in includes],
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-c", BINDING_SRC, "-o", obj]
-    return cmd, obj
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    objs = [(src, os.path.join(BUILD, "binding_" + os.path.basename(src)[:-4] + ".o"))
+            for src in sorted(glob.glob(os.path.join(CSRC_BINDING, "*.cpp")))]
+    return [([*cmd, "-c", src, "-o", obj], obj) for src, obj in objs]
 
 
 def _binding_key() -> str:
@@ -69,7 +70,7 @@ def _binding_key() -> str:
 
 def binding_stale() -> bool:
     """Whether the binding is missing, older than its sources, or built for another PyTorch or Python."""
-    if _stale(BINDING, [BINDING_SRC, *glob.glob(os.path.join(INCLUDE, "*.h")), __file__]):
+    if _stale(BINDING, [*glob.glob(os.path.join(CSRC_BINDING, "*")), *glob.glob(os.path.join(INCLUDE, "*.h")), __file__]):
         return True
     try:
         with open(BINDING_KEY) as f:
@@ -78,12 +79,12 @@ def binding_stale() -> bool:
         return True
 
 
-def _link_binding(obj: str) -> None:
+def _link_binding(objs: list[str]) -> None:
     import torch
 
     lib_dir = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + f".{os.getpid()}.tmp"
-    subprocess.run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L" + os.path.dirname(LIB), "-l:libwtconv.so",
+    subprocess.run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, *objs, "-L" + os.path.dirname(LIB), "-l:libwtconv.so",
                     "-Wl,-rpath,$ORIGIN", "-L" + lib_dir, "-Wl,-rpath," + lib_dir, "-ltorch_python", "-ltorch", "-ltorch_cpu",
                     "-ltorch_cuda", "-lc10", "-lc10_cuda"], check=True)
     os.replace(tmp, BINDING)
@@ -138,24 +139,25 @@ def build(force: bool = False, verbose: bool = False, binding: bool = True) -> s
     """Build what is missing or stale: the library, and with ``binding`` the compiled binding beside it;
     returns the library's path.  The library needs nothing of the binding, and is built where that fails."""
     os.makedirs(BUILD, exist_ok=True)
-    compiling, failure = None, None
+    compiling, failure, objs = [], None, []
     if binding and (force or binding_stale()):
-        cmd, obj = _compile_binding()
         try:
-            compiling = _start(cmd, verbose)
+            for cmd, obj in _compile_binding():
+                compiling.append(_start(cmd, verbose))
+                objs.append(obj)
         except OSError as e:  # no compiler for it
             failure = e
     try:
         _build_library(force, verbose)
     except BaseException:
-        if compiling is not None:
-            compiling[1].communicate()
+        for _, p in compiling:
+            p.communicate()
         raise
     if failure is not None:
         raise failure
-    if compiling is not None:
-        _finish([compiling])
-        _link_binding(obj)
+    if compiling:
+        _finish(compiling)
+        _link_binding(objs)
     return LIB
 
 

@@ -11,25 +11,10 @@ int check_shape(int B, int T, int C, int layout, int dtype) {
     return dtype_ok(dtype) ? WTCONV_OK : WTCONV_ERR_UNSUPPORTED;
 }
 
-// Strides of one activation: >= 0, offsets far from 2^63, and for an output no two elements at
-// one place (the axis of smaller stride must end before the other's next step).
 bool check_tensor(const ScanTensor &s, const ScanArgs &a, bool output) {
     const long long inner = a.layout == WTCONV_SCAN_PLANES ? a.T : a.C, rows = a.layout == WTCONV_SCAN_PLANES ? a.C : a.T;
-    const long long limit = 1ll << 59;
-    if (s.p == nullptr || !aligned_to(s.p, elem_bytes_of(a.dtype)) || s.batch < 0 || s.row < 0) return false;
-    if ((a.B > 1 && s.batch > limit / a.B) || (rows > 1 && s.row > limit / rows)) return false;
-    if (!output) return true;
-    const bool by_row = rows > 1, by_batch = a.B > 1;
-    if (by_row && by_batch) {
-        const bool row_first = s.row <= s.batch;
-        const long long small = row_first ? s.row : s.batch, large = row_first ? s.batch : s.row;
-        const long long count = row_first ? rows : a.B;
-        return small >= inner && large >= small * (count - 1) + inner;
-    }
-    return (!by_row || s.row >= inner) && (!by_batch || s.batch >= inner);
+    return activation_ok(s.p, s.batch, s.row, a.B, rows, inner, a.dtype, output);
 }
-
-bool f32_ok(const void *p, bool optional) { return (p != nullptr || optional) && aligned_to(p, 4); }
 
 ScanTensor input(const void *p, long long batch, long long row) { return {const_cast<void *>(p), batch, row}; }
 

@@ -24,6 +24,26 @@ inline bool fault_injected() {
 }
 inline int status_of(cudaError_t e) { return e == cudaSuccess ? WTCONV_OK : WTCONV_ERR_CUDA; }
 
+// Strides of an activation [B][rows][inner] whose innermost axis is contiguous: >= 0, offsets far from
+// 2^63, and for an output no two elements at one place (the axis of smaller stride must end before the
+// other's next step).
+inline bool activation_ok(const void *p, long long batch, long long row, long long B, long long rows, long long inner, int dtype,
+                          bool output) {
+    const long long limit = 1ll << 59;
+    if (p == nullptr || !aligned_to(p, elem_bytes_of(dtype)) || batch < 0 || row < 0) return false;
+    if ((B > 1 && batch > limit / B) || (rows > 1 && row > limit / rows)) return false;
+    if (!output) return true;
+    const bool by_row = rows > 1, by_batch = B > 1;
+    if (by_row && by_batch) {
+        const bool row_first = row <= batch;
+        const long long small = row_first ? row : batch, large = row_first ? batch : row;
+        const long long count = row_first ? rows : B;
+        return small >= inner && large >= small * (count - 1) + inner;
+    }
+    return (!by_row || row >= inner) && (!by_batch || batch >= inner);
+}
+inline bool f32_ok(const void *p, bool optional) { return (p != nullptr || optional) && aligned_to(p, 4); }
+
 // SMs of the current device (148 if it cannot be asked: a plan is then only less balanced)
 inline int sm_count() {
     int dev = 0, sms = 0;

@@ -69,6 +69,22 @@ __device__ __forceinline__ Pair abs(Pair a) {
     return r;
 }
 
+// V neighbouring elements, in one access of up to 16 bytes (several where they are more).
+template <typename T, int V> struct alignas(sizeof(T) * V > 16 ? 16 : sizeof(T) * V) Vec {
+    T v[V];
+};
+template <typename T, int V> __device__ __forceinline__ void load_vec(const T *p, float (&to)[V]) {
+    const Vec<T, V> q = *reinterpret_cast<const Vec<T, V> *>(p);
+#pragma unroll
+    for (int i = 0; i < V; ++i) to[i] = to_f32(q.v[i]);
+}
+template <typename T, int V> __device__ __forceinline__ void store_vec(T *p, const float (&from)[V]) {
+    Vec<T, V> q;
+#pragma unroll
+    for (int i = 0; i < V; ++i) q.v[i] = from_f32<T>(from[i]);
+    *reinterpret_cast<Vec<T, V> *>(p) = q;
+}
+
 __device__ __forceinline__ float reciprocal(float v) {  // to about one unit of the last place
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
