@@ -5,6 +5,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "train_common.h"
 #include "wtconv_ssm.h"
 
@@ -23,6 +25,7 @@ struct SelectiveArgs {
     int channels;       // of a group
     int tiles;          // of a group, kSelTile channels each (the last may have fewer)
     int lanes, padded;  // selective_lanes(N), and 4 states for each
+    bool wide;          // pairs of neighbours lie at multiples of their size in every activation but B and C
     int keep;           // kept states of a sequence, ceil(T / kSelKeep)
     int segments, segment;  // parts of a sequence that different CTAs scan, and positions of each
     wtconv_ssm_tensor y, dy;
@@ -37,6 +40,22 @@ struct SelectiveArgs {
     float *part_c;  // [2][B][segments][C]: dD, d_dt_bias
     __host__ __device__ int ctas() const { return s.B * s.G * tiles; }  // of one segment
 };
+
+// f(lanes, planes, wide) as constants.
+template <typename F> cudaError_t with_selective_shape(const SelectiveArgs &a, F f) {
+    const auto with_lanes = [&](auto planes, auto wide) {
+        switch (a.lanes) {
+            case 2: return f(std::integral_constant<int, 2>(), planes, wide);
+            case 4: return f(std::integral_constant<int, 4>(), planes, wide);
+            case 8: return f(std::integral_constant<int, 8>(), planes, wide);
+            default: return f(std::integral_constant<int, 16>(), planes, wide);
+        }
+    };
+    const bool planes = a.s.layout == WTCONV_SCAN_PLANES;
+    const std::true_type yes;
+    const std::false_type no;
+    return planes ? (a.wide ? with_lanes(yes, yes) : with_lanes(yes, no)) : (a.wide ? with_lanes(no, yes) : with_lanes(no, no));
+}
 
 template <typename T> cudaError_t launch_selective_forward(const SelectiveArgs &a, cudaStream_t st);
 template <typename T> cudaError_t launch_selective_backward(const SelectiveArgs &a, cudaStream_t st);

@@ -30,10 +30,24 @@ bool inputs_ok(const SelectiveArgs &a) {
            f32_ok(in.dt_bias, true) && f32_ok(in.h0, true) && f32_ok(in.lengths, true);
 }
 
+// Whether pairs of neighbours along the contiguous axis lie at multiples of their size.
+bool pairs(const wtconv_ssm_tensor &t, const wtconv_selective_shape &s) {
+    const bool rows = (s.layout == WTCONV_SCAN_PLANES ? s.C : s.T) > 1;
+    return t.p == nullptr || (aligned_to(t.p, 2 * elem_bytes_of(s.dtype)) && (!rows || t.row % 2 == 0) && (s.B == 1 || t.batch % 2 == 0));
+}
+// (a group's first channel has to be even too, where channels are neighbours)
+bool pairs(const SelectiveArgs &a) {
+    if (a.s.layout == WTCONV_SCAN_TOKENS && a.s.G > 1 && a.channels % 2 != 0) return false;
+    for (const wtconv_ssm_tensor *t : {&a.in.x, &a.in.dt, &a.in.z, &a.y, &a.dy, &a.g.dx, &a.g.d_dt, &a.g.dz})
+        if (!pairs(*t, a.s)) return false;
+    return true;
+}
+
 // Parts that a sequence is cut into.  Cutting costs a second pass over x, dt and B (the forward) or dy, z and
 // C, so it is for shapes whose sequences and channels alone leave the GPU's SMs short of warps.
 void plan(int op, SelectiveArgs &a) {
-    const int threads = kSelTile * a.lanes, wanted = sm_count() * (op == WTCONV_SCAN_OP_FORWARD ? 512 : 384) / threads;
+    const char *env = getenv(op == WTCONV_SCAN_OP_FORWARD ? "SEL_F" : "SEL_B");  // TEMP
+    const int threads = kSelTile * a.lanes, wanted = sm_count() * (env ? atoi(env) : op == WTCONV_SCAN_OP_FORWARD ? 512 : 384) / threads;
     const int rounds = ceil_div(a.s.T, kSelRound), most = std::max(1, std::min(rounds / 4, 256));
     const int parts = std::min(most, std::max(1, wanted / std::max(1, a.ctas())));
     const int per = ceil_div(rounds, parts);
@@ -106,6 +120,7 @@ int wtconv_selective_forward(const wtconv_selective_shape *shape, const wtconv_s
     a.in = *in, a.y = *y, a.h_last = h_last, a.states_out = states;
     if (!grid_ok(a) || !inputs_ok(a) || !check_tensor(a.y, a.s, a.s.C, true) || !f32_ok(h_last, true) || !aligned_to(states, 16))
         return WTCONV_ERR_INVALID_ARG;
+    a.wide = pairs(a);
     plan(WTCONV_SCAN_OP_FORWARD, a);
     const size_t need = place(WTCONV_SCAN_OP_FORWARD, a, workspace);
     if ((rc = check_workspace(need, workspace, workspace_bytes)) != WTCONV_OK) return rc;
@@ -131,6 +146,8 @@ int wtconv_selective_backward(const wtconv_selective_shape *shape, const wtconv_
         return WTCONV_ERR_INVALID_ARG;
     if (a.in.D == nullptr) a.g.dD = nullptr;
     if (a.in.dt_bias == nullptr) a.g.d_dt_bias = nullptr;
+    if (a.in.z.p == nullptr) a.g.dz = {};
+    a.wide = pairs(a);
     plan(WTCONV_SCAN_OP_BACKWARD, a);
     const size_t need = place(WTCONV_SCAN_OP_BACKWARD, a, workspace);
     if ((rc = check_workspace(need, workspace, workspace_bytes)) != WTCONV_OK) return rc;

@@ -25,20 +25,27 @@ __device__ __forceinline__ Pair exp2_fast(Pair v) { return {exp2_fast(v.lo()), e
 
 // softplus(v) = max(v, 0) + log(1 + e) with e = exp(-|v|) in (0, 1]: nothing cancels.  With s = e / (2 + e)
 // <= 1/3, log(1 + e) = 2 artanh s = 2 (s + s^3/3 + ... + s^13/13); the next term is 1.4e-8 of the value.
-// slope: sigmoid(v), from the same e.
-struct Softplus {
-    float value, slope;
-};
-__device__ __forceinline__ Softplus softplus_of(float v) {
-    const float e = exp2_fast(-kSelLog2E * fabsf(v));
-    const float s = e * reciprocal(2.f + e), q = s * s;
-    float p = 1.f / 13;
-    p = fmaf(p, q, 1.f / 11), p = fmaf(p, q, 1.f / 9), p = fmaf(p, q, 1.f / 7);
-    p = fmaf(p, q, 1.f / 5), p = fmaf(p, q, 1.f / 3), p = fmaf(p, q, 1.f);
-    const float r = reciprocal(1.f + e);
-    return {fmaxf(v, 0.f) + 2.f * s * p, v >= 0.f ? r : e * r};
+__device__ __forceinline__ Pair exp_of_minus_abs(Pair v) {
+    return {exp2_fast(-kSelLog2E * fabsf(v.lo())), exp2_fast(-kSelLog2E * fabsf(v.hi()))};
 }
-__device__ __forceinline__ float sigmoid_of(float v) { return reciprocal(1.f + exp2_fast(-kSelLog2E * v)); }
+__device__ __forceinline__ Pair reciprocal(Pair v) { return {reciprocal(v.lo()), reciprocal(v.hi())}; }
+__device__ __forceinline__ Pair softplus_of(Pair v, Pair e) {
+    const Pair s = mul(e, reciprocal(add(e, Pair(2.f)))), q = mul(s, s);
+    Pair p = fma(Pair(1.f / 13), q, Pair(1.f / 11));
+    p = fma(p, q, Pair(1.f / 9)), p = fma(p, q, Pair(1.f / 7)), p = fma(p, q, Pair(1.f / 5)), p = fma(p, q, Pair(1.f / 3));
+    p = fma(p, q, Pair(1.f));
+    return fma(add(s, s), p, Pair(fmaxf(v.lo(), 0.f), fmaxf(v.hi(), 0.f)));
+}
+__device__ __forceinline__ Pair softplus_of(Pair v) { return softplus_of(v, exp_of_minus_abs(v)); }
+// Its slope sigmoid(v), from the same e.
+__device__ __forceinline__ Pair softplus_slope(Pair v, Pair e) {
+    const Pair r = reciprocal(add(e, Pair(1.f))), s = mul(e, r);
+    return {v.lo() >= 0.f ? r.lo() : s.lo(), v.hi() >= 0.f ? r.hi() : s.hi()};
+}
+__device__ __forceinline__ Pair sigmoid_of(Pair v) {
+    const Pair w = mul(v, Pair(-kSelLog2E));
+    return reciprocal(add(exp2_fast(w), Pair(1.f)));
+}
 
 // Element (position, channel) of an activation.
 template <typename T, bool PLANES>
@@ -47,9 +54,9 @@ __device__ __forceinline__ T *at(const wtconv_ssm_tensor &t, int b, int position
     return static_cast<T *>(t.p) + b * t.batch + outer * t.row + inner;
 }
 
-// Sums v[0..COUNT) over the lanes that differ in the COUNT * FIRST ... bits: lanes FIRST, 2 FIRST, ... apart
-// exchange halves, so that COUNT sums over COUNT lanes take COUNT - 1 exchanges.  A lane ends with the sum
-// of v[i] in v[0], i its index among the COUNT lanes.
+// Sums v[0..COUNT) over COUNT lanes whose numbers differ by multiples of FIRST below COUNT * FIRST: they exchange
+// halves, so that COUNT sums take COUNT - 1 exchanges.  A lane ends with the sum of v[i] in v[0], i its index
+// among the COUNT lanes.
 template <int COUNT, int FIRST> __device__ __forceinline__ void sum_exchange(float (&v)[COUNT], int index) {
 #pragma unroll
     for (int w = COUNT / 2; w >= 1; w /= 2) {
@@ -61,6 +68,19 @@ template <int COUNT, int FIRST> __device__ __forceinline__ void sum_exchange(flo
         }
     }
 }
+
+// A lane's place in a CTA of LANES warps: a warp has 32 / LANES channels, neighbouring lanes neighbouring channels,
+// and LANES lanes with four states each to a channel.  (Lanes that read the same 16 bytes of B or C are then
+// neighbours: such a load takes two cycles of the shared memory, and four where they lie apart.)
+template <int LANES> struct LanePlace {
+    static constexpr int CHANNELS = 32 / LANES;
+    int warp, cl, c, quad, n0;
+    __device__ __forceinline__ LanePlace() {
+        const int lane = threadIdx.x % 32;
+        warp = threadIdx.x / 32, cl = lane % CHANNELS, quad = lane / CHANNELS;
+        c = warp * CHANNELS + cl, n0 = 4 * quad;
+    }
+};
 
 // What a CTA works on: a tile of channels of one group, a segment of one sequence.
 struct Place {
@@ -76,6 +96,163 @@ struct Place {
         length = a.in.lengths == nullptr ? a.s.T : min(max(a.in.lengths[b], 0), a.s.T);
         first = segment * a.segment;
         end = min(first + a.segment, a.s.T);  // (segment * segments < 2^31: segments are at most 256 rounds more than T)
+    }
+};
+
+// A pair of neighbours, and a single element, as they lie in memory.  What is fetched ahead stays a whole register in
+// this form until it is used: packed or converted, it would have to arrive first.
+template <typename T> struct Raw {
+    using Two = typename std::conditional<sizeof(T) == 2, uint32_t, unsigned long long>::type;
+    using One = uint32_t;
+};
+template <typename T> __device__ __forceinline__ uint32_t load_one(const T *p) {
+    if constexpr (sizeof(T) == 2) return *reinterpret_cast<const unsigned short *>(p);
+    else return *reinterpret_cast<const uint32_t *>(p);
+}
+template <typename T> __device__ __forceinline__ typename Raw<T>::Two two_of(uint32_t first, uint32_t second) {
+    if constexpr (sizeof(T) == 2) return first | second << 16;
+    else return first | (unsigned long long)second << 32;
+}
+template <typename T> __device__ __forceinline__ Pair pair_of(typename Raw<T>::Two v) {
+    if constexpr (std::is_same<T, float>::value) return Pair(v);
+    else if constexpr (std::is_same<T, __half>::value) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v));
+        return {f.x, f.y};
+    } else return {__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)};
+}
+template <typename T> __device__ __forceinline__ float f32_of(uint32_t v) {
+    if constexpr (std::is_same<T, float>::value) return __uint_as_float(v);
+    else if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half((unsigned short)v));
+    else return __uint_as_float(v << 16);
+}
+// Where a fetched value is first used: the compiler would otherwise move what is done with it up to the load.
+__device__ __forceinline__ void arrived(uint32_t &v) { asm volatile("" : "+r"(v)); }
+__device__ __forceinline__ void arrived(unsigned long long &v) { asm volatile("" : "+l"(v)); }
+template <typename V, int COUNT> __device__ __forceinline__ void arrived(V (&v)[COUNT]) {
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) arrived(v[i]);
+}
+
+// A thread's part of ROUND positions of 32 channels: pairs of neighbours along the axis that is contiguous.  All
+// of a round's loads are issued before the first is used (a load that waits behind a branch on another's value
+// makes a round as long as all their latencies together).  WIDE: pairs lie at multiples of their size.
+// A round of the tile in shared memory has 32 channels to a position (tokens) or ROUND positions to a channel
+// (planes), rows apart such that neither pairs nor a warp's lanes, one position or one channel apart, meet on a bank.
+template <bool PLANES, int LANES, int ROUND, bool WIDE> struct Share {
+    static constexpr int THREADS = kSelTile * LANES, INNER = (PLANES ? ROUND : kSelTile) / 2, PAIRS = kSelTile * ROUND / 2;
+    static constexpr int COUNT = PAIRS < THREADS ? 1 : PAIRS / THREADS, STEP = THREADS / INNER, OWN = PLANES ? COUNT : 1;
+    // rows of coefficients (two floats) and of values that the lanes write (one).  Of a channel's lanes PARTS write their
+    // part of a sum (with 8 or 16 lanes, 2 or 4 of them meet by exchanges first); parts lie APART.
+    static constexpr int COEF = PLANES ? ROUND + 2 : kSelTile, COEFS = COEF * (PLANES ? kSelTile : ROUND);
+    static constexpr int VALUE = PLANES ? ROUND + 4 : kSelTile, VALUES = VALUE * (PLANES ? kSelTile : ROUND);
+    static constexpr int PARTS = LANES < 4 ? LANES : 4, TOGETHER = LANES / PARTS, APART = VALUES + (PLANES ? 2 : kSelTile / PARTS);
+    static __device__ __forceinline__ int coef(int t, int c) { return PLANES ? c * COEF + t : t * COEF + c; }
+    static __device__ __forceinline__ int value(int t, int c) { return PLANES ? c * VALUE + t : t * VALUE + c; }
+    // the lane's part of TOGETHER positions' sums from t on
+    static __device__ __forceinline__ void put_sums(float *sums, int t, int c, int quad, float (&v)[TOGETHER]) {
+        if (TOGETHER > 1) sum_exchange<TOGETHER, 32 / LANES>(v, quad % TOGETHER);
+        sums[quad / TOGETHER * APART + value(t + quad % TOGETHER, c)] = v[0];
+    }
+    static __device__ __forceinline__ Pair get_sums(const float *sums, int place) {
+        Pair s(*reinterpret_cast<const unsigned long long *>(sums + place));
+#pragma unroll
+        for (int i = 1; i < PARTS; ++i) s = add(s, Pair(*reinterpret_cast<const unsigned long long *>(sums + i * APART + place)));
+        return s;
+    }
+    int inner, outer;  // of the first pair
+    __device__ __forceinline__ Share() : inner(threadIdx.x % INNER * 2), outer(threadIdx.x / INNER) {}
+    static __device__ __forceinline__ bool busy() { return PAIRS >= THREADS || threadIdx.x < PAIRS; }
+    __device__ __forceinline__ int channel(int i) const { return PLANES ? outer + i * STEP : inner; }
+    __device__ __forceinline__ int position(int i) const { return PLANES ? inner : outer + i * STEP; }
+    // whether the pair's k-th element is one of `channels` and `count`
+    __device__ __forceinline__ bool in(int i, int k, int channels, int count) const {
+        return busy() && channel(i) + (PLANES ? 0 : k) < channels && position(i) + (PLANES ? k : 0) < count;
+    }
+    // base: of the round's first position and the tile's first channel
+    template <typename T>
+    __device__ __forceinline__ void load(const T *base, long long row, int channels, int count, typename Raw<T>::Two (&v)[COUNT]) const {
+        const T *p = base + outer * row + inner;
+        const long long step = STEP * row;
+        if (WIDE && PAIRS >= THREADS && channels == kSelTile && count >= ROUND) {
+#pragma unroll
+            for (int i = 0; i < COUNT; ++i) v[i] = *reinterpret_cast<const typename Raw<T>::Two *>(p + i * step);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            uint32_t first = 0, second = 0;
+            if (in(i, 0, channels, count)) first = load_one(p + i * step);
+            if (in(i, 1, channels, count)) second = load_one(p + i * step + 1);
+            v[i] = two_of<T>(first, second);
+        }
+    }
+    // value(i), a Pair, to its place
+    template <typename T, typename F> __device__ __forceinline__ void store(T *base, long long row, int channels, int count, F value) const {
+        T *p = base + outer * row + inner;
+        const long long step = STEP * row;
+        if (WIDE && PAIRS >= THREADS && channels == kSelTile && count >= ROUND) {
+#pragma unroll
+            for (int i = 0; i < COUNT; ++i) {
+                const Pair v = value(i);
+                Vec<T, 2> q;
+                q.v[0] = from_f32<T>(v.lo()), q.v[1] = from_f32<T>(v.hi());
+                *reinterpret_cast<Vec<T, 2> *>(p + i * step) = q;
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            if (!in(i, 0, channels, count)) continue;
+            const Pair v = value(i);
+            p[i * step] = from_f32<T>(v.lo());
+            if (in(i, 1, channels, count)) p[i * step + 1] = from_f32<T>(v.hi());
+        }
+    }
+    // 0 to a round that may begin at an odd position: an element at a time
+    template <typename T> __device__ __forceinline__ void clear(T *base, long long row, int channels, int count) const {
+        T *p = base + outer * row + inner;
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            if (in(i, 0, channels, count)) p[i * STEP * row] = from_f32<T>(0.f);
+            if (in(i, 1, channels, count)) p[i * STEP * row + 1] = from_f32<T>(0.f);
+        }
+    }
+    // one fp32 parameter for each channel of the thread's pairs
+    __device__ __forceinline__ void parameters(const float *of_tile, int channels, Pair (&v)[OWN]) const {
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            const int c = channel(i);
+            const float a = of_tile != nullptr && c < channels ? of_tile[c] : 0.f;
+            v[i] = Pair(a, PLANES ? a : of_tile != nullptr && c + 1 < channels ? of_tile[c + 1] : 0.f);
+        }
+    }
+};
+// The same of ROUND positions of a group's N states (padded to PAD).
+template <bool PLANES, int LANES, int ROUND> struct MapShare {
+    static constexpr int THREADS = kSelTile * LANES, PAD = 4 * LANES, COUNT = PAD * ROUND / THREADS;
+    static_assert(THREADS % ROUND == 0 && THREADS % PAD == 0, "");
+    int first_state, first_position;
+    __device__ __forceinline__ MapShare() {
+        first_state = PLANES ? threadIdx.x / ROUND : threadIdx.x % PAD;
+        first_position = PLANES ? threadIdx.x % ROUND : threadIdx.x / PAD;
+    }
+    __device__ __forceinline__ int state(int i) const { return PLANES ? first_state + i * (THREADS / ROUND) : first_state; }
+    __device__ __forceinline__ int position(int i) const { return PLANES ? first_position : first_position + i * (THREADS / PAD); }
+    template <typename T> __device__ __forceinline__ void load(const T *base, long long row, int N, int count, uint32_t (&v)[COUNT]) const {
+        const T *p = base + (PLANES ? first_state * row + first_position : first_position * row + first_state);
+        const long long step = (PLANES ? THREADS / ROUND : THREADS / PAD) * row;
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i, p += step) {
+            v[i] = 0;
+            if (state(i) < N && position(i) < count) v[i] = load_one(p);
+        }
+    }
+    // COPIES of the states in other orders, APART floats from one another: copy k has state n at n ^ (k * 4 / COPIES)
+    template <typename T, int COPIES, int APART> __device__ __forceinline__ void put(const uint32_t (&v)[COUNT], float *to) const {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i)
+#pragma unroll
+            for (int k = 0; k < COPIES; ++k) to[k * APART + position(i) * PAD + (state(i) ^ (k * (4 / COPIES)))] = f32_of<T>(v[i]);
     }
 };
 
@@ -96,9 +273,10 @@ __device__ __forceinline__ void store_quad(float *row, int n0, int N, const Quad
 }
 __device__ __forceinline__ Quad quad_of(const float4 &v) { return {Pair(v.x, v.y), Pair(v.z, v.w)}; }
 __device__ __forceinline__ float4 float4_of(const Quad &q) { return make_float4(q.a.lo(), q.a.hi(), q.b.lo(), q.b.hi()); }
-__device__ __forceinline__ float sum_of(const Quad &q) {
-    const Pair s = add(q.a, q.b);
-    return s.lo() + s.hi();
+// Element i to place i ^ order (and back).
+__device__ __forceinline__ Quad reordered(const Quad &q, int order) {
+    const Pair a = order & 2 ? q.b : q.a, b = order & 2 ? q.a : q.b;
+    return order & 1 ? Quad{Pair(a.hi(), a.lo()), Pair(b.hi(), b.lo())} : Quad{a, b};
 }
 
 }  // namespace wtconv

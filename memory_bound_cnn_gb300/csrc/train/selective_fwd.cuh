@@ -11,18 +11,38 @@ namespace wtconv {
 // meet by exchanges between lanes, and the epilogue (D, gate, store) goes by the share again.
 // LOCAL: only the state that the segment ends with if it begins with 0, and the sum of its steps; the CTAs of
 // later segments begin with what these compose to.
-template <typename T, int LANES, bool PLANES, bool LOCAL>
+template <typename T, int LANES, bool PLANES, bool WIDE, bool LOCAL>
 __global__ void __launch_bounds__(kSelTile *LANES) selective_forward_kernel(const __grid_constant__ SelectiveArgs a) {
-    constexpr int THREADS = kSelTile * LANES, SHARE = kSelTile * kSelRound / THREADS, PAD = 4 * LANES, ROW = kSelTile + 1;
-    __shared__ float2 coef[kSelRound * ROW];  // d, d x
+    constexpr int PAD = 4 * LANES;
+    using Part = Share<PLANES, LANES, kSelRound, WIDE>;
+    using Maps = MapShare<PLANES, LANES, kSelRound>;
+    __shared__ __align__(16) float2 coef[Part::COEFS];  // d, d x
     __shared__ float4 bs[kSelRound * LANES], cs[LOCAL ? 1 : kSelRound * LANES];
-    __shared__ float sums[LOCAL ? 1 : kSelRound * ROW];
+    __shared__ __align__(8) float sums[LOCAL ? 2 : Part::PARTS * Part::APART];
     begin_kernel();
     const Place at_(a, blockIdx.x);
     if (LOCAL && at_.segment == a.segments - 1) return;  // its end is nobody's beginning
-    const int tid = threadIdx.x, b = at_.b, N = a.s.N, stop = min(at_.end, at_.length);
-    const int c = tid / LANES, quad = tid % LANES, n0 = 4 * quad;  // the lane's channel and states
-    const bool live = c < at_.channels;
+    const int b = at_.b, N = a.s.N, stop = min(at_.end, at_.length);
+    const LanePlace<LANES> lane;
+    const int c = lane.c, quad = lane.quad, n0 = lane.n0;  // the lane's channel and states
+    const bool live = c < at_.channels, gated = !LOCAL && a.in.z.p != nullptr;
+    const Part part;
+    const Maps maps;
+    typename Raw<T>::Two x_next[Part::COUNT], d_next[Part::COUNT], z_next[Part::COUNT];
+    uint32_t b_next[Maps::COUNT], c_next[Maps::COUNT];
+    const auto fetch = [&](int t0) {
+        const int count = stop - t0;
+        part.load(at<const T, PLANES>(a.in.dt, b, t0, at_.c0), a.in.dt.row, at_.channels, count, d_next);
+        part.load(at<const T, PLANES>(a.in.x, b, t0, at_.c0), a.in.x.row, at_.channels, count, x_next);
+        maps.load(at<const T, PLANES>(a.in.Bm, b, t0, at_.group * N), a.in.Bm.row, N, count, b_next);
+        if (!LOCAL) maps.load(at<const T, PLANES>(a.in.Cm, b, t0, at_.group * N), a.in.Cm.row, N, count, c_next);
+        if (gated) part.load(at<const T, PLANES>(a.in.z, b, t0, at_.c0), a.in.z.row, at_.channels, count, z_next);
+    };
+    if (at_.first < stop) fetch(at_.first);
+    Pair bias[Part::OWN], D[Part::OWN];
+    part.parameters(a.in.dt_bias == nullptr ? nullptr : a.in.dt_bias + at_.c0, at_.channels, bias);
+    part.parameters(a.in.D == nullptr ? nullptr : a.in.D + at_.c0, at_.channels, D);
+
     Quad decay = {Pair(0.f), Pair(0.f)}, h = {Pair(0.f), Pair(0.f)};
     if (live) {
         decay = load_quad(a.in.A + (long long)(at_.c0 + c) * N, n0, N);
@@ -39,82 +59,111 @@ __global__ void __launch_bounds__(kSelTile *LANES) selective_forward_kernel(cons
             }
     }
     float step_sum = 0.f;
+    float *states = nullptr;  // the lane's of the next kept position
+    if (!LOCAL && live && a.states_out != nullptr)
+        states = a.states_out + (((long long)b * a.keep + at_.first / kSelKeep) * a.s.C + at_.c0 + c) * PAD + n0;
 
     for (int t0 = at_.first; t0 < stop; t0 += kSelRound) {
         const int count = min(kSelRound, stop - t0);
-        float x[SHARE], z[SHARE];
+        typename Raw<T>::Two x[Part::COUNT], z[Part::COUNT];
+        arrived(d_next), arrived(x_next), arrived(b_next);
+        if (!LOCAL) arrived(c_next);
 #pragma unroll
-        for (int i = 0; i < SHARE; ++i) {
-            const int e = tid + i * THREADS, pc = PLANES ? e / kSelRound : e % kSelTile, pt = PLANES ? e % kSelRound : e / kSelTile;
-            float d = 0.f;
-            x[i] = z[i] = 0.f;
-            if (pc < at_.channels && pt < count) {
-                x[i] = to_f32(*at<const T, PLANES>(a.in.x, b, t0 + pt, at_.c0 + pc));
-                if (!LOCAL && a.in.z.p != nullptr) z[i] = to_f32(*at<const T, PLANES>(a.in.z, b, t0 + pt, at_.c0 + pc));
-                d = to_f32(*at<const T, PLANES>(a.in.dt, b, t0 + pt, at_.c0 + pc));
-                if (a.in.dt_bias != nullptr) d += a.in.dt_bias[at_.c0 + pc];
-                if (a.s.softplus) d = softplus_of(d).value;
-            }
-            coef[pt * ROW + pc] = make_float2(d, d * x[i]);
-        }
+        for (int i = 0; i < Part::COUNT; ++i) x[i] = x_next[i], z[i] = z_next[i];
+        const auto put = [&](int i, Pair d) {
+            const Pair dx = mul(d, pair_of<T>(x[i]));
+            const int t = part.position(i), at_c = part.channel(i);
+            if (!part.busy()) return;
+            // (past the end d x is what it may be: those positions are not scanned)
+            *reinterpret_cast<float4 *>(coef + part.coef(t, at_c)) = make_float4(d.lo(), dx.lo(), d.hi(), dx.hi());
+        };
+        if (a.s.softplus) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = tid + i * THREADS, n = PLANES ? e / kSelRound : e % PAD, pt = PLANES ? e % kSelRound : e / PAD;
-            const bool ok = n < N && pt < count;
-            const int state = at_.group * N + n;
-            reinterpret_cast<float *>(bs)[pt * PAD + n] = ok ? to_f32(*at<const T, PLANES>(a.in.Bm, b, t0 + pt, state)) : 0.f;
-            if (!LOCAL)
-                reinterpret_cast<float *>(cs)[pt * PAD + n] = ok ? to_f32(*at<const T, PLANES>(a.in.Cm, b, t0 + pt, state)) : 0.f;
+            for (int i = 0; i < Part::COUNT; ++i) put(i, softplus_of(add(pair_of<T>(d_next[i]), bias[PLANES ? i : 0])));
+        } else {
+#pragma unroll
+            for (int i = 0; i < Part::COUNT; ++i) put(i, add(pair_of<T>(d_next[i]), bias[PLANES ? i : 0]));
         }
+        maps.template put<T, 1, 0>(b_next, reinterpret_cast<float *>(bs));
+        if (!LOCAL) maps.template put<T, 1, 0>(c_next, reinterpret_cast<float *>(cs));
         __syncthreads();
+        if (t0 + kSelRound < stop) fetch(t0 + kSelRound);  // while this round is scanned
 
-        const auto step = [&](int t) {  // one position; its sum over the lane's states
-            const float2 q = coef[t * ROW + c];
-            const Quad u = quad_of(bs[t * LANES + quad]);
-            const Pair d(q.x), dx(q.y);
+        // Four positions at a time, what the next four need is loaded before their sums are stored: a load of shared
+        // memory is not moved above a store, and would wait for all that the store waits for.
+        constexpr int TOGETHER = Part::TOGETHER, BATCH = 4;
+        struct Operands {
+            float2 q;
+            float4 u, o;
+        };
+        const auto operands = [&](int t) {
+            Operands p;
+            p.q = coef[part.coef(t, c)], p.u = bs[t * LANES + quad];
+            if (!LOCAL) p.o = cs[t * LANES + quad];
+            return p;
+        };
+        const auto step = [&](const Operands &p) {  // one position; its sum over the lane's states
+            const Quad u = quad_of(p.u);
+            const Pair d(p.q.x), dx(p.q.y);
             h.a = fma(exp2_fast(mul(d, decay.a)), h.a, mul(dx, u.a));
             h.b = fma(exp2_fast(mul(d, decay.b)), h.b, mul(dx, u.b));
             if (LOCAL) {
-                step_sum += q.x;
+                step_sum += p.q.x;
                 return 0.f;
             }
-            const Quad o = quad_of(cs[t * LANES + quad]);
+            const Quad o = quad_of(p.o);
             const Pair s = fma(o.a, h.a, mul(o.b, h.b));
             return s.lo() + s.hi();
         };
         const auto keep = [&](int t) {
-            if (!LOCAL && t % kSelKeep == 0 && a.states_out != nullptr && live) {
-                const long long k = (long long)b * a.keep + (t0 + t) / kSelKeep;
-                *reinterpret_cast<float4 *>(a.states_out + (k * a.s.C + at_.c0 + c) * PAD + n0) = float4_of(h);
+            if (!LOCAL && t % kSelKeep == 0 && states != nullptr) {
+                *reinterpret_cast<float4 *>(states) = float4_of(h);
+                states += (long long)a.s.C * PAD;
             }
         };
-        for (int t = 0; t < count; t += LANES) {
-            keep(t);
-            float s[LANES];
-            if (t + LANES <= count) {
+        if (count == kSelRound) {
+            Operands now[BATCH], next[BATCH];
 #pragma unroll
-                for (int j = 0; j < LANES; ++j) s[j] = step(t + j);
-            } else {
+            for (int j = 0; j < BATCH; ++j) now[j] = operands(j);
+#pragma unroll(kSelKeep / BATCH)
+            for (int t = 0; t < kSelRound; t += BATCH) {
+                keep(t);
+                const int ahead = min(t + BATCH, kSelRound - BATCH);
 #pragma unroll
-                for (int j = 0; j < LANES; ++j) s[j] = t + j < count ? step(t + j) : 0.f;
+                for (int j = 0; j < BATCH; ++j) next[j] = operands(ahead + j);
+                float s[BATCH / TOGETHER][TOGETHER];
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j) s[j / TOGETHER][j % TOGETHER] = step(now[j]);
+                if (!LOCAL) {
+#pragma unroll
+                    for (int j = 0; j < BATCH / TOGETHER; ++j) part.put_sums(sums, t + j * TOGETHER, c, quad, s[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j) now[j] = next[j];
             }
-            if (!LOCAL) {
-                sum_exchange<LANES, 1>(s, quad);
-                sums[(t + quad) * ROW + c] = s[0];
+        } else {
+            for (int t = 0; t < count; t += TOGETHER) {
+                keep(t);
+                float s[TOGETHER];
+#pragma unroll
+                for (int j = 0; j < TOGETHER; ++j) s[j] = t + j < count ? step(operands(t + j)) : 0.f;
+                if (!LOCAL) part.put_sums(sums, t, c, quad, s);
             }
         }
         __syncthreads();
-        if (!LOCAL) {
-#pragma unroll
-            for (int i = 0; i < SHARE; ++i) {
-                const int e = tid + i * THREADS, pc = PLANES ? e / kSelRound : e % kSelTile, pt = PLANES ? e % kSelRound : e / kSelTile;
-                if (pc >= at_.channels || pt >= count) continue;
-                float v = sums[pt * ROW + pc];
-                if (a.in.D != nullptr) v = fmaf(a.in.D[at_.c0 + pc], x[i], v);
-                if (a.in.z.p != nullptr) v *= z[i] * sigmoid_of(z[i]);
-                *at<T, PLANES>(a.y, b, t0 + pt, at_.c0 + pc) = from_f32<T>(v);
-            }
-        }
+        if (LOCAL) continue;
+        if (gated) arrived(z);
+        const auto value = [&](int i) {
+            return fma(D[PLANES ? i : 0], pair_of<T>(x[i]), part.get_sums(sums, part.value(part.position(i), part.channel(i))));
+        };
+        T *const to = at<T, PLANES>(a.y, b, t0, at_.c0);
+        if (gated)
+            part.store(to, a.y.row, at_.channels, count, [&](int i) {
+                const Pair g = pair_of<T>(z[i]);
+                return mul(value(i), mul(g, sigmoid_of(g)));
+            });
+        else
+            part.store(to, a.y.row, at_.channels, count, value);
     }
 
     if (LOCAL) {
@@ -129,32 +178,23 @@ __global__ void __launch_bounds__(kSelTile *LANES) selective_forward_kernel(cons
     if (a.h_last != nullptr && live && (at_.segment == 0 ? at_.length <= at_.end : at_.first < at_.length && at_.length <= at_.end))
         store_quad(a.h_last + ((long long)b * a.s.C + at_.c0 + c) * N, n0, N, h);
     // positions past its end
-    for (int t0 = max(at_.first, at_.length); t0 < at_.end; t0 += kSelRound) {
-#pragma unroll
-        for (int i = 0; i < SHARE; ++i) {
-            const int e = tid + i * THREADS, pc = PLANES ? e / kSelRound : e % kSelTile, pt = PLANES ? e % kSelRound : e / kSelTile;
-            if (pc < at_.channels && pt < at_.end - t0) *at<T, PLANES>(a.y, b, t0 + pt, at_.c0 + pc) = from_f32<T>(0.f);
-        }
-    }
+    for (int t0 = max(at_.first, at_.length); t0 < at_.end; t0 += kSelRound)
+        part.clear(at<T, PLANES>(a.y, b, t0, at_.c0), a.y.row, at_.channels, at_.end - t0);
 }
 
-template <typename T, int LANES, bool PLANES> cudaError_t launch_selective_forward_as(const SelectiveArgs &a, cudaStream_t st) {
+template <typename T, int LANES, bool PLANES, bool WIDE> cudaError_t launch_selective_forward_as(const SelectiveArgs &a, cudaStream_t st) {
     const unsigned threads = kSelTile * LANES, grid = (unsigned)a.ctas() * a.segments;
     if (a.segments > 1) {
-        const cudaError_t e = launch_kernel(selective_forward_kernel<T, LANES, PLANES, true>, grid, threads, 0, st, 1, a);
+        const cudaError_t e = launch_kernel(selective_forward_kernel<T, LANES, PLANES, WIDE, true>, grid, threads, 0, st, 1, a);
         if (e != cudaSuccess) return e;
     }
-    return launch_kernel(selective_forward_kernel<T, LANES, PLANES, false>, grid, threads, 0, st, 1, a);
+    return launch_kernel(selective_forward_kernel<T, LANES, PLANES, WIDE, false>, grid, threads, 0, st, 1, a);
 }
 
 template <typename T> cudaError_t launch_selective_forward(const SelectiveArgs &a, cudaStream_t st) {
-    const bool planes = a.s.layout == WTCONV_SCAN_PLANES;
-    switch (a.lanes) {
-        case 2: return planes ? launch_selective_forward_as<T, 2, true>(a, st) : launch_selective_forward_as<T, 2, false>(a, st);
-        case 4: return planes ? launch_selective_forward_as<T, 4, true>(a, st) : launch_selective_forward_as<T, 4, false>(a, st);
-        case 8: return planes ? launch_selective_forward_as<T, 8, true>(a, st) : launch_selective_forward_as<T, 8, false>(a, st);
-        default: return planes ? launch_selective_forward_as<T, 16, true>(a, st) : launch_selective_forward_as<T, 16, false>(a, st);
-    }
+    return with_selective_shape(a, [&](auto lanes, auto planes, auto wide) {
+        return launch_selective_forward_as<T, decltype(lanes)::value, decltype(planes)::value, decltype(wide)::value>(a, st);
+    });
 }
 
 // One position of every sequence: LANES lanes to a channel, each with four of its states.
@@ -187,7 +227,7 @@ __global__ void __launch_bounds__(128) selective_step_kernel(const __grid_consta
         x = to_f32(static_cast<const T *>(a.in.x.p)[b * a.in.x.row + c]);
         float d = to_f32(static_cast<const T *>(a.in.dt.p)[b * a.in.dt.row + c]);
         if (a.in.dt_bias != nullptr) d += a.in.dt_bias[c];
-        if (a.s.softplus) d = softplus_of(d).value;
+        if (a.s.softplus) d = softplus_of(Pair(d)).lo();
         const Pair rate(d * kSelLog2E), dx(d * x);
         h.a = fma(exp2_fast(mul(rate, A.a)), h.a, mul(dx, in.a)), h.b = fma(exp2_fast(mul(rate, A.b)), h.b, mul(dx, in.b));
         if (WIDE && n0 < N) *reinterpret_cast<float4 *>(row + n0) = float4_of(h);
@@ -202,7 +242,7 @@ __global__ void __launch_bounds__(128) selective_step_kernel(const __grid_consta
         if (a.in.D != nullptr) v = fmaf(a.in.D[c], x, v);
         if (a.in.z.p != nullptr) {
             const float z = to_f32(static_cast<const T *>(a.in.z.p)[b * a.in.z.row + c]);
-            v *= z * sigmoid_of(z);
+            v *= z * sigmoid_of(Pair(z)).lo();
         }
     }
     static_cast<T *>(a.y.p)[b * a.y.row + c] = from_f32<T>(v);

@@ -23,6 +23,7 @@ struct Pair {
     __device__ __forceinline__ Pair() {}
     __device__ __forceinline__ Pair(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(q) : "f"(lo), "f"(hi)); }
     __device__ __forceinline__ explicit Pair(float v) : Pair(v, v) {}
+    __device__ __forceinline__ explicit Pair(unsigned long long both) : q(both) {}
     __device__ __forceinline__ float lo() const {
         float a;
         asm("mov.b64 {%0, _}, %1;" : "=f"(a) : "l"(q));
