@@ -35,23 +35,35 @@ bool pairs(const wtconv_ssm_tensor &t, const wtconv_selective_shape &s) {
     const bool rows = (s.layout == WTCONV_SCAN_PLANES ? s.C : s.T) > 1;
     return t.p == nullptr || (aligned_to(t.p, 2 * elem_bytes_of(s.dtype)) && (!rows || t.row % 2 == 0) && (s.B == 1 || t.batch % 2 == 0));
 }
-// (a group's first channel has to be even too, where channels are neighbours)
+// (a group's first channel has to be even too, where channels are neighbours; its first state is where pairs of
+// states are read at once, as their number is then a multiple of 8)
 bool pairs(const SelectiveArgs &a) {
     if (a.s.layout == WTCONV_SCAN_TOKENS && a.s.G > 1 && a.channels % 2 != 0) return false;
-    for (const wtconv_ssm_tensor *t : {&a.in.x, &a.in.dt, &a.in.z, &a.y, &a.dy, &a.g.dx, &a.g.d_dt, &a.g.dz})
+    for (const wtconv_ssm_tensor *t : {&a.in.x, &a.in.dt, &a.in.Bm, &a.in.Cm, &a.in.z, &a.y, &a.dy, &a.g.dx, &a.g.d_dt, &a.g.dz})
         if (!pairs(*t, a.s)) return false;
     return true;
 }
 
-// Parts that a sequence is cut into.  Cutting costs a second pass over x, dt and B (the forward) or dy, z and
-// C, so it is for shapes whose sequences and channels alone leave the GPU's SMs short of warps.
+// Parts that a sequence is cut into.  Cutting fills the GPU where sequences and tiles of channels are few, or their
+// number leaves a last round of CTAs small; it costs a pass of its own (over x, dt and B in the forward, about half of
+// the work, over dy, dt, z and C in the backward, a fifth) and the composition of the parts before a CTA's own.
+// Time is counted in rounds of 32 positions of a CTA that has an SM for itself: two that share one take 1.3
+// times as long, three 1.6, and more wait.  (8 x 4096 x 1024 tokens with 16 states, 256 CTAs: forward 236 us in one part, 308
+// in two, backward 906 and 1032; 65,536 pixels of 64 channels, 2 CTAs: 62 us in 76 parts, 83 in 305.)
 void plan(int op, SelectiveArgs &a) {
-    const char *env = getenv(op == WTCONV_SCAN_OP_FORWARD ? "SEL_F" : "SEL_B");  // TEMP
-    const int threads = kSelTile * a.lanes, wanted = sm_count() * (env ? atoi(env) : op == WTCONV_SCAN_OP_FORWARD ? 512 : 384) / threads;
-    const int rounds = ceil_div(a.s.T, kSelRound), most = std::max(1, std::min(rounds / 4, 256));
-    const int parts = std::min(most, std::max(1, wanted / std::max(1, a.ctas())));
-    const int per = ceil_div(rounds, parts);
-    a.segment = per * kSelRound, a.segments = ceil_div(rounds, per);
+    const bool forward = op == WTCONV_SCAN_OP_FORWARD;
+    const int sms = sm_count(), rounds = ceil_div(a.s.T, kSelRound), most = std::max(1, std::min(rounds / 2, 256));
+    const int resident = a.lanes == 2 ? (forward ? 3 : 2) : a.lanes == 4 ? 2 : 1;
+    const double share[4] = {1, 1, 1.3, 1.6}, pass = forward ? 1.5 : 1.2, start = forward ? 4 : 1, join = forward ? 0.05 : 0.02;
+    double best = 0;
+    for (int parts = 1; parts <= most; ++parts) {
+        const int per = ceil_div(rounds, parts), used = ceil_div(rounds, per);
+        const long long on_sm = ((long long)a.ctas() * used + sms - 1) / sms;
+        const double load = on_sm <= resident ? share[on_sm] : on_sm * share[resident] / resident;
+        const double time = per * load * (used > 1 ? pass : 1) + (used > 1 ? start + join * used : 0);
+        if (parts > 1 && time >= best) continue;
+        best = time, a.segment = per * kSelRound, a.segments = used;
+    }
     if (a.segments == 1) a.segment = a.s.T;
 }
 

@@ -9,70 +9,216 @@
 
 namespace wtconv {
 
+constexpr float kSelCut = 1.0003662109375f;  // 1 + 3 x 2^-13
+
+// d += A B with A 16 x 8 and B 8 x 8: of A, a lane holds (row, column) (lane / 4, lane % 4) in `low` and (8 + lane / 4,
+// 4 + lane % 4) in `high`, the rest is 0; of B (lane % 4, lane / 4) and (4 + lane % 4, lane / 4); of d (lane / 4, 2 (lane %
+// 4) + 0 and 1), then the same of row 8 + lane / 4.
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t low, uint32_t high, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %5, %6}, {%7, %8}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(low), "r"(0), "r"(high), "r"(b0), "r"(b1));
+}
+
 // A CTA takes 32 channels of a sequence (or of a segment), from the end to the beginning, in blocks of 16
-// positions, LANES lanes with four states each to a channel.  A block's states are recomputed from the kept one
-// before it and stay in registers (4 x 16 a lane), then the positions are gone through backwards.  Of the
-// sums, those over a channel's states are put down by its lanes and meet in the epilogue; those over channels (dB, dC)
-// meet by exchanges between the warp's channels, then between warps in shared memory, then between CTAs in
-// selective_sums_kernel.  Lanes of neighbouring channels hold their four states in different orders (state n0 +
-// (i ^ order) in place i), so that what a lane sends in such an exchange and what it keeps are the same places in
-// all lanes; B and C lie in shared memory in each of the orders.
+// positions.  LANES lanes with four states each recompute a channel's states of a block from the kept one before it and
+// hold them in registers (4 x 16 a lane), then go through the positions backwards; the CTA's other warps, the
+// helpers, prepare the next block and finish the one before, as in the forward.
+// Sums over a channel's states are put down by its lanes and meet in the helpers.  Those over channels (dB, dC) are the
+// larger part: 8 values of every lane and position, over 32 / LANES channels of a warp.  The tensor cores add them up:
+// for two positions at a time, the lanes' values of state s of B or C are the columns of a matrix whose rows are
+// four channels at one position and the same four at the other, and a product with a matrix of ones in row r of
+// the first four columns and row 8 + r of the others leaves the sums in row r (one position) and 8 + r; each of the 8
+// values has an r of its own.  The tensor cores read a value's leading 11 bits and leave the rest out.  For sums that
+// are stored in bf16 that is enough: cut to 11 bits, m 2^e with 1 <= m < 2 loses less than 2^-10 2^e, half of that on
+// average; times 1 + 3 x 2^-13 beforehand, it is off by -6.1e-4 to 3.7e-4 of itself, at random, where rounding the sum to
+// bf16 costs up to 3.9e-3 (8 x 4096 x 1024 with 16 states: 906 us; 1172 in fp32, where the rest enters too).  In other types
+// it enters as a second product, which keeps 22 bits.
+// Then warps meet in shared memory, and CTAs in selective_sums_kernel.
 // LOCAL: only the gradient that the segment's beginning passes on if nothing enters at its end, and the sum
 // of its steps; the CTAs of earlier segments begin with what these compose to.
 template <int LANES, bool PLANES> struct BackwardShared {
-    using Part = Share<PLANES, LANES, kSelKeep, false>;
-    static constexpr int PAD = 4 * LANES, COPIES = LANES == 16 ? 2 : 4;
-    float2 coef[Part::COEFS];                       // d, d x
-    float r[Part::VALUES];                          // dy silu(z)
-    float sums[3][Part::PARTS * Part::APART];       // over a channel's states: g B, k A, C h
-    static constexpr int APART = kSelKeep * PAD + (LANES == 16 ? 16 : 8);  // of two copies: their lanes meet on no bank
-    alignas(16) float maps[2][COPIES][APART];                   // B, C
-    float2 stash[2][Part::COUNT][Part::THREADS];    // of a thread's pairs, for the epilogue: slope of d, dy silu'(z)
-    float part[LANES][kSelKeep][2][PAD];            // dB and dC of a warp's channels
+    using L = Layout<LANES, PLANES, kSelKeep>;
+    using Part = Share<PLANES, kSelTile, kSelKeep, Roles<LANES>::HELPERS, false>;
+    static constexpr int ROWS = LANES / LanePlace<LANES>::HALVES;  // warps that have the same states
+    alignas(16) float2 coef[L::COEFS];                                 // d, d x
+    alignas(16) float r[L::VALUES];                                    // dy silu(z)
+    alignas(16) float maps[2][kSelKeep * L::MAP];                      // B, C
+    alignas(16) float sums[3][L::PARTS * L::APART];                    // over a channel's states: g B, k A, C h
+    float2 stash[2][Part::COUNT][Roles<LANES>::HELPERS];               // of a helper's pairs: slope of d, dy silu'(z)
+    float part[ROWS][kSelKeep][2][L::PAD];                             // dB and dC of a row of warps' channels
 };
 
 template <typename T, int LANES, bool PLANES, bool WIDE, bool LOCAL>
-__global__ void __launch_bounds__(kSelTile *LANES, LANES == 16 ? 1 : 12 / LANES) selective_backward_kernel(const __grid_constant__ SelectiveArgs a) {
-    constexpr int THREADS = kSelTile * LANES, BLOCK = kSelKeep, PAD = 4 * LANES, CHANNELS = 32 / LANES;
-    using Part = Share<PLANES, LANES, BLOCK, WIDE>;
-    using Maps = MapShare<PLANES, LANES, BLOCK>;
+__global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) selective_backward_kernel(const __grid_constant__ SelectiveArgs a) {
+    constexpr int BLOCK = kSelKeep;
+    using L = Layout<LANES, PLANES, BLOCK>;
+    using R = Roles<LANES>;
     using Shared = BackwardShared<LANES, PLANES>;
-    constexpr int COUNT = Part::COUNT, OWN = Part::OWN, TOGETHER = Part::TOGETHER;
+    using Place2 = LanePlace<LANES>;
     extern __shared__ float4 shared_memory[];
-    Shared &s = *reinterpret_cast<Shared *>(shared_memory);
+    Shared *const blocks = reinterpret_cast<Shared *>(shared_memory);  // two
     begin_kernel();
     const Place at_(a, blockIdx.x);
     if (LOCAL && at_.segment == 0) return;  // nobody is before it
-    const int tid = threadIdx.x, b = at_.b, N = a.s.N, stop = min(at_.end, at_.length);
-    const LanePlace<LANES> lane;
-    const int c = lane.c, quad = lane.quad, n0 = lane.n0;
-    // (two lanes that read the same order are neighbours, as those that read the same states: see LanePlace)
-    const int order = CHANNELS >= 8 ? lane.cl >> 1 & 3 : CHANNELS == 4 ? lane.cl : 2 * lane.cl;
-    const bool live = c < at_.channels, gated = a.in.z.p != nullptr;
-    const long long row = (long long)b * a.s.C + at_.c0 + c;  // of [B][C]
-    const Part mine;
-    const Maps maps;
-    const int blocks = stop > at_.first ? (stop - at_.first + BLOCK - 1) / BLOCK : 0;
-    typename Raw<T>::Two x_next[COUNT], d_next[COUNT], z_next[COUNT], dy_next[COUNT];
-    uint32_t b_next[Maps::COUNT], c_next[Maps::COUNT];
-    float4 kept_next = make_float4(0.f, 0.f, 0.f, 0.f);
-    const auto fetch = [&](int k) {
-        const int t0 = at_.first + k * BLOCK, count = stop - t0;
-        mine.load(at<const T, PLANES>(a.in.dt, b, t0, at_.c0), a.in.dt.row, at_.channels, count, d_next);
-        mine.load(at<const T, PLANES>(a.dy, b, t0, at_.c0), a.dy.row, at_.channels, count, dy_next);
-        if (gated) mine.load(at<const T, PLANES>(a.in.z, b, t0, at_.c0), a.in.z.row, at_.channels, count, z_next);
-        maps.load(at<const T, PLANES>(a.in.Cm, b, t0, at_.group * N), a.in.Cm.row, N, count, c_next);
+    const int b = at_.b, N = a.s.N, stop = min(at_.end, at_.length);
+    const int count_blocks = stop > at_.first ? (stop - at_.first + BLOCK - 1) / BLOCK : 0;
+    const long long first_sum = ((long long)b * a.segments + at_.segment) * a.s.C + at_.c0;  // of [B][segments][C]
+    // the i-th block from the end
+    const auto start = [&](int i) { return at_.first + (count_blocks - 1 - i) * BLOCK; };
+
+    if (!R::scans()) {
+        if (!LOCAL) R::give();
+        using Part = Share<PLANES, kSelTile, BLOCK, R::HELPERS, WIDE>;
+        using Maps = Share<PLANES, L::PAD, BLOCK, R::HELPERS, WIDE>;
+        using Two = typename Raw<T>::Two;
+        constexpr int COUNT = Part::COUNT, OWN = Part::OWN;
+        const int me = R::helper();
+        const Part mine(me);
+        const Maps maps(me);
+        const bool gated = a.in.z.p != nullptr;
+        Pair bias[OWN], D[OWN], dD[OWN], d_bias[OWN];
+        mine.parameters(a.in.dt_bias == nullptr ? nullptr : a.in.dt_bias + at_.c0, at_.channels, bias);
+        mine.parameters(a.in.D == nullptr ? nullptr : a.in.D + at_.c0, at_.channels, D);
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) dD[i] = d_bias[i] = Pair(0.f);
+        struct Fetched {
+            Two d[COUNT], x[COUNT], z[COUNT], dy[COUNT], b[Maps::COUNT], c[Maps::COUNT];
+        } even, odd;
+        Two x[COUNT] = {}, x_old[COUNT] = {};  // of the scanned block, the one finished
+        const auto fetch = [&](int i, Fetched &f) {
+            if (i >= count_blocks) return;
+            const int t0 = start(i), count = stop - t0;
+            mine.load(at<const T, PLANES>(a.in.dt, b, t0, at_.c0), a.in.dt.row, at_.channels, count, f.d);
+            mine.load(at<const T, PLANES>(a.dy, b, t0, at_.c0), a.dy.row, at_.channels, count, f.dy);
+            if (gated) mine.load(at<const T, PLANES>(a.in.z, b, t0, at_.c0), a.in.z.row, at_.channels, count, f.z);
+            maps.load(at<const T, PLANES>(a.in.Cm, b, t0, at_.group * N), a.in.Cm.row, N, count, f.c);
+            if (LOCAL) return;
+            mine.load(at<const T, PLANES>(a.in.x, b, t0, at_.c0), a.in.x.row, at_.channels, count, f.x);
+            maps.load(at<const T, PLANES>(a.in.Bm, b, t0, at_.group * N), a.in.Bm.row, N, count, f.b);
+        };
+        const auto prepare = [&](int i, Fetched &f) {
+            if (i >= count_blocks) return;
+            Shared &s = blocks[i & 1];
+            arrived(f.d), arrived(f.dy), arrived(f.c);
+            if (!LOCAL) arrived(f.x), arrived(f.b);
+            if (gated) arrived(f.z);
+#pragma unroll
+            for (int j = 0; j < COUNT; ++j) {
+                x[j] = f.x[j];
+                if (!mine.busy()) continue;
+                const int t = mine.position(j), c = mine.channel(j);
+                Pair d = add(pair_of<T>(f.d[j]), bias[PLANES ? j : 0]), r = pair_of<T>(f.dy[j]);
+                if (a.s.softplus) {
+                    const Pair e = exp_of_minus_abs(d);
+                    if (!LOCAL) *reinterpret_cast<unsigned long long *>(&s.stash[0][j][me]) = softplus_slope(d, e).q;
+                    d = softplus_of(d, e);
+                }
+                if (gated) {
+                    const Pair z = pair_of<T>(f.z[j]), p = sigmoid_of(z), zp = mul(z, p);
+                    // silu'(z) = p + z p (1 - p)
+                    if (!LOCAL) *reinterpret_cast<unsigned long long *>(&s.stash[1][j][me]) = mul(r, fma(zp, sub(Pair(1.f), p), p)).q;
+                    r = mul(r, zp);
+                }
+                const Pair dx = LOCAL ? Pair(0.f) : mul(d, pair_of<T>(x[j]));
+                *reinterpret_cast<float4 *>(s.coef + L::coef(t, c)) = make_float4(d.lo(), dx.lo(), d.hi(), dx.hi());
+                *reinterpret_cast<unsigned long long *>(s.r + L::value(t, c)) = r.q;
+            }
+            if (!LOCAL) L::template put_map<T>(maps, f.b, s.maps[0]);
+            L::template put_map<T>(maps, f.c, s.maps[1]);
+        };
+        const auto finish = [&](int i) {
+            Shared &s = blocks[i & 1];
+            const int t0 = start(i), count = min(BLOCK, stop - t0);
+            Pair dx[COUNT], dd[COUNT], dz[COUNT];
+            const auto stashed = [&](int which, int j) { return Pair(*reinterpret_cast<const unsigned long long *>(&s.stash[which][j][me])); };
+#pragma unroll
+            for (int j = 0; j < COUNT; ++j) {
+                if (!mine.busy()) continue;
+                const int t = mine.position(j), c = mine.channel(j), place = L::value(t, c);
+                // (an element past the end or beside the tile has whatever an earlier block left: it is neither stored nor summed)
+                const float4 q = *reinterpret_cast<const float4 *>(s.coef + L::coef(t, c));
+                const Pair into = L::get_sums(s.sums[0], place), xj = pair_of<T>(x_old[j]), Dj = D[PLANES ? j : 0];
+                const Pair r(*reinterpret_cast<const unsigned long long *>(s.r + place));
+                dd[j] = fma(xj, into, mul(L::get_sums(s.sums[1], place), Pair(kSelLn2)));
+                if (a.s.softplus) dd[j] = mul(dd[j], stashed(0, j));
+                dx[j] = fma(Dj, r, mul(Pair(q.x, q.z), into));
+                if (gated) dz[j] = mul(stashed(1, j), fma(Dj, xj, L::get_sums(s.sums[2], place)));
+                Pair rx = mul(r, xj), di = dd[j];
+                if (count < BLOCK || at_.channels < kSelTile) {
+                    const bool first = mine.in(j, 0, at_.channels, count), second = mine.in(j, 1, at_.channels, count);
+                    rx = {first ? rx.lo() : 0.f, second ? rx.hi() : 0.f}, di = {first ? di.lo() : 0.f, second ? di.hi() : 0.f};
+                }
+                dD[PLANES ? j : 0] = add(dD[PLANES ? j : 0], rx), d_bias[PLANES ? j : 0] = add(d_bias[PLANES ? j : 0], di);
+            }
+            mine.store(at<T, PLANES>(a.g.dx, b, t0, at_.c0), a.g.dx.row, at_.channels, count, [&](int j) { return dx[j]; });
+            mine.store(at<T, PLANES>(a.g.d_dt, b, t0, at_.c0), a.g.d_dt.row, at_.channels, count, [&](int j) { return dd[j]; });
+            if (gated) mine.store(at<T, PLANES>(a.g.dz, b, t0, at_.c0), a.g.dz.row, at_.channels, count, [&](int j) { return dz[j]; });
+            float *const to = a.part_bc + (((long long)at_.tile * a.s.B + b) * a.s.T + t0) * 2 * L::PAD;
+            for (int e = 2 * me; e < count * 2 * L::PAD; e += 2 * R::HELPERS) {
+                const float *const from = &s.part[0][0][0][0] + e;
+                Pair v(*reinterpret_cast<const unsigned long long *>(from));
+#pragma unroll
+                for (int w = 1; w < Shared::ROWS; ++w)
+                    v = add(v, Pair(*reinterpret_cast<const unsigned long long *>(from + w * BLOCK * 2 * L::PAD)));
+                *reinterpret_cast<unsigned long long *>(to + e) = v.q;
+            }
+        };
+        const auto during = [&](int i, Fetched &next, Fetched &after) {  // block i is scanned
+            fetch(i + 2, after);
+            if (!LOCAL && i > 0) finish(i - 1);
+#pragma unroll
+            for (int j = 0; j < COUNT; ++j) x_old[j] = x[j];
+            prepare(i + 1, next);
+            R::meet();
+        };
+        fetch(0, even), fetch(1, odd), prepare(0, even);
+        R::meet();
+        for (int i = 0; i < count_blocks; i += 2) {
+            during(i, odd, even);
+            if (i + 1 < count_blocks) during(i + 1, even, odd);
+        }
         if (LOCAL) return;
-        mine.load(at<const T, PLANES>(a.in.x, b, t0, at_.c0), a.in.x.row, at_.channels, count, x_next);
-        maps.load(at<const T, PLANES>(a.in.Bm, b, t0, at_.group * N), a.in.Bm.row, N, count, b_next);
-        if (live)
-            kept_next = *reinterpret_cast<const float4 *>(
-                a.states_in + (((long long)b * a.keep + t0 / kSelKeep) * a.s.C + at_.c0 + c) * PAD + n0);
-    };
-    if (blocks > 0) fetch(blocks - 1);
-    Pair bias[OWN], D[OWN];
-    mine.parameters(a.in.dt_bias == nullptr ? nullptr : a.in.dt_bias + at_.c0, at_.channels, bias);
-    mine.parameters(a.in.D == nullptr ? nullptr : a.in.D + at_.c0, at_.channels, D);
+        if (count_blocks > 0) finish(count_blocks - 1);
+        // dD and d_dt_bias: the helpers that share a channel
+        const long long half = (long long)a.s.B * a.segments * a.s.C;
+        if (PLANES) {  // neighbouring lanes
+#pragma unroll
+            for (int j = 0; j < OWN; ++j) {
+                float v = dD[j].lo() + dD[j].hi(), w = d_bias[j].lo() + d_bias[j].hi();
+#pragma unroll
+                for (int m = Part::INNER / 2; m >= 1; m /= 2) v += __shfl_xor_sync(0xffffffffu, v, m), w += __shfl_xor_sync(0xffffffffu, w, m);
+                const int c = mine.channel(j);
+                if (mine.busy() && mine.inner == 0 && c < at_.channels) a.part_c[first_sum + c] = v, a.part_c[half + first_sum + c] = w;
+            }
+        } else {
+            R::helpers_meet();
+            float2 *const meet = reinterpret_cast<float2 *>(blocks[0].sums);  // [2][HELPERS]
+            *reinterpret_cast<unsigned long long *>(meet + me) = dD[0].q, *reinterpret_cast<unsigned long long *>(meet + R::HELPERS + me) = d_bias[0].q;
+            R::helpers_meet();
+            if (me < at_.channels) {
+                float v = 0.f, w = 0.f;
+                for (int j = 0; j < R::HELPERS / Part::INNER; ++j) {
+                    const float *const p = reinterpret_cast<const float *>(meet + j * Part::INNER) + me;
+                    v += p[0], w += p[2 * R::HELPERS];
+                }
+                a.part_c[first_sum + me] = v, a.part_c[half + first_sum + me] = w;
+            }
+        }
+        // positions past the sequence's end
+        for (int t0 = max(at_.first, at_.length); t0 < at_.end; t0 += BLOCK) {
+            mine.clear(at<T, PLANES>(a.g.dx, b, t0, at_.c0), a.g.dx.row, at_.channels, at_.end - t0);
+            mine.clear(at<T, PLANES>(a.g.d_dt, b, t0, at_.c0), a.g.d_dt.row, at_.channels, at_.end - t0);
+            if (gated) mine.clear(at<T, PLANES>(a.g.dz, b, t0, at_.c0), a.g.dz.row, at_.channels, at_.end - t0);
+        }
+        return;
+    }
+
+    if (!LOCAL) R::take();
+    const Place2 lane;
+    const int c = lane.c, quad = lane.quad, n0 = lane.n0;
+    const bool live = c < at_.channels;
+    const long long row = (long long)b * a.s.C + at_.c0 + c;  // of [B][C]
     Quad decay = {Pair(0.f), Pair(0.f)}, carry = decay, dA = decay;
     if (live) {
         decay = load_quad(a.in.A + (long long)(at_.c0 + c) * N, n0, N);
@@ -80,61 +226,34 @@ __global__ void __launch_bounds__(kSelTile *LANES, LANES == 16 ? 1 : 12 / LANES)
     }
     if (!LOCAL && live) {
         if (a.dh_last != nullptr) carry = load_quad(a.dh_last + row * N, n0, N);
-        if (at_.first < at_.length)
+        if (count_blocks > 0)
+#pragma unroll 4
             for (int k = (at_.length - 1) / a.segment; k > at_.segment; --k) {
                 const long long i = ((long long)b * a.segments + k) * a.s.C + at_.c0 + c;
                 const Pair d(a.steps[i]);
-                const Quad u = quad_of(*reinterpret_cast<const float4 *>(a.ends + i * PAD + n0));
+                const Quad u = quad_of(*reinterpret_cast<const float4 *>(a.ends + i * L::PAD + n0));
                 carry.a = fma(exp2_fast(mul(d, decay.a)), carry.a, u.a), carry.b = fma(exp2_fast(mul(d, decay.b)), carry.b, u.b);
             }
     }
-    decay = reordered(decay, order), carry = reordered(carry, order);
     float step_sum = 0.f;
-    Pair dD[OWN], d_bias[OWN];
+    const auto kept = [&](int i) {
+        if (!live || i >= count_blocks) return make_float4(0.f, 0.f, 0.f, 0.f);
+        return *reinterpret_cast<const float4 *>(a.states_in + (((long long)b * a.keep + start(i) / kSelKeep) * a.s.C + at_.c0 + c) * L::PAD + n0);
+    };
+    float4 kept_next = LOCAL ? make_float4(0.f, 0.f, 0.f, 0.f) : kept(0);
+    uint32_t one[8];  // the 1 of a row r of the matrix of ones
 #pragma unroll
-    for (int i = 0; i < OWN; ++i) dD[i] = d_bias[i] = Pair(0.f);
-    const float4 *const bs = reinterpret_cast<const float4 *>(s.maps[0][order / (4 / Shared::COPIES)]) + quad;
-    const float4 *const cs = reinterpret_cast<const float4 *>(s.maps[1][order / (4 / Shared::COPIES)]) + quad;
-
-    for (int k = blocks - 1; k >= 0; --k) {
-        const int t0 = at_.first + k * BLOCK, count = min(BLOCK, stop - t0);
-        if (!LOCAL) asm volatile("" : "+f"(kept_next.x), "+f"(kept_next.y), "+f"(kept_next.z), "+f"(kept_next.w));  // (see arrived)
-        const Quad before = reordered(quad_of(kept_next), order);
-        typename Raw<T>::Two x[COUNT];
-        arrived(d_next), arrived(dy_next), arrived(c_next);
-        if (!LOCAL) arrived(x_next), arrived(b_next);
-        if (gated) arrived(z_next);
-#pragma unroll
-        for (int i = 0; i < COUNT; ++i) {
-            x[i] = x_next[i];
-            if (!mine.busy()) continue;
-            const int t = mine.position(i), at_c = mine.channel(i);
-            Pair d = add(pair_of<T>(d_next[i]), bias[PLANES ? i : 0]), r = pair_of<T>(dy_next[i]);
-            if (a.s.softplus) {
-                const Pair e = exp_of_minus_abs(d);
-                if (!LOCAL) *reinterpret_cast<unsigned long long *>(&s.stash[0][i][tid]) = softplus_slope(d, e).q;
-                d = softplus_of(d, e);
-            }
-            if (gated) {
-                const Pair z = pair_of<T>(z_next[i]), p = sigmoid_of(z), zp = mul(z, p);
-                // silu'(z) = p + z p (1 - p)
-                if (!LOCAL) *reinterpret_cast<unsigned long long *>(&s.stash[1][i][tid]) = mul(r, fma(zp, sub(Pair(1.f), p), p)).q;
-                r = mul(r, zp);
-            }
-            const Pair dx = LOCAL ? Pair(0.f) : mul(d, pair_of<T>(x[i]));
-            *reinterpret_cast<float4 *>(s.coef + mine.coef(t, at_c)) = make_float4(d.lo(), dx.lo(), d.hi(), dx.hi());
-            *reinterpret_cast<unsigned long long *>(s.r + mine.value(t, at_c)) = r.q;
-        }
-        if (!LOCAL) maps.template put<T, Shared::COPIES, Shared::APART>(b_next, s.maps[0][0]);
-        maps.template put<T, Shared::COPIES, Shared::APART>(c_next, s.maps[1][0]);
-        __syncthreads();
-        if (k > 0) fetch(k - 1);  // while this block is gone through
-
+    for (int r = 0; r < 8; ++r) one[r] = lane.lane / 4 == r ? 0x3f800000u : 0u;
+    R::meet();
+    for (int i = 0; i < count_blocks; ++i) {
+        Shared &s = blocks[i & 1];
+        const int count = min(BLOCK, stop - start(i));
+        const auto map = [&](int which, int t) { return *reinterpret_cast<const float4 *>(s.maps[which] + t * L::MAP + n0); };
         if (LOCAL) {
             const auto pass = [&](int t) {
-                const float2 q = s.coef[mine.coef(t, c)];
-                const Quad o = quad_of(cs[t * LANES]);
-                const Pair d(q.x), r(s.r[mine.value(t, c)]);
+                const float2 q = s.coef[L::coef(t, c)];
+                const Quad o = quad_of(map(1, t));
+                const Pair d(q.x), r(s.r[L::value(t, c)]);
                 carry.a = mul(exp2_fast(mul(d, decay.a)), fma(o.a, r, carry.a));
                 carry.b = mul(exp2_fast(mul(d, decay.b)), fma(o.b, r, carry.b));
                 step_sum += q.x;
@@ -145,18 +264,23 @@ __global__ void __launch_bounds__(kSelTile *LANES, LANES == 16 ? 1 : 12 / LANES)
             } else {
                 for (int t = count - 1; t >= 0; --t) pass(t);
             }
-            __syncthreads();
+            R::meet();
             continue;
         }
 
+        asm volatile("" : "+f"(kept_next.x), "+f"(kept_next.y), "+f"(kept_next.z), "+f"(kept_next.w));  // (see arrived)
+        const Quad before = quad_of(kept_next);
+        kept_next = kept(i + 1);
         const auto scan = [&](auto full) {
             constexpr bool FULL = decltype(full)::value;
+            constexpr int TOGETHER = L::TOGETHER, PAIRS = BLOCK / 2;
+            constexpr bool CUT = std::is_same<T, __nv_bfloat16>::value;  // products are cut to 11 bits
             Quad h[BLOCK];
 #pragma unroll
             for (int t = 0; t < BLOCK; ++t) {
                 if (!FULL && t >= count) break;
-                const float2 q = s.coef[mine.coef(t, c)];
-                const Quad u = quad_of(bs[t * LANES]), last = t == 0 ? before : h[t == 0 ? 0 : t - 1];
+                const float2 q = s.coef[L::coef(t, c)];
+                const Quad u = quad_of(map(0, t)), last = t == 0 ? before : h[t == 0 ? 0 : t - 1];
                 const Pair d(q.x), dx(q.y);
                 h[t].a = fma(exp2_fast(mul(d, decay.a)), last.a, mul(dx, u.a));
                 h[t].b = fma(exp2_fast(mul(d, decay.b)), last.b, mul(dx, u.b));
@@ -168,138 +292,87 @@ __global__ void __launch_bounds__(kSelTile *LANES, LANES == 16 ? 1 : 12 / LANES)
                 float4 u, o;
                 float r;
             };
-            const auto operands = [&](int t) { return Operands{s.coef[mine.coef(t, c)], bs[t * LANES], cs[t * LANES], s.r[mine.value(t, c)]}; };
+            const auto operands = [&](int t) { return Operands{s.coef[L::coef(t, c)], map(0, t), map(1, t), s.r[L::value(t, c)]}; };
             Operands next = operands(FULL ? BLOCK - 1 : count - 1);
+            float s1[TOGETHER] = {}, s2[TOGETHER] = {}, s3[TOGETHER] = {};
+            // Position t; v: its products of the lane's states, B's and C's.
+            const auto pass = [&](int t, float (&v)[8]) {
+                const Operands now = next;
+                if (t > 0) next = operands(t - 1);
+                const Quad u = quad_of(now.u), o = quad_of(now.o), last = t == 0 ? before : h[t == 0 ? 0 : t - 1];
+                const Pair d(now.q.x), dx(now.q.y), r(now.r);
+                const Quad g = {fma(o.a, r, carry.a), fma(o.b, r, carry.b)};
+                carry.a = mul(exp2_again(mul(d, decay.a)), g.a), carry.b = mul(exp2_again(mul(d, decay.b)), g.b);
+                const Quad kk = {mul(carry.a, last.a), mul(carry.b, last.b)};
+                dA_block.a = fma(kk.a, d, dA_block.a), dA_block.b = fma(kk.b, d, dA_block.b);
+                const Pair p1 = fma(g.a, u.a, mul(g.b, u.b)), p2 = fma(kk.a, decay.a, mul(kk.b, decay.b));
+                const Pair p3 = fma(o.a, h[t].a, mul(o.b, h[t].b));
+                s1[t % TOGETHER] = p1.lo() + p1.hi(), s2[t % TOGETHER] = p2.lo() + p2.hi(), s3[t % TOGETHER] = p3.lo() + p3.hi();
+                const Pair to_b = CUT ? Pair(now.q.y * kSelCut) : dx, to_c = CUT ? Pair(now.r * kSelCut) : r;
+                const Pair b0 = mul(g.a, to_b), b1 = mul(g.b, to_b), c0 = mul(h[t].a, to_c), c1 = mul(h[t].b, to_c);
+                v[0] = b0.lo(), v[1] = b0.hi(), v[2] = b1.lo(), v[3] = b1.hi();
+                v[4] = c0.lo(), v[5] = c0.hi(), v[6] = c1.lo(), v[7] = c1.hi();
+            };
+            float sums[4];  // of the last two positions
+            const auto put_part = [&](int p) {
+                // row lane / 4: value (state, B or C); columns: the group of four channels, then the quad of states
+                const int r = lane.lane / 4, j = lane.lane % 4, which = r / 4, state = r % 4;
+                constexpr int FOURS = Place2::CHANNELS / 4;  // columns of a quad: 4, 2 or 1
 #pragma unroll
-            for (int batch = BLOCK / TOGETHER - 1; batch >= 0; --batch) {
-                if (!FULL && batch * TOGETHER >= count) continue;
-                float s1[TOGETHER], s2[TOGETHER], s3[TOGETHER];
-#pragma unroll
-                for (int j = TOGETHER - 1; j >= 0; --j) {
-                    const int t = batch * TOGETHER + j;
-                    s1[j] = s2[j] = s3[j] = 0.f;
-                    if (!FULL && t >= count) continue;
-                    const Operands now = next;
-                    if (t > 0) next = operands(t - 1);
-                    const Quad u = quad_of(now.u), o = quad_of(now.o), last = t == 0 ? before : h[t == 0 ? 0 : t - 1];
-                    const Pair d(now.q.x), dx(now.q.y), r(now.r);
-                    const Quad g = {fma(o.a, r, carry.a), fma(o.b, r, carry.b)};
-                    carry.a = mul(exp2_again(mul(d, decay.a)), g.a), carry.b = mul(exp2_again(mul(d, decay.b)), g.b);
-                    const Quad kk = {mul(carry.a, last.a), mul(carry.b, last.b)};
-                    dA_block.a = fma(kk.a, d, dA_block.a), dA_block.b = fma(kk.b, d, dA_block.b);
-                    const Pair p1 = fma(g.a, u.a, mul(g.b, u.b)), p2 = fma(kk.a, decay.a, mul(kk.b, decay.b));
-                    const Pair p3 = fma(o.a, h[t].a, mul(o.b, h[t].b));
-                    s1[j] = p1.lo() + p1.hi(), s2[j] = p2.lo() + p2.hi(), s3[j] = p3.lo() + p3.hi();
-                    // over the warp's channels: first lanes whose orders differ in 2 (a lane keeps its places 0 and 1), then
-                    // in 1 (it keeps place 0)
-                    constexpr int FIRST = CHANNELS >= 8 ? 4 : CHANNELS / 2;
-                    const auto swap = [](float v, int m) { return __shfl_xor_sync(0xffffffffu, v, m); };
-                    const Pair b1 = mul(g.b, dx), c1 = mul(h[t].b, r);
-                    const Pair db = fma(g.a, dx, Pair(swap(b1.lo(), FIRST), swap(b1.hi(), FIRST)));
-                    const Pair dc = fma(h[t].a, r, Pair(swap(c1.lo(), FIRST), swap(c1.hi(), FIRST)));
-                    float(&to)[2][PAD] = s.part[lane.warp][t];
-                    if constexpr (CHANNELS == 2) {
-                        float(&mine_of)[PAD] = to[0], (&other)[PAD] = to[1];
-                        mine_of[n0 + order] = db.lo(), mine_of[n0 + (order ^ 1)] = db.hi();
-                        other[n0 + order] = dc.lo(), other[n0 + (order ^ 1)] = dc.hi();
+                for (int k = 0; k < 2; ++k) {
+                    float *const to = s.part[lane.row][2 * p + k][which] + lane.warp % Place2::HALVES * 4 * Place2::WITHIN + state;
+                    const float v0 = sums[2 * k], v1 = sums[2 * k + 1];
+                    if constexpr (FOURS == 1) {
+                        to[8 * j] = v0, to[8 * j + 4] = v1;
                     } else {
-                        const float vb = db.lo() + swap(db.hi(), FIRST / 2), vc = dc.lo() + swap(dc.hi(), FIRST / 2);
-                        if constexpr (CHANNELS == 4) {
-                            to[0][n0 + order] = vb, to[1][n0 + order] = vc;
-                        } else {
-                            const bool odd = lane.cl & 1;
-                            float v = (odd ? vc : vb) + swap(odd ? vb : vc, 1);
-                            if (CHANNELS == 16) v += swap(v, 8);
-                            if (CHANNELS == 8 || lane.cl < 8) to[odd][n0 + order] = v;
-                        }
+                        float v = v0 + v1;
+                        if (FOURS == 4) v += __shfl_xor_sync(0xffffffffu, v, 1);
+                        if (FOURS == 2) to[4 * j] = v;
+                        else if (j % 2 == 0) to[2 * j] = v;
                     }
                 }
-                Part::put_sums(s.sums[0], batch * TOGETHER, c, quad, s1);
-                Part::put_sums(s.sums[1], batch * TOGETHER, c, quad, s2);
-                Part::put_sums(s.sums[2], batch * TOGETHER, c, quad, s3);
+            };
+#pragma unroll
+            for (int p = PAIRS - 1; p >= 0; --p) {
+                if (!FULL && 2 * p >= count) continue;
+                float v0[8], v1[8] = {};
+                const auto put_sums = [&](int t) {  // once its TOGETHER positions are through
+                    if (t % TOGETHER != 0) return;
+                    L::put_sums(s.sums[0], t, c, quad, s1), L::put_sums(s.sums[1], t, c, quad, s2), L::put_sums(s.sums[2], t, c, quad, s3);
+                };
+                if (FULL || 2 * p + 1 < count) pass(2 * p + 1, v1), put_sums(2 * p + 1);
+                else if (TOGETHER > 1) s1[(2 * p + 1) % TOGETHER] = s2[(2 * p + 1) % TOGETHER] = s3[(2 * p + 1) % TOGETHER] = 0.f;
+                pass(2 * p, v0), put_sums(2 * p);
+                if (FULL ? p < PAIRS - 1 : 2 * p + 2 < count) put_part(p + 1);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sums[k] = 0.f;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const uint32_t h0 = __float_as_uint(v0[r]), h1 = __float_as_uint(v1[r]);
+                    mma(sums, one[r], one[r], h0, h1);
+                    if (!CUT) {  // what the product with the upper 11 bits left
+                        const float l0 = v0[r] - __uint_as_float(h0 & 0xffffe000u), l1 = v1[r] - __uint_as_float(h1 & 0xffffe000u);
+                        mma(sums, one[r], one[r], __float_as_uint(l0), __float_as_uint(l1));
+                    }
+                }
             }
+            put_part(0);
             dA.a = add(dA.a, dA_block.a), dA.b = add(dA.b, dA_block.b);
         };
         if (count == BLOCK) scan(std::true_type{});
         else scan(std::false_type{});
-        __syncthreads();
-
-        Pair dx[COUNT], dd[COUNT], dz[COUNT];
-        const auto sum = [&](int which, int place) { return Part::get_sums(s.sums[which], place); };
-#pragma unroll
-        for (int i = 0; i < COUNT; ++i) {
-            if (!mine.busy()) continue;
-            const int t = mine.position(i), at_c = mine.channel(i), place = mine.value(t, at_c);
-            // (an element past the end or beside the tile has whatever an earlier block left: it is neither stored nor summed)
-            const float4 q = *reinterpret_cast<const float4 *>(s.coef + mine.coef(t, at_c));
-            const Pair into = sum(0, place), xi = pair_of<T>(x[i]), r(*reinterpret_cast<const unsigned long long *>(s.r + place)), Di = D[PLANES ? i : 0];
-            dd[i] = fma(xi, into, mul(sum(1, place), Pair(kSelLn2)));
-            if (a.s.softplus) dd[i] = mul(dd[i], Pair(*reinterpret_cast<const unsigned long long *>(&s.stash[0][i][tid])));
-            dx[i] = fma(Di, r, mul(Pair(q.x, q.z), into));
-            if (gated) dz[i] = mul(Pair(*reinterpret_cast<const unsigned long long *>(&s.stash[1][i][tid])), fma(Di, xi, sum(2, place)));
-            Pair rx = mul(r, xi), di = dd[i];
-            if (count < BLOCK || at_.channels < kSelTile) {
-                const bool first = mine.in(i, 0, at_.channels, count), second = mine.in(i, 1, at_.channels, count);
-                rx = {first ? rx.lo() : 0.f, second ? rx.hi() : 0.f}, di = {first ? di.lo() : 0.f, second ? di.hi() : 0.f};
-            }
-            dD[PLANES ? i : 0] = add(dD[PLANES ? i : 0], rx), d_bias[PLANES ? i : 0] = add(d_bias[PLANES ? i : 0], di);
-        }
-        mine.store(at<T, PLANES>(a.g.dx, b, t0, at_.c0), a.g.dx.row, at_.channels, count, [&](int i) { return dx[i]; });
-        mine.store(at<T, PLANES>(a.g.d_dt, b, t0, at_.c0), a.g.d_dt.row, at_.channels, count, [&](int i) { return dd[i]; });
-        if (gated) mine.store(at<T, PLANES>(a.g.dz, b, t0, at_.c0), a.g.dz.row, at_.channels, count, [&](int i) { return dz[i]; });
-        float *const to = a.part_bc + (((long long)at_.tile * a.s.B + b) * a.s.T + t0) * 2 * PAD;
-        for (int e = tid; e < count * 2 * PAD; e += THREADS) {
-            const float *const from = &s.part[0][0][0][0] + e;
-            float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < LANES; ++w) v += from[w * BLOCK * 2 * PAD];
-            to[e] = v;
-        }
-        // (the next block's coefficients are read by the thread that writes them here, the rest after its first barrier)
+        R::meet();
     }
 
     if (LOCAL) {
-        if (live && at_.first < at_.length) {
-            const long long i = ((long long)b * a.segments + at_.segment) * a.s.C + at_.c0 + c;
-            *reinterpret_cast<float4 *>(a.ends + i * PAD + n0) = float4_of(reordered(carry, order));
-            if (quad == 0) a.steps[i] = step_sum;
+        if (live && count_blocks > 0) {
+            *reinterpret_cast<float4 *>(a.ends + (first_sum + c) * L::PAD + n0) = float4_of(carry);
+            if (quad == 0) a.steps[first_sum + c] = step_sum;
         }
         return;
     }
-    if (at_.segment == 0 && live && a.g.d_h0 != nullptr) store_quad(a.g.d_h0 + row * N, n0, N, reordered(carry, order));
-    const long long i = ((long long)b * a.segments + at_.segment) * a.s.C + at_.c0;
-    if (live) store_quad(a.part_a + (i + c) * N, n0, N, reordered(dA, order));
-    // dD and d_dt_bias: the threads that share a channel
-    const long long half = (long long)a.s.B * a.segments * a.s.C;
-    if (PLANES) {  // neighbouring lanes
-#pragma unroll
-        for (int j = 0; j < OWN; ++j) {
-            float v = dD[j].lo() + dD[j].hi(), w = d_bias[j].lo() + d_bias[j].hi();
-#pragma unroll
-            for (int m = Part::INNER / 2; m >= 1; m /= 2) v += __shfl_xor_sync(0xffffffffu, v, m), w += __shfl_xor_sync(0xffffffffu, w, m);
-            const int pc = mine.channel(j);
-            if (mine.busy() && mine.inner == 0 && pc < at_.channels) a.part_c[i + pc] = v, a.part_c[half + i + pc] = w;
-        }
-    } else {
-        __syncthreads();
-        float2 *const meet = reinterpret_cast<float2 *>(s.part);  // [2][THREADS]
-        *reinterpret_cast<unsigned long long *>(meet + tid) = dD[0].q, *reinterpret_cast<unsigned long long *>(meet + THREADS + tid) = d_bias[0].q;
-        __syncthreads();
-        if (tid < at_.channels) {
-            float v = 0.f, w = 0.f;
-            for (int j = 0; j < THREADS / Part::INNER; ++j) {
-                const float *const p = reinterpret_cast<const float *>(meet + j * Part::INNER) + tid;
-                v += p[0], w += p[2 * THREADS];
-            }
-            a.part_c[i + tid] = v, a.part_c[half + i + tid] = w;
-        }
-    }
-    // positions past the sequence's end
-    for (int t0 = max(at_.first, at_.length); t0 < at_.end; t0 += BLOCK) {
-        mine.clear(at<T, PLANES>(a.g.dx, b, t0, at_.c0), a.g.dx.row, at_.channels, at_.end - t0);
-        mine.clear(at<T, PLANES>(a.g.d_dt, b, t0, at_.c0), a.g.d_dt.row, at_.channels, at_.end - t0);
-        if (gated) mine.clear(at<T, PLANES>(a.g.dz, b, t0, at_.c0), a.g.dz.row, at_.channels, at_.end - t0);
-    }
+    if (at_.segment == 0 && live && a.g.d_h0 != nullptr) store_quad(a.g.d_h0 + row * N, n0, N, carry);
+    if (live) store_quad(a.part_a + (first_sum + c) * N, n0, N, dA);
 }
 
 // dB and dC: the sums over a group's tiles, in their order; 0 past a sequence's end.
@@ -329,8 +402,8 @@ template <typename T, bool PLANES> __global__ void __launch_bounds__(256) select
 }
 
 template <typename T, int LANES, bool PLANES, bool WIDE> cudaError_t launch_selective_backward_as(const SelectiveArgs &a, cudaStream_t st) {
-    const unsigned threads = kSelTile * LANES, grid = (unsigned)a.ctas() * a.segments;
-    const size_t shared = sizeof(BackwardShared<LANES, PLANES>);
+    const unsigned threads = Roles<LANES>::THREADS, grid = (unsigned)a.ctas() * a.segments;
+    const size_t shared = 2 * sizeof(BackwardShared<LANES, PLANES>);
     const auto local = selective_backward_kernel<T, LANES, PLANES, WIDE, true>, whole = selective_backward_kernel<T, LANES, PLANES, WIDE, false>;
     cudaError_t e = cudaSuccess;
     if (a.segments > 1) {

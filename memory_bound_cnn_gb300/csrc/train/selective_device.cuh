@@ -69,17 +69,39 @@ template <int COUNT, int FIRST> __device__ __forceinline__ void sum_exchange(flo
     }
 }
 
-// A lane's place in a CTA of LANES warps: a warp has 32 / LANES channels, neighbouring lanes neighbouring channels,
-// and LANES lanes with four states each to a channel.  (Lanes that read the same 16 bytes of B or C are then
-// neighbours: such a load takes two cycles of the shared memory, and four where they lie apart.)
+// A scanning lane's place in a CTA: of a warp's lanes `CHANNELS` neighbours have neighbouring channels, and WITHIN lanes
+// with four states each share a channel (with 16 lanes to a channel, two warps have half of its states each).  Lanes
+// that read the same 16 bytes of B or C are then neighbours: such a load takes two cycles of the shared memory,
+// and four where they lie apart.
 template <int LANES> struct LanePlace {
-    static constexpr int CHANNELS = 32 / LANES;
-    int warp, cl, c, quad, n0;
+    static constexpr int WITHIN = LANES < 8 ? LANES : 8, HALVES = LANES / WITHIN, CHANNELS = 32 / WITHIN;
+    int lane, warp, row, c, quad, n0;  // row: of the warps that have the same states
     __device__ __forceinline__ LanePlace() {
-        const int lane = threadIdx.x % 32;
-        warp = threadIdx.x / 32, cl = lane % CHANNELS, quad = lane / CHANNELS;
-        c = warp * CHANNELS + cl, n0 = 4 * quad;
+        lane = threadIdx.x % 32, warp = threadIdx.x / 32, row = warp / HALVES;
+        c = row * CHANNELS + lane % CHANNELS, quad = warp % HALVES * WITHIN + lane / CHANNELS, n0 = 4 * quad;
     }
+};
+
+// Of a CTA's threads, the first 32 LANES scan; the others prepare the round after the scanned one and finish
+// the one before.  All meet once a round.
+template <int LANES> struct Roles {
+    static constexpr int SCANNERS = kSelTile * LANES, HELPERS = 128, THREADS = SCANNERS + HELPERS;
+    static __device__ __forceinline__ bool scans() { return threadIdx.x < SCANNERS; }
+    static __device__ __forceinline__ int helper() { return threadIdx.x - SCANNERS; }
+    // Registers of a thread, from what the CTA was launched with (LAUNCHED): scanners take what helpers give.  Whole
+    // groups of four warps do so together; the sum over the CTA stays.
+    static constexpr bool TRADE = LANES >= 4;
+    static constexpr int LAUNCHED = LANES == 4 ? 128 : LANES == 8 ? 168 : 96, GROUPS = SCANNERS / 128;
+    static constexpr int SCAN_REGS = LANES == 4 ? 184 : LANES == 8 ? 208 : 104, HELP_REGS = LANES == 4 ? 72 : LANES == 8 ? 88 : 64;
+    static_assert(!TRADE || (GROUPS * SCAN_REGS + HELP_REGS == (GROUPS + 1) * LAUNCHED && SCANNERS % 128 == 0), "");
+    static __device__ __forceinline__ void take() {
+        if constexpr (TRADE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SCAN_REGS));
+    }
+    static __device__ __forceinline__ void give() {
+        if constexpr (TRADE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(HELP_REGS));
+    }
+    static __device__ __forceinline__ void meet() { asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory"); }
+    static __device__ __forceinline__ void helpers_meet() { asm volatile("bar.sync 2, %0;" ::"n"(HELPERS) : "memory"); }
 };
 
 // What a CTA works on: a tile of channels of one group, a segment of one sequence.
@@ -133,47 +155,29 @@ template <typename V, int COUNT> __device__ __forceinline__ void arrived(V (&v)[
     for (int i = 0; i < COUNT; ++i) arrived(v[i]);
 }
 
-// A thread's part of ROUND positions of 32 channels: pairs of neighbours along the axis that is contiguous.  All
-// of a round's loads are issued before the first is used (a load that waits behind a branch on another's value
-// makes a round as long as all their latencies together).  WIDE: pairs lie at multiples of their size.
-// A round of the tile in shared memory has 32 channels to a position (tokens) or ROUND positions to a channel
-// (planes), rows apart such that neither pairs nor a warp's lanes, one position or one channel apart, meet on a bank.
-template <bool PLANES, int LANES, int ROUND, bool WIDE> struct Share {
-    static constexpr int THREADS = kSelTile * LANES, INNER = (PLANES ? ROUND : kSelTile) / 2, PAIRS = kSelTile * ROUND / 2;
+// A helper's part of ROUND positions of WIDTH channels (or states): pairs of neighbours along the axis that is
+// contiguous.  All of a round's loads are issued before the first is used (a load that waits behind a branch on
+// another's value makes a round as long as all their latencies together).  WIDE: pairs lie at multiples of their size.
+template <bool PLANES, int WIDTH, int ROUND, int THREADS, bool WIDE> struct Share {
+    static constexpr int INNER = (PLANES ? ROUND : WIDTH) / 2, PAIRS = WIDTH * ROUND / 2;
     static constexpr int COUNT = PAIRS < THREADS ? 1 : PAIRS / THREADS, STEP = THREADS / INNER, OWN = PLANES ? COUNT : 1;
-    // rows of coefficients (two floats) and of values that the lanes write (one).  Of a channel's lanes PARTS write their
-    // part of a sum (with 8 or 16 lanes, 2 or 4 of them meet by exchanges first); parts lie APART.
-    static constexpr int COEF = PLANES ? ROUND + 2 : kSelTile, COEFS = COEF * (PLANES ? kSelTile : ROUND);
-    static constexpr int VALUE = PLANES ? ROUND + 4 : kSelTile, VALUES = VALUE * (PLANES ? kSelTile : ROUND);
-    static constexpr int PARTS = LANES < 4 ? LANES : 4, TOGETHER = LANES / PARTS, APART = VALUES + (PLANES ? 2 : kSelTile / PARTS);
-    static __device__ __forceinline__ int coef(int t, int c) { return PLANES ? c * COEF + t : t * COEF + c; }
-    static __device__ __forceinline__ int value(int t, int c) { return PLANES ? c * VALUE + t : t * VALUE + c; }
-    // the lane's part of TOGETHER positions' sums from t on
-    static __device__ __forceinline__ void put_sums(float *sums, int t, int c, int quad, float (&v)[TOGETHER]) {
-        if (TOGETHER > 1) sum_exchange<TOGETHER, 32 / LANES>(v, quad % TOGETHER);
-        sums[quad / TOGETHER * APART + value(t + quad % TOGETHER, c)] = v[0];
-    }
-    static __device__ __forceinline__ Pair get_sums(const float *sums, int place) {
-        Pair s(*reinterpret_cast<const unsigned long long *>(sums + place));
-#pragma unroll
-        for (int i = 1; i < PARTS; ++i) s = add(s, Pair(*reinterpret_cast<const unsigned long long *>(sums + i * APART + place)));
-        return s;
-    }
+    static constexpr bool ALL = PAIRS >= THREADS;  // every thread has pairs
+    static_assert(THREADS % INNER == 0 && (ALL ? PAIRS % THREADS == 0 : true), "");
     int inner, outer;  // of the first pair
-    __device__ __forceinline__ Share() : inner(threadIdx.x % INNER * 2), outer(threadIdx.x / INNER) {}
-    static __device__ __forceinline__ bool busy() { return PAIRS >= THREADS || threadIdx.x < PAIRS; }
+    __device__ __forceinline__ explicit Share(int thread) : inner(thread % INNER * 2), outer(thread / INNER) {}
+    __device__ __forceinline__ bool busy() const { return ALL || outer < (PLANES ? WIDTH : ROUND); }
     __device__ __forceinline__ int channel(int i) const { return PLANES ? outer + i * STEP : inner; }
     __device__ __forceinline__ int position(int i) const { return PLANES ? inner : outer + i * STEP; }
-    // whether the pair's k-th element is one of `channels` and `count`
-    __device__ __forceinline__ bool in(int i, int k, int channels, int count) const {
-        return busy() && channel(i) + (PLANES ? 0 : k) < channels && position(i) + (PLANES ? k : 0) < count;
+    // whether the pair's k-th element is one of `width` and `count`
+    __device__ __forceinline__ bool in(int i, int k, int width, int count) const {
+        return busy() && channel(i) + (PLANES ? 0 : k) < width && position(i) + (PLANES ? k : 0) < count;
     }
-    // base: of the round's first position and the tile's first channel
+    // base: of the round's first position and the first channel
     template <typename T>
-    __device__ __forceinline__ void load(const T *base, long long row, int channels, int count, typename Raw<T>::Two (&v)[COUNT]) const {
+    __device__ __forceinline__ void load(const T *base, long long row, int width, int count, typename Raw<T>::Two (&v)[COUNT]) const {
         const T *p = base + outer * row + inner;
         const long long step = STEP * row;
-        if (WIDE && PAIRS >= THREADS && channels == kSelTile && count >= ROUND) {
+        if (WIDE && ALL && width == WIDTH && count >= ROUND) {
 #pragma unroll
             for (int i = 0; i < COUNT; ++i) v[i] = *reinterpret_cast<const typename Raw<T>::Two *>(p + i * step);
             return;
@@ -181,16 +185,16 @@ template <bool PLANES, int LANES, int ROUND, bool WIDE> struct Share {
 #pragma unroll
         for (int i = 0; i < COUNT; ++i) {
             uint32_t first = 0, second = 0;
-            if (in(i, 0, channels, count)) first = load_one(p + i * step);
-            if (in(i, 1, channels, count)) second = load_one(p + i * step + 1);
+            if (in(i, 0, width, count)) first = load_one(p + i * step);
+            if (in(i, 1, width, count)) second = load_one(p + i * step + 1);
             v[i] = two_of<T>(first, second);
         }
     }
     // value(i), a Pair, to its place
-    template <typename T, typename F> __device__ __forceinline__ void store(T *base, long long row, int channels, int count, F value) const {
+    template <typename T, typename F> __device__ __forceinline__ void store(T *base, long long row, int width, int count, F value) const {
         T *p = base + outer * row + inner;
         const long long step = STEP * row;
-        if (WIDE && PAIRS >= THREADS && channels == kSelTile && count >= ROUND) {
+        if (WIDE && ALL && width == WIDTH && count >= ROUND) {
 #pragma unroll
             for (int i = 0; i < COUNT; ++i) {
                 const Pair v = value(i);
@@ -202,57 +206,63 @@ template <bool PLANES, int LANES, int ROUND, bool WIDE> struct Share {
         }
 #pragma unroll
         for (int i = 0; i < COUNT; ++i) {
-            if (!in(i, 0, channels, count)) continue;
+            if (!in(i, 0, width, count)) continue;
             const Pair v = value(i);
             p[i * step] = from_f32<T>(v.lo());
-            if (in(i, 1, channels, count)) p[i * step + 1] = from_f32<T>(v.hi());
+            if (in(i, 1, width, count)) p[i * step + 1] = from_f32<T>(v.hi());
         }
     }
     // 0 to a round that may begin at an odd position: an element at a time
-    template <typename T> __device__ __forceinline__ void clear(T *base, long long row, int channels, int count) const {
+    template <typename T> __device__ __forceinline__ void clear(T *base, long long row, int width, int count) const {
         T *p = base + outer * row + inner;
 #pragma unroll
         for (int i = 0; i < COUNT; ++i) {
-            if (in(i, 0, channels, count)) p[i * STEP * row] = from_f32<T>(0.f);
-            if (in(i, 1, channels, count)) p[i * STEP * row + 1] = from_f32<T>(0.f);
+            if (in(i, 0, width, count)) p[i * STEP * row] = from_f32<T>(0.f);
+            if (in(i, 1, width, count)) p[i * STEP * row + 1] = from_f32<T>(0.f);
         }
     }
     // one fp32 parameter for each channel of the thread's pairs
-    __device__ __forceinline__ void parameters(const float *of_tile, int channels, Pair (&v)[OWN]) const {
+    __device__ __forceinline__ void parameters(const float *of_tile, int width, Pair (&v)[OWN]) const {
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
             const int c = channel(i);
-            const float a = of_tile != nullptr && c < channels ? of_tile[c] : 0.f;
-            v[i] = Pair(a, PLANES ? a : of_tile != nullptr && c + 1 < channels ? of_tile[c + 1] : 0.f);
+            const float a = of_tile != nullptr && c < width ? of_tile[c] : 0.f;
+            v[i] = Pair(a, PLANES ? a : of_tile != nullptr && c + 1 < width ? of_tile[c + 1] : 0.f);
         }
     }
 };
-// The same of ROUND positions of a group's N states (padded to PAD).
-template <bool PLANES, int LANES, int ROUND> struct MapShare {
-    static constexpr int THREADS = kSelTile * LANES, PAD = 4 * LANES, COUNT = PAD * ROUND / THREADS;
-    static_assert(THREADS % ROUND == 0 && THREADS % PAD == 0, "");
-    int first_state, first_position;
-    __device__ __forceinline__ MapShare() {
-        first_state = PLANES ? threadIdx.x / ROUND : threadIdx.x % PAD;
-        first_position = PLANES ? threadIdx.x % ROUND : threadIdx.x / PAD;
+
+// A round of the tile in shared memory has 32 channels to a position (tokens) or ROUND positions to a channel (planes),
+// rows apart such that neither the helpers' pairs nor a warp's lanes, one channel apart, meet on a bank.
+template <int LANES, bool PLANES, int ROUND> struct Layout {
+    static constexpr int COEF = PLANES ? ROUND + 2 : kSelTile, COEFS = COEF * (PLANES ? kSelTile : ROUND);    // of two floats
+    static constexpr int VALUE = PLANES ? ROUND + 4 : kSelTile, VALUES = VALUE * (PLANES ? kSelTile : ROUND);  // of one
+    // Of a channel's lanes PARTS write their part of a sum (with 8 or 16 lanes, 2 or 4 of them meet by exchanges first).
+    static constexpr int PARTS = LANES < 4 ? LANES : 4, TOGETHER = LANES / PARTS, APART = VALUES + (PLANES ? 2 : kSelTile / PARTS);
+    // B and C: a row of the states to a position (planes: rows apart for the helpers, who write one state at a time)
+    static constexpr int PAD = 4 * LANES, MAP = PLANES && LANES < 16 ? PAD + 4 : PAD;
+    static __device__ __forceinline__ int coef(int t, int c) { return PLANES ? c * COEF + t : t * COEF + c; }
+    static __device__ __forceinline__ int value(int t, int c) { return PLANES ? c * VALUE + t : t * VALUE + c; }
+    // the lane's part of TOGETHER positions' sums from t on
+    static __device__ __forceinline__ void put_sums(float *sums, int t, int c, int quad, float (&v)[TOGETHER]) {
+        if (TOGETHER > 1) sum_exchange<TOGETHER, LanePlace<LANES>::CHANNELS>(v, quad % TOGETHER);
+        sums[quad / TOGETHER * APART + value(t + quad % TOGETHER, c)] = v[0];
     }
-    __device__ __forceinline__ int state(int i) const { return PLANES ? first_state + i * (THREADS / ROUND) : first_state; }
-    __device__ __forceinline__ int position(int i) const { return PLANES ? first_position : first_position + i * (THREADS / PAD); }
-    template <typename T> __device__ __forceinline__ void load(const T *base, long long row, int N, int count, uint32_t (&v)[COUNT]) const {
-        const T *p = base + (PLANES ? first_state * row + first_position : first_position * row + first_state);
-        const long long step = (PLANES ? THREADS / ROUND : THREADS / PAD) * row;
+    static __device__ __forceinline__ Pair get_sums(const float *sums, int place) {
+        Pair s(*reinterpret_cast<const unsigned long long *>(sums + place));
 #pragma unroll
-        for (int i = 0; i < COUNT; ++i, p += step) {
-            v[i] = 0;
-            if (state(i) < N && position(i) < count) v[i] = load_one(p);
+        for (int i = 1; i < PARTS; ++i) s = add(s, Pair(*reinterpret_cast<const unsigned long long *>(sums + i * APART + place)));
+        return s;
+    }
+    template <typename T, typename M> static __device__ __forceinline__ void put_map(const M &maps, typename Raw<T>::Two (&v)[M::COUNT], float *to) {
+#pragma unroll
+        for (int i = 0; i < M::COUNT; ++i) {
+            if (!maps.busy()) continue;
+            const Pair p = pair_of<T>(v[i]);
+            float *const q = to + maps.position(i) * MAP + maps.channel(i);
+            if (PLANES) q[0] = p.lo(), q[MAP] = p.hi();
+            else *reinterpret_cast<unsigned long long *>(q) = p.q;
         }
-    }
-    // COPIES of the states in other orders, APART floats from one another: copy k has state n at n ^ (k * 4 / COPIES)
-    template <typename T, int COPIES, int APART> __device__ __forceinline__ void put(const uint32_t (&v)[COUNT], float *to) const {
-#pragma unroll
-        for (int i = 0; i < COUNT; ++i)
-#pragma unroll
-            for (int k = 0; k < COPIES; ++k) to[k * APART + position(i) * PAD + (state(i) ^ (k * (4 / COPIES)))] = f32_of<T>(v[i]);
     }
 };
 
@@ -273,10 +283,4 @@ __device__ __forceinline__ void store_quad(float *row, int n0, int N, const Quad
 }
 __device__ __forceinline__ Quad quad_of(const float4 &v) { return {Pair(v.x, v.y), Pair(v.z, v.w)}; }
 __device__ __forceinline__ float4 float4_of(const Quad &q) { return make_float4(q.a.lo(), q.a.hi(), q.b.lo(), q.b.hi()); }
-// Element i to place i ^ order (and back).
-__device__ __forceinline__ Quad reordered(const Quad &q, int order) {
-    const Pair a = order & 2 ? q.b : q.a, b = order & 2 ? q.a : q.b;
-    return order & 1 ? Quad{Pair(a.hi(), a.lo()), Pair(b.hi(), b.lo())} : Quad{a, b};
-}
-
 }  // namespace wtconv

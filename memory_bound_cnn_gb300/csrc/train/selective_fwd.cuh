@@ -5,44 +5,118 @@
 
 namespace wtconv {
 
-// A CTA scans 32 channels of one sequence (or of a segment of it), LANES lanes with four states each to a
-// channel.  It works in rounds of 32 positions: every thread computes d and d x of its share of the round's
-// 32 x 32 positions and channels once, all lanes then scan the round out of shared memory, sums over the states
-// meet by exchanges between lanes, and the epilogue (D, gate, store) goes by the share again.
+// A CTA takes 32 channels of one sequence (or of a segment of it) in rounds of 32 positions.  LANES lanes with four states
+// each scan a channel; the CTA's other warps, the helpers, compute d and d x of the next round's 32 x 32
+// positions and channels once for all lanes, and finish the round before (sum the lanes' parts, D, gate, store).
 // LOCAL: only the state that the segment ends with if it begins with 0, and the sum of its steps; the CTAs of
 // later segments begin with what these compose to.
+template <int LANES, bool PLANES> struct ForwardShared {
+    using L = Layout<LANES, PLANES, kSelRound>;
+    alignas(16) float2 coef[L::COEFS];  // d, d x
+    alignas(16) float maps[2][kSelRound * L::MAP];
+    alignas(16) float sums[L::PARTS * L::APART];  // over a channel's states
+};
+
 template <typename T, int LANES, bool PLANES, bool WIDE, bool LOCAL>
-__global__ void __launch_bounds__(kSelTile *LANES) selective_forward_kernel(const __grid_constant__ SelectiveArgs a) {
-    constexpr int PAD = 4 * LANES;
-    using Part = Share<PLANES, LANES, kSelRound, WIDE>;
-    using Maps = MapShare<PLANES, LANES, kSelRound>;
-    __shared__ __align__(16) float2 coef[Part::COEFS];  // d, d x
-    __shared__ float4 bs[kSelRound * LANES], cs[LOCAL ? 1 : kSelRound * LANES];
-    __shared__ __align__(8) float sums[LOCAL ? 2 : Part::PARTS * Part::APART];
+__global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES == 2 ? 3 : LANES == 4 ? 2 : 1) selective_forward_kernel(const __grid_constant__ SelectiveArgs a) {
+    using L = Layout<LANES, PLANES, kSelRound>;
+    using R = Roles<LANES>;
+    extern __shared__ float4 shared_memory[];
+    ForwardShared<LANES, PLANES> *const rounds = reinterpret_cast<ForwardShared<LANES, PLANES> *>(shared_memory);  // two
     begin_kernel();
     const Place at_(a, blockIdx.x);
     if (LOCAL && at_.segment == a.segments - 1) return;  // its end is nobody's beginning
     const int b = at_.b, N = a.s.N, stop = min(at_.end, at_.length);
-    const LanePlace<LANES> lane;
-    const int c = lane.c, quad = lane.quad, n0 = lane.n0;  // the lane's channel and states
-    const bool live = c < at_.channels, gated = !LOCAL && a.in.z.p != nullptr;
-    const Part part;
-    const Maps maps;
-    typename Raw<T>::Two x_next[Part::COUNT], d_next[Part::COUNT], z_next[Part::COUNT];
-    uint32_t b_next[Maps::COUNT], c_next[Maps::COUNT];
-    const auto fetch = [&](int t0) {
-        const int count = stop - t0;
-        part.load(at<const T, PLANES>(a.in.dt, b, t0, at_.c0), a.in.dt.row, at_.channels, count, d_next);
-        part.load(at<const T, PLANES>(a.in.x, b, t0, at_.c0), a.in.x.row, at_.channels, count, x_next);
-        maps.load(at<const T, PLANES>(a.in.Bm, b, t0, at_.group * N), a.in.Bm.row, N, count, b_next);
-        if (!LOCAL) maps.load(at<const T, PLANES>(a.in.Cm, b, t0, at_.group * N), a.in.Cm.row, N, count, c_next);
-        if (gated) part.load(at<const T, PLANES>(a.in.z, b, t0, at_.c0), a.in.z.row, at_.channels, count, z_next);
-    };
-    if (at_.first < stop) fetch(at_.first);
-    Pair bias[Part::OWN], D[Part::OWN];
-    part.parameters(a.in.dt_bias == nullptr ? nullptr : a.in.dt_bias + at_.c0, at_.channels, bias);
-    part.parameters(a.in.D == nullptr ? nullptr : a.in.D + at_.c0, at_.channels, D);
+    const int count_rounds = stop > at_.first ? (stop - at_.first + kSelRound - 1) / kSelRound : 0;
 
+    if (!R::scans()) {
+        using Part = Share<PLANES, kSelTile, kSelRound, R::HELPERS, WIDE>;
+        using Maps = Share<PLANES, L::PAD, kSelRound, R::HELPERS, WIDE>;
+        using Two = typename Raw<T>::Two;
+        const Part part(R::helper());
+        const Maps maps(R::helper());
+        const bool gated = !LOCAL && a.in.z.p != nullptr;
+        Pair bias[Part::OWN], D[Part::OWN];
+        part.parameters(a.in.dt_bias == nullptr ? nullptr : a.in.dt_bias + at_.c0, at_.channels, bias);
+        part.parameters(a.in.D == nullptr ? nullptr : a.in.D + at_.c0, at_.channels, D);
+        // two rounds ahead, in turns (moved from one place to another, a value would have to arrive first)
+        struct Fetched {
+            Two d[Part::COUNT], x[Part::COUNT], z[Part::COUNT], b[Maps::COUNT], c[Maps::COUNT];
+        } even, odd;
+        Two x[Part::COUNT], z[Part::COUNT], x_old[Part::COUNT] = {}, z_old[Part::COUNT] = {};  // of the scanned round, the one before
+        const auto fetch = [&](int r, Fetched &f) {
+            if (r >= count_rounds) return;
+            const int t0 = at_.first + r * kSelRound, count = stop - t0;
+            part.load(at<const T, PLANES>(a.in.dt, b, t0, at_.c0), a.in.dt.row, at_.channels, count, f.d);
+            part.load(at<const T, PLANES>(a.in.x, b, t0, at_.c0), a.in.x.row, at_.channels, count, f.x);
+            maps.load(at<const T, PLANES>(a.in.Bm, b, t0, at_.group * N), a.in.Bm.row, N, count, f.b);
+            if (!LOCAL) maps.load(at<const T, PLANES>(a.in.Cm, b, t0, at_.group * N), a.in.Cm.row, N, count, f.c);
+            if (gated) part.load(at<const T, PLANES>(a.in.z, b, t0, at_.c0), a.in.z.row, at_.channels, count, f.z);
+        };
+        const auto prepare = [&](int r, Fetched &f) {
+            if (r >= count_rounds) return;
+            ForwardShared<LANES, PLANES> &to = rounds[r & 1];
+            arrived(f.d), arrived(f.x), arrived(f.b);
+            if (!LOCAL) arrived(f.c);
+            if (gated) arrived(f.z);
+            const auto put = [&](int i, Pair d) {
+                const Pair dx = mul(d, pair_of<T>(f.x[i]));
+                // (past the end d x is what it may be: those positions are not scanned)
+                if (part.busy())
+                    *reinterpret_cast<float4 *>(to.coef + L::coef(part.position(i), part.channel(i))) = make_float4(d.lo(), dx.lo(), d.hi(), dx.hi());
+            };
+            if (a.s.softplus) {
+#pragma unroll
+                for (int i = 0; i < Part::COUNT; ++i) put(i, softplus_of(add(pair_of<T>(f.d[i]), bias[PLANES ? i : 0])));
+            } else {
+#pragma unroll
+                for (int i = 0; i < Part::COUNT; ++i) put(i, add(pair_of<T>(f.d[i]), bias[PLANES ? i : 0]));
+            }
+            L::template put_map<T>(maps, f.b, to.maps[0]);
+            if (!LOCAL) L::template put_map<T>(maps, f.c, to.maps[1]);
+#pragma unroll
+            for (int i = 0; i < Part::COUNT; ++i) x[i] = f.x[i], z[i] = f.z[i];
+        };
+        const auto finish = [&](int r) {
+            const int t0 = at_.first + r * kSelRound, count = stop - t0;
+            const float *const sums = rounds[r & 1].sums;
+            const auto value = [&](int i) {
+                const Pair s = L::get_sums(sums, L::value(part.position(i), part.channel(i)));
+                return fma(D[PLANES ? i : 0], pair_of<T>(x_old[i]), s);
+            };
+            T *const to = at<T, PLANES>(a.y, b, t0, at_.c0);
+            if (gated)
+                part.store(to, a.y.row, at_.channels, count, [&](int i) {
+                    const Pair g = pair_of<T>(z_old[i]);
+                    return mul(value(i), mul(g, sigmoid_of(g)));
+                });
+            else
+                part.store(to, a.y.row, at_.channels, count, value);
+        };
+        const auto during = [&](int r, Fetched &next, Fetched &after) {  // round r is scanned
+            fetch(r + 2, after);
+            if (!LOCAL && r > 0) finish(r - 1);
+#pragma unroll
+            for (int i = 0; i < Part::COUNT; ++i) x_old[i] = x[i], z_old[i] = z[i];
+            prepare(r + 1, next);
+            R::meet();
+        };
+        fetch(0, even), fetch(1, odd), prepare(0, even);
+        R::meet();
+        for (int r = 0; r < count_rounds; r += 2) {
+            during(r, odd, even);
+            if (r + 1 < count_rounds) during(r + 1, even, odd);
+        }
+        if (!LOCAL && count_rounds > 0) finish(count_rounds - 1);
+        if (!LOCAL)  // positions past the sequence's end
+            for (int t0 = max(at_.first, at_.length); t0 < at_.end; t0 += kSelRound)
+                part.clear(at<T, PLANES>(a.y, b, t0, at_.c0), a.y.row, at_.channels, at_.end - t0);
+        return;
+    }
+
+    const LanePlace<LANES> lane;
+    const int c = lane.c, quad = lane.quad, n0 = lane.n0;
+    const bool live = c < at_.channels;
     Quad decay = {Pair(0.f), Pair(0.f)}, h = {Pair(0.f), Pair(0.f)};
     if (live) {
         decay = load_quad(a.in.A + (long long)(at_.c0 + c) * N, n0, N);
@@ -50,56 +124,34 @@ __global__ void __launch_bounds__(kSelTile *LANES) selective_forward_kernel(cons
     }
     if (!LOCAL && live) {
         if (a.in.h0 != nullptr) h = load_quad(a.in.h0 + ((long long)b * a.s.C + at_.c0 + c) * N, n0, N);
-        if (at_.first < at_.length)
+        if (count_rounds > 0)
+#pragma unroll 4
             for (int k = 0; k < at_.segment; ++k) {
                 const long long i = ((long long)b * a.segments + k) * a.s.C + at_.c0 + c;
                 const Pair d(a.steps[i]);
-                const Quad u = quad_of(*reinterpret_cast<const float4 *>(a.ends + i * PAD + n0));
+                const Quad u = quad_of(*reinterpret_cast<const float4 *>(a.ends + i * L::PAD + n0));
                 h.a = fma(exp2_fast(mul(d, decay.a)), h.a, u.a), h.b = fma(exp2_fast(mul(d, decay.b)), h.b, u.b);
             }
     }
     float step_sum = 0.f;
     float *states = nullptr;  // the lane's of the next kept position
     if (!LOCAL && live && a.states_out != nullptr)
-        states = a.states_out + (((long long)b * a.keep + at_.first / kSelKeep) * a.s.C + at_.c0 + c) * PAD + n0;
-
-    for (int t0 = at_.first; t0 < stop; t0 += kSelRound) {
-        const int count = min(kSelRound, stop - t0);
-        typename Raw<T>::Two x[Part::COUNT], z[Part::COUNT];
-        arrived(d_next), arrived(x_next), arrived(b_next);
-        if (!LOCAL) arrived(c_next);
-#pragma unroll
-        for (int i = 0; i < Part::COUNT; ++i) x[i] = x_next[i], z[i] = z_next[i];
-        const auto put = [&](int i, Pair d) {
-            const Pair dx = mul(d, pair_of<T>(x[i]));
-            const int t = part.position(i), at_c = part.channel(i);
-            if (!part.busy()) return;
-            // (past the end d x is what it may be: those positions are not scanned)
-            *reinterpret_cast<float4 *>(coef + part.coef(t, at_c)) = make_float4(d.lo(), dx.lo(), d.hi(), dx.hi());
-        };
-        if (a.s.softplus) {
-#pragma unroll
-            for (int i = 0; i < Part::COUNT; ++i) put(i, softplus_of(add(pair_of<T>(d_next[i]), bias[PLANES ? i : 0])));
-        } else {
-#pragma unroll
-            for (int i = 0; i < Part::COUNT; ++i) put(i, add(pair_of<T>(d_next[i]), bias[PLANES ? i : 0]));
-        }
-        maps.template put<T, 1, 0>(b_next, reinterpret_cast<float *>(bs));
-        if (!LOCAL) maps.template put<T, 1, 0>(c_next, reinterpret_cast<float *>(cs));
-        __syncthreads();
-        if (t0 + kSelRound < stop) fetch(t0 + kSelRound);  // while this round is scanned
-
+        states = a.states_out + (((long long)b * a.keep + at_.first / kSelKeep) * a.s.C + at_.c0 + c) * L::PAD + n0;
+    R::meet();
+    for (int r = 0; r < count_rounds; ++r) {
+        ForwardShared<LANES, PLANES> &s = rounds[r & 1];
+        const int count = min(kSelRound, stop - at_.first - r * kSelRound);
         // Four positions at a time, what the next four need is loaded before their sums are stored: a load of shared
         // memory is not moved above a store, and would wait for all that the store waits for.
-        constexpr int TOGETHER = Part::TOGETHER, BATCH = 4;
+        constexpr int TOGETHER = L::TOGETHER, BATCH = 4;
         struct Operands {
             float2 q;
             float4 u, o;
         };
         const auto operands = [&](int t) {
             Operands p;
-            p.q = coef[part.coef(t, c)], p.u = bs[t * LANES + quad];
-            if (!LOCAL) p.o = cs[t * LANES + quad];
+            p.q = s.coef[L::coef(t, c)], p.u = *reinterpret_cast<const float4 *>(s.maps[0] + t * L::MAP + n0);
+            if (!LOCAL) p.o = *reinterpret_cast<const float4 *>(s.maps[1] + t * L::MAP + n0);
             return p;
         };
         const auto step = [&](const Operands &p) {  // one position; its sum over the lane's states
@@ -112,13 +164,13 @@ __global__ void __launch_bounds__(kSelTile *LANES) selective_forward_kernel(cons
                 return 0.f;
             }
             const Quad o = quad_of(p.o);
-            const Pair s = fma(o.a, h.a, mul(o.b, h.b));
-            return s.lo() + s.hi();
+            const Pair v = fma(o.a, h.a, mul(o.b, h.b));
+            return v.lo() + v.hi();
         };
         const auto keep = [&](int t) {
             if (!LOCAL && t % kSelKeep == 0 && states != nullptr) {
                 *reinterpret_cast<float4 *>(states) = float4_of(h);
-                states += (long long)a.s.C * PAD;
+                states += (long long)a.s.C * L::PAD;
             }
         };
         if (count == kSelRound) {
@@ -131,12 +183,12 @@ __global__ void __launch_bounds__(kSelTile *LANES) selective_forward_kernel(cons
                 const int ahead = min(t + BATCH, kSelRound - BATCH);
 #pragma unroll
                 for (int j = 0; j < BATCH; ++j) next[j] = operands(ahead + j);
-                float s[BATCH / TOGETHER][TOGETHER];
+                float v[BATCH / TOGETHER][TOGETHER];
 #pragma unroll
-                for (int j = 0; j < BATCH; ++j) s[j / TOGETHER][j % TOGETHER] = step(now[j]);
+                for (int j = 0; j < BATCH; ++j) v[j / TOGETHER][j % TOGETHER] = step(now[j]);
                 if (!LOCAL) {
 #pragma unroll
-                    for (int j = 0; j < BATCH / TOGETHER; ++j) part.put_sums(sums, t + j * TOGETHER, c, quad, s[j]);
+                    for (int j = 0; j < BATCH / TOGETHER; ++j) L::put_sums(s.sums, t + j * TOGETHER, c, quad, v[j]);
                 }
 #pragma unroll
                 for (int j = 0; j < BATCH; ++j) now[j] = next[j];
@@ -144,32 +196,19 @@ __global__ void __launch_bounds__(kSelTile *LANES) selective_forward_kernel(cons
         } else {
             for (int t = 0; t < count; t += TOGETHER) {
                 keep(t);
-                float s[TOGETHER];
+                float v[TOGETHER];
 #pragma unroll
-                for (int j = 0; j < TOGETHER; ++j) s[j] = t + j < count ? step(operands(t + j)) : 0.f;
-                if (!LOCAL) part.put_sums(sums, t, c, quad, s);
+                for (int j = 0; j < TOGETHER; ++j) v[j] = t + j < count ? step(operands(t + j)) : 0.f;
+                if (!LOCAL) L::put_sums(s.sums, t, c, quad, v);
             }
         }
-        __syncthreads();
-        if (LOCAL) continue;
-        if (gated) arrived(z);
-        const auto value = [&](int i) {
-            return fma(D[PLANES ? i : 0], pair_of<T>(x[i]), part.get_sums(sums, part.value(part.position(i), part.channel(i))));
-        };
-        T *const to = at<T, PLANES>(a.y, b, t0, at_.c0);
-        if (gated)
-            part.store(to, a.y.row, at_.channels, count, [&](int i) {
-                const Pair g = pair_of<T>(z[i]);
-                return mul(value(i), mul(g, sigmoid_of(g)));
-            });
-        else
-            part.store(to, a.y.row, at_.channels, count, value);
+        R::meet();
     }
 
     if (LOCAL) {
-        if (live && at_.first < at_.length) {
+        if (live && count_rounds > 0) {
             const long long i = ((long long)b * a.segments + at_.segment) * a.s.C + at_.c0 + c;
-            *reinterpret_cast<float4 *>(a.ends + i * PAD + n0) = float4_of(h);
+            *reinterpret_cast<float4 *>(a.ends + i * L::PAD + n0) = float4_of(h);
             if (quad == 0) a.steps[i] = step_sum;
         }
         return;
@@ -177,18 +216,19 @@ __global__ void __launch_bounds__(kSelTile *LANES) selective_forward_kernel(cons
     // the sequence ends in this segment
     if (a.h_last != nullptr && live && (at_.segment == 0 ? at_.length <= at_.end : at_.first < at_.length && at_.length <= at_.end))
         store_quad(a.h_last + ((long long)b * a.s.C + at_.c0 + c) * N, n0, N, h);
-    // positions past its end
-    for (int t0 = max(at_.first, at_.length); t0 < at_.end; t0 += kSelRound)
-        part.clear(at<T, PLANES>(a.y, b, t0, at_.c0), a.y.row, at_.channels, at_.end - t0);
 }
 
 template <typename T, int LANES, bool PLANES, bool WIDE> cudaError_t launch_selective_forward_as(const SelectiveArgs &a, cudaStream_t st) {
-    const unsigned threads = kSelTile * LANES, grid = (unsigned)a.ctas() * a.segments;
+    const unsigned threads = Roles<LANES>::THREADS, grid = (unsigned)a.ctas() * a.segments;
+    const size_t shared = 2 * sizeof(ForwardShared<LANES, PLANES>);
+    const auto local = selective_forward_kernel<T, LANES, PLANES, WIDE, true>, whole = selective_forward_kernel<T, LANES, PLANES, WIDE, false>;
+    cudaError_t e = cudaSuccess;
     if (a.segments > 1) {
-        const cudaError_t e = launch_kernel(selective_forward_kernel<T, LANES, PLANES, WIDE, true>, grid, threads, 0, st, 1, a);
-        if (e != cudaSuccess) return e;
+        if ((e = allow_shared(local, shared)) != cudaSuccess) return e;
+        if ((e = launch_kernel(local, grid, threads, shared, st, 1, a)) != cudaSuccess) return e;
     }
-    return launch_kernel(selective_forward_kernel<T, LANES, PLANES, WIDE, false>, grid, threads, 0, st, 1, a);
+    if ((e = allow_shared(whole, shared)) != cudaSuccess) return e;
+    return launch_kernel(whole, grid, threads, shared, st, 1, a);
 }
 
 template <typename T> cudaError_t launch_selective_forward(const SelectiveArgs &a, cudaStream_t st) {
