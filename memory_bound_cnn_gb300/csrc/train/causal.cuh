@@ -11,17 +11,22 @@ namespace wtconv {
 
 constexpr float kCausalLog2E = 1.4426950408889634f;
 
-__device__ __forceinline__ float causal_sigmoid(float v) {
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-kCausalLog2E * v));
-    return reciprocal(1.f + e);
+__device__ __forceinline__ Pair causal_sigmoid(Pair v) {
+    const Pair w = mul(v, Pair(-kCausalLog2E));
+    float a, b;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(w.lo()));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(w.hi()));
+    const Pair s = add(Pair(a, b), Pair(1.f));
+    return {reciprocal(s.lo()), reciprocal(s.hi())};
 }
-__device__ __forceinline__ float causal_f(float pre, int silu) { return silu ? pre * causal_sigmoid(pre) : pre; }
-__device__ __forceinline__ float causal_slope(float pre, int silu) {
-    if (!silu) return 1.f;
-    const float p = causal_sigmoid(pre);
-    return p * fmaf(pre, 1.f - p, 1.f);
+template <bool SILU> __device__ __forceinline__ Pair causal_f(Pair pre) { return SILU ? mul(pre, causal_sigmoid(pre)) : pre; }
+template <bool SILU> __device__ __forceinline__ Pair causal_slope(Pair pre) {
+    if (!SILU) return Pair(1.f);
+    const Pair p = causal_sigmoid(pre);
+    return mul(p, fma(pre, sub(Pair(1.f), p), Pair(1.f)));
 }
+__device__ __forceinline__ float causal_f(float pre, int silu) { return silu ? causal_f<true>(Pair(pre)).lo() : pre; }
+__device__ __forceinline__ float causal_slope(float pre, int silu) { return silu ? causal_slope<true>(Pair(pre)).lo() : 1.f; }
 __device__ __forceinline__ int length_of(const CausalArgs &a, int b) {
     return a.lengths == nullptr ? a.s.T : min(max(a.lengths[b], 0), a.s.T);
 }
@@ -74,169 +79,195 @@ template <typename T, int K> __device__ __forceinline__ void write_d_state(const
 
 // --------------------------------------------------------------------------------------- tokens
 
-// A warp's lanes take neighbouring vectors of channels, a thread goes along its strip of positions with the last K
-// inputs in registers.
-template <typename T, int K, int V> __global__ void __launch_bounds__(256) causal_tokens_forward_kernel(const __grid_constant__ CausalArgs a) {
-    constexpr int AHEAD = 4;  // positions loaded before the first is used
-    begin_kernel();
-    const int columns = (a.s.C + 32 * V - 1) / (32 * V), groups = (a.strips + 7) / 8;
-    const unsigned main = (unsigned)a.s.B * groups * columns;
-    if (blockIdx.x >= main) return write_state_last<T, K>(a, (long long)(blockIdx.x - main) * 256 + threadIdx.x);
-    const int column = blockIdx.x % columns, rest = blockIdx.x / columns, b = rest / groups;
-    const int strip = rest % groups * 8 + threadIdx.x / 32, c = (column * 32 + threadIdx.x % 32) * V;
-    if (strip >= a.strips || c >= a.s.C) return;
-    const int first = strip * a.strip, end = min(first + a.strip, a.s.T), length = length_of(a, b), stop = min(end, length);
-    const T *x = static_cast<const T *>(a.x.p) + b * a.x.batch + c;
-    T *y = static_cast<T *>(a.y.p) + b * a.y.batch + c;
-    if (first < stop) {
-        float w[K][V], bias[V], in[K - 1 + AHEAD][V];
+// A pair of neighbouring channels: at once where WIDE, else one at a time; `both`: the second is one of the tensor's.
+template <typename T, bool WIDE> __device__ __forceinline__ typename Raw<T>::Two load_two(const T *p, bool both) {
+    if (WIDE) return *reinterpret_cast<const typename Raw<T>::Two *>(p);
+    return two_of<T>(load_one(p), both ? load_one(p + 1) : 0);
+}
+template <typename T, bool WIDE> __device__ __forceinline__ void store_two(T *p, bool both, Pair v) {
+    if (WIDE) {
+        Vec<T, 2> q;
+        q.v[0] = from_f32<T>(v.lo()), q.v[1] = from_f32<T>(v.hi());
+        *reinterpret_cast<Vec<T, 2> *>(p) = q;
+        return;
+    }
+    p[0] = from_f32<T>(v.lo());
+    if (both) p[1] = from_f32<T>(v.hi());
+}
+
+// A warp's lanes take neighbouring pairs of channels, a thread goes along its strip of positions with the last K inputs
+// in registers.  What bounds it is how much is on its way from memory: loads run a batch of eight positions ahead, and
+// two channels a thread leave registers for many warps (8 x 4096 x 2048 in bf16, K = 4: with eight channels a thread and
+// four positions ahead the forward took 86 us, with four channels the backward 247 us).
+constexpr int kCausalAhead = 8;
+
+// What a thread of the tokens' kernels works on.
+template <typename T, int K> struct Strip {
+    int b, c, first, end, length, stop;
+    bool both;  // whether the pair's second channel is one
+    Pair w[K], bias;
+    // false: nothing
+    __device__ __forceinline__ bool find(const CausalArgs &a) {
+        const int columns = (a.s.C + 63) / 64, groups = (a.strips + 7) / 8;
+        const int strip = blockIdx.x / columns % groups * 8 + threadIdx.x / 32;
+        b = blockIdx.x / columns / groups, c = (blockIdx.x % columns * 32 + threadIdx.x % 32) * 2;
+        both = c + 1 < a.s.C;
+        if (strip >= a.strips || c >= a.s.C) return false;
+        first = strip * a.strip, end = min(first + a.strip, a.s.T), length = length_of(a, b), stop = min(end, length);
+        const int c1 = both ? c + 1 : c;
+        bias = a.bias == nullptr ? Pair(0.f) : Pair(a.bias[c], a.bias[c1]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            bias[i] = a.bias == nullptr ? 0.f : a.bias[c + i];
+        for (int k = 0; k < K; ++k) w[k] = Pair(a.w[(long long)c * K + k], a.w[(long long)c1 * K + k]);
+        return true;
+    }
+    __device__ __forceinline__ Pair sum(const Pair *in) const {
+        Pair v = bias;
 #pragma unroll
-            for (int k = 0; k < K; ++k) w[k][i] = a.w[(long long)(c + i) * K + k];
-        }
+        for (int k = 0; k < K; ++k) v = fma(w[k], in[k], v);
+        return v;
+    }
+    // the K-1 inputs before the strip
+    __device__ __forceinline__ void before(const CausalArgs &a, Pair (&in)[K - 1]) const {
 #pragma unroll
         for (int k = 0; k < K - 1; ++k) {
             const int t = first - K + 1 + k;
-            if (t >= 0) load_vec<T, V>(x + t * a.x.row, in[k]);
-            else
-#pragma unroll
-                for (int i = 0; i < V; ++i) in[k][i] = input_at<T, K>(a, b, c + i, t);
-        }
-        for (int t0 = first; t0 < stop; t0 += AHEAD) {
-#pragma unroll
-            for (int j = 0; j < AHEAD; ++j)
-                if (t0 + j < stop) load_vec<T, V>(x + (t0 + j) * a.x.row, in[K - 1 + j]);
-#pragma unroll
-            for (int j = 0; j < AHEAD; ++j) {
-                if (t0 + j >= stop) break;
-                float v[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    v[i] = bias[i];
-#pragma unroll
-                    for (int k = 0; k < K; ++k) v[i] = fmaf(w[k][i], in[j + k][i], v[i]);
-                    v[i] = causal_f(v[i], a.s.silu);
-                }
-                store_vec<T, V>(y + (t0 + j) * a.y.row, v);
-            }
-#pragma unroll
-            for (int k = 0; k < K - 1; ++k)
-#pragma unroll
-                for (int i = 0; i < V; ++i) in[k][i] = in[AHEAD + k][i];
+            in[k] = Pair(input_at<T, K>(a, b, c, t), both ? input_at<T, K>(a, b, c + 1, t) : 0.f);
         }
     }
-    const float zero[V] = {};
-    for (int t = max(first, length); t < end; ++t) store_vec<T, V>(y + t * a.y.row, zero);
+};
+
+template <typename T, int K, bool WIDE, bool SILU> __global__ void __launch_bounds__(256) causal_tokens_forward_kernel(const __grid_constant__ CausalArgs a) {
+    constexpr int AHEAD = kCausalAhead;
+    using Two = typename Raw<T>::Two;
+    begin_kernel();
+    const unsigned main = (unsigned)a.s.B * ((a.strips + 7) / 8) * ((a.s.C + 63) / 64);
+    if (blockIdx.x >= main) return write_state_last<T, K>(a, (long long)(blockIdx.x - main) * 256 + threadIdx.x);
+    Strip<T, K> s;
+    if (!s.find(a)) return;
+    const T *const x = static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c;
+    T *const y = static_cast<T *>(a.y.p) + s.b * a.y.batch + s.c;
+    if (s.first < s.stop) {
+        const auto fetch = [&](int t0, Two(&v)[AHEAD]) {
+            const T *p = x + t0 * a.x.row;
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j)
+                if (t0 + j < s.stop) v[j] = load_two<T, WIDE>(p + j * a.x.row, s.both);
+        };
+        Two even[AHEAD] = {}, odd[AHEAD] = {};
+        fetch(s.first, even);
+        Pair window[K - 1];
+        s.before(a, window);
+        const auto batch = [&](int t0, Two(&now)[AHEAD], Two(&next)[AHEAD]) {
+            fetch(t0 + AHEAD, next);
+            arrived(now);
+            Pair in[K - 1 + AHEAD];
+#pragma unroll
+            for (int k = 0; k < K - 1; ++k) in[k] = window[k];
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) in[K - 1 + j] = pair_of<T>(now[j]);
+            T *const to = y + t0 * a.y.row;
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j)
+                if (t0 + j < s.stop) store_two<T, WIDE>(to + j * a.y.row, s.both, causal_f<SILU>(s.sum(in + j)));
+#pragma unroll
+            for (int k = 0; k < K - 1; ++k) window[k] = in[AHEAD + k];
+        };
+        for (int t0 = s.first; t0 < s.stop; t0 += 2 * AHEAD) {
+            batch(t0, even, odd);
+            if (t0 + AHEAD < s.stop) batch(t0 + AHEAD, odd, even);
+        }
+    }
+    for (int t = max(s.first, s.length); t < s.end; ++t) store_two<T, WIDE>(y + t * a.y.row, s.both, Pair(0.f));
 }
 
 // The strip's K-1 following positions are computed too, for the gradients of its own inputs; dw and d_bias count
 // the strip's own positions.
-template <typename T, int K, int V> __global__ void __launch_bounds__(256) causal_tokens_backward_kernel(const __grid_constant__ CausalArgs a) {
-    __shared__ float meet[8][32 * V];
-    constexpr int AHEAD = 4;
+template <typename T, int K, bool WIDE, bool SILU> __global__ void __launch_bounds__(256) causal_tokens_backward_kernel(const __grid_constant__ CausalArgs a) {
+    constexpr int AHEAD = kCausalAhead;
+    using Two = typename Raw<T>::Two;
+    __shared__ float meet[8][K + 1][64];
     begin_kernel();
-    const int columns = (a.s.C + 32 * V - 1) / (32 * V), groups = (a.strips + 7) / 8;
-    const unsigned main = (unsigned)a.s.B * groups * columns;
+    const int columns = (a.s.C + 63) / 64;
+    const unsigned main = (unsigned)a.s.B * ((a.strips + 7) / 8) * columns;
     if (blockIdx.x >= main) return write_d_state<T, K>(a, (long long)(blockIdx.x - main) * 256 + threadIdx.x);
-    const int column = blockIdx.x % columns, part = blockIdx.x / columns, b = part / groups, warp = threadIdx.x / 32;
-    const int strip = part % groups * 8 + warp, c = (column * 32 + threadIdx.x % 32) * V;
-    float dw[K][V] = {}, db[V] = {};
-    if (strip < a.strips && c < a.s.C) {
-        const int first = strip * a.strip, end = min(first + a.strip, a.s.T), length = length_of(a, b);
-        const int stop = min(end, length), beyond = min(end + K - 1, length);  // last position that reaches the strip
-        const T *x = static_cast<const T *>(a.x.p) + b * a.x.batch + c, *dy = static_cast<const T *>(a.dy.p) + b * a.dy.batch + c;
-        T *dx = static_cast<T *>(a.dx.p) + b * a.dx.batch + c;
-        const long long row = (long long)b * a.s.C + c;
-        if (first < stop) {
-            float w[K][V], bias[V], in[K - 1 + AHEAD][V], slope[K - 1 + AHEAD][V];
+    Pair dw[K], db(0.f);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                bias[i] = a.bias == nullptr ? 0.f : a.bias[c + i];
+    for (int k = 0; k < K; ++k) dw[k] = Pair(0.f);
+    Strip<T, K> s;
+    if (s.find(a)) {
+        const int beyond = min(s.end + K - 1, s.length);  // the last position that reaches the strip
+        const T *const x = static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c, *const dy = static_cast<const T *>(a.dy.p) + s.b * a.dy.batch + s.c;
+        T *const dx = static_cast<T *>(a.dx.p) + s.b * a.dx.batch + s.c;
+        if (s.first < s.stop) {
+            struct Fetched {
+                Two x[AHEAD], dy[AHEAD];
+            } even = {}, odd = {};
+            const auto fetch = [&](int t0, Fetched &f) {
+                const T *const p = x + t0 * a.x.row, *const q = dy + t0 * a.dy.row;
 #pragma unroll
-                for (int k = 0; k < K; ++k) w[k][i] = a.w[(long long)(c + i) * K + k];
-            }
+                for (int j = 0; j < AHEAD; ++j)
+                    if (t0 + j < beyond) f.x[j] = load_two<T, WIDE>(p + j * a.x.row, s.both), f.dy[j] = load_two<T, WIDE>(q + j * a.dy.row, s.both);
+            };
+            fetch(s.first, even);
+            Pair window[K - 1], slopes[K - 1];
+            s.before(a, window);
 #pragma unroll
-            for (int k = 0; k < K - 1; ++k) {
-                const int t = first - K + 1 + k;
-                if (t >= 0) load_vec<T, V>(x + t * a.x.row, in[k]);
-                else
+            for (int k = 0; k < K - 1; ++k) slopes[k] = Pair(0.f);
+            const auto batch = [&](int t0, Fetched &now, Fetched &next) {
+                fetch(t0 + AHEAD, next);
+                arrived(now.x), arrived(now.dy);
+                Pair in[K - 1 + AHEAD], slope[K - 1 + AHEAD];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) in[k][i] = input_at<T, K>(a, b, c + i, t);
-#pragma unroll
-                for (int i = 0; i < V; ++i) slope[k][i] = 0.f;
-            }
-            for (int t0 = first; t0 < stop + K - 1; t0 += AHEAD) {
-                float g[AHEAD][V];
-#pragma unroll
-                for (int j = 0; j < AHEAD; ++j) {
-                    if (t0 + j < beyond) {
-                        load_vec<T, V>(x + (t0 + j) * a.x.row, in[K - 1 + j]);
-                        load_vec<T, V>(dy + (t0 + j) * a.dy.row, g[j]);
-                    }
-                }
+                for (int k = 0; k < K - 1; ++k) in[k] = window[k], slope[k] = slopes[k];
+                T *const to = dx + (t0 - K + 1) * a.dx.row;
 #pragma unroll
                 for (int j = 0; j < AHEAD; ++j) {
                     const int t = t0 + j, own = t - K + 1;  // the input whose last reader t is
-                    if (t < beyond) {
+                    in[K - 1 + j] = pair_of<T>(now.x[j]);
+                    const Pair g = mul(pair_of<T>(now.dy[j]), causal_slope<SILU>(s.sum(in + j)));
+                    slope[K - 1 + j] = t < beyond ? g : Pair(0.f);
+                    if (t < s.stop) {
+                        db = add(db, g);
 #pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            float pre = bias[i];
-#pragma unroll
-                            for (int k = 0; k < K; ++k) pre = fmaf(w[k][i], in[j + k][i], pre);
-                            const float s = g[j][i] * causal_slope(pre, a.s.silu);
-                            slope[K - 1 + j][i] = s;
-                            if (t < stop) {
-                                db[i] += s;
-#pragma unroll
-                                for (int k = 0; k < K; ++k) dw[k][i] = fmaf(s, in[j + k][i], dw[k][i]);
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) slope[K - 1 + j][i] = 0.f;
+                        for (int k = 0; k < K; ++k) dw[k] = fma(g, in[j + k], dw[k]);
                     }
-                    if (own >= first && own < stop) {
-                        float v[V] = {};
+                    if (own >= s.first && own < s.stop) {
+                        Pair v(0.f);
 #pragma unroll
-                        for (int i = 0; i < V; ++i)
-#pragma unroll
-                            for (int k = 0; k < K; ++k) v[i] = fmaf(w[K - 1 - k][i], slope[j + k][i], v[i]);
-                        if (a.d_last != nullptr && own >= length - K + 1) {
-#pragma unroll
-                            for (int i = 0; i < V; ++i)
-                                v[i] += to_f32(static_cast<const T *>(a.d_last)[(row + i) * (K - 1) + own - (length - K + 1)]);
+                        for (int k = 0; k < K; ++k) v = fma(s.w[K - 1 - k], slope[j + k], v);
+                        if (a.d_last != nullptr && own >= s.length - K + 1) {
+                            const T *const last = static_cast<const T *>(a.d_last) + ((long long)s.b * a.s.C + s.c) * (K - 1) + own - (s.length - K + 1);
+                            v = add(v, Pair(to_f32(last[0]), s.both ? to_f32(last[K - 1]) : 0.f));
                         }
-                        store_vec<T, V>(dx + own * a.dx.row, v);
+                        store_two<T, WIDE>(to + j * a.dx.row, s.both, v);
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < K - 1; ++k)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) in[k][i] = in[AHEAD + k][i], slope[k][i] = slope[AHEAD + k][i];
+                for (int k = 0; k < K - 1; ++k) window[k] = in[AHEAD + k], slopes[k] = slope[AHEAD + k];
+            };
+            for (int t0 = s.first; t0 < s.stop + K - 1; t0 += 2 * AHEAD) {
+                batch(t0, even, odd);
+                if (t0 + AHEAD < s.stop + K - 1) batch(t0 + AHEAD, odd, even);
             }
         }
-        const float zero[V] = {};
-        for (int t = max(first, length); t < end; ++t) store_vec<T, V>(dx + t * a.dx.row, zero);
+        for (int t = max(s.first, s.length); t < s.end; ++t) store_two<T, WIDE>(dx + t * a.dx.row, s.both, Pair(0.f));
     }
     // over the CTA's strips
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = blockIdx.x / columns;
 #pragma unroll
     for (int k = 0; k <= K; ++k) {
+        const Pair v = k == K ? db : dw[k == K ? 0 : k];
+        meet[warp][k][2 * lane] = v.lo(), meet[warp][k][2 * lane + 1] = v.hi();
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 64 * (K + 1); e += 256) {
+        const int k = e / 64, to = blockIdx.x % columns * 64 + e % 64;
+        float v = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) meet[warp][i * 32 + threadIdx.x % 32] = k == K ? db[i] : dw[k == K ? 0 : k][i];
-        __syncthreads();
-        for (int e = threadIdx.x; e < 32 * V; e += 256) {
-            float v = 0.f;
-#pragma unroll
-            for (int m = 0; m < 8; ++m) v += meet[m][e];
-            const int to = (column * 32 + e % 32) * V + e / 32;
-            if (to < a.s.C) {
-                if (k == K) a.part_b[(long long)part * a.s.C + to] = v;
-                else a.part_w[((long long)part * a.s.C + to) * K + k] = v;
-            }
-        }
-        __syncthreads();
+        for (int m = 0; m < 8; ++m) v += meet[m][k][e % 64];
+        if (to >= a.s.C) continue;
+        if (k == K) a.part_b[(long long)part * a.s.C + to] = v;
+        else a.part_w[((long long)part * a.s.C + to) * K + k] = v;
     }
 }
 
@@ -368,31 +399,35 @@ template <typename T, int K, int V> __global__ void __launch_bounds__(256) causa
 
 // ---------------------------------------------------------------------------------------- launch
 
-template <bool BACKWARD, typename T, int K, int V> cudaError_t launch_causal_as(const CausalArgs &a, cudaStream_t st) {
+template <bool BACKWARD, typename T, int K, bool WIDE> cudaError_t launch_causal_as(const CausalArgs &a, cudaStream_t st) {
     const bool planes = a.s.layout == WTCONV_SCAN_PLANES, ends = BACKWARD ? a.d_state != nullptr : a.state_last != nullptr;
     const long long rows = (long long)a.s.B * a.s.C;
     long long grid = planes ? (rows * a.strips + (256 >> a.row_bits) - 1) / (256 >> a.row_bits)
-                            : (long long)a.s.B * ceil_div(a.strips, 8) * ceil_div(a.s.C, 32 * V);
+                            : (long long)a.s.B * ceil_div(a.strips, 8) * ceil_div(a.s.C, 64);
     if (ends) grid += (rows + 255) / 256;
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-    if constexpr (BACKWARD)
-        return planes ? launch_kernel(causal_planes_backward_kernel<T, K, V>, (unsigned)grid, 256, 0, st, 1, a)
-                      : launch_kernel(causal_tokens_backward_kernel<T, K, V>, (unsigned)grid, 256, 0, st, 1, a);
-    else
-        return planes ? launch_kernel(causal_planes_forward_kernel<T, K, V>, (unsigned)grid, 256, 0, st, 1, a)
-                      : launch_kernel(causal_tokens_forward_kernel<T, K, V>, (unsigned)grid, 256, 0, st, 1, a);
+    const auto launch = [&](auto kernel) { return launch_kernel(kernel, (unsigned)grid, 256, 0, st, 1, a); };
+    if constexpr (BACKWARD) {
+        constexpr int V = WIDE ? 4 : 1;
+        if (planes) return launch(causal_planes_backward_kernel<T, K, V>);
+        return a.s.silu ? launch(causal_tokens_backward_kernel<T, K, WIDE, true>) : launch(causal_tokens_backward_kernel<T, K, WIDE, false>);
+    } else {
+        constexpr int V = WIDE ? 16 / sizeof(T) : 1;
+        if (planes) return launch(causal_planes_forward_kernel<T, K, V>);
+        return a.s.silu ? launch(causal_tokens_forward_kernel<T, K, WIDE, true>) : launch(causal_tokens_forward_kernel<T, K, WIDE, false>);
+    }
 }
-template <bool BACKWARD, typename T, int V> cudaError_t launch_causal_taps(const CausalArgs &a, cudaStream_t st) {
-    return a.s.K == 2   ? launch_causal_as<BACKWARD, T, 2, V>(a, st)
-           : a.s.K == 3 ? launch_causal_as<BACKWARD, T, 3, V>(a, st)
-                        : launch_causal_as<BACKWARD, T, 4, V>(a, st);
+template <bool BACKWARD, typename T, bool WIDE> cudaError_t launch_causal_taps(const CausalArgs &a, cudaStream_t st) {
+    return a.s.K == 2   ? launch_causal_as<BACKWARD, T, 2, WIDE>(a, st)
+           : a.s.K == 3 ? launch_causal_as<BACKWARD, T, 3, WIDE>(a, st)
+                        : launch_causal_as<BACKWARD, T, 4, WIDE>(a, st);
 }
 
 template <typename T> cudaError_t launch_causal_forward(const CausalArgs &a, cudaStream_t st) {
-    return a.wide > 1 ? launch_causal_taps<false, T, 16 / sizeof(T)>(a, st) : launch_causal_taps<false, T, 1>(a, st);
+    return a.wide ? launch_causal_taps<false, T, true>(a, st) : launch_causal_taps<false, T, false>(a, st);
 }
 template <typename T> cudaError_t launch_causal_backward(const CausalArgs &a, cudaStream_t st) {
-    const cudaError_t e = a.wide > 1 ? launch_causal_taps<true, T, 4>(a, st) : launch_causal_taps<true, T, 1>(a, st);
+    const cudaError_t e = a.wide ? launch_causal_taps<true, T, true>(a, st) : launch_causal_taps<true, T, false>(a, st);
     if (e != cudaSuccess) return e;
     ColumnSums s = {};
     s.parts = a.parts;

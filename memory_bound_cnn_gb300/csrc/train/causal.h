@@ -18,8 +18,8 @@ struct CausalArgs {
     void *state_last, *d_state;
     const int *lengths;
     float *dw, *d_bias;
-    int wide;        // elements of a vector, 1 where an address or a stride does not allow more
-    // tokens: a thread takes `strip` positions of a vector of channels, a CTA 8 strips;
+    bool wide;       // whether addresses and strides allow vectors
+    // tokens: a thread takes `strip` positions of a few channels, a CTA 8 strips;
     // planes: 2^row_bits lanes take the vectors of `strip` positions of a row
     int strip, strips, row_bits;
     float *part_w, *part_b;  // [parts][C][K], [parts][C]: a part is a sequence's strips of a CTA, or a row's strip

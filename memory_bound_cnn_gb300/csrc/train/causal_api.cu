@@ -33,7 +33,7 @@ void plan(CausalArgs &a, bool backward) {
     const wtconv_causal_shape &s = a.s;
     if (s.layout == WTCONV_SCAN_TOKENS) {
         // A strip repeats K-1 positions of its neighbours; shorter ones keep the SMs busy where there is little.
-        const long long threads = (long long)s.B * s.C * s.T / (backward ? 4 : 16 / elem_bytes_of(s.dtype));
+        const long long threads = (long long)s.B * s.C * s.T / 2;
         a.strip = 64;
         while (a.strip > 8 && threads / a.strip < (long long)sm_count() * 1024) a.strip /= 2;
         a.strips = ceil_div(s.T, a.strip);
@@ -87,8 +87,9 @@ int wtconv_causal_forward(const wtconv_causal_shape *shape, const wtconv_ssm_ten
     if (!counts_ok(a) || !check_tensor(a.x, a.s, false) || !check_tensor(a.y, a.s, true) || !f32_ok(w, false) || !f32_ok(bias, true) ||
         !element_ok(state, a.s) || !f32_ok(lengths, true) || !element_ok(state_last, a.s))
         return WTCONV_ERR_INVALID_ARG;
-    const int v = 16 / elem_bytes_of(a.s.dtype);
-    a.wide = vectors(a.x, a.s, v) && vectors(a.y, a.s, v) && (a.s.layout == WTCONV_SCAN_PLANES || a.s.C % v == 0) ? v : 1;
+    const bool planes = a.s.layout == WTCONV_SCAN_PLANES;
+    const int v = planes ? 16 / elem_bytes_of(a.s.dtype) : 2;
+    a.wide = vectors(a.x, a.s, v) && vectors(a.y, a.s, v) && (planes || a.s.C % v == 0);
     if (fault_injected()) return WTCONV_ERR_INJECTED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return status_of(by_type(a.s.dtype, [&](auto t) { return launch_causal_forward<decltype(t)>(a, st); }));
@@ -111,10 +112,9 @@ int wtconv_causal_backward(const wtconv_causal_shape *shape, const wtconv_ssm_te
         return WTCONV_ERR_INVALID_ARG;
     if (workspace != nullptr && !aligned_to(workspace, 16)) return WTCONV_ERR_INVALID_ARG;
     if (workspace == nullptr || workspace_bytes < place(a, workspace)) return WTCONV_ERR_WORKSPACE;
-    a.wide = vectors(a.x, a.s, 4) && vectors(a.dy, a.s, 4) && vectors(a.dx, a.s, 4) &&
-                     (a.s.layout == WTCONV_SCAN_PLANES || a.s.C % 4 == 0)
-                 ? 4
-                 : 1;
+    const bool planes = a.s.layout == WTCONV_SCAN_PLANES;
+    const int v = planes ? 4 : 2;
+    a.wide = vectors(a.x, a.s, v) && vectors(a.dy, a.s, v) && vectors(a.dx, a.s, v) && (planes || a.s.C % v == 0);
     if (fault_injected()) return WTCONV_ERR_INJECTED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return status_of(by_type(a.s.dtype, [&](auto t) { return launch_causal_backward<decltype(t)>(a, st); }));

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace wtconv {
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
@@ -35,6 +37,39 @@ struct Pair {
         return b;
     }
 };
+// A pair of neighbours, and a single element, as they lie in memory.  What is fetched ahead stays a whole register in
+// this form until it is used: packed or converted, it would have to arrive first.
+template <typename T> struct Raw {
+    using Two = typename std::conditional<sizeof(T) == 2, uint32_t, unsigned long long>::type;
+};
+template <typename T> __device__ __forceinline__ uint32_t load_one(const T *p) {
+    if constexpr (sizeof(T) == 2) return *reinterpret_cast<const unsigned short *>(p);
+    else return *reinterpret_cast<const uint32_t *>(p);
+}
+template <typename T> __device__ __forceinline__ typename Raw<T>::Two two_of(uint32_t first, uint32_t second) {
+    if constexpr (sizeof(T) == 2) return first | second << 16;
+    else return first | (unsigned long long)second << 32;
+}
+template <typename T> __device__ __forceinline__ Pair pair_of(typename Raw<T>::Two v) {
+    if constexpr (std::is_same<T, float>::value) return Pair(v);
+    else if constexpr (std::is_same<T, __half>::value) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v));
+        return {f.x, f.y};
+    } else return {__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)};
+}
+template <typename T> __device__ __forceinline__ float f32_of(uint32_t v) {
+    if constexpr (std::is_same<T, float>::value) return __uint_as_float(v);
+    else if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half((unsigned short)v));
+    else return __uint_as_float(v << 16);
+}
+// Where a fetched value is first used: the compiler would otherwise move what is done with it up to the load.
+__device__ __forceinline__ void arrived(uint32_t &v) { asm volatile("" : "+r"(v)); }
+__device__ __forceinline__ void arrived(unsigned long long &v) { asm volatile("" : "+l"(v)); }
+template <typename V, int COUNT> __device__ __forceinline__ void arrived(V (&v)[COUNT]) {
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) arrived(v[i]);
+}
+
 __device__ __forceinline__ Pair mul(Pair a, Pair b) {
     Pair r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.q) : "l"(a.q), "l"(b.q));
