@@ -147,11 +147,17 @@ template <typename T, int K, bool WIDE, bool SILU> __global__ void __launch_boun
     const T *const x = static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c;
     T *const y = static_cast<T *>(a.y.p) + s.b * a.y.batch + s.c;
     if (s.first < s.stop) {
+        // (all of a batch's positions at once where they are the strip's: its checks are a third of the instructions)
         const auto fetch = [&](int t0, Two(&v)[AHEAD]) {
             const T *p = x + t0 * a.x.row;
+            if (t0 + AHEAD <= s.stop) {
 #pragma unroll
-            for (int j = 0; j < AHEAD; ++j)
-                if (t0 + j < s.stop) v[j] = load_two<T, WIDE>(p + j * a.x.row, s.both);
+                for (int j = 0; j < AHEAD; ++j) v[j] = load_two<T, WIDE>(p + j * a.x.row, s.both);
+            } else {
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j)
+                    if (t0 + j < s.stop) v[j] = load_two<T, WIDE>(p + j * a.x.row, s.both);
+            }
         };
         Two even[AHEAD] = {}, odd[AHEAD] = {};
         fetch(s.first, even);
@@ -166,9 +172,14 @@ template <typename T, int K, bool WIDE, bool SILU> __global__ void __launch_boun
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) in[K - 1 + j] = pair_of<T>(now[j]);
             T *const to = y + t0 * a.y.row;
+            if (t0 + AHEAD <= s.stop) {
 #pragma unroll
-            for (int j = 0; j < AHEAD; ++j)
-                if (t0 + j < s.stop) store_two<T, WIDE>(to + j * a.y.row, s.both, causal_f<SILU>(s.sum(in + j)));
+                for (int j = 0; j < AHEAD; ++j) store_two<T, WIDE>(to + j * a.y.row, s.both, causal_f<SILU>(s.sum(in + j)));
+            } else {
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j)
+                    if (t0 + j < s.stop) store_two<T, WIDE>(to + j * a.y.row, s.both, causal_f<SILU>(s.sum(in + j)));
+            }
 #pragma unroll
             for (int k = 0; k < K - 1; ++k) window[k] = in[AHEAD + k];
         };
@@ -204,6 +215,11 @@ template <typename T, int K, bool WIDE, bool SILU> __global__ void __launch_boun
             } even = {}, odd = {};
             const auto fetch = [&](int t0, Fetched &f) {
                 const T *const p = x + t0 * a.x.row, *const q = dy + t0 * a.dy.row;
+                if (t0 + AHEAD <= beyond) {
+#pragma unroll
+                    for (int j = 0; j < AHEAD; ++j) f.x[j] = load_two<T, WIDE>(p + j * a.x.row, s.both), f.dy[j] = load_two<T, WIDE>(q + j * a.dy.row, s.both);
+                    return;
+                }
 #pragma unroll
                 for (int j = 0; j < AHEAD; ++j)
                     if (t0 + j < beyond) f.x[j] = load_two<T, WIDE>(p + j * a.x.row, s.both), f.dy[j] = load_two<T, WIDE>(q + j * a.dy.row, s.both);
@@ -220,28 +236,34 @@ template <typename T, int K, bool WIDE, bool SILU> __global__ void __launch_boun
 #pragma unroll
                 for (int k = 0; k < K - 1; ++k) in[k] = window[k], slope[k] = slopes[k];
                 T *const to = dx + (t0 - K + 1) * a.dx.row;
+                const auto positions = [&](auto full) {
+                    constexpr bool FULL = decltype(full)::value;
 #pragma unroll
-                for (int j = 0; j < AHEAD; ++j) {
-                    const int t = t0 + j, own = t - K + 1;  // the input whose last reader t is
-                    in[K - 1 + j] = pair_of<T>(now.x[j]);
-                    const Pair g = mul(pair_of<T>(now.dy[j]), causal_slope<SILU>(s.sum(in + j)));
-                    slope[K - 1 + j] = t < beyond ? g : Pair(0.f);
-                    if (t < s.stop) {
-                        db = add(db, g);
+                    for (int j = 0; j < AHEAD; ++j) {
+                        const int t = t0 + j, own = t - K + 1;  // the input whose last reader t is
+                        in[K - 1 + j] = pair_of<T>(now.x[j]);
+                        const Pair g = mul(pair_of<T>(now.dy[j]), causal_slope<SILU>(s.sum(in + j)));
+                        slope[K - 1 + j] = FULL || t < beyond ? g : Pair(0.f);
+                        if (FULL || t < s.stop) {
+                            db = add(db, g);
 #pragma unroll
-                        for (int k = 0; k < K; ++k) dw[k] = fma(g, in[j + k], dw[k]);
-                    }
-                    if (own >= s.first && own < s.stop) {
+                            for (int k = 0; k < K; ++k) dw[k] = fma(g, in[j + k], dw[k]);
+                        }
+                        if (!FULL && (own < s.first || own >= s.stop)) continue;
                         Pair v(0.f);
 #pragma unroll
                         for (int k = 0; k < K; ++k) v = fma(s.w[K - 1 - k], slope[j + k], v);
-                        if (a.d_last != nullptr && own >= s.length - K + 1) {
+                        if (!FULL && a.d_last != nullptr && own >= s.length - K + 1) {
                             const T *const last = static_cast<const T *>(a.d_last) + ((long long)s.b * a.s.C + s.c) * (K - 1) + own - (s.length - K + 1);
                             v = add(v, Pair(to_f32(last[0]), s.both ? to_f32(last[K - 1]) : 0.f));
                         }
                         store_two<T, WIDE>(to + j * a.dx.row, s.both, v);
                     }
-                }
+                };
+                // whole batches of the strip's own positions whose inputs are its own too; the last state's inputs (K-1 before
+                // the end) come with the batch after them
+                if (t0 >= s.first + K - 1 && t0 + AHEAD <= s.stop) positions(std::true_type{});
+                else positions(std::false_type{});
 #pragma unroll
                 for (int k = 0; k < K - 1; ++k) window[k] = in[AHEAD + k], slopes[k] = slope[AHEAD + k];
             };

@@ -34,7 +34,7 @@ void plan(CausalArgs &a, bool backward) {
     if (s.layout == WTCONV_SCAN_TOKENS) {
         // A strip repeats K-1 positions of its neighbours; shorter ones keep the SMs busy where there is little.
         const long long threads = (long long)s.B * s.C * s.T / 2;
-        a.strip = 64;
+        a.strip = backward ? 128 : 64;
         while (a.strip > 8 && threads / a.strip < (long long)sm_count() * 1024) a.strip /= 2;
         a.strips = ceil_div(s.T, a.strip);
         a.parts = s.B * ceil_div(a.strips, 8);

@@ -22,7 +22,7 @@ static __global__ void __launch_bounds__(1024) column_sums_kernel(const __grid_c
     const int width = s.width[which], lane = threadIdx.x % 32, slice = threadIdx.x / 32, i = block * 32 + lane;
     float v = 0.f;
     if (i < width) {
-#pragma unroll 4
+#pragma unroll 8
         for (int p = slice; p < s.parts; p += 32) v += s.part[which][(long long)p * width + i];
     }
     meet[slice][lane] = v;

@@ -48,7 +48,7 @@ bool pairs(const SelectiveArgs &a) {
 // number leaves a last round of CTAs small; it costs a pass of its own (over x, dt and B in the forward, about half of
 // the work, over dy, dt, z and C in the backward, a fifth, and two fifths with few states) and the composition of the parts before a CTA's own.
 // Time is counted in rounds of 32 positions of a CTA that has an SM for itself: two that share one take 1.3
-// times as long, three 1.6, and more wait.  (8 x 4096 x 1024 tokens with 16 states, 256 CTAs: forward 236 us in one part, 308
+// times as long, three 1.6, and more wait; a part's first and last rounds add one and a half.  (8 x 4096 x 1024 tokens with 16 states, 256 CTAs: forward 236 us in one part, 308
 // in two, backward 906 and 1032; 65,536 pixels of 64 channels, 2 CTAs: 62 us in 76 parts, 83 in 305.)
 void plan(int op, SelectiveArgs &a) {
     const bool forward = op == WTCONV_SCAN_OP_FORWARD;
@@ -60,7 +60,7 @@ void plan(int op, SelectiveArgs &a) {
         const int per = ceil_div(rounds, parts), used = ceil_div(rounds, per);
         const long long on_sm = ((long long)a.ctas() * used + sms - 1) / sms;
         const double load = on_sm <= resident ? share[on_sm] : on_sm * share[resident] / resident;
-        const double time = per * load * (used > 1 ? pass : 1) + (used > 1 ? start + join * used : 0);
+        const double time = (per + 1.5) * load * (used > 1 ? pass : 1) + (used > 1 ? start + join * used : 0);
         if (parts > 1 && time >= best) continue;
         best = time, a.segment = per * kSelRound, a.segments = used;
     }
@@ -98,8 +98,10 @@ int check_workspace(size_t need, const void *workspace, size_t bytes) {
     return workspace == nullptr || bytes < need ? WTCONV_ERR_WORKSPACE : WTCONV_OK;
 }
 
-// A grid has at most 2^31 - 1 CTAs.
-bool grid_ok(const SelectiveArgs &a) { return (long long)a.s.B * a.s.G * a.tiles * 256 <= 0x7fffffffll; }
+// A grid has at most 2^31 - 1 CTAs: of up to 256 parts of sequences, or of 32 positions.
+bool grid_ok(const SelectiveArgs &a) {
+    return (long long)a.s.B * a.s.G * a.tiles * 256 <= 0x7fffffffll && (long long)a.s.B * a.s.G * ceil_div(a.s.T, kSelRound) <= 0x7fffffffll;
+}
 
 template <typename F> cudaError_t by_type(int dtype, F f) {
     return dtype == WTCONV_F32 ? f(0.f) : dtype == WTCONV_BF16 ? f(__nv_bfloat16()) : f(__half());

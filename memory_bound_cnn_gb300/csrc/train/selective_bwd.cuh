@@ -1,7 +1,6 @@
 // Backward of the selective scan.
 #pragma once
 
-#include <algorithm>
 #include <type_traits>
 
 #include "column_sums.cuh"
@@ -375,29 +374,30 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
     if (live) store_quad(a.part_a + (first_sum + c) * N, n0, N, dA);
 }
 
-// dB and dC: the sums over a group's tiles, in their order; 0 past a sequence's end.
-template <typename T, bool PLANES> __global__ void __launch_bounds__(256) selective_sums_kernel(const __grid_constant__ SelectiveArgs a) {
+// dB and dC: the sums over a group's tiles, in their order, of 32 positions; 0 past a sequence's end.
+constexpr int kSelSumsThreads = 256;
+template <typename T, int LANES, bool PLANES> __global__ void __launch_bounds__(kSelSumsThreads) selective_sums_kernel(const __grid_constant__ SelectiveArgs a) {
+    constexpr int PAD = 4 * LANES, WIDTH = 2 * PAD, TURN = 32;
+    __shared__ float sums[WIDTH][TURN + 1];
     begin_kernel();
-    const int N = a.s.N, width = 2 * a.padded;
-    const long long per = (long long)a.s.B * a.s.T * width, all = (long long)a.s.B * a.s.T * a.s.G * 2 * N;
-    for (long long e = (long long)blockIdx.x * 256 + threadIdx.x; e < all; e += (long long)gridDim.x * 256) {
-        // in the order of the outputs' memory
-        long long rest = e;
-        int n, g, t, b, which;
-        if (PLANES) {
-            t = rest % a.s.T, rest /= a.s.T, n = rest % N, rest /= N, which = rest % 2, rest /= 2;
-            g = rest % a.s.G, b = rest / a.s.G;
-        } else {
-            n = rest % N, rest /= N, which = rest % 2, rest /= 2, g = rest % a.s.G, rest /= a.s.G;
-            t = rest % a.s.T, b = rest / a.s.T;
-        }
-        const int length = a.in.lengths == nullptr ? a.s.T : a.in.lengths[b];
+    const int turns = (a.s.T + TURN - 1) / TURN, N = a.s.N;
+    const int t0 = blockIdx.x % turns * TURN, g = blockIdx.x / turns % a.s.G, b = blockIdx.x / turns / a.s.G;
+    const int length = a.in.lengths == nullptr ? a.s.T : min(max(a.in.lengths[b], 0), a.s.T);
+    const int live = max(min(TURN, length - t0), 0), count = min(TURN, a.s.T - t0);
+    const long long per = (long long)a.s.B * a.s.T * WIDTH;  // of a tile
+    const float *const from = a.part_bc + (long long)g * a.tiles * per + ((long long)b * a.s.T + t0) * WIDTH;
+    for (int e = threadIdx.x; e < TURN * WIDTH; e += kSelSumsThreads) {
         float v = 0.f;
-        if (t < length) {
-            const float *p = a.part_bc + (long long)g * a.tiles * per + ((long long)b * a.s.T + t) * width + which * a.padded + n;
-            for (int i = 0; i < a.tiles; ++i) v += p[i * per];
+        if (e / WIDTH < live) {
+#pragma unroll 8
+            for (int i = 0; i < a.tiles; ++i) v += from[i * per + e];
         }
-        *at<T, PLANES>(which ? a.g.dC : a.g.dB, b, t, g * N + n) = from_f32<T>(v);
+        sums[e % WIDTH][e / WIDTH] = v;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < TURN * WIDTH; e += kSelSumsThreads) {
+        const int t = PLANES ? e % TURN : e / WIDTH, j = PLANES ? e / TURN : e % WIDTH, n = j % PAD;
+        if (t < count && n < N) *at<T, PLANES>(j / PAD ? a.g.dC : a.g.dB, b, t0 + t, g * N + n) = from_f32<T>(sums[j][t]);
     }
 }
 
@@ -412,9 +412,8 @@ template <typename T, int LANES, bool PLANES, bool WIDE> cudaError_t launch_sele
     }
     if ((e = allow_shared(whole, shared)) != cudaSuccess) return e;
     if ((e = launch_kernel(whole, grid, threads, shared, st, 1, a)) != cudaSuccess) return e;
-    const long long outputs = (long long)a.s.B * a.s.T * a.s.G * 2 * a.s.N;
-    const unsigned blocks = (unsigned)std::min<long long>((outputs + 255) / 256, 1 << 16);
-    if ((e = launch_kernel(selective_sums_kernel<T, PLANES>, blocks, 256, 0, st, 1, a)) != cudaSuccess) return e;
+    const unsigned turns = (unsigned)a.s.B * a.s.G * ceil_div(a.s.T, 32);
+    if ((e = launch_kernel(selective_sums_kernel<T, LANES, PLANES>, turns, kSelSumsThreads, 0, st, 1, a)) != cudaSuccess) return e;
     ColumnSums s = {};
     s.parts = a.s.B * a.segments;
     const size_t half = (size_t)s.parts * a.s.C;
