@@ -48,19 +48,20 @@ bool pairs(const SelectiveArgs &a) {
 // number leaves a last round of CTAs small; it costs a pass of its own (over x, dt and B in the forward, about half of
 // the work, over dy, dt, z and C in the backward, a fifth, and two fifths with few states) and the composition of the parts before a CTA's own.
 // Time is counted in rounds of 32 positions of a CTA that has an SM for itself: two that share one take 1.3
-// times as long, three 1.6, and more wait; a part's first and last rounds add one and a half.  (8 x 4096 x 1024 tokens with 16 states, 256 CTAs: forward 236 us in one part, 308
+// times as long, three 1.6, and more wait; a part's first and last
+// rounds add some (ends).  (8 x 4096 x 1024 tokens with 16 states, 256 CTAs: forward 236 us in one part, 308
 // in two, backward 906 and 1032; 65,536 pixels of 64 channels, 2 CTAs: 62 us in 76 parts, 83 in 305.)
 void plan(int op, SelectiveArgs &a) {
     const bool forward = op == WTCONV_SCAN_OP_FORWARD;
     const int sms = sm_count(), rounds = ceil_div(a.s.T, kSelRound), most = std::max(1, std::min(rounds / 2, 256));
     const int resident = a.lanes == 2 ? (forward ? 3 : 2) : a.lanes == 4 ? 2 : 1;
-    const double share[4] = {1, 1, 1.3, 1.6}, pass = forward ? 1.5 : a.lanes == 2 ? 1.4 : 1.2, start = forward ? 4 : 1, join = forward ? 0.05 : 0.02;
+    const double share[4] = {1, 1, 1.3, 1.6}, pass = forward ? 1.5 : a.lanes == 2 ? 1.4 : 1.2, start = forward ? 4 : 1, join = forward ? 0.05 : 0.02, ends = forward ? 0.5 : 1.5;
     double best = 0;
     for (int parts = 1; parts <= most; ++parts) {
         const int per = ceil_div(rounds, parts), used = ceil_div(rounds, per);
         const long long on_sm = ((long long)a.ctas() * used + sms - 1) / sms;
         const double load = on_sm <= resident ? share[on_sm] : on_sm * share[resident] / resident;
-        const double time = (per + 1.5) * load * (used > 1 ? pass : 1) + (used > 1 ? start + join * used : 0);
+        const double time = (per + ends) * load * (used > 1 ? pass : 1) + (used > 1 ? start + join * used : 0);
         if (parts > 1 && time >= best) continue;
         best = time, a.segment = per * kSelRound, a.segments = used;
     }

@@ -1,6 +1,7 @@
 // Backward of the selective scan.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "column_sums.cuh"
@@ -34,6 +35,8 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t low, uint32_t high, 
 // bf16 costs up to 3.9e-3 (8 x 4096 x 1024 with 16 states: 906 us; 1172 in fp32, where the rest enters too).  In other types
 // it enters as a second product, which keeps 22 bits.
 // Then warps meet in shared memory, and CTAs in selective_sums_kernel.
+// With 8 and with 64 states the lanes hold half of a block's states at a time and recompute the first half twice: fewer
+// registers are worth it there (8 x 4096 x 1024 in bf16: 565 us instead of 612 with 8 states, 1143 instead of 821 with 16).
 // LOCAL: only the gradient that the segment's beginning passes on if nothing enters at its end, and the sum
 // of its steps; the CTAs of earlier segments begin with what these compose to.
 template <int LANES, bool PLANES> struct BackwardShared {
@@ -50,7 +53,7 @@ template <int LANES, bool PLANES> struct BackwardShared {
 
 template <typename T, int LANES, bool PLANES, bool WIDE, bool LOCAL>
 __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) selective_backward_kernel(const __grid_constant__ SelectiveArgs a) {
-    constexpr int BLOCK = kSelKeep;
+    constexpr int BLOCK = kSelKeep, HELD = LANES == 2 || LANES == 16 ? 8 : 16;
     using L = Layout<LANES, PLANES, BLOCK>;
     using R = Roles<LANES>;
     using Shared = BackwardShared<LANES, PLANES>;
@@ -67,7 +70,7 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
     const auto start = [&](int i) { return at_.first + (count_blocks - 1 - i) * BLOCK; };
 
     if (!R::scans()) {
-        if (!LOCAL) R::give();
+        if (!LOCAL) R::template give<T>();
         using Part = Share<PLANES, kSelTile, BLOCK, R::HELPERS, WIDE>;
         using Maps = Share<PLANES, L::PAD, BLOCK, R::HELPERS, WIDE>;
         using Two = typename Raw<T>::Two;
@@ -85,16 +88,21 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
             Two d[COUNT], x[COUNT], z[COUNT], dy[COUNT], b[Maps::COUNT], c[Maps::COUNT];
         } even, odd;
         Two x[COUNT] = {}, x_old[COUNT] = {};  // of the scanned block, the one finished
+        using In = Cursor<const T, PLANES>;
+        using Out = Cursor<T, PLANES>;
+        const int last = start(0);  // (of no block: nothing is read or written there)
+        In d_at(mine, a.in.dt, b, last, at_.c0), x_at(mine, a.in.x, b, last, at_.c0), z_at(mine, a.in.z, b, last, at_.c0);
+        In dy_at(mine, a.dy, b, last, at_.c0), b_at(maps, a.in.Bm, b, last, at_.group * N), c_at(maps, a.in.Cm, b, last, at_.group * N);
         const auto fetch = [&](int i, Fetched &f) {
             if (i >= count_blocks) return;
-            const int t0 = start(i), count = stop - t0;
-            mine.load(at<const T, PLANES>(a.in.dt, b, t0, at_.c0), a.in.dt.row, at_.channels, count, f.d);
-            mine.load(at<const T, PLANES>(a.dy, b, t0, at_.c0), a.dy.row, at_.channels, count, f.dy);
-            if (gated) mine.load(at<const T, PLANES>(a.in.z, b, t0, at_.c0), a.in.z.row, at_.channels, count, f.z);
-            maps.load(at<const T, PLANES>(a.in.Cm, b, t0, at_.group * N), a.in.Cm.row, N, count, f.c);
+            const int count = stop - start(i);
+            mine.load(d_at.p, d_at.row, at_.channels, count, f.d), d_at.step(-BLOCK);
+            mine.load(dy_at.p, dy_at.row, at_.channels, count, f.dy), dy_at.step(-BLOCK);
+            if (gated) mine.load(z_at.p, z_at.row, at_.channels, count, f.z), z_at.step(-BLOCK);
+            maps.load(c_at.p, c_at.row, N, count, f.c), c_at.step(-BLOCK);
             if (LOCAL) return;
-            mine.load(at<const T, PLANES>(a.in.x, b, t0, at_.c0), a.in.x.row, at_.channels, count, f.x);
-            maps.load(at<const T, PLANES>(a.in.Bm, b, t0, at_.group * N), a.in.Bm.row, N, count, f.b);
+            mine.load(x_at.p, x_at.row, at_.channels, count, f.x), x_at.step(-BLOCK);
+            maps.load(b_at.p, b_at.row, N, count, f.b), b_at.step(-BLOCK);
         };
         const auto prepare = [&](int i, Fetched &f) {
             if (i >= count_blocks) return;
@@ -126,9 +134,11 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
             if (!LOCAL) L::template put_map<T>(maps, f.b, s.maps[0]);
             L::template put_map<T>(maps, f.c, s.maps[1]);
         };
+        Out dx_at(mine, a.g.dx, b, last, at_.c0), dd_at(mine, a.g.d_dt, b, last, at_.c0), dz_at(mine, a.g.dz, b, last, at_.c0);
+        float *part_at = a.part_bc + (((long long)at_.tile * a.s.B + b) * a.s.T + last) * 2 * L::PAD;
         const auto finish = [&](int i) {
             Shared &s = blocks[i & 1];
-            const int t0 = start(i), count = min(BLOCK, stop - t0);
+            const int count = min(BLOCK, stop - start(i));
             Pair dx[COUNT], dd[COUNT], dz[COUNT];
             const auto stashed = [&](int which, int j) { return Pair(*reinterpret_cast<const unsigned long long *>(&s.stash[which][j][me])); };
 #pragma unroll
@@ -150,18 +160,25 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
                 }
                 dD[PLANES ? j : 0] = add(dD[PLANES ? j : 0], rx), d_bias[PLANES ? j : 0] = add(d_bias[PLANES ? j : 0], di);
             }
-            mine.store(at<T, PLANES>(a.g.dx, b, t0, at_.c0), a.g.dx.row, at_.channels, count, [&](int j) { return dx[j]; });
-            mine.store(at<T, PLANES>(a.g.d_dt, b, t0, at_.c0), a.g.d_dt.row, at_.channels, count, [&](int j) { return dd[j]; });
-            if (gated) mine.store(at<T, PLANES>(a.g.dz, b, t0, at_.c0), a.g.dz.row, at_.channels, count, [&](int j) { return dz[j]; });
-            float *const to = a.part_bc + (((long long)at_.tile * a.s.B + b) * a.s.T + t0) * 2 * L::PAD;
-            for (int e = 2 * me; e < count * 2 * L::PAD; e += 2 * R::HELPERS) {
+            mine.store(dx_at.p, dx_at.row, at_.channels, count, [&](int j) { return dx[j]; }), dx_at.step(-BLOCK);
+            mine.store(dd_at.p, dd_at.row, at_.channels, count, [&](int j) { return dd[j]; }), dd_at.step(-BLOCK);
+            if (gated) mine.store(dz_at.p, dz_at.row, at_.channels, count, [&](int j) { return dz[j]; }), dz_at.step(-BLOCK);
+            const auto part_sum = [&](int e) {
                 const float *const from = &s.part[0][0][0][0] + e;
                 Pair v(*reinterpret_cast<const unsigned long long *>(from));
 #pragma unroll
                 for (int w = 1; w < Shared::ROWS; ++w)
                     v = add(v, Pair(*reinterpret_cast<const unsigned long long *>(from + w * BLOCK * 2 * L::PAD)));
-                *reinterpret_cast<unsigned long long *>(to + e) = v.q;
+                *reinterpret_cast<unsigned long long *>(part_at + e) = v.q;
+            };
+            if (count == BLOCK) {
+#pragma unroll
+                for (int e = 0; e < BLOCK * 2 * L::PAD; e += 2 * R::HELPERS)
+                    if (BLOCK * 2 * L::PAD % (2 * R::HELPERS) == 0 || e + 2 * me < BLOCK * 2 * L::PAD) part_sum(e + 2 * me);
+            } else {
+                for (int e = 2 * me; e < count * 2 * L::PAD; e += 2 * R::HELPERS) part_sum(e);
             }
+            part_at -= BLOCK * 2 * L::PAD;
         };
         const auto during = [&](int i, Fetched &next, Fetched &after) {  // block i is scanned
             fetch(i + 2, after);
@@ -206,14 +223,14 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
         }
         // positions past the sequence's end
         for (int t0 = max(at_.first, at_.length); t0 < at_.end; t0 += BLOCK) {
-            mine.clear(at<T, PLANES>(a.g.dx, b, t0, at_.c0), a.g.dx.row, at_.channels, at_.end - t0);
-            mine.clear(at<T, PLANES>(a.g.d_dt, b, t0, at_.c0), a.g.d_dt.row, at_.channels, at_.end - t0);
-            if (gated) mine.clear(at<T, PLANES>(a.g.dz, b, t0, at_.c0), a.g.dz.row, at_.channels, at_.end - t0);
+            mine.clear(mine.mine(at<T, PLANES>(a.g.dx, b, t0, at_.c0), a.g.dx.row), a.g.dx.row, at_.channels, at_.end - t0);
+            mine.clear(mine.mine(at<T, PLANES>(a.g.d_dt, b, t0, at_.c0), a.g.d_dt.row), a.g.d_dt.row, at_.channels, at_.end - t0);
+            if (gated) mine.clear(mine.mine(at<T, PLANES>(a.g.dz, b, t0, at_.c0), a.g.dz.row), a.g.dz.row, at_.channels, at_.end - t0);
         }
         return;
     }
 
-    if (!LOCAL) R::take();
+    if (!LOCAL) R::template take<T>();
     const Place2 lane;
     const int c = lane.c, quad = lane.quad, n0 = lane.n0;
     const bool live = c < at_.channels;
@@ -272,19 +289,15 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
         kept_next = kept(i + 1);
         const auto scan = [&](auto full) {
             constexpr bool FULL = decltype(full)::value;
-            constexpr int TOGETHER = L::TOGETHER, PAIRS = BLOCK / 2;
+            constexpr int TOGETHER = L::TOGETHER;
             constexpr bool CUT = std::is_same<T, __nv_bfloat16>::value;  // products are cut to 11 bits
-            Quad h[BLOCK];
-#pragma unroll
-            for (int t = 0; t < BLOCK; ++t) {
-                if (!FULL && t >= count) break;
-                const float2 q = s.coef[L::coef(t, c)];
-                const Quad u = quad_of(map(0, t)), last = t == 0 ? before : h[t == 0 ? 0 : t - 1];
-                const Pair d(q.x), dx(q.y);
-                h[t].a = fma(exp2_fast(mul(d, decay.a)), last.a, mul(dx, u.a));
-                h[t].b = fma(exp2_fast(mul(d, decay.b)), last.b, mul(dx, u.b));
-            }
             Quad dA_block = {Pair(0.f), Pair(0.f)};
+            const auto advance = [&](const Quad &h, int t) {
+                const float2 q = s.coef[L::coef(t, c)];
+                const Quad u = quad_of(map(0, t));
+                const Pair d(q.x), dx(q.y);
+                return Quad{fma(exp2_fast(mul(d, decay.a)), h.a, mul(dx, u.a)), fma(exp2_fast(mul(d, decay.b)), h.b, mul(dx, u.b))};
+            };
             // (what a position needs is loaded before the one after it is stored, as in the forward)
             struct Operands {
                 float2 q;
@@ -294,32 +307,14 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
             const auto operands = [&](int t) { return Operands{s.coef[L::coef(t, c)], map(0, t), map(1, t), s.r[L::value(t, c)]}; };
             Operands next = operands(FULL ? BLOCK - 1 : count - 1);
             float s1[TOGETHER] = {}, s2[TOGETHER] = {}, s3[TOGETHER] = {};
-            // Position t; v: its products of the lane's states, B's and C's.
-            const auto pass = [&](int t, float (&v)[8]) {
-                const Operands now = next;
-                if (t > 0) next = operands(t - 1);
-                const Quad u = quad_of(now.u), o = quad_of(now.o), last = t == 0 ? before : h[t == 0 ? 0 : t - 1];
-                const Pair d(now.q.x), dx(now.q.y), r(now.r);
-                const Quad g = {fma(o.a, r, carry.a), fma(o.b, r, carry.b)};
-                carry.a = mul(exp2_again(mul(d, decay.a)), g.a), carry.b = mul(exp2_again(mul(d, decay.b)), g.b);
-                const Quad kk = {mul(carry.a, last.a), mul(carry.b, last.b)};
-                dA_block.a = fma(kk.a, d, dA_block.a), dA_block.b = fma(kk.b, d, dA_block.b);
-                const Pair p1 = fma(g.a, u.a, mul(g.b, u.b)), p2 = fma(kk.a, decay.a, mul(kk.b, decay.b));
-                const Pair p3 = fma(o.a, h[t].a, mul(o.b, h[t].b));
-                s1[t % TOGETHER] = p1.lo() + p1.hi(), s2[t % TOGETHER] = p2.lo() + p2.hi(), s3[t % TOGETHER] = p3.lo() + p3.hi();
-                const Pair to_b = CUT ? Pair(now.q.y * kSelCut) : dx, to_c = CUT ? Pair(now.r * kSelCut) : r;
-                const Pair b0 = mul(g.a, to_b), b1 = mul(g.b, to_b), c0 = mul(h[t].a, to_c), c1 = mul(h[t].b, to_c);
-                v[0] = b0.lo(), v[1] = b0.hi(), v[2] = b1.lo(), v[3] = b1.hi();
-                v[4] = c0.lo(), v[5] = c0.hi(), v[6] = c1.lo(), v[7] = c1.hi();
-            };
             float sums[4];  // of the last two positions
-            const auto put_part = [&](int p) {
+            const auto put_part = [&](int t) {
                 // row lane / 4: value (state, B or C); columns: the group of four channels, then the quad of states
                 const int r = lane.lane / 4, j = lane.lane % 4, which = r / 4, state = r % 4;
                 constexpr int FOURS = Place2::CHANNELS / 4;  // columns of a quad: 4, 2 or 1
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    float *const to = s.part[lane.row][2 * p + k][which] + lane.warp % Place2::HALVES * 4 * Place2::WITHIN + state;
+                    float *const to = s.part[lane.row][t + k][which] + lane.warp % Place2::HALVES * 4 * Place2::WITHIN + state;
                     const float v0 = sums[2 * k], v1 = sums[2 * k + 1];
                     if constexpr (FOURS == 1) {
                         to[8 * j] = v0, to[8 * j + 4] = v1;
@@ -331,27 +326,62 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
                     }
                 }
             };
+            bool first = true;
+            // parts of the block, from the last: a part's states are held in registers
+#pragma unroll 1
+            for (int from = BLOCK - HELD; from >= 0; from -= HELD) {
+                if (!FULL && from >= count) continue;
+                Quad before_part = before;
+                for (int t = 0; t < from; ++t) before_part = advance(before_part, t);
+                Quad h[HELD];
 #pragma unroll
-            for (int p = PAIRS - 1; p >= 0; --p) {
-                if (!FULL && 2 * p >= count) continue;
-                float v0[8], v1[8] = {};
+                for (int t = 0; t < HELD; ++t) {
+                    if (!FULL && from + t >= count) break;
+                    h[t] = advance(t == 0 ? before_part : h[t == 0 ? 0 : t - 1], from + t);
+                }
+                // Position from + t; v: its products of the lane's states, B's and C's.
+                const auto pass = [&](int t, float (&v)[8]) {
+                    const Operands now = next;
+                    if (HELD < BLOCK || t > 0) next = operands(max(from + t - 1, 0));
+                    const Quad u = quad_of(now.u), o = quad_of(now.o), last = t == 0 ? before_part : h[t == 0 ? 0 : t - 1];
+                    const Pair d(now.q.x), dx(now.q.y), r(now.r);
+                    const Quad g = {fma(o.a, r, carry.a), fma(o.b, r, carry.b)};
+                    carry.a = mul(exp2_again(mul(d, decay.a)), g.a), carry.b = mul(exp2_again(mul(d, decay.b)), g.b);
+                    const Quad kk = {mul(carry.a, last.a), mul(carry.b, last.b)};
+                    dA_block.a = fma(kk.a, d, dA_block.a), dA_block.b = fma(kk.b, d, dA_block.b);
+                    const Pair p1 = fma(g.a, u.a, mul(g.b, u.b)), p2 = fma(kk.a, decay.a, mul(kk.b, decay.b));
+                    const Pair p3 = fma(o.a, h[t].a, mul(o.b, h[t].b));
+                    s1[t % TOGETHER] = p1.lo() + p1.hi(), s2[t % TOGETHER] = p2.lo() + p2.hi(), s3[t % TOGETHER] = p3.lo() + p3.hi();
+                    const Pair to_b = CUT ? Pair(now.q.y * kSelCut) : dx, to_c = CUT ? Pair(now.r * kSelCut) : r;
+                    const Pair b0 = mul(g.a, to_b), b1 = mul(g.b, to_b), c0 = mul(h[t].a, to_c), c1 = mul(h[t].b, to_c);
+                    v[0] = b0.lo(), v[1] = b0.hi(), v[2] = b1.lo(), v[3] = b1.hi();
+                    v[4] = c0.lo(), v[5] = c0.hi(), v[6] = c1.lo(), v[7] = c1.hi();
+                };
                 const auto put_sums = [&](int t) {  // once its TOGETHER positions are through
                     if (t % TOGETHER != 0) return;
-                    L::put_sums(s.sums[0], t, c, quad, s1), L::put_sums(s.sums[1], t, c, quad, s2), L::put_sums(s.sums[2], t, c, quad, s3);
+                    const int at_t = from + t;
+                    L::put_sums(s.sums[0], at_t, c, quad, s1), L::put_sums(s.sums[1], at_t, c, quad, s2), L::put_sums(s.sums[2], at_t, c, quad, s3);
                 };
-                if (FULL || 2 * p + 1 < count) pass(2 * p + 1, v1), put_sums(2 * p + 1);
-                else if (TOGETHER > 1) s1[(2 * p + 1) % TOGETHER] = s2[(2 * p + 1) % TOGETHER] = s3[(2 * p + 1) % TOGETHER] = 0.f;
-                pass(2 * p, v0), put_sums(2 * p);
-                if (FULL ? p < PAIRS - 1 : 2 * p + 2 < count) put_part(p + 1);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) sums[k] = 0.f;
+                for (int t = HELD - 2; t >= 0; t -= 2) {
+                    if (!FULL && from + t >= count) continue;
+                    float v0[8], v1[8] = {};
+                    if (FULL || from + t + 1 < count) pass(t + 1, v1), put_sums(t + 1);
+                    else if (TOGETHER > 1) s1[(t + 1) % TOGETHER] = s2[(t + 1) % TOGETHER] = s3[(t + 1) % TOGETHER] = 0.f;
+                    pass(t, v0), put_sums(t);
+                    // (the sums of the two positions after these: the products have had the time of two more)
+                    if (HELD == BLOCK && FULL ? t < HELD - 2 : !first) put_part(from + t + 2);
+                    first = false;
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const uint32_t h0 = __float_as_uint(v0[r]), h1 = __float_as_uint(v1[r]);
-                    mma(sums, one[r], one[r], h0, h1);
-                    if (!CUT) {  // what the product with the upper 11 bits left
-                        const float l0 = v0[r] - __uint_as_float(h0 & 0xffffe000u), l1 = v1[r] - __uint_as_float(h1 & 0xffffe000u);
-                        mma(sums, one[r], one[r], __float_as_uint(l0), __float_as_uint(l1));
+                    for (int k = 0; k < 4; ++k) sums[k] = 0.f;
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const uint32_t h0 = __float_as_uint(v0[r]), h1 = __float_as_uint(v1[r]);
+                        mma(sums, one[r], one[r], h0, h1);
+                        if (!CUT) {  // what the product with the upper 11 bits left
+                            const float l0 = v0[r] - __uint_as_float(h0 & 0xffffe000u), l1 = v1[r] - __uint_as_float(h1 & 0xffffe000u);
+                            mma(sums, one[r], one[r], __float_as_uint(l0), __float_as_uint(l1));
+                        }
                     }
                 }
             }
@@ -404,6 +434,17 @@ template <typename T, int LANES, bool PLANES> __global__ void __launch_bounds__(
 template <typename T, int LANES, bool PLANES, bool WIDE> cudaError_t launch_selective_backward_as(const SelectiveArgs &a, cudaStream_t st) {
     const unsigned threads = Roles<LANES>::THREADS, grid = (unsigned)a.ctas() * a.segments;
     const size_t shared = 2 * sizeof(BackwardShared<LANES, PLANES>);
+    // (the scanners would wait for registers that the CTA does not have)
+    if (Roles<LANES>::TRADE) {
+        static std::atomic<int> registers{0};
+        if (registers == 0) {
+            cudaFuncAttributes attributes;
+            const cudaError_t e = cudaFuncGetAttributes(&attributes, selective_backward_kernel<T, LANES, PLANES, WIDE, false>);
+            if (e != cudaSuccess) return e;
+            registers = attributes.numRegs;
+        }
+        if (registers != Roles<LANES>::LAUNCHED) return cudaErrorLaunchOutOfResources;
+    }
     const auto local = selective_backward_kernel<T, LANES, PLANES, WIDE, true>, whole = selective_backward_kernel<T, LANES, PLANES, WIDE, false>;
     cudaError_t e = cudaSuccess;
     if (a.segments > 1) {

@@ -88,17 +88,18 @@ template <int LANES> struct Roles {
     static constexpr int SCANNERS = kSelTile * LANES, HELPERS = 128, THREADS = SCANNERS + HELPERS;
     static __device__ __forceinline__ bool scans() { return threadIdx.x < SCANNERS; }
     static __device__ __forceinline__ int helper() { return threadIdx.x - SCANNERS; }
-    // Registers of a thread, from what the CTA was launched with (LAUNCHED): scanners take what helpers give.  Whole
-    // groups of four warps do so together; the sum over the CTA stays.
+    // Registers of a thread, from what the CTA was launched with: scanners take what helpers give.  Whole groups of four
+    // warps do so together; the sum over the CTA stays.  (16 states in bf16: 184 and 72 take 1126 us where 176 and 80 take
+    // 838 and 168 and 88 858; in fp32, whose helpers hold wider words, 168 and 88 take 1267, 144 and 112 1140.)
     static constexpr bool TRADE = LANES >= 4;
     static constexpr int LAUNCHED = LANES == 4 ? 128 : LANES == 8 ? 168 : 96, GROUPS = SCANNERS / 128;
-    static constexpr int SCAN_REGS = LANES == 4 ? 184 : LANES == 8 ? 208 : 104, HELP_REGS = LANES == 4 ? 72 : LANES == 8 ? 88 : 64;
-    static_assert(!TRADE || (GROUPS * SCAN_REGS + HELP_REGS == (GROUPS + 1) * LAUNCHED && SCANNERS % 128 == 0), "");
-    static __device__ __forceinline__ void take() {
-        if constexpr (TRADE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SCAN_REGS));
+    template <typename T> static constexpr int GIVEN = LANES == 4 ? (sizeof(T) == 4 ? 16 : 48) : LANES == 8 ? 64 : 32;  // by a helper
+    template <typename T> static __device__ __forceinline__ void take() {
+        static_assert(!TRADE || (SCANNERS % 128 == 0 && GIVEN<T> % (8 * (TRADE ? GROUPS : 1)) == 0), "");
+        if constexpr (TRADE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LAUNCHED + GIVEN<T> / GROUPS));
     }
-    static __device__ __forceinline__ void give() {
-        if constexpr (TRADE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(HELP_REGS));
+    template <typename T> static __device__ __forceinline__ void give() {
+        if constexpr (TRADE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LAUNCHED - GIVEN<T>));
     }
     static __device__ __forceinline__ void meet() { asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory"); }
     static __device__ __forceinline__ void helpers_meet() { asm volatile("bar.sync 2, %0;" ::"n"(HELPERS) : "memory"); }
@@ -138,10 +139,11 @@ template <bool PLANES, int WIDTH, int ROUND, int THREADS, bool WIDE> struct Shar
     __device__ __forceinline__ bool in(int i, int k, int width, int count) const {
         return busy() && channel(i) + (PLANES ? 0 : k) < width && position(i) + (PLANES ? k : 0) < count;
     }
-    // base: of the round's first position and the first channel
+    // The thread's first pair of a round, from the round's first position and the first channel.  (A pointer that moves
+    // along, kept from round to round: made anew, it is 20 instructions.)
+    template <typename T> __device__ __forceinline__ T *mine(T *base, long long row) const { return base + outer * row + inner; }
     template <typename T>
-    __device__ __forceinline__ void load(const T *base, long long row, int width, int count, typename Raw<T>::Two (&v)[COUNT]) const {
-        const T *p = base + outer * row + inner;
+    __device__ __forceinline__ void load(const T *p, long long row, int width, int count, typename Raw<T>::Two (&v)[COUNT]) const {
         const long long step = STEP * row;
         if (WIDE && ALL && width == WIDTH && count >= ROUND) {
 #pragma unroll
@@ -157,8 +159,7 @@ template <bool PLANES, int WIDTH, int ROUND, int THREADS, bool WIDE> struct Shar
         }
     }
     // value(i), a Pair, to its place
-    template <typename T, typename F> __device__ __forceinline__ void store(T *base, long long row, int width, int count, F value) const {
-        T *p = base + outer * row + inner;
+    template <typename T, typename F> __device__ __forceinline__ void store(T *p, long long row, int width, int count, F value) const {
         const long long step = STEP * row;
         if (WIDE && ALL && width == WIDTH && count >= ROUND) {
 #pragma unroll
@@ -179,8 +180,7 @@ template <bool PLANES, int WIDTH, int ROUND, int THREADS, bool WIDE> struct Shar
         }
     }
     // 0 to a round that may begin at an odd position: an element at a time
-    template <typename T> __device__ __forceinline__ void clear(T *base, long long row, int width, int count) const {
-        T *p = base + outer * row + inner;
+    template <typename T> __device__ __forceinline__ void clear(T *p, long long row, int width, int count) const {
 #pragma unroll
         for (int i = 0; i < COUNT; ++i) {
             if (in(i, 0, width, count)) p[i * STEP * row] = from_f32<T>(0.f);
@@ -196,6 +196,16 @@ template <bool PLANES, int WIDTH, int ROUND, int THREADS, bool WIDE> struct Shar
             v[i] = Pair(a, PLANES ? a : of_tile != nullptr && c + 1 < width ? of_tile[c + 1] : 0.f);
         }
     }
+};
+
+// A tensor's place of a thread, round after round: `by` positions on with every step.
+template <typename T, bool PLANES> struct Cursor {
+    T *p;
+    long long row;
+    template <typename S> __device__ __forceinline__ Cursor(const S &share, const wtconv_ssm_tensor &t, int b, int position, int first) : row(t.row) {
+        p = t.p == nullptr ? nullptr : share.mine(at<T, PLANES>(t, b, position, first), row);
+    }
+    __device__ __forceinline__ void step(int by) { p += PLANES ? by : by * row; }
 };
 
 // A round of the tile in shared memory has 32 channels to a position (tokens) or ROUND positions to a channel (planes),

@@ -44,14 +44,17 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES == 2 ? 3 : LANES 
             Two d[Part::COUNT], x[Part::COUNT], z[Part::COUNT], b[Maps::COUNT], c[Maps::COUNT];
         } even, odd;
         Two x[Part::COUNT], z[Part::COUNT], x_old[Part::COUNT] = {}, z_old[Part::COUNT] = {};  // of the scanned round, the one before
+        using In = Cursor<const T, PLANES>;
+        In d_at(part, a.in.dt, b, at_.first, at_.c0), x_at(part, a.in.x, b, at_.first, at_.c0), z_at(part, a.in.z, b, at_.first, at_.c0);
+        In b_at(maps, a.in.Bm, b, at_.first, at_.group * N), c_at(maps, a.in.Cm, b, at_.first, at_.group * N);
         const auto fetch = [&](int r, Fetched &f) {
             if (r >= count_rounds) return;
-            const int t0 = at_.first + r * kSelRound, count = stop - t0;
-            part.load(at<const T, PLANES>(a.in.dt, b, t0, at_.c0), a.in.dt.row, at_.channels, count, f.d);
-            part.load(at<const T, PLANES>(a.in.x, b, t0, at_.c0), a.in.x.row, at_.channels, count, f.x);
-            maps.load(at<const T, PLANES>(a.in.Bm, b, t0, at_.group * N), a.in.Bm.row, N, count, f.b);
-            if (!LOCAL) maps.load(at<const T, PLANES>(a.in.Cm, b, t0, at_.group * N), a.in.Cm.row, N, count, f.c);
-            if (gated) part.load(at<const T, PLANES>(a.in.z, b, t0, at_.c0), a.in.z.row, at_.channels, count, f.z);
+            const int count = stop - at_.first - r * kSelRound;
+            part.load(d_at.p, d_at.row, at_.channels, count, f.d), d_at.step(kSelRound);
+            part.load(x_at.p, x_at.row, at_.channels, count, f.x), x_at.step(kSelRound);
+            maps.load(b_at.p, b_at.row, N, count, f.b), b_at.step(kSelRound);
+            if (!LOCAL) maps.load(c_at.p, c_at.row, N, count, f.c), c_at.step(kSelRound);
+            if (gated) part.load(z_at.p, z_at.row, at_.channels, count, f.z), z_at.step(kSelRound);
         };
         const auto prepare = [&](int r, Fetched &f) {
             if (r >= count_rounds) return;
@@ -77,21 +80,22 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES == 2 ? 3 : LANES 
 #pragma unroll
             for (int i = 0; i < Part::COUNT; ++i) x[i] = f.x[i], z[i] = f.z[i];
         };
+        Cursor<T, PLANES> y_at(part, a.y, b, at_.first, at_.c0);
         const auto finish = [&](int r) {
-            const int t0 = at_.first + r * kSelRound, count = stop - t0;
+            const int count = stop - at_.first - r * kSelRound;
             const float *const sums = rounds[r & 1].sums;
             const auto value = [&](int i) {
                 const Pair s = L::get_sums(sums, L::value(part.position(i), part.channel(i)));
                 return fma(D[PLANES ? i : 0], pair_of<T>(x_old[i]), s);
             };
-            T *const to = at<T, PLANES>(a.y, b, t0, at_.c0);
             if (gated)
-                part.store(to, a.y.row, at_.channels, count, [&](int i) {
+                part.store(y_at.p, y_at.row, at_.channels, count, [&](int i) {
                     const Pair g = pair_of<T>(z_old[i]);
                     return mul(value(i), mul(g, sigmoid_of(g)));
                 });
             else
-                part.store(to, a.y.row, at_.channels, count, value);
+                part.store(y_at.p, y_at.row, at_.channels, count, value);
+            y_at.step(kSelRound);
         };
         const auto during = [&](int r, Fetched &next, Fetched &after) {  // round r is scanned
             fetch(r + 2, after);
@@ -110,7 +114,7 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES == 2 ? 3 : LANES 
         if (!LOCAL && count_rounds > 0) finish(count_rounds - 1);
         if (!LOCAL)  // positions past the sequence's end
             for (int t0 = max(at_.first, at_.length); t0 < at_.end; t0 += kSelRound)
-                part.clear(at<T, PLANES>(a.y, b, t0, at_.c0), a.y.row, at_.channels, at_.end - t0);
+                part.clear(part.mine(at<T, PLANES>(a.y, b, t0, at_.c0), a.y.row), a.y.row, at_.channels, at_.end - t0);
         return;
     }
 
