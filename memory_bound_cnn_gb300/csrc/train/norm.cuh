@@ -162,6 +162,8 @@ __global__ void __launch_bounds__(LANES == 32 ? kNormThreads : LANES) norm_backw
         float n[EACH], g[EACH];
         load_row<R, LANES, EACH, V>(static_cast<const R *>(a.total.p) + row * a.total.row, lane, C, n);
         load_row<T, LANES, EACH, V>(static_cast<const T *>(a.dy.p) + row * a.dy.row, lane, C, g);
+        float d[EACH] = {};
+        if (a.d_total.p != nullptr) load_row<R, LANES, EACH, V>(static_cast<const R *>(a.d_total.p) + row * a.d_total.row, lane, C, d);
         const float rstd = a.rstd_in[row];
         float w[EACH], s = 0.f;
         load_row<float, LANES, EACH, V>(a.w, lane, C, w);
@@ -173,15 +175,8 @@ __global__ void __launch_bounds__(LANES == 32 ? kNormThreads : LANES) norm_backw
             s = fmaf(g[i], n[i], s);
         }
         const float mean = across_row<LANES, false>(s, meet[turn]) / C;
-        if (a.d_total.p != nullptr) {
-            float d[EACH];
-            load_row<R, LANES, EACH, V>(static_cast<const R *>(a.d_total.p) + row * a.d_total.row, lane, C, d);
 #pragma unroll
-            for (int i = 0; i < EACH; ++i) g[i] = fmaf(rstd, fmaf(-n[i], mean, g[i]), d[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < EACH; ++i) g[i] = rstd * fmaf(-n[i], mean, g[i]);
-        }
+        for (int i = 0; i < EACH; ++i) g[i] = fmaf(rstd, fmaf(-n[i], mean, g[i]), d[i]);
         if (a.dx.p != nullptr) store_row<T, LANES, EACH, V>(static_cast<T *>(a.dx.p) + row * a.dx.row, lane, C, g);
         if (a.d_residual.p != nullptr)
             store_row<R, LANES, EACH, V>(static_cast<R *>(a.d_residual.p) + row * a.d_residual.row, lane, C, g);
@@ -223,12 +218,15 @@ template <typename T, typename R> cudaError_t launch_norm_forward(const NormArgs
     return with_row_shape(a.s.C, [&](auto lanes, auto each) {
         constexpr int LANES = lanes.value, EACH = each.value, V = 16 / sizeof(T);
         constexpr unsigned THREADS = LANES == 32 ? kNormThreads : LANES;
-        const unsigned grid = (unsigned)std::min(ceil_div(a.s.rows, LANES == 32 ? kNormThreads / 32 : 1), sm_count() * (2048 / (int)THREADS));
+        // as many CTAs as run at once, or fewer where there are fewer rows (with 8 to an SM where 6 ran at once, 16,384 rows of
+        // 2048 took 78 us)
+        const auto launch = [&](auto kernel) {
+            const int most = sm_count() * resident_ctas(kernel, THREADS);
+            return launch_kernel(kernel, (unsigned)std::min(ceil_div(a.s.rows, LANES == 32 ? kNormThreads / 32 : 1), most), THREADS, 0, st, 1, a);
+        };
         if (a.q != nullptr)
-            return a.wide ? launch_kernel(norm_forward_kernel<T, R, LANES, EACH, V, true>, grid, THREADS, 0, st, 1, a)
-                          : launch_kernel(norm_forward_kernel<T, R, LANES, EACH, 1, true>, grid, THREADS, 0, st, 1, a);
-        return a.wide ? launch_kernel(norm_forward_kernel<T, R, LANES, EACH, V, false>, grid, THREADS, 0, st, 1, a)
-                      : launch_kernel(norm_forward_kernel<T, R, LANES, EACH, 1, false>, grid, THREADS, 0, st, 1, a);
+            return a.wide ? launch(norm_forward_kernel<T, R, LANES, EACH, V, true>) : launch(norm_forward_kernel<T, R, LANES, EACH, 1, true>);
+        return a.wide ? launch(norm_forward_kernel<T, R, LANES, EACH, V, false>) : launch(norm_forward_kernel<T, R, LANES, EACH, 1, false>);
     });
 }
 template <typename T, typename R> cudaError_t launch_norm_backward(const NormArgs &a, cudaStream_t st) {

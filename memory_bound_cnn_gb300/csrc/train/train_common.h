@@ -75,6 +75,24 @@ template <typename... P> cudaError_t allow_shared(void (*kernel)(P...), size_t s
     }
 }
 
+// CTAs of a kernel that an SM of the current device holds at once (1 if it cannot be asked).  Asked of the runtime
+// once per kernel and device.
+template <typename... P> int resident_ctas(void (*kernel)(P...), int threads) noexcept {
+    int dev = 0, ctas = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    try {
+        static std::mutex lock;
+        static std::map<std::pair<void (*)(P...), int>, int> known;
+        std::lock_guard<std::mutex> guard(lock);
+        int &have = known[{kernel, dev}];
+        if (have == 0 && cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kernel, threads, 0) == cudaSuccess) have = ctas;
+        if (have > 0) return have;
+    } catch (...) {  // no memory for the entry
+    }
+    cudaGetLastError();
+    return 1;
+}
+
 // Launches a kernel that may be set up while the one before it on the stream still runs: every kernel
 // of these operators waits for that one's end by itself (begin_kernel in train_device.cuh).  Between
 // the two kernels of a short call that is most of the gap.  cluster: CTAs that share a cluster.
