@@ -295,126 +295,155 @@ template <typename T, int K, bool WIDE, bool SILU> __global__ void __launch_boun
 
 // --------------------------------------------------------------------------------------- planes
 
-// 2^row_bits neighbouring lanes go along a strip of a row, a vector of positions each; inputs beside it come from
-// the first-level cache.
-template <typename T, int K, int V> __global__ void __launch_bounds__(256) causal_planes_forward_kernel(const __grid_constant__ CausalArgs a) {
-    begin_kernel();
-    const int lanes = 1 << a.row_bits, per = 256 >> a.row_bits;  // strips of a CTA
-    const long long all = (long long)a.s.B * a.s.C * a.strips;
-    const unsigned main = (unsigned)((all + per - 1) / per);
-    if (blockIdx.x >= main) return write_state_last<T, K>(a, (long long)(blockIdx.x - main) * 256 + threadIdx.x);
-    const long long unit = (long long)blockIdx.x * per + (threadIdx.x >> a.row_bits);
-    if (unit >= all) return;
-    const int row = unit / a.strips, strip = unit % a.strips, b = row / a.s.C, c = row % a.s.C, length = length_of(a, b);
-    const int first = strip * a.strip, end = min(first + a.strip, a.s.T), lane = threadIdx.x & (lanes - 1);
-    const T *x = static_cast<const T *>(a.x.p) + b * a.x.batch + c * a.x.row;
-    T *y = static_cast<T *>(a.y.p) + b * a.y.batch + c * a.y.row;
-    float w[K];
+// f or its slope of COUNT values, two at a time.
+template <bool SLOPE, bool SILU, int COUNT> __device__ __forceinline__ void causal_map(float (&v)[COUNT]) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) w[k] = a.w[(long long)c * K + k];
-    const float bias = a.bias == nullptr ? 0.f : a.bias[c];
-    for (int t0 = first + lane * V; t0 < end; t0 += lanes * V) {
-        float in[V + K - 1], v[V];
-        const bool whole = t0 + V <= a.s.T;
-        if (t0 + V <= length) {
-            float q[V];
-            load_vec<T, V>(x + t0, q);
-#pragma unroll
-            for (int i = 0; i < V; ++i) in[K - 1 + i] = q[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) in[K - 1 + i] = t0 + i < length ? to_f32(x[t0 + i]) : 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < K - 1; ++k) {
-            const int t = t0 - K + 1 + k;
-            in[k] = t >= 0 ? (t < length ? to_f32(x[t]) : 0.f) : input_at<T, K>(a, b, c, t);
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            v[i] = bias;
-#pragma unroll
-            for (int k = 0; k < K; ++k) v[i] = fmaf(w[k], in[i + k], v[i]);
-            v[i] = t0 + i < length ? causal_f(v[i], a.s.silu) : 0.f;
-        }
-        if (whole) store_vec<T, V>(y + t0, v);
-        else
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (t0 + i < a.s.T) y[t0 + i] = from_f32<T>(v[i]);
+    for (int i = 0; i < COUNT; i += 2) {
+        const Pair p(v[i], v[i + 1 < COUNT ? i + 1 : i]), q = SLOPE ? causal_slope<SILU>(p) : causal_f<SILU>(p);
+        v[i] = q.lo();
+        if (i + 1 < COUNT) v[i + 1] = q.hi();
     }
 }
 
-template <typename T, int K, int V> __global__ void __launch_bounds__(256) causal_planes_backward_kernel(const __grid_constant__ CausalArgs a) {
+// Positions [t0 - BEFORE, t0 + V + AFTER) of a row, 0 past `length`, the state before position 0.  Inside the row the
+// vectors beside t0's come whole, from the first-level cache.
+template <typename T, int K, int V, int BEFORE, int AFTER>
+__device__ __forceinline__ void load_around(const CausalArgs &a, const T *row, int b, int c, int t0, int length, float (&v)[BEFORE + V + AFTER]) {
+    if (V > 1 && (BEFORE == 0 || t0 >= V) && t0 + V + (AFTER > 0 ? V : 0) <= length) {
+        float q[V];
+        if (BEFORE > 0) {
+            load_vec<T, V>(row + t0 - V, q);
+#pragma unroll
+            for (int i = 0; i < BEFORE; ++i) v[i] = q[V - BEFORE + i];
+        }
+        load_vec<T, V>(row + t0, q);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[BEFORE + i] = q[i];
+        if (AFTER > 0) {
+            load_vec<T, V>(row + t0 + V, q);
+#pragma unroll
+            for (int i = 0; i < AFTER; ++i) v[BEFORE + V + i] = q[i];
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < BEFORE + V + AFTER; ++i) {
+        const int t = t0 - BEFORE + i;
+        v[i] = t >= 0 ? (t < length ? to_f32(row[t]) : 0.f) : input_at<T, K>(a, b, c, t);
+    }
+}
+template <typename T, int V> __device__ __forceinline__ void store_some(T *row, int t0, int T_, const float (&v)[V]) {
+    if (t0 + V <= T_) return store_vec<T, V>(row + t0, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (t0 + i < T_) row[t0 + i] = from_f32<T>(v[i]);
+}
+
+// 2^row_bits neighbouring lanes go along a strip of a row, a vector of positions each.
+struct RowStrip {
+    bool used;
+    int b, c, row, strip, lane, lanes, length, first, end;
+    __device__ __forceinline__ explicit RowStrip(const CausalArgs &a) {
+        const int per = 256 >> a.row_bits;  // strips of a CTA
+        const long long unit = (long long)blockIdx.x * per + (threadIdx.x >> a.row_bits);
+        used = unit < (long long)a.s.B * a.s.C * a.strips;
+        lanes = 1 << a.row_bits, lane = threadIdx.x & (lanes - 1);
+        row = used ? (int)(unit / a.strips) : 0, strip = used ? (int)(unit % a.strips) : 0;
+        b = row / a.s.C, c = row % a.s.C, length = length_of(a, b);
+        first = strip * a.strip, end = used ? min(first + a.strip, a.s.T) : 0;
+    }
+    static __device__ __forceinline__ unsigned ctas(const CausalArgs &a) {
+        const int per = 256 >> a.row_bits;
+        return (unsigned)(((long long)a.s.B * a.s.C * a.strips + per - 1) / per);
+    }
+};
+
+template <typename T, int K, int V, bool SILU> __global__ void __launch_bounds__(256) causal_planes_forward_kernel(const __grid_constant__ CausalArgs a) {
     begin_kernel();
-    const int lanes = 1 << a.row_bits, per = 256 >> a.row_bits;
-    const long long all = (long long)a.s.B * a.s.C * a.strips;
-    const unsigned main = (unsigned)((all + per - 1) / per);
+    const unsigned main = RowStrip::ctas(a);
+    if (blockIdx.x >= main) return write_state_last<T, K>(a, (long long)(blockIdx.x - main) * 256 + threadIdx.x);
+    const RowStrip s(a);
+    const T *x = static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c * a.x.row;
+    T *y = static_cast<T *>(a.y.p) + s.b * a.y.batch + s.c * a.y.row;
+    float w[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k] = a.w[(long long)s.c * K + k];
+    const float bias = a.bias == nullptr ? 0.f : a.bias[s.c];
+    for (int t0 = s.first + s.lane * V; t0 < s.end; t0 += s.lanes * V) {
+        float v[V] = {};
+        if (t0 < s.length) {
+            float in[K - 1 + V];
+            load_around<T, K, V, K - 1, 0>(a, x, s.b, s.c, t0, s.length, in);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                v[i] = bias;
+#pragma unroll
+                for (int k = 0; k < K; ++k) v[i] = fmaf(w[k], in[i + k], v[i]);
+            }
+            causal_map<false, SILU>(v);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = t0 + i < s.length ? v[i] : 0.f;
+        }
+        store_some<T, V>(y, t0, a.s.T, v);
+    }
+}
+
+template <typename T, int K, int V, bool SILU> __global__ void __launch_bounds__(256) causal_planes_backward_kernel(const __grid_constant__ CausalArgs a) {
+    begin_kernel();
+    const unsigned main = RowStrip::ctas(a);
     if (blockIdx.x >= main) return write_d_state<T, K>(a, (long long)(blockIdx.x - main) * 256 + threadIdx.x);
-    const long long unit = (long long)blockIdx.x * per + (threadIdx.x >> a.row_bits);
-    const bool used = unit < all;
-    const int row = used ? unit / a.strips : 0, strip = used ? unit % a.strips : 0, b = row / a.s.C, c = row % a.s.C;
-    const int length = length_of(a, b), lane = threadIdx.x & (lanes - 1);
-    const int first = strip * a.strip, end = used ? min(first + a.strip, a.s.T) : 0;
-    const T *x = static_cast<const T *>(a.x.p) + b * a.x.batch + c * a.x.row, *dy = static_cast<const T *>(a.dy.p) + b * a.dy.batch + c * a.dy.row;
-    T *dx = static_cast<T *>(a.dx.p) + b * a.dx.batch + c * a.dx.row;
+    const RowStrip s(a);
+    const T *x = static_cast<const T *>(a.x.p) + s.b * a.x.batch + s.c * a.x.row, *dy = static_cast<const T *>(a.dy.p) + s.b * a.dy.batch + s.c * a.dy.row;
+    T *dx = static_cast<T *>(a.dx.p) + s.b * a.dx.batch + s.c * a.dx.row;
     float w[K], dw[K] = {}, db = 0.f;
 #pragma unroll
-    for (int k = 0; k < K; ++k) w[k] = a.w[(long long)c * K + k];
-    const float bias = a.bias == nullptr ? 0.f : a.bias[c];
-    for (int t0 = first + lane * V; t0 < end; t0 += lanes * V) {
-        float in[V + 2 * (K - 1)], g[V + K - 1], v[V];  // inputs t0 - (K-1) ..., dy t0 ...
-        if (t0 + V <= length) {
-            float q[V], r[V];
-            load_vec<T, V>(x + t0, q), load_vec<T, V>(dy + t0, r);
+    for (int k = 0; k < K; ++k) w[k] = a.w[(long long)s.c * K + k];
+    const float bias = a.bias == nullptr ? 0.f : a.bias[s.c];
+    for (int t0 = s.first + s.lane * V; t0 < s.end; t0 += s.lanes * V) {
+        float v[V] = {};
+        if (t0 < s.length) {
+            float in[V + 2 * (K - 1)], g[V + K - 1], slope[V + K - 1];  // inputs from t0 - (K-1) on, gradients from t0 on
+            load_around<T, K, V, K - 1, K - 1>(a, x, s.b, s.c, t0, s.length, in);
+            load_around<T, K, V, 0, K - 1>(a, dy, s.b, s.c, t0, s.length, g);
 #pragma unroll
-            for (int i = 0; i < V; ++i) in[K - 1 + i] = q[i], g[i] = r[i];
-        } else {
+            for (int i = 0; i < V + K - 1; ++i) {
+                slope[i] = bias;
 #pragma unroll
-            for (int i = 0; i < V; ++i) in[K - 1 + i] = t0 + i < length ? to_f32(x[t0 + i]) : 0.f, g[i] = t0 + i < length ? to_f32(dy[t0 + i]) : 0.f;
-        }
+                for (int k = 0; k < K; ++k) slope[i] = fmaf(w[k], in[i + k], slope[i]);
+            }
+            causal_map<true, SILU>(slope);
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k) {
-            const int t = t0 - K + 1 + k, u = t0 + V + k;
-            in[k] = t >= 0 ? (t < length ? to_f32(x[t]) : 0.f) : input_at<T, K>(a, b, c, t);
-            in[V + K - 1 + k] = u < length ? to_f32(x[u]) : 0.f, g[V + k] = u < length ? to_f32(dy[u]) : 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < V + K - 1; ++i) {  // g: the gradient before f
-            float pre = bias;
-#pragma unroll
-            for (int k = 0; k < K; ++k) pre = fmaf(w[k], in[i + k], pre);
-            g[i] = t0 + i < length ? g[i] * causal_slope(pre, a.s.silu) : 0.f;
-            if (i < V) {
+            for (int i = 0; i < V + K - 1; ++i) {
+                g[i] = t0 + i < s.length ? g[i] * slope[i] : 0.f;
+                if (i >= V) continue;
                 db += g[i];
 #pragma unroll
                 for (int k = 0; k < K; ++k) dw[k] = fmaf(g[i], in[i + k], dw[k]);
             }
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            v[i] = 0.f;
-#pragma unroll
-            for (int k = 0; k < K; ++k) v[i] = fmaf(w[K - 1 - k], g[i + k], v[i]);
-            const int t = t0 + i;
-            if (t >= length) v[i] = 0.f;
-            else if (a.d_last != nullptr && t >= length - K + 1)
-                v[i] += to_f32(static_cast<const T *>(a.d_last)[(long long)row * (K - 1) + t - (length - K + 1)]);
-        }
-        if (t0 + V <= a.s.T) store_vec<T, V>(dx + t0, v);
-        else
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (t0 + i < a.s.T) dx[t0 + i] = from_f32<T>(v[i]);
+#pragma unroll
+                for (int k = 0; k < K; ++k) v[i] = fmaf(w[K - 1 - k], g[i + k], v[i]);
+            if (t0 + V > s.length - K + 1) {  // the end: inputs that the last state holds, and none past it
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int t = t0 + i;
+                    if (t >= s.length) v[i] = 0.f;
+                    else if (a.d_last != nullptr && t >= s.length - K + 1)
+                        v[i] += to_f32(static_cast<const T *>(a.d_last)[(long long)s.row * (K - 1) + t - (s.length - K + 1)]);
+                }
+            }
+        }
+        store_some<T, V>(dx, t0, a.s.T, v);
     }
-    const long long part = (long long)b * a.strips + strip;
+    const long long part = (long long)s.b * a.strips + s.strip;
 #pragma unroll
     for (int k = 0; k <= K; ++k) {
-        float s = k == K ? db : dw[k == K ? 0 : k];
-        for (int m = lanes / 2; m >= 1; m /= 2) s += __shfl_xor_sync(0xffffffffu, s, m);
-        if (used && lane == 0) {
-            if (k == K) a.part_b[part * a.s.C + c] = s;
-            else a.part_w[(part * a.s.C + c) * K + k] = s;
+        float v = k == K ? db : dw[k == K ? 0 : k];
+        for (int m = s.lanes / 2; m >= 1; m /= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
+        if (s.used && s.lane == 0) {
+            if (k == K) a.part_b[part * a.s.C + s.c] = v;
+            else a.part_w[(part * a.s.C + s.c) * K + k] = v;
         }
     }
 }
@@ -431,11 +460,11 @@ template <bool BACKWARD, typename T, int K, bool WIDE> cudaError_t launch_causal
     const auto launch = [&](auto kernel) { return launch_kernel(kernel, (unsigned)grid, 256, 0, st, 1, a); };
     if constexpr (BACKWARD) {
         constexpr int V = WIDE ? 4 : 1;
-        if (planes) return launch(causal_planes_backward_kernel<T, K, V>);
+        if (planes) return a.s.silu ? launch(causal_planes_backward_kernel<T, K, V, true>) : launch(causal_planes_backward_kernel<T, K, V, false>);
         return a.s.silu ? launch(causal_tokens_backward_kernel<T, K, WIDE, true>) : launch(causal_tokens_backward_kernel<T, K, WIDE, false>);
     } else {
         constexpr int V = WIDE ? 16 / sizeof(T) : 1;
-        if (planes) return launch(causal_planes_forward_kernel<T, K, V>);
+        if (planes) return a.s.silu ? launch(causal_planes_forward_kernel<T, K, V, true>) : launch(causal_planes_forward_kernel<T, K, V, false>);
         return a.s.silu ? launch(causal_tokens_forward_kernel<T, K, WIDE, true>) : launch(causal_tokens_forward_kernel<T, K, WIDE, false>);
     }
 }
