@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(LANES == 32 ? kNormThreads : LANES) norm_forwa
         float w[EACH];
         load_row<float, LANES, EACH, V>(a.w, lane, C, w);
 #pragma unroll
-        for (int i = 0; i < EACH; ++i) v[i] *= rstd * w[i];
+        for (int i = 0; i < EACH; ++i) v[i] *= E4M3 ? w[i] : rstd * w[i];  // (codes do not depend on rstd: it is in the scale alone)
         if constexpr (!E4M3) {
             store_row<T, LANES, EACH, V>(static_cast<T *>(a.y.p) + row * a.y.row, lane, C, v);
         } else {
@@ -135,14 +135,15 @@ __global__ void __launch_bounds__(LANES == 32 ? kNormThreads : LANES) norm_forwa
             for (int j = 0; j < EACH / V; ++j) {
                 const int at = (j * LANES + lane) * V;
                 if (at >= C) continue;
-                const bool nothing = top[j] < 7.7037197775489434e-34f;  // 2^-110
+                const float most = top[j] * rstd;
+                const bool nothing = most < 7.7037197775489434e-34f;  // 2^-110
                 const float inverse = nothing ? 0.f : 448.f / top[j];
                 Vec<unsigned char, V> q;
 #pragma unroll
                 for (int i = 0; i < V; ++i) q.v[i] = __nv_cvt_float_to_fp8(v[j * V + i] * inverse, __NV_SATFINITE, __NV_E4M3);
                 *reinterpret_cast<Vec<unsigned char, V> *>(a.q + row * C + at) = q;
                 if (a.block == 0 ? at == 0 : at % 128 == 0)
-                    a.scales[row * a.blocks + (a.block == 0 ? 0 : at / 128)] = nothing ? 0.f : top[j] / 448.f;
+                    a.scales[row * a.blocks + (a.block == 0 ? 0 : at / 128)] = nothing ? 0.f : most / 448.f;
             }
         }
     }

@@ -59,6 +59,7 @@ void plan(int op, SelectiveArgs &a) {
     double best = 0;
     for (int parts = 1; parts <= most; ++parts) {
         const int per = ceil_div(rounds, parts), used = ceil_div(rounds, per);
+        if (used > 1 && (long long)a.ctas() * used > 0x7fffffffll) break;
         const long long on_sm = ((long long)a.ctas() * used + sms - 1) / sms;
         const double load = on_sm <= resident ? share[on_sm] : on_sm * share[resident] / resident;
         const double time = (per + ends) * load * (used > 1 ? pass : 1) + (used > 1 ? start + join * used : 0);
@@ -99,9 +100,9 @@ int check_workspace(size_t need, const void *workspace, size_t bytes) {
     return workspace == nullptr || bytes < need ? WTCONV_ERR_WORKSPACE : WTCONV_OK;
 }
 
-// A grid has at most 2^31 - 1 CTAs: of up to 256 parts of sequences, or of 32 positions.
-bool grid_ok(const SelectiveArgs &a) {
-    return (long long)a.s.B * a.s.G * a.tiles * 256 <= 0x7fffffffll && (long long)a.s.B * a.s.G * ceil_div(a.s.T, kSelRound) <= 0x7fffffffll;
+// The backward's last sums take a CTA for 32 positions of a group; a grid has at most 2^31 - 1.
+bool grid_ok(int op, const wtconv_selective_shape &s) {
+    return op == WTCONV_SCAN_OP_FORWARD || (long long)s.B * s.G <= 0x7fffffffll / ceil_div(s.T, kSelRound);
 }
 
 template <typename F> cudaError_t by_type(int dtype, F f) {
@@ -120,8 +121,8 @@ size_t wtconv_selective_states_size(const wtconv_selective_shape *shape) {
 
 size_t wtconv_selective_workspace_size(int op, const wtconv_selective_shape *shape) {
     if (check_shape(shape) != WTCONV_OK || (op != WTCONV_SCAN_OP_FORWARD && op != WTCONV_SCAN_OP_BACKWARD)) return 0;
+    if (!grid_ok(op, *shape)) return 0;
     SelectiveArgs a = args_of(*shape);
-    if (!grid_ok(a)) return 0;
     plan(op, a);
     return place(op, a, nullptr);
 }
@@ -133,7 +134,7 @@ int wtconv_selective_forward(const wtconv_selective_shape *shape, const wtconv_s
     if (in == nullptr || y == nullptr) return WTCONV_ERR_INVALID_ARG;
     SelectiveArgs a = args_of(*shape);
     a.in = *in, a.y = *y, a.h_last = h_last, a.states_out = states;
-    if (!grid_ok(a) || !inputs_ok(a) || !check_tensor(a.y, a.s, a.s.C, true) || !f32_ok(h_last, true) || !aligned_to(states, 16))
+    if (!inputs_ok(a) || !check_tensor(a.y, a.s, a.s.C, true) || !f32_ok(h_last, true) || !aligned_to(states, 16))
         return WTCONV_ERR_INVALID_ARG;
     a.wide = pairs(a);
     plan(WTCONV_SCAN_OP_FORWARD, a);
@@ -153,7 +154,7 @@ int wtconv_selective_backward(const wtconv_selective_shape *shape, const wtconv_
     SelectiveArgs a = args_of(*shape);
     a.in = *in, a.dy = *dy, a.states_in = states, a.dh_last = dh_last, a.g = *grads;
     const int width = a.s.G * a.s.N;
-    if (!grid_ok(a) || !inputs_ok(a) || !check_tensor(a.dy, a.s, a.s.C, false) || !check_tensor(a.g.dx, a.s, a.s.C, true) ||
+    if (!grid_ok(WTCONV_SCAN_OP_BACKWARD, a.s) || !inputs_ok(a) || !check_tensor(a.dy, a.s, a.s.C, false) || !check_tensor(a.g.dx, a.s, a.s.C, true) ||
         !check_tensor(a.g.d_dt, a.s, a.s.C, true) || !check_tensor(a.g.dB, a.s, width, true) ||
         !check_tensor(a.g.dC, a.s, width, true) || (a.in.z.p != nullptr && !check_tensor(a.g.dz, a.s, a.s.C, true)) ||
         states == nullptr || !aligned_to(states, 16) || !f32_ok(dh_last, true) || !f32_ok(a.g.dA, false) || !f32_ok(a.g.dD, true) ||
@@ -182,7 +183,7 @@ int wtconv_selective_step(const wtconv_selective_shape *shape, const wtconv_sele
     a.in = *in, a.y = *y;
     // one position: the rows are the batch's
     for (wtconv_ssm_tensor *t : {&a.in.x, &a.in.dt, &a.in.Bm, &a.in.Cm, &a.in.z, &a.y}) t->batch = t->row;
-    if (!grid_ok(a) || !inputs_ok(a) || !check_tensor(a.y, a.s, a.s.C, true) || !f32_ok(pool, false) || !f32_ok(slots, true) ||
+    if (!inputs_ok(a) || !check_tensor(a.y, a.s, a.s.C, true) || !f32_ok(pool, false) || !f32_ok(slots, true) ||
         n_states <= 0 || (slots == nullptr && n_states < s.B))
         return WTCONV_ERR_INVALID_ARG;
     if (fault_injected()) return WTCONV_ERR_INJECTED;

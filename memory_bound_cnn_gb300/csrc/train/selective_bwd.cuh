@@ -270,8 +270,8 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
                 const float2 q = s.coef[L::coef(t, c)];
                 const Quad o = quad_of(map(1, t));
                 const Pair d(q.x), r(s.r[L::value(t, c)]);
-                carry.a = mul(exp2_fast(mul(d, decay.a)), fma(o.a, r, carry.a));
-                carry.b = mul(exp2_fast(mul(d, decay.b)), fma(o.b, r, carry.b));
+                carry.a = mul(decays_of(d, decay.a), fma(o.a, r, carry.a));
+                carry.b = mul(decays_of(d, decay.b), fma(o.b, r, carry.b));
                 step_sum += q.x;
             };
             if (count == BLOCK) {
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
                 const float2 q = s.coef[L::coef(t, c)];
                 const Quad u = quad_of(map(0, t));
                 const Pair d(q.x), dx(q.y);
-                return Quad{fma(exp2_fast(mul(d, decay.a)), h.a, mul(dx, u.a)), fma(exp2_fast(mul(d, decay.b)), h.b, mul(dx, u.b))};
+                return Quad{fma(decays_of(d, decay.a), h.a, mul(dx, u.a)), fma(decays_of(d, decay.b), h.b, mul(dx, u.b))};
             };
             // (what a position needs is loaded before the one after it is stored, as in the forward)
             struct Operands {
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
                     const Quad u = quad_of(now.u), o = quad_of(now.o), last = t == 0 ? before_part : h[t == 0 ? 0 : t - 1];
                     const Pair d(now.q.x), dx(now.q.y), r(now.r);
                     const Quad g = {fma(o.a, r, carry.a), fma(o.b, r, carry.b)};
-                    carry.a = mul(exp2_again(mul(d, decay.a)), g.a), carry.b = mul(exp2_again(mul(d, decay.b)), g.b);
+                    carry.a = mul(decays_again(d, decay.a), g.a), carry.b = mul(decays_again(d, decay.b), g.b);
                     const Quad kk = {mul(carry.a, last.a), mul(carry.b, last.b)};
                     dA_block.a = fma(kk.a, d, dA_block.a), dA_block.b = fma(kk.b, d, dA_block.b);
                     const Pair p1 = fma(g.a, u.a, mul(g.b, u.b)), p2 = fma(kk.a, decay.a, mul(kk.b, decay.b));

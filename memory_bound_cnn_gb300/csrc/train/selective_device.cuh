@@ -23,6 +23,13 @@ __device__ __forceinline__ float exp2_again(float v) {
 __device__ __forceinline__ Pair exp2_again(Pair v) { return {exp2_again(v.lo()), exp2_again(v.hi())}; }
 __device__ __forceinline__ Pair exp2_fast(Pair v) { return {exp2_fast(v.lo()), exp2_fast(v.hi())}; }
 
+// A position's decays of two states: exp2 of d times A log2 e.  The approximate exp2 of a value between -0.7 and 0 is low
+// by 1.4e-8 of itself on average (measured over 2^20 of them); a state multiplies it up for as many positions as it
+// remembers, a thousand and more, so the argument is raised by as much.
+constexpr float kSelRaise = 2.0e-8f;  // log2(1 + 1.4e-8)
+__device__ __forceinline__ Pair decays_of(Pair d, Pair rate) { return exp2_fast(fma(d, rate, Pair(kSelRaise))); }
+__device__ __forceinline__ Pair decays_again(Pair d, Pair rate) { return exp2_again(fma(d, rate, Pair(kSelRaise))); }
+
 // softplus(v) = max(v, 0) + log(1 + e) with e = exp(-|v|) in (0, 1]: nothing cancels.  With s = e / (2 + e)
 // <= 1/3, log(1 + e) = 2 artanh s = 2 (s + s^3/3 + ... + s^13/13); the next term is 1.4e-8 of the value.
 __device__ __forceinline__ Pair exp_of_minus_abs(Pair v) {

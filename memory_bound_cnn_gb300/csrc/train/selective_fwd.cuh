@@ -161,8 +161,8 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES == 2 ? 3 : LANES 
         const auto step = [&](const Operands &p) {  // one position; its sum over the lane's states
             const Quad u = quad_of(p.u);
             const Pair d(p.q.x), dx(p.q.y);
-            h.a = fma(exp2_fast(mul(d, decay.a)), h.a, mul(dx, u.a));
-            h.b = fma(exp2_fast(mul(d, decay.b)), h.b, mul(dx, u.b));
+            h.a = fma(decays_of(d, decay.a), h.a, mul(dx, u.a));
+            h.b = fma(decays_of(d, decay.b), h.b, mul(dx, u.b));
             if (LOCAL) {
                 step_sum += p.q.x;
                 return 0.f;
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(128) selective_step_kernel(const __grid_consta
         if (a.in.dt_bias != nullptr) d += a.in.dt_bias[c];
         if (a.s.softplus) d = softplus_of(Pair(d)).lo();
         const Pair rate(d * kSelLog2E), dx(d * x);
-        h.a = fma(exp2_fast(mul(rate, A.a)), h.a, mul(dx, in.a)), h.b = fma(exp2_fast(mul(rate, A.b)), h.b, mul(dx, in.b));
+        h.a = fma(decays_of(rate, A.a), h.a, mul(dx, in.a)), h.b = fma(decays_of(rate, A.b), h.b, mul(dx, in.b));
         if (WIDE && n0 < N) *reinterpret_cast<float4 *>(row + n0) = float4_of(h);
         if (!WIDE) store_quad(row, n0, N, h);
         const Pair s = fma(out.a, h.a, mul(out.b, h.b));

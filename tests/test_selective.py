@@ -141,7 +141,7 @@ def _forward(s=None, y=None, h_last=None, states=None, ws=FAKE, nbytes=1 << 30, 
 @pytest.mark.parametrize("kw,status", [
     (dict(B=0), W.ERR_INVALID_ARG), (dict(T=0), W.ERR_INVALID_ARG), (dict(C=-2), W.ERR_INVALID_ARG), (dict(N=0), W.ERR_INVALID_ARG),
     (dict(N=65), W.ERR_INVALID_ARG), (dict(G=0), W.ERR_INVALID_ARG), (dict(G=3), W.ERR_INVALID_ARG),
-    (dict(T=(1 << 30) + 1), W.ERR_INVALID_ARG), (dict(B=1 << 16, C=1 << 15), W.ERR_INVALID_ARG), (dict(B=1 << 24), W.ERR_INVALID_ARG),
+    (dict(T=(1 << 30) + 1), W.ERR_INVALID_ARG), (dict(B=1 << 16, C=1 << 15), W.ERR_INVALID_ARG),
     (dict(layout=2), W.ERR_INVALID_ARG), (dict(softplus=2), W.ERR_INVALID_ARG), (dict(dtype=3), W.ERR_UNSUPPORTED)])
 def test_shapes_are_refused(kw, status):
     s = shape(**kw)
@@ -175,6 +175,10 @@ def test_backward_and_step_refuse(monkeypatch):
         assert backward(**{k: act(None)}) == backward(**{k: act(FAKE, 128, 8)}) == W.ERR_INVALID_ARG
     for k in ("dA", "dD", "d_dt_bias", "d_h0"):
         assert backward(**{k: ODD}) == W.ERR_INVALID_ARG
+    many = shape(B=1 << 16, T=1 << 30)  # a sum of 32 positions has a CTA of its own
+    assert lib.wtconv_selective_workspace_size(S.OP_SCAN_BACKWARD, ref(many)) == 0
+    g = M.SelectiveGrads(good, good, good, good, good, FAKE, FAKE, FAKE, FAKE)
+    assert lib.wtconv_selective_backward(ref(many), ref(inputs()), FAKE, ref(good), None, ref(g), FAKE, 1 << 60, None) == W.ERR_INVALID_ARG
     assert backward(dA=None) == backward(dy=act(None)) == backward(ws=ODD) == W.ERR_INVALID_ARG
     assert backward(nbytes=1) == backward(ws=None) == W.ERR_WORKSPACE
 
@@ -261,6 +265,28 @@ def test_a_state_that_is_not_finite_stays_in_its_channel(layout):
     assert torch.equal(y, clean_y)
     others = [c for c in range(33) if c != 3]
     assert torch.isfinite(got["dA"][others]).all() and torch.equal(got["d_h0"][1], clean["d_h0"][1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_steps_of_zero_leave_the_state(layout):
+    d = make(2, 300, 33, 7, layout, torch.float32, seed=2, softplus=False, absent=("dt_bias",))
+    d["dt"].zero_()
+    got = run(d, layout)
+    assert torch.equal(got["h_last"], d["h0"]) and (got["dx"] != 0).any() and (got["dB"] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_an_infinite_input_reaches_no_gradient_before_its_two_positions(layout):
+    d = make(2, 40, 33, 5, layout, torch.bfloat16, seed=2)
+    clean = run(d, layout)
+    (d["x"][0].T if layout == "planes" else d["x"][0])[20, 3] = float("inf")
+    got = run(d, layout)
+    for k in ("dB", "dC"):
+        a, b = (time_first(v[k], layout) for v in (got, clean))
+        assert np.array_equal(a[:20], b[:20]) and np.array_equal(a[:, 1], b[:, 1])
+    assert not np.isfinite(time_first(got["dC"], layout)[20, 0]).all()
 
 
 def embed(t, before, after, pad, rows_at):
