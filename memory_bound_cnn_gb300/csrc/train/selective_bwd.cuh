@@ -416,13 +416,17 @@ template <typename T, int LANES, bool PLANES> __global__ void __launch_bounds__(
     const int live = max(min(TURN, length - t0), 0), count = min(TURN, a.s.T - t0);
     const long long per = (long long)a.s.B * a.s.T * WIDTH;  // of a tile
     const float *const from = a.part_bc + (long long)g * a.tiles * per + ((long long)b * a.s.T + t0) * WIDTH;
-    for (int e = threadIdx.x; e < TURN * WIDTH; e += kSelSumsThreads) {
-        float v = 0.f;
+    for (int e = 4 * threadIdx.x; e < TURN * WIDTH; e += 4 * kSelSumsThreads) {  // (67 MB: 14 us; one value at a time 42)
+        Quad v = {Pair(0.f), Pair(0.f)};
         if (e / WIDTH < live) {
 #pragma unroll 8
-            for (int i = 0; i < a.tiles; ++i) v += from[i * per + e];
+            for (int i = 0; i < a.tiles; ++i) {
+                const Quad q = quad_of(*reinterpret_cast<const float4 *>(from + i * per + e));
+                v.a = add(v.a, q.a), v.b = add(v.b, q.b);
+            }
         }
-        sums[e % WIDTH][e / WIDTH] = v;
+        const int j = e % WIDTH, t = e / WIDTH;
+        sums[j][t] = v.a.lo(), sums[j + 1][t] = v.a.hi(), sums[j + 2][t] = v.b.lo(), sums[j + 3][t] = v.b.hi();
     }
     __syncthreads();
     for (int e = threadIdx.x; e < TURN * WIDTH; e += kSelSumsThreads) {
