@@ -14,7 +14,14 @@ constexpr float kSelCut = 1.0003662109375f;  // 1 + 3 x 2^-13
 // d += A B with A 16 x 8 and B 8 x 8: of A, a lane holds (row, column) (lane / 4, lane % 4) in `low` and (8 + lane / 4,
 // 4 + lane % 4) in `high`, the rest is 0; of B (lane % 4, lane / 4) and (4 + lane % 4, lane / 4); of d (lane / 4, 2 (lane %
 // 4) + 0 and 1), then the same of row 8 + lane / 4.
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t low, uint32_t high, uint32_t b0, uint32_t b1) {
+// FIRST: d = A B.
+template <bool FIRST> __device__ __forceinline__ void mma(float (&d)[4], uint32_t low, uint32_t high, uint32_t b0, uint32_t b1) {
+    if constexpr (FIRST) {
+        asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %5, %6}, {%7, %8}, {%9, %9, %9, %9};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(low), "r"(0), "r"(high), "r"(b0), "r"(b1), "f"(0.f));
+        return;
+    }
     asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %5, %6}, {%7, %8}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(low), "r"(0), "r"(high), "r"(b0), "r"(b1));
@@ -31,8 +38,8 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t low, uint32_t high, 
 // the first four columns and row 8 + r of the others leaves the sums in row r (one position) and 8 + r; each of the 8
 // values has an r of its own.  The tensor cores read a value's leading 11 bits and leave the rest out.  For sums that
 // are stored in bf16 that is enough: cut to 11 bits, m 2^e with 1 <= m < 2 loses less than 2^-10 2^e, half of that on
-// average; times 1 + 3 x 2^-13 beforehand, it is off by -6.1e-4 to 3.7e-4 of itself, at random, where rounding the sum to
-// bf16 costs up to 3.9e-3 (8 x 4096 x 1024 with 16 states: 906 us; 1172 in fp32, where the rest enters too).  In other types
+// average; with a factor 1 + 3 x 2^-13 on the sum, each is off by -6.1e-4 to 3.7e-4 of itself, at random, where rounding the
+// sum to bf16 costs up to 3.9e-3 (8 x 4096 x 1024 with 16 states: 906 us; 1172 in fp32, where the rest enters too).  In other types
 // it enters as a second product, which keeps 22 bits.
 // Then warps meet in shared memory, and CTAs in selective_sums_kernel.
 // With 8 and with 64 states the lanes hold half of a block's states at a time and recompute the first half twice: fewer
@@ -352,8 +359,7 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
                     const Pair p1 = fma(g.a, u.a, mul(g.b, u.b)), p2 = fma(kk.a, decay.a, mul(kk.b, decay.b));
                     const Pair p3 = fma(o.a, h[t].a, mul(o.b, h[t].b));
                     s1[t % TOGETHER] = p1.lo() + p1.hi(), s2[t % TOGETHER] = p2.lo() + p2.hi(), s3[t % TOGETHER] = p3.lo() + p3.hi();
-                    const Pair to_b = CUT ? Pair(now.q.y * kSelCut) : dx, to_c = CUT ? Pair(now.r * kSelCut) : r;
-                    const Pair b0 = mul(g.a, to_b), b1 = mul(g.b, to_b), c0 = mul(h[t].a, to_c), c1 = mul(h[t].b, to_c);
+                    const Pair b0 = mul(g.a, dx), b1 = mul(g.b, dx), c0 = mul(h[t].a, r), c1 = mul(h[t].b, r);
                     v[0] = b0.lo(), v[1] = b0.hi(), v[2] = b1.lo(), v[3] = b1.hi();
                     v[4] = c0.lo(), v[5] = c0.hi(), v[6] = c1.lo(), v[7] = c1.hi();
                 };
@@ -373,14 +379,13 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
                     if (HELD == BLOCK && FULL ? t < HELD - 2 : !first) put_part(from + t + 2);
                     first = false;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) sums[k] = 0.f;
-#pragma unroll
                     for (int r = 0; r < 8; ++r) {
                         const uint32_t h0 = __float_as_uint(v0[r]), h1 = __float_as_uint(v1[r]);
-                        mma(sums, one[r], one[r], h0, h1);
+                        if (r == 0) mma<true>(sums, one[r], one[r], h0, h1);
+                        else mma<false>(sums, one[r], one[r], h0, h1);
                         if (!CUT) {  // what the product with the upper 11 bits left
                             const float l0 = v0[r] - __uint_as_float(h0 & 0xffffe000u), l1 = v1[r] - __uint_as_float(h1 & 0xffffe000u);
-                            mma(sums, one[r], one[r], __float_as_uint(l0), __float_as_uint(l1));
+                            mma<false>(sums, one[r], one[r], __float_as_uint(l0), __float_as_uint(l1));
                         }
                     }
                 }
@@ -425,6 +430,7 @@ template <typename T, int LANES, bool PLANES> __global__ void __launch_bounds__(
                 v.a = add(v.a, q.a), v.b = add(v.b, q.b);
             }
         }
+        if (std::is_same<T, __nv_bfloat16>::value) v.a = mul(v.a, Pair(kSelCut)), v.b = mul(v.b, Pair(kSelCut));  // of cut products
         const int j = e % WIDTH, t = e / WIDTH;
         sums[j][t] = v.a.lo(), sums[j + 1][t] = v.a.hi(), sums[j + 2][t] = v.b.lo(), sums[j + 3][t] = v.b.hi();
     }

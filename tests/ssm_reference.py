@@ -98,9 +98,9 @@ def selective(d):
     res["dC"] = (per_group(zero(r[..., None] * h[1:])), per_group(zero(np.abs(r)[..., None] * (E[1:] + H[1:] * (rr[..., None] + many)))))
     dx_abs = np.abs(step * x)[..., None]
     res["dB"] = (per_group((step * x)[..., None] * g), per_group(dx_abs * (EG + Gm * (rd[..., None] + many))))
-    # In bf16 the products that dB and dC sum are cut to 11 bits after a factor 1 + 3 x 2^-13.  With m 2^e, 1 <= m < 2, cutting
-    # loses l 2^e with 0 <= l < 2^-10; (m (1 + 3 x 2^-13) - l) / m - 1 = 3 x 2^-13 - l / m lies between 3 x 2^-13 - 2^-10 =
-    # -6.104e-4 and 3.67e-4.
+    # In bf16 the products that dB and dC sum are cut to 11 bits, and the sum gets a factor 1 + f, f = 3 x 2^-13.  With m 2^e,
+    # 1 <= m < 2, cutting loses l 2^e with 0 <= l < 2^-10; (m - l) (1 + f) / m - 1 = f - (1 + f) l / m lies between f -
+    # (1 + f) 2^-10 = -6.107e-4 and f = 3.663e-4.
     res["cut"] = {"dC": 6.11e-4 * per_group(zero(np.abs(r[..., None] * h[1:]))), "dB": 6.11e-4 * per_group(dx_abs * np.abs(g))}
     into, into_abs, into_err = (g * Bc).sum(-1), (Gm * np.abs(Bc)).sum(-1), (np.abs(Bc) * (EG + 8 * U * Gm)).sum(-1)
     dx, dx_err = step * into, step * (into_err + into_abs * (rd + 2 * U))
