@@ -32,8 +32,8 @@ bool inputs_ok(const SelectiveArgs &a) {
 
 // Whether pairs of neighbours along the contiguous axis lie at multiples of their size.
 bool pairs(const wtconv_ssm_tensor &t, const wtconv_selective_shape &s) {
-    const bool rows = (s.layout == WTCONV_SCAN_PLANES ? s.C : s.T) > 1;
-    return t.p == nullptr || (aligned_to(t.p, 2 * elem_bytes_of(s.dtype)) && (!rows || t.row % 2 == 0) && (s.B == 1 || t.batch % 2 == 0));
+    // (a row's stride counts with one channel too: B and C have a row to a state)
+    return t.p == nullptr || (aligned_to(t.p, 2 * elem_bytes_of(s.dtype)) && t.row % 2 == 0 && (s.B == 1 || t.batch % 2 == 0));
 }
 // (a group's first channel has to be even too, where channels are neighbours; its first state is where pairs of
 // states are read at once, as their number is then a multiple of 8)

@@ -220,6 +220,17 @@ def test_sizes(size, dtype, layout):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dtype", DTYPES, ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+@pytest.mark.parametrize("B,T", [(1, 35), (2, 70)])
+def test_one_channel(B, T, N, dtype, layout):
+    """One channel with all the states of its lanes, whose rows of planes lie at any distance."""
+    d = make(B, T, 1, N, layout, dtype, seed=N)
+    check(run(d, layout), reference(d, layout), layout, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
 @pytest.mark.parametrize("C,G", [(6, 2), (70, 2), (96, 3), (4, 4)])
 def test_groups(C, G, layout):
     d = make(2, 40, C, 5, layout, torch.bfloat16, G=G, seed=1)
