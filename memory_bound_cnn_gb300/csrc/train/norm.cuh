@@ -88,10 +88,13 @@ __global__ void __launch_bounds__(LANES == 32 ? kNormThreads : LANES) norm_forwa
         s = across_row<LANES, false>(s, meet[turn][0]);
         const float rstd = rsqrtf(s / C + a.s.eps);
         if (a.rstd != nullptr && lane == 0) a.rstd[row] = rstd;
+        // Of rstd = power (rstd / power) the power of two alone is in what the codes are made of: they do not depend on rstd's
+        // rounding, and largest values keep clear of the type's ends.
+        const float power = E4M3 && rstd > 0.f && rstd < INFINITY ? __uint_as_float(__float_as_uint(rstd) & 0x7f800000u) : 1.f;
         float w[EACH];
         load_row<float, LANES, EACH, V>(a.w, lane, C, w);
 #pragma unroll
-        for (int i = 0; i < EACH; ++i) v[i] *= E4M3 ? w[i] : rstd * w[i];  // (codes do not depend on rstd: it is in the scale alone)
+        for (int i = 0; i < EACH; ++i) v[i] = E4M3 ? v[i] * power * w[i] : v[i] * (rstd * w[i]);
         if constexpr (!E4M3) {
             store_row<T, LANES, EACH, V>(static_cast<T *>(a.y.p) + row * a.y.row, lane, C, v);
         } else {
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(LANES == 32 ? kNormThreads : LANES) norm_forwa
             for (int j = 0; j < EACH / V; ++j) {
                 const int at = (j * LANES + lane) * V;
                 if (at >= C) continue;
-                const float most = top[j] * rstd;
+                const float most = top[j] * (rstd / power);
                 const bool nothing = most < 7.7037197775489434e-34f;  // 2^-110
                 const float inverse = nothing ? 0.f : 448.f / top[j];
                 Vec<unsigned char, V> q;

@@ -194,6 +194,28 @@ def test_e4m3(size, types, block):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("block", [0, 128])
+@pytest.mark.parametrize("C", [96, 768, 1000, 5000])
+@pytest.mark.parametrize("x_power,w_power,eps", [(-100, -20, 2.0 ** -20), (-60, -68, 0.0), (55, 80, 2.0 ** -20), (-60, 30, 0.0), (3, -112, 2.0 ** -20)], ids=str)
+def test_e4m3_of_small_and_large_values(C, block, x_power, w_power, eps):
+    """Rows and weights of any size have y of theirs: codes do not change with a power of two that all of a row share.
+    Where all values are below 2^-110, scales and codes are 0."""
+    d = make(4, C, torch.float32, torch.float32, seed=6, residual=False)
+    x, w = d["x"] * 2.0 ** x_power, d["weight"] * 2.0 ** w_power
+    q, scales, _ = M.wtconv_rms_forward_e4m3(x, w, None, eps, block)
+    t, w = x.double().cpu().numpy(), w.double().cpu().numpy()
+    y = t / np.sqrt((t * t).mean(1, keepdims=True) + eps) * w
+    per = block or C
+    most = np.abs(np.pad(y, ((0, 0), (0, -C % per)))).reshape(4, -1, per).max(2)
+    got = scales.double().cpu().numpy()
+    small = most < 2.0 ** -110
+    assert (got[small] == 0).all() and (np.abs(got - most / 448) <= 44 * U * most / 448)[~small].all()
+    plain = M.wtconv_rms_forward_e4m3(d["x"], d["weight"], None, 0.0, block)[0].float()
+    keep = torch.from_numpy(np.repeat(~small, per, 1)[:, :C].copy()).cuda()
+    assert torch.equal(q.float(), torch.where(keep, plain, torch.zeros_like(plain)))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("C", [96, 768, 1000, 5000])
 def test_values_that_are_not_finite_stay_in_their_row(C):
     d = make(6, C, torch.float32, torch.float32, seed=3)
