@@ -63,16 +63,20 @@ __device__ __forceinline__ void store_row(S *row, int lane, int C, const float (
 
 constexpr int kNormThreads = 128;  // of a CTA whose warps have a row each
 
+// CTAs to an SM that registers have to suffice for, 40 a thread (16,384 rows of 2048 in e4m3 with an fp32 residual:
+// 62.7 us; with 44 and a CTA less 67.7).
+constexpr int norm_ctas(int threads, int each, int v) { return each == 8 && v > 1 ? 1536 / threads : 1; }
+
 // LANES threads to a row, EACH values to a thread; V neighbours (C is a multiple of V).
 template <typename T, typename R, int LANES, int EACH, int V, bool E4M3>
-__global__ void __launch_bounds__(LANES == 32 ? kNormThreads : LANES) norm_forward_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(LANES == 32 ? kNormThreads : LANES, norm_ctas(LANES == 32 ? kNormThreads : LANES, EACH, V)) norm_forward_kernel(const __grid_constant__ NormArgs a) {
     constexpr int ROWS = LANES == 32 ? kNormThreads / 32 : 1, WARPS = LANES / 32;
     __shared__ float meet[2][2][WARPS];
     __shared__ float tops[E4M3 && V == 1 ? ROWS : 1][E4M3 && V == 1 ? EACH * WARPS : 1];  // max |y| of 32 neighbours
     begin_kernel();
     const int lane = threadIdx.x % LANES, slot = threadIdx.x / LANES, C = a.s.C;
     int turn = 0;
-    for (long long row = (long long)blockIdx.x * ROWS + slot; row < a.s.rows; row += (long long)gridDim.x * ROWS, turn ^= 1) {
+    for (int row = blockIdx.x * ROWS + slot; row < a.s.rows; row += gridDim.x * ROWS, turn ^= 1) {  // (at most 2^30)
         float v[EACH];
         load_row<T, LANES, EACH, V>(static_cast<const T *>(a.x.p) + row * a.x.row, lane, C, v);
         if (a.residual.p != nullptr) {
@@ -86,11 +90,13 @@ __global__ void __launch_bounds__(LANES == 32 ? kNormThreads : LANES) norm_forwa
 #pragma unroll
         for (int i = 0; i < EACH; ++i) s = fmaf(v[i], v[i], s);
         s = across_row<LANES, false>(s, meet[turn][0]);
-        const float rstd = rsqrtf(s / C + a.s.eps);
+        float rstd = rsqrtf(s / C + a.s.eps);
         if (a.rstd != nullptr && lane == 0) a.rstd[row] = rstd;
-        // Of rstd = power (rstd / power) the power of two alone is in what the codes are made of: they do not depend on rstd's
+        // Of rstd = power x rest the power of two alone is in what the codes are made of: they do not depend on the root's
         // rounding, and largest values keep clear of the type's ends.
-        const float power = E4M3 && rstd > 0.f && rstd < INFINITY ? __uint_as_float(__float_as_uint(rstd) & 0x7f800000u) : 1.f;
+        const uint32_t bits = __float_as_uint(rstd), regular = rstd > 0.f && rstd < INFINITY;
+        const float power = __uint_as_float(regular ? bits & 0x7f800000u : 0x3f800000u);
+        if (E4M3) rstd = __uint_as_float(regular ? (bits & 0x007fffffu) | 0x3f800000u : bits);
         float w[EACH];
         load_row<float, LANES, EACH, V>(a.w, lane, C, w);
 #pragma unroll
@@ -138,15 +144,15 @@ __global__ void __launch_bounds__(LANES == 32 ? kNormThreads : LANES) norm_forwa
             for (int j = 0; j < EACH / V; ++j) {
                 const int at = (j * LANES + lane) * V;
                 if (at >= C) continue;
-                const float most = top[j] * (rstd / power);
+                const float most = top[j] * rstd;
                 const bool nothing = most < 7.7037197775489434e-34f;  // 2^-110
                 const float inverse = nothing ? 0.f : 448.f / top[j];
                 Vec<unsigned char, V> q;
 #pragma unroll
                 for (int i = 0; i < V; ++i) q.v[i] = __nv_cvt_float_to_fp8(v[j * V + i] * inverse, __NV_SATFINITE, __NV_E4M3);
-                *reinterpret_cast<Vec<unsigned char, V> *>(a.q + row * C + at) = q;
+                *reinterpret_cast<Vec<unsigned char, V> *>(a.q + (long long)row * C + at) = q;
                 if (a.block == 0 ? at == 0 : at % 128 == 0)
-                    a.scales[row * a.blocks + (a.block == 0 ? 0 : at / 128)] = nothing ? 0.f : most / 448.f;
+                    a.scales[(long long)row * a.blocks + (a.block == 0 ? 0 : at / 128)] = nothing ? 0.f : most / 448.f;
             }
         }
     }
