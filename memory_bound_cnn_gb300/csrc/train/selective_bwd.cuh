@@ -39,7 +39,7 @@ template <bool FIRST> __device__ __forceinline__ void mma(float (&d)[4], uint32_
 // values has an r of its own.  The tensor cores read a value's leading 11 bits and leave the rest out.  For sums that
 // are stored in bf16 that is enough: cut to 11 bits, m 2^e with 1 <= m < 2 loses less than 2^-10 2^e, half of that on
 // average; with a factor 1 + 3 x 2^-13 on the sum, each is off by -6.1e-4 to 3.7e-4 of itself, at random, where rounding the
-// sum to bf16 costs up to 3.9e-3 (8 x 4096 x 1024 with 16 states: 906 us; 1172 in fp32, where the rest enters too).  In other types
+// sum to bf16 costs up to 3.9e-3 (8 x 4096 x 1024 with 16 states: 831 us; 1158 in fp32, where the rest enters too).  In other types
 // it enters as a second product, which keeps 22 bits.
 // Then warps meet in shared memory, and CTAs in selective_sums_kernel.
 // With 8 and with 64 states the lanes hold half of a block's states at a time and recompute the first half twice: fewer
