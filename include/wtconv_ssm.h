@@ -36,13 +36,15 @@
  *     overlap themselves, and no output may overlap an input or another output.
  *   - dtype is the type of the activations, their gradients and the convolution's states; A, D, dt_bias, h0,
  *     h_last, the scan's states, w, bias and their gradients are fp32 and contiguous.  The recurrence and all
- *     sums run in fp32; an activation is rounded once, when it is stored.  A is finite.
+ *     sums run in fp32; an activation is rounded once, when it is stored.  (Of each product that the scan's dB
+ *     and dC sum over channels the leading 22 bits enter, in every dtype: it is off by less than 2^-21 of itself.)  A is
+ *     finite.
  *   - Pointers need only their element's alignment.
  *   - 0 < B, T, C; B*C, C*N and C*K < 2^31 (the convolution's C < 2^29); T <= 2^30;
  *     N <= WTCONV_SELECTIVE_MAX_STATES; C a multiple of G; for the scan's backward B*G*ceil(T / 32) < 2^31.
  *   - A value that is not finite stays in its sequence and channel, as the formulas have it, but in the scan's dB and
- *     dC: there it also reaches the other states of its four neighbours 4i to 4i+3 and the other of its two
- *     positions 2i and 2i+1 (the tensor cores add them up with factors of 0 and 1).
+ *     dC: there it is a NaN, which also reaches the other states of its four neighbours 4i to 4i+3 and the other of
+ *     its two positions 2i and 2i+1 (the tensor cores add them up with factors of 0 and 1).
  *   - Results are the same from call to call (no atomics; sums in a fixed order).
  */
 #ifndef WTCONV_SSM_H

@@ -9,8 +9,6 @@
 
 namespace wtconv {
 
-constexpr float kSelCut = 1.0003662109375f;  // 1 + 3 x 2^-13
-
 // d += A B with A 16 x 8 and B 8 x 8: of A, a lane holds (row, column) (lane / 4, lane % 4) in `low` and (8 + lane / 4,
 // 4 + lane % 4) in `high`, the rest is 0; of B (lane % 4, lane / 4) and (4 + lane % 4, lane / 4); of d (lane / 4, 2 (lane %
 // 4) + 0 and 1), then the same of row 8 + lane / 4.
@@ -36,14 +34,13 @@ template <bool FIRST> __device__ __forceinline__ void mma(float (&d)[4], uint32_
 // for two positions at a time, the lanes' values of state s of B or C are the columns of a matrix whose rows are
 // four channels at one position and the same four at the other, and a product with a matrix of ones in row r of
 // the first four columns and row 8 + r of the others leaves the sums in row r (one position) and 8 + r; each of the 8
-// values has an r of its own.  The tensor cores read a value's leading 11 bits and leave the rest out.  For sums that
-// are stored in bf16 that is enough: cut to 11 bits, m 2^e with 1 <= m < 2 loses less than 2^-10 2^e, half of that on
-// average; with a factor 1 + 3 x 2^-13 on the sum, each is off by -6.1e-4 to 3.7e-4 of itself, at random, where rounding the
-// sum to bf16 costs up to 3.9e-3 (8 x 4096 x 1024 with 16 states: 831 us; 1158 in fp32, where the rest enters too).  In other types
-// it enters as a second product, which keeps 22 bits.
+// values has an r of its own.  The tensor cores read a value's leading 11 bits and leave the rest out; the rest enters as
+// a second product, of which they read 11 bits again: a value loses less than 2^-21 of itself, in every type.  (8 x 4096 x
+// 1024 with 16 states in bf16: 1087 us, with the leading bits alone 812; but where the channels' values cancel to a hundredth, what
+// they lose is then six times what rounding the sum to bf16 costs.  The rests of two values at once, as pairs: 1135.)
 // Then warps meet in shared memory, and CTAs in selective_sums_kernel.
 // With 8 and with 64 states the lanes hold half of a block's states at a time and recompute the first half twice: fewer
-// registers are worth it there (8 x 4096 x 1024 in bf16: 565 us instead of 612 with 8 states, 1143 instead of 821 with 16).
+// registers are worth it there (8 x 4096 x 1024 in bf16: 720 us instead of 812 with 8 states, 1214 instead of 1087 with 16).
 // LOCAL: only the gradient that the segment's beginning passes on if nothing enters at its end, and the sum
 // of its steps; the CTAs of earlier segments begin with what these compose to.
 template <int LANES, bool PLANES> struct BackwardShared {
@@ -297,7 +294,6 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
         const auto scan = [&](auto full) {
             constexpr bool FULL = decltype(full)::value;
             constexpr int TOGETHER = L::TOGETHER;
-            constexpr bool CUT = std::is_same<T, __nv_bfloat16>::value;  // products are cut to 11 bits
             Quad dA_block = {Pair(0.f), Pair(0.f)};
             const auto advance = [&](const Quad &h, int t) {
                 const float2 q = s.coef[L::coef(t, c)];
@@ -383,10 +379,9 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
                         const uint32_t h0 = __float_as_uint(v0[r]), h1 = __float_as_uint(v1[r]);
                         if (r == 0) mma<true>(sums, one[r], one[r], h0, h1);
                         else mma<false>(sums, one[r], one[r], h0, h1);
-                        if (!CUT) {  // what the product with the upper 11 bits left
-                            const float l0 = v0[r] - __uint_as_float(h0 & 0xffffe000u), l1 = v1[r] - __uint_as_float(h1 & 0xffffe000u);
-                            mma<false>(sums, one[r], one[r], __float_as_uint(l0), __float_as_uint(l1));
-                        }
+                        // what the product with the upper 11 bits left
+                        const float l0 = v0[r] - __uint_as_float(h0 & 0xffffe000u), l1 = v1[r] - __uint_as_float(h1 & 0xffffe000u);
+                        mma<false>(sums, one[r], one[r], __float_as_uint(l0), __float_as_uint(l1));
                     }
                 }
             }
@@ -430,7 +425,6 @@ template <typename T, int LANES, bool PLANES> __global__ void __launch_bounds__(
                 v.a = add(v.a, q.a), v.b = add(v.b, q.b);
             }
         }
-        if (std::is_same<T, __nv_bfloat16>::value) v.a = mul(v.a, Pair(kSelCut)), v.b = mul(v.b, Pair(kSelCut));  // of cut products
         const int j = e % WIDTH, t = e / WIDTH;
         sums[j][t] = v.a.lo(), sums[j + 1][t] = v.a.hi(), sums[j + 2][t] = v.b.lo(), sums[j + 3][t] = v.b.hi();
     }

@@ -96,8 +96,8 @@ template <int LANES> struct Roles {
     static __device__ __forceinline__ bool scans() { return threadIdx.x < SCANNERS; }
     static __device__ __forceinline__ int helper() { return threadIdx.x - SCANNERS; }
     // Registers of a thread, from what the CTA was launched with: scanners take what helpers give.  Whole groups of four
-    // warps do so together; the sum over the CTA stays.  (16 states in bf16: 184 and 72 take 1126 us where 176 and 80 take
-    // 838 and 168 and 88 858; in fp32, whose helpers hold wider words, 168 and 88 take 1267, 144 and 112 1140.)
+    // warps do so together; the sum over the CTA stays.  (8 x 4096 x 1024 with 16 states in bf16: 184 and 72 take 1143 us where
+    // 176 and 80 take 1087 and 168 and 88 1100; in fp32, whose helpers hold wider words, 160 and 96 take 1227, 144 and 112 1136.)
     static constexpr bool TRADE = LANES >= 4;
     static constexpr int LAUNCHED = LANES == 4 ? 128 : LANES == 8 ? 168 : 96, GROUPS = SCANNERS / 128;
     template <typename T> static constexpr int GIVEN = LANES == 4 ? (sizeof(T) == 4 ? 16 : 48) : LANES == 8 ? 64 : 32;  // by a helper
