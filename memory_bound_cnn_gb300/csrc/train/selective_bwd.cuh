@@ -250,9 +250,9 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
 #pragma unroll 4
             for (int k = (at_.length - 1) / a.segment; k > at_.segment; --k) {
                 const long long i = ((long long)b * a.segments + k) * a.s.C + at_.c0 + c;
-                const Pair d(a.steps[i]);
+                const Pair d(0.25f * a.steps[i]);
                 const Quad u = quad_of(*reinterpret_cast<const float4 *>(a.ends + i * L::PAD + n0));
-                carry.a = fma(exp2_fast(mul(d, decay.a)), carry.a, u.a), carry.b = fma(exp2_fast(mul(d, decay.b)), carry.b, u.b);
+                carry.a = through_part(mul(d, decay.a), carry.a, u.a), carry.b = through_part(mul(d, decay.b), carry.b, u.b);
             }
     }
     float step_sum = 0.f;

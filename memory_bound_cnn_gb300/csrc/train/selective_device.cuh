@@ -30,6 +30,14 @@ constexpr float kSelRaise = 2.0e-8f;  // log2(1 + 1.4e-8)
 __device__ __forceinline__ Pair decays_of(Pair d, Pair rate) { return exp2_fast(fma(d, rate, Pair(kSelRaise))); }
 __device__ __forceinline__ Pair decays_again(Pair d, Pair rate) { return exp2_again(fma(d, rate, Pair(kSelRaise))); }
 
+// What a part of a sequence makes of the states h that enter it: exp2 of 4 q times h, and u.  The decay over a part may leave
+// the range of fp32 where the product does not (and is 0 where h is), so it is multiplied up in four steps.  Bounded at
+// 2^127, each of them is finite; four such take all but a 0 past the range, as the decay would.
+__device__ __forceinline__ Pair through_part(Pair q, Pair h, Pair u) {
+    const Pair f = exp2_fast(Pair(fminf(q.lo(), 127.f), fminf(q.hi(), 127.f)));
+    return fma(mul(mul(mul(h, f), f), f), f, u);
+}
+
 // softplus(v) = max(v, 0) + log(1 + e) with e = exp(-|v|) in (0, 1]: nothing cancels.  With s = e / (2 + e)
 // <= 1/3, log(1 + e) = 2 artanh s = 2 (s + s^3/3 + ... + s^13/13); the next term is 1.4e-8 of the value.
 __device__ __forceinline__ Pair exp_of_minus_abs(Pair v) {

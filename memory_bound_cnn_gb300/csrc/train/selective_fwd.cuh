@@ -132,9 +132,9 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES == 2 ? 3 : LANES 
 #pragma unroll 4
             for (int k = 0; k < at_.segment; ++k) {
                 const long long i = ((long long)b * a.segments + k) * a.s.C + at_.c0 + c;
-                const Pair d(a.steps[i]);
+                const Pair d(0.25f * a.steps[i]);
                 const Quad u = quad_of(*reinterpret_cast<const float4 *>(a.ends + i * L::PAD + n0));
-                h.a = fma(exp2_fast(mul(d, decay.a)), h.a, u.a), h.b = fma(exp2_fast(mul(d, decay.b)), h.b, u.b);
+                h.a = through_part(mul(d, decay.a), h.a, u.a), h.b = through_part(mul(d, decay.b), h.b, u.b);
             }
     }
     float step_sum = 0.f;

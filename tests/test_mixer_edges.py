@@ -1,8 +1,15 @@
-"""Corners of the selective scan: sums over channels that cancel."""
+"""Corners of the selective scan: sums over channels that cancel, parts of a sequence whose decays leave the range of
+fp32."""
+import ctypes
+
+import numpy as np
 import pytest
 import ssm_reference as R
 import torch
 from test_selective import DTYPES, LAYOUTS, make, reference, run
+
+from memory_bound_cnn_gb300 import scan as S
+from memory_bound_cnn_gb300 import ssm as M
 
 
 # ------------------------------------------------------------------------ sums over channels
@@ -24,3 +31,55 @@ def test_sums_over_channels_that_cancel(N, dtype, layout):
     got, want = run(d, layout), reference(d, layout)
     for k in ("dB", "dC"):
         R.assert_within(k, got[k].movedim(1 if layout == "tokens" else -1, 0), *want[k], dtype)
+
+
+# ------------------------------------------------------------------------- parts of a sequence
+
+def parted(dt, A, **of_positions):
+    """A sequence of 256 positions of few channels, cut into parts, whose steps are dt (256,)."""
+    T, C, N = 256, 6, 4
+    size = M._load().wtconv_selective_workspace_size(S.OP_SCAN_FORWARD, ctypes.byref(M.SelectiveShape(1, T, C, N, 1, 1, 0, 0)))
+    assert size > 0  # (in one part the forward needs no workspace)
+    d = make(1, T, C, N, "tokens", torch.float32, seed=3, softplus=False, absent=("dt_bias",))
+    d["dt"].copy_(dt[None, :, None].expand(1, T, C))
+    d["A"] = torch.tensor(A, device="cuda").repeat(C, 1)
+    for k, keep in of_positions.items():  # 0 at other positions
+        d[k] *= keep[None, :, None]
+    return d
+
+
+def check_parted(d, layout):
+    """All results against the definition, which knows no parts, in tokens and as planes; not those that fp32 cannot hold."""
+    if layout == "planes":
+        d = {**d, **{k: d[k].movedim(1, -1).contiguous() for k in ("x", "dt", "z", "dy", "B", "C")}}
+    got, want = run(d, layout), reference(d, layout)
+    for k, t in got.items():
+        if t is not None and np.abs(want[k][0]).max() < torch.finfo(torch.float32).max:
+            inner = k in ("y", "dx", "d_dt", "dB", "dC", "dz")
+            R.assert_within(k, t.movedim(1 if layout == "tokens" else -1, 0) if inner else t, *want[k])
+    return got
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_growth_over_parts_that_hold_nothing(layout):
+    """States grow by exp(128) in a part of 64 positions, but are 0 up to the last 8; so are the gradients behind the
+    first 8."""
+    at = torch.arange(256, device="cuda")
+    d = parted(torch.full((256,), 2.0, device="cuda"), [1.0, 0.5, -1.0, 2.0], x=at >= 248, dy=at < 8)
+    d["h0"] = d["dh_last"] = None
+    got = check_parted(d, layout)
+    assert (got["h_last"] != 0).all() and (got["dx"].movedim(1 if layout == "tokens" else -1, 0)[:8] != 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("rate,size", [(1.0, 1e-30), (-1.0, 1e30)])
+def test_a_part_whose_factor_leaves_the_range(rate, size, layout):
+    """Over 48 positions of the second part the states change by exp(96) or exp(-96), which is no normal fp32 number; what
+    they make of a state of 1e-30 or 1e30 is.  (Of 1e30, d_dt and dA are not: a state times its gradient times exp(-24), 4e49.)"""
+    at = torch.arange(256, device="cuda")
+    zone = (at >= 64) & (at < 112)
+    d = parted(2.0 * zone, [rate, 0.5 * rate, 0.25 * rate, rate], x=~zone, dy=at < 64)
+    d["h0"], d["dh_last"] = d["h0"] * size, d["dh_last"] * size
+    check_parted(d, layout)
