@@ -415,7 +415,7 @@ template <typename T, int K, int V, bool SILU> __global__ void __launch_bounds__
 #pragma unroll
             for (int i = 0; i < V + K - 1; ++i) {
                 g[i] = t0 + i < s.length ? g[i] * slope[i] : 0.f;
-                if (i >= V) continue;
+                if (i >= V || t0 + i >= s.length) continue;  // (past the length: inputs before it may be infinite, 0 times them is not 0)
                 db += g[i];
 #pragma unroll
                 for (int k = 0; k < K; ++k) dw[k] = fmaf(g[i], in[i + k], dw[k]);

@@ -1,10 +1,11 @@
-"""Corners of the selective scan: sums over channels that cancel, parts of a sequence whose decays leave the range of
-fp32."""
+"""Corners of the selective scan and the causal convolution: sums over channels that cancel, parts of a sequence whose
+decays leave the range of fp32, inputs that are not finite."""
 import ctypes
 
 import numpy as np
 import pytest
 import ssm_reference as R
+import test_causal
 import torch
 from test_selective import DTYPES, LAYOUTS, make, reference, run
 
@@ -83,3 +84,25 @@ def test_a_part_whose_factor_leaves_the_range(rate, size, layout):
     d = parted(2.0 * zone, [rate, 0.5 * rate, 0.25 * rate, rate], x=~zone, dy=at < 64)
     d["h0"], d["dh_last"] = d["h0"] * size, d["dh_last"] * size
     check_parted(d, layout)
+
+
+# --------------------------------------------------------------------- what is not finite
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dtype", DTYPES, ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("K", [2, 3, 4])
+def test_an_infinite_last_input_reaches_the_last_tap_alone(K, dtype, layout):
+    """The input at a sequence's last position meets the last tap only; positions past the length sum nothing."""
+    T, C, lengths = 16, 5, [5, 16, 10, 7]
+    d = test_causal.make(4, T, C, K, layout, dtype, seed=K, lengths=lengths, silu=False)
+    x = d["x"] if layout == "tokens" else d["x"].transpose(1, 2)
+    for b, n in enumerate(lengths):
+        x[b, n - 1] = 0
+    want = test_causal.reference(d, layout)  # (of the other taps: their sums do not have that input)
+    for b, n in enumerate(lengths):
+        x[b, n - 1] = float("inf")
+    got = test_causal.run(d, layout)
+    R.assert_within("dw", got["dw"][:, :-1], want["dw"][0][:, :-1], want["dw"][1][:, :-1])
+    R.assert_within("d_bias", got["d_bias"], *want["d_bias"])
+    assert not torch.isfinite(got["dw"][:, -1]).any()
