@@ -150,6 +150,12 @@ class _Refused(torch.autograd.Function):
         raise RuntimeError(f"the {ctx.what} has no second derivative")
 
 
+def _recorded(*inputs):
+    """Whether a backward can follow on these inputs.  (To be asked before Function.apply: in its forward gradients are off, and
+    ``needs_input_grad`` does not tell that they were off before.)"""
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)
+
+
 def _gradients(what, run, *inputs):
     """run(), whose results depend on ``inputs``; under ``create_graph`` such that their derivative is refused."""
     return _Refused.apply(what, run, *inputs) if torch.is_grad_enabled() else run()
@@ -157,12 +163,12 @@ def _gradients(what, run, *inputs):
 
 class WTConvSelectiveFunction(torch.autograd.Function):
     """Autograd wrapper: (y, h_last) through wtconv_selective_forward, gradients through wtconv_selective_backward.
-    A derivative of those gradients (``create_graph=True``) is refused."""
+    A derivative of those gradients (``create_graph=True``) is refused.  Without ``keep`` no backward can follow."""
 
     @staticmethod
-    def forward(ctx, x, dt, A, B, C, D, z, dt_bias, h0, lengths, layout, softplus):
+    def forward(ctx, x, dt, A, B, C, D, z, dt_bias, h0, lengths, layout, softplus, keep=True):
         y, h_last, states = wtconv_selective_forward(x, dt, A, B, C, D, z, dt_bias, h0, lengths, layout, softplus,
-                                                     keep_states=any(ctx.needs_input_grad))
+                                                     keep_states=keep and any(ctx.needs_input_grad))
         ctx.save_for_backward(x, dt, A, B, C, D, z, dt_bias, lengths, states)
         ctx.how = layout, softplus
         ctx.h0 = h0  # for its place in the graph only: the backward does not read its values, which may change
@@ -179,12 +185,13 @@ class WTConvSelectiveFunction(torch.autograd.Function):
             return wtconv_selective_backward(x, dt, A, B, C, states, dy, D, z, dt_bias, _rows(dh_last), lengths, layout, softplus)
 
         dx, d_dt, dA, dB, dC, dD, dz, d_bias, d_h0 = _gradients("selective scan", run, x, dt, A, B, C, D, z, dt_bias, ctx.h0, dy, dh_last)
-        return dx, d_dt, dA, dB, dC, dD, dz, d_bias, None if ctx.h0 is None else d_h0, None, None, None
+        return dx, d_dt, dA, dB, dC, dD, dz, d_bias, None if ctx.h0 is None else d_h0, None, None, None, None
 
 
 def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, lengths=None, layout="planes", softplus=True):
     """Differentiable selective scan: (y, h_last); arguments as wtconv_selective_forward's.  First derivatives only."""
-    return WTConvSelectiveFunction.apply(x, dt, A, B, C, D, z, dt_bias, h0, lengths, layout, softplus)
+    keep = _recorded(x, dt, A, B, C, D, z, dt_bias, h0)
+    return WTConvSelectiveFunction.apply(x, dt, A, B, C, D, z, dt_bias, h0, lengths, layout, softplus, keep)
 
 
 class WTConvCausalFunction(torch.autograd.Function):

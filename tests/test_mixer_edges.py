@@ -1,5 +1,5 @@
 """Corners of the selective scan and the causal convolution: sums over channels that cancel, parts of a sequence whose
-decays leave the range of fp32, inputs that are not finite."""
+decays leave the range of fp32, inputs that are not finite, calls without gradients."""
 import ctypes
 
 import numpy as np
@@ -106,3 +106,30 @@ def test_an_infinite_last_input_reaches_the_last_tap_alone(K, dtype, layout):
     R.assert_within("dw", got["dw"][:, :-1], want["dw"][0][:, :-1], want["dw"][1][:, :-1])
     R.assert_within("d_bias", got["d_bias"], *want["d_bias"])
     assert not torch.isfinite(got["dw"][:, -1]).any()
+
+
+# ------------------------------------------------------------------------ without gradients
+
+def test_states_are_kept_for_a_backward_only(monkeypatch):
+    """Under no_grad, and where no input needs a gradient, the forward is not asked for what the backward reads."""
+    kept = []
+
+    def forward(*args, keep_states=False, **kw):
+        kept.append(keep_states)
+        x = args[0]
+        return x.clone(), x.new_zeros(2), (x.new_zeros(1) if keep_states else None)
+
+    monkeypatch.setattr(M, "wtconv_selective_forward", forward)
+    x, w = torch.zeros(1, 2, 3), torch.zeros(2, requires_grad=True)
+
+    def call(w):
+        return M.selective_scan(x, x, w, x, x)
+
+    with torch.no_grad():
+        y, _ = call(w)
+    assert kept == [False] and not y.requires_grad
+    with torch.inference_mode():
+        call(w)
+    call(w.detach())
+    y, _ = call(w)
+    assert kept == [False, False, False, True] and y.requires_grad
