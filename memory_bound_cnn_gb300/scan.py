@@ -96,6 +96,12 @@ def wtconv_scan_step(x, gate, gate_bias, pool, slots=None, y=None, stream=None):
     return (_ext or _load_ext()).scan_step(x, gate, gate_bias, pool, slots, y, stream)
 
 
+def _recorded(*inputs):
+    """Whether a backward can follow on these inputs.  (To be asked before Function.apply: in its forward gradients are off, and
+    ``needs_input_grad`` does not tell that they were off before.)"""
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)
+
+
 class _ScanGradients(torch.autograd.Function):
     """wtconv_scan_backward as an operation of its own, so that a second derivative meets its refusal."""
 
@@ -111,12 +117,12 @@ class _ScanGradients(torch.autograd.Function):
 
 class WTConvScanFunction(torch.autograd.Function):
     """Autograd wrapper: (y, h_last) through wtconv_scan_forward, gradients through wtconv_scan_backward.
-    A derivative of those gradients (``create_graph=True``) is refused."""
+    A derivative of those gradients (``create_graph=True``) is refused.  Without ``keep`` no backward can follow."""
 
     @staticmethod
-    def forward(ctx, x, gate, gate_bias, h0, lengths, layout):
+    def forward(ctx, x, gate, gate_bias, h0, lengths, layout, keep=True):
         y, h_last, states = wtconv_scan_forward(x, gate, gate_bias, h0, lengths, layout,
-                                                keep_states=any(ctx.needs_input_grad))
+                                                keep_states=keep and any(ctx.needs_input_grad))
         ctx.save_for_backward(x, gate, gate_bias, states, lengths)
         ctx.layout = layout
         ctx.h0 = h0  # for its place in the graph only: the backward does not read its values, which may change
@@ -133,9 +139,9 @@ class WTConvScanFunction(torch.autograd.Function):
         else:
             grads = wtconv_scan_backward(x, gate, gate_bias, states, dy, dh_last, lengths, ctx.layout)
         dx, d_gate, d_bias, d_h0 = grads
-        return dx, d_gate, d_bias, None if ctx.h0 is None else d_h0, None, None
+        return dx, d_gate, d_bias, None if ctx.h0 is None else d_h0, None, None, None
 
 
 def gated_scan(x, gate, gate_bias, h0=None, lengths=None, layout="planes"):
     """Differentiable gated scan: (y, h_last); arguments as wtconv_scan_forward's.  First derivatives only."""
-    return WTConvScanFunction.apply(x, gate, gate_bias, h0, lengths, layout)
+    return WTConvScanFunction.apply(x, gate, gate_bias, h0, lengths, layout, _recorded(x, gate, gate_bias, h0))

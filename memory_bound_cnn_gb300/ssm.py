@@ -18,6 +18,7 @@ import ctypes
 
 import torch
 
+from .scan import _recorded
 from .wtconv import load, load_binding
 
 SELECTIVE_KEEP = 16        # WTCONV_SELECTIVE_KEEP
@@ -148,12 +149,6 @@ class _Refused(torch.autograd.Function):
     @staticmethod
     def backward(ctx, *grads):
         raise RuntimeError(f"the {ctx.what} has no second derivative")
-
-
-def _recorded(*inputs):
-    """Whether a backward can follow on these inputs.  (To be asked before Function.apply: in its forward gradients are off, and
-    ``needs_input_grad`` does not tell that they were off before.)"""
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)
 
 
 def _gradients(what, run, *inputs):

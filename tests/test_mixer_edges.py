@@ -110,7 +110,8 @@ def test_an_infinite_last_input_reaches_the_last_tap_alone(K, dtype, layout):
 
 # ------------------------------------------------------------------------ without gradients
 
-def test_states_are_kept_for_a_backward_only(monkeypatch):
+@pytest.mark.parametrize("operator", ["selective", "gated"])
+def test_states_are_kept_for_a_backward_only(operator, monkeypatch):
     """Under no_grad, and where no input needs a gradient, the forward is not asked for what the backward reads."""
     kept = []
 
@@ -120,10 +121,11 @@ def test_states_are_kept_for_a_backward_only(monkeypatch):
         return x.clone(), x.new_zeros(2), (x.new_zeros(1) if keep_states else None)
 
     monkeypatch.setattr(M, "wtconv_selective_forward", forward)
+    monkeypatch.setattr(S, "wtconv_scan_forward", forward)
     x, w = torch.zeros(1, 2, 3), torch.zeros(2, requires_grad=True)
 
     def call(w):
-        return M.selective_scan(x, x, w, x, x)
+        return M.selective_scan(x, x, w, x, x) if operator == "selective" else S.gated_scan(x, x, w)
 
     with torch.no_grad():
         y, _ = call(w)
