@@ -1,6 +1,6 @@
 // Short causal convolution of every channel along its sequence (wtconv_ssm.h).  Bound by memory: each activation
-// is read once (a strip's first K-1 inputs twice) and each result written once, in vectors of 16 bytes where
-// addresses allow it.
+// is read once (a strip's first K-1 inputs twice) and each result written once.  Where addresses allow it, a thread of
+// planes takes 16 bytes at once (8 in the backward of 16-bit types), one of tokens a pair of channels.
 #pragma once
 
 #include "causal.h"

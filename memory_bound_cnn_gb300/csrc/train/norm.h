@@ -22,7 +22,8 @@ struct NormArgs {
     float *part;         // [grid][C]: dw of a CTA's rows
 };
 
-// CTAs of the backward for this shape: as many as are resident, or fewer where there are fewer rows.
+// CTAs of the backward for this shape, 1024 threads to an SM, or fewer where there are fewer rows.  As many run at once with 512
+// < C <= 2048; with other widths registers let a half to three quarters of them, and the others follow.
 int norm_backward_grid(int rows, int C);
 
 // T: of the activations, R: of the residual stream

@@ -50,7 +50,7 @@ bool pairs(const SelectiveArgs &a) {
 // Time is counted in rounds of 32 positions of a CTA that has an SM for itself: two that share one take 1.3
 // times as long, three 1.6, and more wait; a part's first and last
 // rounds add some (ends).  (8 x 4096 x 1024 tokens with 16 states, 256 CTAs: forward 236 us in one part, 308
-// in two, the backward of that time 906 and 1032; 65,536 pixels of 64 channels, 2 CTAs: 62 us in 76 parts, 83 in 305.)
+// in two, the backward of that time 906 and 1032; 65,536 pixels of 64 channels, 2 CTAs: 62 us in 76 parts, 52 in the 147 that this gives.)
 void plan(int op, SelectiveArgs &a) {
     const bool forward = op == WTCONV_SCAN_OP_FORWARD;
     const int sms = sm_count(), rounds = ceil_div(a.s.T, kSelRound), most = std::max(1, std::min(rounds / 2, 256));

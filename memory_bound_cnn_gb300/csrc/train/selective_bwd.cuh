@@ -36,8 +36,8 @@ template <bool FIRST> __device__ __forceinline__ void mma(float (&d)[4], uint32_
 // the first four columns and row 8 + r of the others leaves the sums in row r (one position) and 8 + r; each of the 8
 // values has an r of its own.  The tensor cores read a value's leading 11 bits and leave the rest out; the rest enters as
 // a second product, of which they read 11 bits again: a value loses less than 2^-21 of itself, in every type.  (8 x 4096 x
-// 1024 with 16 states in bf16: 1087 us, with the leading bits alone 812; but where the channels' values cancel to a hundredth, what
-// they lose is then six times what rounding the sum to bf16 costs.  The rests of two values at once, as pairs: 1135.)
+// 1024 with 16 states in bf16: 1087 us, with the leading bits alone 812; but of sums whose channels cancel to a hundredth those are
+// 3.0e-2 off, where rounding to bf16 costs 1.7e-3.  The rests of two values at once, as pairs: 1135.)
 // Then warps meet in shared memory, and CTAs in selective_sums_kernel.
 // With 8 and with 64 states the lanes hold half of a block's states at a time and recompute the first half twice: fewer
 // registers are worth it there (8 x 4096 x 1024 in bf16: 720 us instead of 812 with 8 states, 1214 instead of 1087 with 16).

@@ -25,7 +25,8 @@ __device__ __forceinline__ Pair exp2_fast(Pair v) { return {exp2_fast(v.lo()), e
 
 // A position's decays of two states: exp2 of d times A log2 e.  The approximate exp2 of a value between -0.7 and 0 is low
 // by 1.4e-8 of itself on average (measured over 2^20 of them); a state multiplies it up for as many positions as it
-// remembers, a thousand and more, so the argument is raised by as much.
+// remembers, a thousand and more, so the argument is raised by as much.  That is the average of steps that differ: a channel
+// whose step is always the same has one argument, whose own error, up to two units, stays.
 constexpr float kSelRaise = 2.0e-8f;  // log2(1 + 1.4e-8)
 __device__ __forceinline__ Pair decays_of(Pair d, Pair rate) { return exp2_fast(fma(d, rate, Pair(kSelRaise))); }
 __device__ __forceinline__ Pair decays_again(Pair d, Pair rate) { return exp2_again(fma(d, rate, Pair(kSelRaise))); }

@@ -21,7 +21,7 @@ from memory_bound_cnn_gb300 import ssm as M
 @pytest.mark.parametrize("N", [5, 16, 32, 64])
 def test_sums_over_channels_that_cancel(N, dtype, layout):
     """Channels in pairs whose products differ in sign and, by about 1/64, in size: dB and dC are as exact as sums in fp32
-    of the products, and rounded once."""
+    of the products, and rounded once.  (The other tests' bounds for bf16 would allow products of 11 bits.)"""
     d = make(2, 50, 64, N, layout, dtype, seed=N)
     for k, factor in (("x", 1 + 1 / 64), ("dt", 1), ("z", 1), ("dy", -1)):
         channels = d[k] if layout == "tokens" else d[k].transpose(1, 2)
