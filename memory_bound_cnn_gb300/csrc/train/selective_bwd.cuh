@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES <= 4 ? 2 : 1) sel
     const long long row = (long long)b * a.s.C + at_.c0 + c;  // of [B][C]
     Quad decay = {Pair(0.f), Pair(0.f)}, carry = decay, dA = decay;
     if (live) {
-        decay = load_quad(a.in.A + (long long)(at_.c0 + c) * N, n0, N);
+        decay = load_rates(a.in.A + (long long)(at_.c0 + c) * N, n0, N);
         decay.a = mul(decay.a, Pair(kSelLog2E)), decay.b = mul(decay.b, Pair(kSelLog2E));
     }
     if (!LOCAL && live) {

@@ -267,6 +267,12 @@ __device__ __forceinline__ Quad load_quad(const float *row, int n0, int N) {
     const float v2 = n0 + 2 < N ? row[n0 + 2] : 0.f, v3 = n0 + 3 < N ? row[n0 + 3] : 0.f;
     return {Pair(v0, v1), Pair(v2, v3)};
 }
+// Rates of the lane's states; those past N have the last one's.  They hold 0 and pass on 0 whatever the step is: with a rate of
+// 0 an infinite step, whose decay is 0, would be a NaN there, and flow back to all positions before it.
+__device__ __forceinline__ Quad load_rates(const float *row, int n0, int N) {
+    const int last = N - 1;
+    return {Pair(row[min(n0, last)], row[min(n0 + 1, last)]), Pair(row[min(n0 + 2, last)], row[min(n0 + 3, last)])};
+}
 __device__ __forceinline__ void store_quad(float *row, int n0, int N, const Quad &q) {
     if (n0 < N) row[n0] = q.a.lo();
     if (n0 + 1 < N) row[n0 + 1] = q.a.hi();

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(Roles<LANES>::THREADS, LANES == 2 ? 3 : LANES 
     const bool live = c < at_.channels;
     Quad decay = {Pair(0.f), Pair(0.f)}, h = {Pair(0.f), Pair(0.f)};
     if (live) {
-        decay = load_quad(a.in.A + (long long)(at_.c0 + c) * N, n0, N);
+        decay = load_rates(a.in.A + (long long)(at_.c0 + c) * N, n0, N);
         decay.a = mul(decay.a, Pair(kSelLog2E)), decay.b = mul(decay.b, Pair(kSelLog2E));
     }
     if (!LOCAL && live) {
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(128) selective_step_kernel(const __grid_consta
             h = quad_of(*reinterpret_cast<const float4 *>(row + n0));
             A = quad_of(*reinterpret_cast<const float4 *>(a.in.A + (long long)c * N + n0));
         } else if (!WIDE) {
-            h = load_quad(row, n0, N), A = load_quad(a.in.A + (long long)c * N, n0, N);
+            h = load_quad(row, n0, N), A = load_rates(a.in.A + (long long)c * N, n0, N);
         }
         const T *bp = static_cast<const T *>(a.in.Bm.p) + b * a.in.Bm.row + state;
         const T *cp = static_cast<const T *>(a.in.Cm.p) + b * a.in.Cm.row + state;

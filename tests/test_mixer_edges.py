@@ -108,6 +108,24 @@ def test_an_infinite_last_input_reaches_the_last_tap_alone(K, dtype, layout):
     assert not torch.isfinite(got["dw"][:, -1]).any()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("T", [40, 256])  # in one part, and in several
+@pytest.mark.parametrize("N", [1, 5, 16])
+def test_an_infinite_step_lets_nothing_flow_back(N, T, layout):
+    """exp(d A) is 0 where d is infinite and A negative: before it the gradients are those of a sequence that ends there,
+    for any number of states."""
+    d = make(1, T, 6, N, layout, torch.float32, seed=4)
+    ended = {**d, "lengths": torch.tensor([20], dtype=torch.int32, device="cuda"), "dh_last": None}
+    want = reference(ended, layout)
+    d["dt"] = d["dt"].clone()
+    (d["dt"][0] if layout == "tokens" else d["dt"][0].T)[20] = float("inf")
+    got = run(d, layout)
+    for k in ("dx", "d_dt"):
+        t = got[k].movedim(1 if layout == "tokens" else -1, 0)
+        R.assert_within(k, t[:20], want[k][0][:20], want[k][1][:20])
+
+
 # ------------------------------------------------------------------------ without gradients
 
 @pytest.mark.parametrize("operator", ["selective", "gated"])
