@@ -43,9 +43,8 @@
  *   - 0 < B, T, C; B*C, C*N and C*K < 2^31 (the convolution's C < 2^29); T <= 2^30;
  *     N <= WTCONV_SELECTIVE_MAX_STATES; C a multiple of G; for the scan's backward B*G*ceil(T / 32) < 2^31.
  *   - A value that is not finite stays in its sequence and channel, where the formulas have it (an infinity of theirs
- *     may come out as a NaN), but in the scan's dB and dC: there it is a NaN, which also reaches the other states of its
- *     four neighbours 4i to 4i+3 and the other of its two positions 2i and 2i+1 (the tensor cores add them up with
- *     factors of 0 and 1).
+ *     may come out as a NaN), but in the scan's dB and dC: where one of them is not finite, both are NaN for four states
+ *     4i to 4i+3 at two positions 2i and 2i+1 (the tensor cores add them up together, with factors of 0 and 1).
  *   - Results are the same from call to call (no atomics; sums in a fixed order).
  */
 #ifndef WTCONV_SSM_H

@@ -7,7 +7,7 @@ import pytest
 import ssm_reference as R
 import test_causal
 import torch
-from test_selective import DTYPES, LAYOUTS, make, reference, run
+from test_selective import DTYPES, LAYOUTS, make, reference, run, time_first
 
 from memory_bound_cnn_gb300 import scan as S
 from memory_bound_cnn_gb300 import ssm as M
@@ -124,6 +124,39 @@ def test_an_infinite_step_lets_nothing_flow_back(N, T, layout):
     for k in ("dx", "d_dt"):
         t = got[k].movedim(1 if layout == "tokens" else -1, 0)
         R.assert_within(k, t[:20], want[k][0][:20], want[k][1][:20])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("N", [5, 16, 40])
+@pytest.mark.parametrize("what,at", [("x", 21), ("C", 21), ("dh_last", 0), ("h0", 0)])
+def test_what_is_not_finite_stays_where_the_formulas_have_it(what, at, N, layout):
+    """Of one infinite input; dB and dC may be NaN for its four states and two positions, wherever either of them is not
+    finite."""
+    d = make(2, 50, 34, N, layout, torch.float32, G=2, seed=N)
+    if what in ("h0", "dh_last"):
+        d[what][1, 20, 3] = float("inf")
+    else:
+        row = d[what][1] if layout == "tokens" else d[what][1].movedim(-1, 0)
+        row[at][(3,) if what == "x" else (0, 3)] = float("inf")
+    got = run(d, layout)
+    ref = {"softplus": True, "lengths": None}
+    for name, k in (("x", "x"), ("dt", "dt"), ("z", "z"), ("dy", "dy"), ("Bm", "B"), ("Cm", "C")):
+        ref[name] = time_first(d[k], layout)
+    for k in ("A", "D", "dt_bias", "h0", "dh_last"):
+        ref[k] = d[k].double().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        want = {k: np.isfinite(v[0]) for k, v in R.selective(ref).items() if k != "cut"}
+    both = want["dB"] & want["dC"]
+    near = np.ones((50, 2, 2, -(-N // 4) * 4), bool)
+    near[:, :, :, :N] = both
+    near = near.reshape(25, 2, 2, 2, -1, 4).all((1, 5), keepdims=True)
+    near = np.broadcast_to(near, (25, 2, 2, 2, near.shape[4], 4)).reshape(50, 2, 2, -1)[..., :N]
+    for k, fine in want.items():
+        inner = k in ("y", "dx", "d_dt", "dB", "dC", "dz")
+        finite = np.isfinite(time_first(got[k], layout) if inner else got[k].cpu().numpy())
+        assert not (finite & ~fine).any(), k
+        assert finite[near if k in ("dB", "dC") else fine].all(), k
 
 
 # ------------------------------------------------------------------------ without gradients
